@@ -1,4 +1,4 @@
-"""Dropless MoE SwiGLU layer forward on one GB300 -- Python binding.
+"""Dropless MoE SwiGLU layer, and the operators around it, on one GB300 -- Python binding.
 
 Thin ctypes binding over the C ABI in ``include/moe.h`` (library
 ``libmoe_gb300.so`` built in-tree by ``build.py``).  Functions carry the C
@@ -26,6 +26,8 @@ __all__ = [
     "mxfp8_quantize", "mxfp8_scales_size", "mxfp8_act_scales_size", "permute_mxfp8",
     "grouped_gemm1_swiglu_mxfp8", "grouped_gemm2_mxfp8", "forward_mxfp8", "forward_mxfp8_views", "MoELayerMXFP8",
     "grouped_gemm2_combine", "grouped_gemm1_swiglu_gather", "last_device_status", "forward_fuses_permute",
+    "RouteRule", "RouteBuffers", "route_scored", "route_scored_backward", "NormResidual", "NormResidualGrads",
+    "norm_residual", "norm_residual_backward", "GradClipper", "MoEBlock",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -46,6 +48,11 @@ class _Layout(ctypes.Structure):
         "router_ws", "x_perm", "h", "y_perm", "x_dev", "y_dev", "total")]
 
 
+class _RouteRule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("n_group", ctypes.c_int), ("topk_group", ctypes.c_int),
+                ("group_top", ctypes.c_int), ("renorm", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
 class _LayoutBW(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in (
         "dw", "dl", "dl_row", "dy_perm", "dh", "a", "da", "dx_perm", "WrT", "rw_part", "tmaps", "total")]
@@ -64,7 +71,8 @@ def _load():
             f"{path} is missing: build the CUDA library first "
             "(python -c 'import __graft_entry__ as g; g.build()')")
     L = ctypes.CDLL(path)
-    P, I, S, U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64
+    P, I, S, U64, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64, ctypes.c_float
+    RULE = ctypes.POINTER(_RouteRule)
     sig = {
         "moe_status_string": (ctypes.c_char_p, [I]),
         "moe_abi_version": (I, []),
@@ -104,6 +112,16 @@ def _load():
         "moe_backward": (I, [P, P, P, P, P, I, I, I, I, I, P, P, S, P, P, P, P, P, P, P, S, P]),
         "moe_combine_counters_size": (S, [I, I]),
         "moe_grouped_gemm2_combine": (I, [P, P, I, I, I, I, P, P, P, P, I, I, P, P, S, P, P]),
+        "moe_route_scored": (I, [P, P, I, I, I, RULE, P, P, P, P, P, P, P, S, P]),
+        "moe_route_scored_backward": (I, [P, P, P, I, I, I, RULE, P, P]),
+        "moe_forward_scored": (I, [P, P, P, P, RULE, P, P, I, I, I, I, I, P, P, S, P, P]),
+        "moe_backward_scored": (I, [P, P, RULE, P, P, I, I, I, I, I, P, P, S, P, P, P, P, P, P, P, S, P]),
+        "moe_norm_residual": (I, [P, I, P, P, P, I, F, P, F, I, I, P, P, P, P, P]),
+        "moe_norm_residual_backward_workspace_size": (S, [I, I]),
+        "moe_norm_residual_backward": (I, [P, I, P, P, P, I, F, P, P, P, P, P, I, I, P, P, P, P, P, P, S, P]),
+        "moe_grad_norm_workspace_size": (S, [I]),
+        "moe_grad_norm": (I, [P, P, P, I, P, P, S, P]),
+        "moe_grad_norm_clip": (I, [P, P, P, P, I, F, P, P, S, P]),
         "moe_device_status": (I, [ctypes.POINTER(I)]),
         "moe_last_device_status": (I, [P, P]),
         "moe_check_bounded_wait": (I, [U64, P]),
@@ -206,6 +224,247 @@ def route(logits, K: int, workspace=None, stream=None) -> Routing:
                          _ptr(r.offsets), _ptr(r.row_of), _ptr(r.src_tok), _ptr(workspace),
                          workspace.numel() * workspace.element_size(), _stream(stream)), "moe_route")
     return r
+
+
+# ------------------------------------------------------------------ routing by scores
+@dataclass(frozen=True)
+class RouteRule:
+    """How route_scored chooses and weighs: ``score`` "sigmoid" or "softmax";
+    ``n_group`` runs of experts of which the ``topk_group`` best stay open, each
+    scored by its ``group_top`` (1 or 2) best experts; weights divided by their
+    sum (``renorm``) and times ``scale``."""
+    score: str = "sigmoid"
+    n_group: int = 1
+    topk_group: int = 1
+    group_top: int = 1
+    renorm: bool = True
+    scale: float = 1.0
+
+    def __post_init__(self):
+        if self.score not in ("sigmoid", "softmax"):
+            raise ValueError(f"score must be 'sigmoid' or 'softmax', got {self.score!r}")
+        object.__setattr__(self, "_c", _RouteRule(int(self.score == "softmax"), self.n_group, self.topk_group,
+                                                  self.group_top, int(self.renorm), self.scale))
+
+
+class RouteBuffers:
+    """The outputs and the workspace of route_scored for one size, to be used
+    again from call to call."""
+
+    def __init__(self, T: int, E: int, K: int, device="cuda"):
+        i32, n = torch.int32, route_workspace_size(T, E, K)
+        if n == 0:
+            raise MoEError(1, "moe_route_workspace_size")
+
+        def make(dtype, *shape):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+        self.size = (T, E, K)
+        self.routing = Routing(make(i32, T, K), make(torch.float32, T, K), make(i32, E), make(i32, E + 1),
+                               make(i32, T, K), make(i32, T * K))
+        self.workspace = make(torch.uint8, n)
+        r = self.routing
+        self._args = (_ptr(r.topk_idx), _ptr(r.topk_w), _ptr(r.counts), _ptr(r.offsets), _ptr(r.row_of),
+                      _ptr(r.src_tok), _ptr(self.workspace), n)
+
+
+def route_scored(logits, K: int, rule: RouteRule, sel_bias=None, buffers: RouteBuffers | None = None,
+                 stream=None) -> Routing:
+    """Routing by scores of all experts (see RouteRule); ``sel_bias`` [E] fp32
+    is added to the scores for the choice only.  Ties go to the lower expert.
+    ``buffers`` holds the outputs (then reused) and the workspace."""
+    T, E = logits.shape
+    _need(logits, torch.float32, (T, E), "logits")
+    if sel_bias is not None:
+        _need(sel_bias, torch.float32, (E,), "sel_bias")
+    if buffers is None:
+        buffers = RouteBuffers(T, E, K, logits.device)
+    elif buffers.size != (T, E, K):
+        raise ValueError(f"buffers are for (T, E, K) = {buffers.size}, not {(T, E, K)}")
+    _check(lib.moe_route_scored(_ptr(logits), _ptr(sel_bias), T, E, K, rule._c, *buffers._args, _stream(stream)),
+           "moe_route_scored")
+    return buffers.routing
+
+
+def route_scored_backward(logits, topk_idx, dw, rule: RouteRule, out=None, stream=None):
+    """dlogits [T, E] fp32 of sum(dw * topk_w) for the forward's choice."""
+    T, E = logits.shape
+    K = topk_idx.shape[1]
+    _need(logits, torch.float32, (T, E), "logits")
+    _need(topk_idx, torch.int32, (T, K), "topk_idx")
+    _need(dw, torch.float32, (T, K), "dw")
+    out = _empty((T, E), torch.float32, logits) if out is None else _need(out, torch.float32, (T, E), "dlogits")
+    _check(lib.moe_route_scored_backward(_ptr(logits), _ptr(topk_idx), _ptr(dw), T, E, K, rule._c, _ptr(out),
+                                         _stream(stream)), "moe_route_scored_backward")
+    return out
+
+
+# ------------------------------------------------------------------ norms, gate and residual
+@dataclass
+class NormResidual:
+    r: torch.Tensor                      # [T, d], the residual stream
+    n: torch.Tensor | None = None        # [T, d] bf16, what the next layer reads
+    rstd_post: torch.Tensor | None = None   # [T] fp32
+    rstd_pre: torch.Tensor | None = None    # [T] fp32
+
+    @classmethod
+    def empty(cls, T: int, d: int, dtype=torch.bfloat16, y=True, post=True, pre=True, device="cuda"):
+        """Output buffers of norm_residual: ``dtype`` of the residual stream;
+        with an output ``y`` to add, its norm (``post``) and the next norm (``pre``)."""
+        def make(on, dt, *shape):
+            return torch.empty(shape, dtype=dt, device=device) if on else None
+
+        return cls(make(y, dtype, T, d), make(pre, torch.bfloat16, T, d), make(post, torch.float32, T),
+                   make(pre, torch.float32, T))
+
+
+@dataclass
+class NormResidualGrads:
+    dr: torch.Tensor                        # [T, d], the residual's type
+    dy: torch.Tensor | None = None          # [T, d] bf16
+    dgamma_pre: torch.Tensor | None = None  # [d] fp32
+    dgamma_post: torch.Tensor | None = None
+    dgate: torch.Tensor | None = None       # shaped like the gate
+    workspace: torch.Tensor | None = None
+
+    @classmethod
+    def empty(cls, T: int, d: int, dtype=torch.bfloat16, y=True, post=True, pre=True, gate="none", device="cuda"):
+        """Output buffers of norm_residual_backward; ``gate``: "none", "channel" or "token"."""
+        def make(on, dt, *shape):
+            return torch.empty(shape, dtype=dt, device=device) if on else None
+
+        f32, n = torch.float32, int(lib.moe_norm_residual_backward_workspace_size(T, d))
+        if n == 0:
+            raise MoEError(2, "moe_norm_residual_backward_workspace_size")
+        return cls(make(True, dtype, T, d), make(y, torch.bfloat16, T, d), make(pre, f32, d), make(post, f32, d),
+                   make(gate != "none", f32, *((d,) if gate == "channel" else (T, 1))), make(True, torch.uint8, n))
+
+
+_GATES = ("none", "channel", "token")
+
+
+def _norm_args(r, y, gamma_post, gate, gamma_pre):
+    """T, d, whether the residual is fp32, the kind of gate; checked."""
+    T, d = r.shape
+    if r.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"the residual stream must be bfloat16 or float32, got {r.dtype}")
+    _need(r, r.dtype, (T, d), "r")
+    if y is not None:
+        _need(y, torch.bfloat16, (T, d), "y")
+    if gamma_post is not None:
+        _need(gamma_post, torch.float32, (d,), "gamma_post")
+    if gamma_pre is not None:
+        _need(gamma_pre, torch.float32, (d,), "gamma_pre")
+    kind = 0
+    if gate is not None:
+        kind = 1 if gate.dim() == 1 else 2
+        _need(gate, torch.float32, (d,) if kind == 1 else (T, 1), "gate")
+    return T, d, int(r.dtype == torch.float32), kind
+
+
+def norm_residual(r, y=None, *, gamma_post=None, gate=None, gamma_pre=None, res_scale: float = 1.0,
+                  eps: float = 1e-6, out: NormResidual | None = None, stream=None) -> NormResidual:
+    """What stands between two layers, in one kernel: r' = res_scale * r +
+    gate * norm(y) * gamma_post and n = norm(r') * gamma_pre (RMS norms; parts
+    without their tensor are left out).  r [T, d] bf16 or fp32, y [T, d] bf16,
+    gammas [d] fp32, gate fp32 [d] (per channel) or [T, 1] (per token).
+    Without y: n = norm(r) * gamma_pre, and the result's r is r itself.
+    ``out.r`` may be r (updated in place)."""
+    T, d, f32, kind = _norm_args(r, y, gamma_post, gate, gamma_pre)
+    post, pre = gamma_post is not None, gamma_pre is not None
+    if out is None:
+        out = NormResidual.empty(T, d, r.dtype, y is not None, post, pre, r.device)
+    else:
+        if y is not None:
+            _need(out.r, r.dtype, (T, d), "out.r")
+        if pre:
+            _need(out.n, torch.bfloat16, (T, d), "out.n")
+            _need(out.rstd_pre, torch.float32, (T,), "out.rstd_pre")
+        if post:
+            _need(out.rstd_post, torch.float32, (T,), "out.rstd_post")
+    _check(lib.moe_norm_residual(_ptr(r), f32, _ptr(y), _ptr(gamma_post), _ptr(gate), kind, res_scale,
+                                 _ptr(gamma_pre), eps, T, d, _ptr(out.r) if y is not None else None, _ptr(out.n),
+                                 _ptr(out.rstd_post), _ptr(out.rstd_pre), _stream(stream)), "moe_norm_residual")
+    if y is None:
+        out.r = r
+    return out
+
+
+def norm_residual_backward(r, dr, dn=None, y=None, *, gamma_post=None, gate=None, gamma_pre=None,
+                           res_scale: float = 1.0, rstd_post=None, rstd_pre=None,
+                           out: NormResidualGrads | None = None, stream=None) -> NormResidualGrads:
+    """Gradients of norm_residual for ``dr`` (of its output stream, the
+    residual's type; None: zero, with gamma_pre) and ``dn`` (with gamma_pre),
+    from its output stream ``r`` as stored, y and the factors it returned."""
+    T, d, f32, kind = _norm_args(r, y, gamma_post, gate, gamma_pre)
+    post, pre = gamma_post is not None, gamma_pre is not None
+    if dr is not None:
+        _need(dr, r.dtype, (T, d), "dr")
+    if pre:
+        _need(dn, torch.bfloat16, (T, d), "dn")
+        _need(rstd_pre, torch.float32, (T,), "rstd_pre")
+    if post:
+        _need(rstd_post, torch.float32, (T,), "rstd_post")
+    if out is None:
+        out = NormResidualGrads.empty(T, d, r.dtype, y is not None, post, pre, _GATES[kind], r.device)
+    else:
+        _need(out.dr, r.dtype, (T, d), "out.dr")
+        if y is not None:
+            _need(out.dy, torch.bfloat16, (T, d), "out.dy")
+        if pre:
+            _need(out.dgamma_pre, torch.float32, (d,), "out.dgamma_pre")
+        if post:
+            _need(out.dgamma_post, torch.float32, (d,), "out.dgamma_post")
+        if kind:
+            _need(out.dgate, torch.float32, gate.shape, "out.dgate")
+        if out.workspace is None:
+            out.workspace = _empty((int(lib.moe_norm_residual_backward_workspace_size(T, d)),), torch.uint8, r)
+    _check(lib.moe_norm_residual_backward(
+        _ptr(r), f32, _ptr(y), _ptr(gamma_post), _ptr(gate), kind, res_scale, _ptr(gamma_pre), _ptr(rstd_post),
+        _ptr(rstd_pre), _ptr(dr), _ptr(dn), T, d, _ptr(out.dr), _ptr(out.dy), _ptr(out.dgamma_pre),
+        _ptr(out.dgamma_post), _ptr(out.dgate), _ptr(out.workspace), out.workspace.numel(), _stream(stream)),
+        "moe_norm_residual_backward")
+    return out
+
+
+# ------------------------------------------------------------------ gradient norm and clipping
+class GradClipper:
+    """The global norm of a fixed set of gradient tensors (contiguous CUDA
+    tensors, fp32 or bf16, of any sizes) and clipping by it.  The tensors, or
+    ``outs`` of the same shapes and types for the clipped ones (None: in
+    place), are held; their values are read at every call.
+
+    ``clipper(max_norm)`` clips and returns the norm [1] (fp32, on the device,
+    reused); ``clipper()`` only returns the norm."""
+
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+        self.outs = None if outs is None else list(outs)
+        if self.outs is not None and len(self.outs) != len(self.grads):
+            raise ValueError("outs must hold one tensor for each gradient")
+        for i, g in enumerate(self.grads):
+            if not isinstance(g, torch.Tensor) or g.dtype not in (torch.float32, torch.bfloat16):
+                raise TypeError(f"grads[{i}] must be a float32 or bfloat16 tensor")
+            _need(g, g.dtype, g.shape, f"grads[{i}]")
+            if self.outs is not None:
+                _need(self.outs[i], g.dtype, g.shape, f"outs[{i}]")
+        n = len(self.grads)
+        device = self.grads[0].device if n else "cuda"
+        self._ptrs = (ctypes.c_void_p * n)(*[g.data_ptr() for g in self.grads])
+        self._outs = None if self.outs is None else (ctypes.c_void_p * n)(*[o.data_ptr() for o in self.outs])
+        self._sizes = (ctypes.c_int64 * n)(*[g.numel() for g in self.grads])
+        self._kinds = (ctypes.c_int32 * n)(*[int(g.dtype == torch.bfloat16) for g in self.grads])
+        self.norm = torch.empty((1,), dtype=torch.float32, device=device)
+        self.workspace = torch.empty((int(lib.moe_grad_norm_workspace_size(n)),), dtype=torch.uint8, device=device)
+
+    def __call__(self, max_norm: float | None = None, stream=None):
+        ws = (_ptr(self.norm), _ptr(self.workspace), self.workspace.numel(), _stream(stream))
+        if max_norm is None:
+            _check(lib.moe_grad_norm(self._ptrs, self._sizes, self._kinds, len(self.grads), *ws), "moe_grad_norm")
+        else:
+            _check(lib.moe_grad_norm_clip(self._ptrs, self._outs, self._sizes, self._kinds, len(self.grads), max_norm,
+                                          *ws), "moe_grad_norm_clip")
+        return self.norm
 
 
 # ------------------------------------------------------------------ a3
@@ -347,10 +606,12 @@ def _weights_check(x, Wr, bias, W1, W2, K):
     return T, d, E, f
 
 
-def forward(x, Wr, bias, W1, W2, K: int, out=None, workspace=None, stream=None, preact=None):
+def forward(x, Wr, bias, W1, W2, K: int, out=None, workspace=None, stream=None, preact=None,
+            rule: RouteRule | None = None, sel_bias=None):
     """The whole layer in one C-ABI call (9 kernel launches, no host sync).
     With ``preact`` ([T*K, 2f] bf16) GEMM1 also stores the pre-activations
-    for a backward pass (moe_forward_train)."""
+    for a backward pass (moe_forward_train).  With ``rule`` the routing is
+    route_scored's (moe_forward_scored)."""
     T, d, E, f = _weights_check(x, Wr, bias, W1, W2, K)
     _need(x, torch.bfloat16, (T, d), "x")
     nbytes = forward_workspace_size(T, d, E, K, f)
@@ -359,11 +620,20 @@ def forward(x, Wr, bias, W1, W2, K: int, out=None, workspace=None, stream=None, 
     if workspace is None:
         workspace = _empty((nbytes,), torch.uint8, x)
     out = _empty((T, d), torch.bfloat16, x) if out is None else _need(out, torch.bfloat16, (T, d), "y")
-    if preact is None:
+    if preact is not None:
+        _need(preact, torch.bfloat16, (T * K, 2 * f), "preact")
+    if rule is not None:
+        if sel_bias is not None:
+            _need(sel_bias, torch.float32, (E,), "sel_bias")
+        _check(lib.moe_forward_scored(_ptr(x), _ptr(Wr), _ptr(bias), _ptr(sel_bias), rule._c, _ptr(W1), _ptr(W2), T, d,
+                                      E, K, f, _ptr(out), _ptr(workspace), workspace.numel(), _ptr(preact),
+                                      _stream(stream)), "moe_forward_scored")
+    elif sel_bias is not None:
+        raise ValueError("sel_bias needs a rule")
+    elif preact is None:
         _check(lib.moe_forward(_ptr(x), _ptr(Wr), _ptr(bias), _ptr(W1), _ptr(W2), T, d, E, K, f, _ptr(out),
                                _ptr(workspace), workspace.numel(), _stream(stream)), "moe_forward")
     else:
-        _need(preact, torch.bfloat16, (T * K, 2 * f), "preact")
         _check(lib.moe_forward_train(_ptr(x), _ptr(Wr), _ptr(bias), _ptr(W1), _ptr(W2), T, d, E, K, f, _ptr(out),
                                      _ptr(workspace), workspace.numel(), _ptr(preact), _stream(stream)),
                "moe_forward_train")
@@ -476,10 +746,15 @@ def launch_count() -> int:
 class MoELayer:
     """Holds one layer's weights and a persistent workspace; ``__call__(x)``
     runs the forward with one C call.  Intermediates can be read back with
-    ``views()`` after a call (they live in the workspace)."""
+    ``views()`` after a call (they live in the workspace).  With ``rule`` (and
+    ``sel_bias`` [E] fp32, which may be changed between calls) it routes by
+    route_scored."""
 
-    def __init__(self, Wr, bias, W1, W2, K: int, T_max: int):
+    def __init__(self, Wr, bias, W1, W2, K: int, T_max: int, rule: RouteRule | None = None, sel_bias=None):
+        if sel_bias is not None and rule is None:
+            raise ValueError("sel_bias needs a rule")
         self.Wr, self.bias, self.W1, self.W2, self.K = Wr, bias, W1, W2, K
+        self.rule, self.sel_bias = rule, sel_bias
         self.d = W1.shape[2]
         self.E = Wr.shape[1]
         self.f = W1.shape[1] // 2
@@ -509,7 +784,7 @@ class MoELayer:
         # unwritten; the training forward (save_preact) always writes it
         self._x_perm_written = save_preact or not forward_fuses_permute(x.shape[0], self.d, self.E, self.K, self.f)
         return forward(x, self.Wr, self.bias, self.W1, self.W2, self.K, out=out, workspace=self.workspace,
-                       stream=stream, preact=pre)
+                       stream=stream, preact=pre, rule=self.rule, sel_bias=self.sel_bias)
 
     def backward(self, x, dy, grads=None, workspace=None, stream=None):
         """Gradients of sum(dy * y) for the last call (same x): dict of dx
@@ -535,11 +810,12 @@ class MoELayer:
             grads = dict(dx=torch.empty((T, d), dtype=torch.bfloat16, device=x.device),
                          dWr=torch.empty(self.Wr.shape, **f32), dbias=torch.empty((self.E,), **f32),
                          dW1=torch.empty(self.W1.shape, **f32), dW2=torch.empty(self.W2.shape, **f32))
-        _check(lib.moe_backward(_ptr(x), _ptr(self.Wr), _ptr(self.bias), _ptr(self.W1), _ptr(self.W2), T, d, self.E,
-                                self.K, self.f, _ptr(dy), _ptr(self.workspace), self.workspace.numel(),
-                                _ptr(pre), _ptr(grads["dx"]), _ptr(grads["dWr"]), _ptr(grads["dbias"]), _ptr(grads["dW1"]),
-                                _ptr(grads["dW2"]), _ptr(workspace), workspace.numel(), _stream(stream)),
-               "moe_backward")
+        fn, name, route = (lib.moe_backward, "moe_backward", _ptr(self.bias)) if self.rule is None else \
+            (lib.moe_backward_scored, "moe_backward_scored", self.rule._c)
+        _check(fn(_ptr(x), _ptr(self.Wr), route, _ptr(self.W1), _ptr(self.W2), T, d, self.E,
+                  self.K, self.f, _ptr(dy), _ptr(self.workspace), self.workspace.numel(),
+                  _ptr(pre), _ptr(grads["dx"]), _ptr(grads["dWr"]), _ptr(grads["dbias"]), _ptr(grads["dW1"]),
+                  _ptr(grads["dW2"]), _ptr(workspace), workspace.numel(), _stream(stream)), name)
         self.bw_workspace = workspace
         return grads
 
@@ -583,6 +859,58 @@ class MoELayer:
             h=v("h", TK * f, torch.bfloat16, (TK, f)),
             y_perm=v("y_perm", TK * d, torch.bfloat16, (TK, d)),
         )
+
+
+class MoEBlock:
+    """A layer inside a residual stream, as a model trains it:
+
+        n  = norm(r) * gamma_pre
+        y  = layer(n)
+        r' = res_scale * r + gate * norm(y) * gamma_post
+
+    ``layer``: a MoELayer; ``gamma_post`` and ``gate`` may be None.  Blocks
+    that follow one another share a kernel: ``block(r, n)`` takes the n that
+    the block before it returned for ``next_gamma=block.gamma_pre``."""
+
+    def __init__(self, layer: MoELayer, gamma_pre, gamma_post=None, gate=None, res_scale: float = 1.0,
+                 eps: float = 1e-6):
+        self.layer, self.gamma_pre, self.gamma_post, self.gate = layer, gamma_pre, gamma_post, gate
+        self.res_scale, self.eps = res_scale, eps
+        self._saved = None
+
+    def __call__(self, r, pre: NormResidual | None = None, next_gamma=None, save: bool = False,
+                 stream=None) -> NormResidual:
+        """The stream after the block, and with ``next_gamma`` its norm for the
+        next block.  ``pre``: what the block before returned for this block's
+        gamma_pre (else the norm is taken here).  ``save`` keeps what backward() needs."""
+        own_pre = pre is None
+        if own_pre:
+            pre = norm_residual(r, gamma_pre=self.gamma_pre, eps=self.eps, stream=stream)
+        y = self.layer(pre.n, stream=stream, save_preact=save)
+        out = norm_residual(r, y, gamma_post=self.gamma_post, gate=self.gate, gamma_pre=next_gamma,
+                            res_scale=self.res_scale, eps=self.eps, stream=stream)
+        self._saved = (pre, y, out, next_gamma, own_pre) if save else None
+        return out
+
+    def backward(self, dr, dn=None, stream=None) -> dict:
+        """Gradients for ``dr`` of the stream after the block and ``dn`` of its
+        norm (with next_gamma): dr [T, d] of the stream before it, dn of its
+        own norm's output (None when the norm was taken here: then it is in
+        dr), the layer's gradients, dgamma_pre, dgamma_post, dgate, dnext_gamma."""
+        if self._saved is None:
+            raise RuntimeError("backward() needs a forward with save=True")
+        pre, y, out, next_gamma, own_pre = self._saved
+        g = norm_residual_backward(out.r, dr, dn, y, gamma_post=self.gamma_post, gate=self.gate,
+                                   gamma_pre=next_gamma, res_scale=self.res_scale, rstd_post=out.rstd_post,
+                                   rstd_pre=out.rstd_pre, stream=stream)
+        grads = self.layer.backward(pre.n, g.dy, stream=stream)
+        grads.update(dgamma_post=g.dgamma_post, dgate=g.dgate, dnext_gamma=g.dgamma_pre, dr=g.dr, dn=grads.pop("dx"))
+        if own_pre:
+            # the stream before the block feeds the sum and the norm
+            h = norm_residual_backward(pre.r, g.dr, grads["dn"], gamma_pre=self.gamma_pre, rstd_pre=pre.rstd_pre,
+                                       stream=stream)
+            grads.update(dr=h.dr, dn=None, dgamma_pre=h.dgamma_pre)
+        return grads
 
 
 # ------------------------------------------------------------------ MXFP8 path

@@ -56,6 +56,64 @@ cudaError_t launch_route(const float *logits, int T, int E, int K, int32_t *topk
                          int32_t *counts, int32_t *offsets, int32_t *row_of, int32_t *src_tok, int32_t *workspace,
                          cudaStream_t stream);
 
+// The scan and scatter of a routing whose top-K kernel has written topk_idx,
+// each pair's rank inside its chunk (row_of) and the per-chunk counts (workspace).
+cudaError_t launch_route_dispatch(const int32_t *topk_idx, int T, int E, int K, int32_t *counts, int32_t *offsets,
+                                  int32_t *row_of, int32_t *src_tok, int32_t *workspace, cudaStream_t stream);
+
+// Routing by scores of all experts (route_scored.cu): the moe_route_rule_t of the C ABI, checked.
+constexpr float kRouteEps = 1e-20f;  // beside the sum of the chosen scores
+struct RouteRule {
+    bool softmax;  // else sigmoid
+    int n_group, topk_group, group_top;
+    bool renorm;
+    float scale;
+};
+cudaError_t launch_route_scored(const float *logits, const float *sel_bias, int T, int E, int K, const RouteRule &rule,
+                                int32_t *topk_idx, float *topk_w, int32_t *counts, int32_t *offsets, int32_t *row_of,
+                                int32_t *src_tok, int32_t *workspace, cudaStream_t stream);
+cudaError_t launch_route_scored_bwd(const float *logits, const int32_t *topk_idx, const float *dw, int T, int E, int K,
+                                    const RouteRule &rule, float *dlogits, cudaStream_t stream);
+// dl [T, K] and dl_row [TK] (by row_of), as launch_router_bwd for the layer's own softmax
+cudaError_t launch_route_scored_bwd_rows(const float *logits, const int32_t *topk_idx, const float *topk_w,
+                                         const float *dw, const int32_t *row_of, int T, int E, int K,
+                                         const RouteRule &rule, float *dl, float *dl_row, cudaStream_t stream);
+
+// Norms, gate and residual between two layers (norm_residual.cu).  Null
+// pointers leave a part out, as in the C ABI; d a multiple of 64, at most
+// kNormMaxD.  res_f32: the residual stream is fp32, else bf16.
+constexpr int kNormMaxD = 16384;
+struct NormResidualArgs {
+    const uint16_t *y;
+    const float *gamma_post, *gate, *gamma_pre;
+    bool gate_per_token;
+    float res_scale, eps;
+    int T, d;
+    bool res_f32;
+};
+cudaError_t launch_norm_residual(const NormResidualArgs &a, const void *r, void *r_out, uint16_t *n, float *rstd_post,
+                                 float *rstd_pre, cudaStream_t stream);
+// `part` holds norm_residual_bwd_part_bytes(T, d) bytes; up to two launches, counted in *launches.
+size_t norm_residual_bwd_part_bytes(int T, int d);
+struct NormResidualGradArgs {
+    const void *r_out, *dr_out;
+    const uint16_t *dn;
+    const float *rstd_post, *rstd_pre;
+    void *dr;
+    uint16_t *dy;
+    float *dgamma_pre, *dgamma_post, *dgate;
+};
+cudaError_t launch_norm_residual_bwd(const NormResidualArgs &a, const NormResidualGradArgs &g, float *part,
+                                     int *launches, cudaStream_t stream);
+
+// Global gradient norm and clipping (grad_clip.cu): tensors of `sizes`
+// elements, kinds 0 fp32, 1 bf16.  outs null: in place.  clip false: the norm
+// alone.  `part` holds grad_clip_part_bytes(n) bytes; launches counted in *launches.
+size_t grad_clip_part_bytes(int n);
+cudaError_t launch_grad_clip(const void *const *grads, void *const *outs, const int64_t *sizes, const int32_t *kinds,
+                             int n, bool clip, float max_norm, float *norm_out, float *part, int *launches,
+                             cudaStream_t stream);
+
 cudaError_t launch_permute(const uint16_t *x, const int32_t *row_of, int T, int K, int d, uint16_t *x_perm,
                            cudaStream_t stream);
 

@@ -1,4 +1,4 @@
-// C ABI of the dropless MoE layer forward (declared in include/moe.h).
+// C ABI of the dropless MoE layer and of the operators around it (declared in include/moe.h).
 //
 // Host-side argument checks run before anything touches CUDA, so a bad call
 // returns an error and launches nothing.  The library allocates nothing: every
@@ -9,6 +9,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <atomic>
+#include <cmath>
 #include <mutex>
 #include <vector>
 
@@ -134,7 +135,39 @@ moe_status_t check_shape(int T, int d, int E, int K, int f, bool need_d, bool ne
     return MOE_OK;
 }
 
+// The caller's routing rule, checked against E and K.
+moe_status_t check_rule(const moe_route_rule_t *rule, int E, int K, moe::RouteRule *out) {
+    if (!rule || (rule->score != MOE_SCORE_SIGMOID && rule->score != MOE_SCORE_SOFTMAX)) return MOE_ERR_INVALID_ARG;
+    if (rule->n_group < 1 || E % rule->n_group != 0) return MOE_ERR_INVALID_ARG;
+    if (rule->topk_group < 1 || rule->topk_group > rule->n_group) return MOE_ERR_INVALID_ARG;
+    if (rule->group_top != 1 && rule->group_top != 2) return MOE_ERR_INVALID_ARG;
+    if (K > rule->topk_group * (E / rule->n_group)) return MOE_ERR_INVALID_ARG;
+    if (!std::isfinite(rule->scale)) return MOE_ERR_INVALID_ARG;
+    *out = moe::RouteRule{rule->score == MOE_SCORE_SOFTMAX, rule->n_group, rule->topk_group, rule->group_top,
+                          rule->renorm != 0, rule->scale};
+    return MOE_OK;
+}
+
 inline moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+// The norm entry points' common arguments.
+moe_status_t check_norm(int residual_fp32, const uint16_t *y, const float *gamma_post, const float *gate,
+                        int gate_kind, float res_scale, const float *gamma_pre, float eps, int T, int d,
+                        moe::NormResidualArgs *out) {
+    if (T < 1 || d < 1 || (residual_fp32 != 0 && residual_fp32 != 1)) return MOE_ERR_INVALID_ARG;
+    if (d % 64 != 0 || d > moe::kNormMaxD) return MOE_ERR_UNSUPPORTED;
+    if (!y && (gamma_post || gate || res_scale != 1.0f)) return MOE_ERR_INVALID_ARG;  // they act on y and its sum
+    if (!y && !gamma_pre) return MOE_ERR_INVALID_ARG;                                 // nothing to do
+    if (gate_kind < MOE_GATE_NONE || gate_kind > MOE_GATE_TOKEN || (gate != nullptr) != (gate_kind != MOE_GATE_NONE))
+        return MOE_ERR_INVALID_ARG;
+    if (!(eps > 0.0f) || !std::isfinite(eps) || !std::isfinite(res_scale)) return MOE_ERR_INVALID_ARG;
+    if ((y && !aligned(y, 16)) || (gamma_post && !aligned(gamma_post, 16)) || (gamma_pre && !aligned(gamma_pre, 16)) ||
+        (gate && !aligned(gate, gate_kind == MOE_GATE_CHANNEL ? 16 : 4)))
+        return MOE_ERR_INVALID_ARG;
+    *out = moe::NormResidualArgs{y, gamma_post, gate, gamma_pre, gate_kind == MOE_GATE_TOKEN, res_scale, eps, T, d,
+                                 residual_fp32 == 1};
+    return MOE_OK;
+}
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
@@ -339,6 +372,139 @@ moe_status_t moe_route(const float *logits, int T, int E, int K, int32_t *topk_i
                                          static_cast<int32_t *>(workspace), stream));
 }
 
+moe_status_t moe_route_scored(const float *logits, const float *sel_bias, int T, int E, int K,
+                              const moe_route_rule_t *rule, int32_t *topk_idx, float *topk_w, int32_t *counts,
+                              int32_t *offsets, int32_t *row_of, int32_t *src_tok, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream) {
+    MOE_RANGE();
+    if (!logits || !topk_idx || !topk_w || !counts || !offsets || !row_of || !src_tok || !workspace)
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(logits, 4) || (sel_bias && !aligned(sel_bias, 4)) || !aligned(topk_idx, 4) || !aligned(topk_w, 4) ||
+        !aligned(counts, 4) || !aligned(offsets, 4) || !aligned(row_of, 4) || !aligned(src_tok, 4) ||
+        !aligned(workspace, 4))
+        return MOE_ERR_INVALID_ARG;
+    moe_status_t st = check_shape(T, 64, E, K, 64, false, false);
+    if (st != MOE_OK) return st;
+    moe::RouteRule r;
+    if ((st = check_rule(rule, E, K, &r)) != MOE_OK) return st;
+    if (workspace_bytes < moe::route_workspace_bytes(T, E)) return MOE_ERR_WORKSPACE;
+    g_launches.fetch_add(3, std::memory_order_relaxed);
+    return cuda_status(moe::launch_route_scored(logits, sel_bias, T, E, K, r, topk_idx, topk_w, counts, offsets,
+                                                row_of, src_tok, static_cast<int32_t *>(workspace), stream));
+}
+
+moe_status_t moe_route_scored_backward(const float *logits, const int32_t *topk_idx, const float *dw, int T, int E,
+                                       int K, const moe_route_rule_t *rule, float *dlogits, cudaStream_t stream) {
+    MOE_RANGE();
+    if (!logits || !topk_idx || !dw || !dlogits) return MOE_ERR_INVALID_ARG;
+    if (!aligned(logits, 4) || !aligned(topk_idx, 4) || !aligned(dw, 4) || !aligned(dlogits, 4))
+        return MOE_ERR_INVALID_ARG;
+    moe_status_t st = check_shape(T, 64, E, K, 64, false, false);
+    if (st != MOE_OK) return st;
+    moe::RouteRule r;
+    if ((st = check_rule(rule, E, K, &r)) != MOE_OK) return st;
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return cuda_status(moe::launch_route_scored_bwd(logits, topk_idx, dw, T, E, K, r, dlogits, stream));
+}
+
+moe_status_t moe_norm_residual(const void *r, int residual_fp32, const uint16_t *y, const float *gamma_post,
+                               const float *gate, int gate_kind, float res_scale, const float *gamma_pre, float eps,
+                               int T, int d, void *r_out, uint16_t *n, float *rstd_post, float *rstd_pre,
+                               cudaStream_t stream) {
+    MOE_RANGE();
+    moe::NormResidualArgs a;
+    moe_status_t st = check_norm(residual_fp32, y, gamma_post, gate, gate_kind, res_scale, gamma_pre, eps, T, d, &a);
+    if (st != MOE_OK) return st;
+    if (!r || !aligned(r, 16)) return MOE_ERR_INVALID_ARG;
+    if (y && (!r_out || !aligned(r_out, 16))) return MOE_ERR_INVALID_ARG;
+    if (gamma_pre && (!n || !rstd_pre || !aligned(n, 16) || !aligned(rstd_pre, 4))) return MOE_ERR_INVALID_ARG;
+    if (gamma_post && (!rstd_post || !aligned(rstd_post, 4))) return MOE_ERR_INVALID_ARG;
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return cuda_status(moe::launch_norm_residual(a, r, r_out, n, rstd_post, rstd_pre, stream));
+}
+
+size_t moe_norm_residual_backward_workspace_size(int T, int d) {
+    if (T < 1 || d < 64 || d % 64 != 0 || d > moe::kNormMaxD) return 0;
+    return moe::norm_residual_bwd_part_bytes(T, d);
+}
+
+moe_status_t moe_norm_residual_backward(const void *r_out, int residual_fp32, const uint16_t *y,
+                                        const float *gamma_post, const float *gate, int gate_kind, float res_scale,
+                                        const float *gamma_pre, const float *rstd_post, const float *rstd_pre,
+                                        const void *dr_out, const uint16_t *dn, int T, int d, void *dr, uint16_t *dy,
+                                        float *dgamma_pre, float *dgamma_post, float *dgate, void *workspace,
+                                        size_t workspace_bytes, cudaStream_t stream) {
+    MOE_RANGE();
+    moe::NormResidualArgs a;
+    moe_status_t st = check_norm(residual_fp32, y, gamma_post, gate, gate_kind, res_scale, gamma_pre, 1.0f, T, d, &a);
+    if (st != MOE_OK) return st;
+    if (!dr || !aligned(dr, 16) || !workspace || !aligned(workspace, 16)) return MOE_ERR_INVALID_ARG;
+    if (dr_out ? !aligned(dr_out, 16) : !gamma_pre) return MOE_ERR_INVALID_ARG;
+    if (gamma_pre && (!r_out || !dn || !rstd_pre || !dgamma_pre || !aligned(r_out, 16) || !aligned(dn, 16) ||
+                      !aligned(rstd_pre, 4) || !aligned(dgamma_pre, 4)))
+        return MOE_ERR_INVALID_ARG;
+    if (y && (!dy || !aligned(dy, 16))) return MOE_ERR_INVALID_ARG;
+    if (gamma_post && (!rstd_post || !dgamma_post || !aligned(rstd_post, 4) || !aligned(dgamma_post, 4)))
+        return MOE_ERR_INVALID_ARG;
+    if (gate && (!dgate || !aligned(dgate, 4))) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < moe::norm_residual_bwd_part_bytes(T, d)) return MOE_ERR_WORKSPACE;
+    const moe::NormResidualGradArgs g{r_out, dr_out, dn, rstd_post, rstd_pre, dr, dy, dgamma_pre, dgamma_post, dgate};
+    int launches = 0;
+    const cudaError_t e = moe::launch_norm_residual_bwd(a, g, static_cast<float *>(workspace), &launches, stream);
+    g_launches.fetch_add(launches, std::memory_order_relaxed);
+    return cuda_status(e);
+}
+
+size_t moe_grad_norm_workspace_size(int n_tensors) {
+    return n_tensors < 0 ? 0 : moe::grad_clip_part_bytes(n_tensors);
+}
+
+}  // extern "C"
+
+namespace {
+
+// moe_grad_norm (clip false) and moe_grad_norm_clip.
+moe_status_t grad_clip_impl(const void *const *grads, void *const *outs, const int64_t *sizes, const int32_t *kinds,
+                            int n, bool clip, float max_norm, float *norm_out, void *workspace,
+                            size_t workspace_bytes, cudaStream_t stream) {
+    if (n < 0 || (n > 0 && (!grads || !sizes || !kinds)) || !norm_out || !aligned(norm_out, 4) || !workspace ||
+        !aligned(workspace, 4))
+        return MOE_ERR_INVALID_ARG;
+    if (clip && !(max_norm > 0.0f)) return MOE_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i) {
+        if (sizes[i] < 0 || (kinds[i] != MOE_GRAD_FP32 && kinds[i] != MOE_GRAD_BF16)) return MOE_ERR_INVALID_ARG;
+        if (sizes[i] > (int64_t(1) << 40)) return MOE_ERR_UNSUPPORTED;
+        const size_t a = kinds[i] == MOE_GRAD_BF16 ? 2 : 4;
+        if (sizes[i] && (!grads[i] || !aligned(grads[i], a) || (outs && (!outs[i] || !aligned(outs[i], a)))))
+            return MOE_ERR_INVALID_ARG;
+    }
+    if (workspace_bytes < moe::grad_clip_part_bytes(n)) return MOE_ERR_WORKSPACE;
+    int launches = 0;
+    const cudaError_t e = moe::launch_grad_clip(grads, outs, sizes, kinds, n, clip, max_norm, norm_out,
+                                                static_cast<float *>(workspace), &launches, stream);
+    g_launches.fetch_add(launches, std::memory_order_relaxed);
+    return cuda_status(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *kinds, int n_tensors,
+                           float *norm_out, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    MOE_RANGE();
+    return grad_clip_impl(grads, nullptr, sizes, kinds, n_tensors, false, 0.0f, norm_out, workspace, workspace_bytes,
+                          stream);
+}
+
+moe_status_t moe_grad_norm_clip(const void *const *grads, void *const *outs, const int64_t *sizes,
+                                const int32_t *kinds, int n_tensors, float max_norm, float *norm_out, void *workspace,
+                                size_t workspace_bytes, cudaStream_t stream) {
+    MOE_RANGE();
+    return grad_clip_impl(grads, outs, sizes, kinds, n_tensors, true, max_norm, norm_out, workspace, workspace_bytes,
+                          stream);
+}
+
 moe_status_t moe_permute(const uint16_t *x, const int32_t *row_of, int T, int K, int d, uint16_t *x_perm,
                          cudaStream_t stream) {
     MOE_RANGE();
@@ -474,12 +640,14 @@ moe_status_t moe_forward_views(int T, int d, int E, int K, int f, moe_forward_la
 
 namespace {
 
-// The forward of moe_forward and moe_forward_train.  `fuse_permute`: GEMM1
-// reads its rows straight from x (the permute fused into its operand load)
-// and x_perm is not written.
+// The forward of moe_forward, moe_forward_train and moe_forward_scored.
+// `fuse_permute`: GEMM1 reads its rows straight from x (the permute fused into
+// its operand load) and x_perm is not written.  `rule`: the routing is
+// moe_route_scored's instead of moe_route's.
 moe_status_t forward_impl(const uint16_t *x, const float *Wr, const float *bias, const uint16_t *W1,
                           const uint16_t *W2, int T, int d, int E, int K, int f, uint16_t *y, void *workspace,
-                          size_t workspace_bytes, uint16_t *preact, bool fuse_permute, cudaStream_t stream) {
+                          size_t workspace_bytes, uint16_t *preact, bool fuse_permute, cudaStream_t stream,
+                          const moe_route_rule_t *rule = nullptr, const float *sel_bias = nullptr) {
     if (!x || !Wr || !W1 || !W2 || !y || !workspace) return MOE_ERR_INVALID_ARG;
     if (preact && !aligned(preact, 16)) return MOE_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(W1, 16) || !aligned(W2, 16) || !aligned(y, 16) || !aligned(workspace, 16) ||
@@ -487,6 +655,11 @@ moe_status_t forward_impl(const uint16_t *x, const float *Wr, const float *bias,
         return MOE_ERR_INVALID_ARG;
     moe_status_t st = check_shape(T, d, E, K, f, true, true);
     if (st != MOE_OK) return st;
+    if (rule) {  // before the router's launches
+        moe::RouteRule checked;
+        if ((st = check_rule(rule, E, K, &checked)) != MOE_OK) return st;
+        if (sel_bias && !aligned(sel_bias, 4)) return MOE_ERR_INVALID_ARG;
+    }
     moe_forward_layout_t L;
     forward_layout(T, d, E, K, f, &L);
     if (workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
@@ -506,9 +679,13 @@ moe_status_t forward_impl(const uint16_t *x, const float *Wr, const float *bias,
     if ((st = moe_router_logits(x, Wr, bias, T, d, E, logits, at(L.router_ws), L.x_perm - L.router_ws,
                                 stream)) != MOE_OK)
         return st;
-    if ((st = moe_route(logits, T, E, K, idx, w, counts, offsets, row_of, src_tok, at(L.route_ws),
-                        L.router_ws - L.route_ws, stream)) != MOE_OK)
-        return st;
+    if (rule)
+        st = moe_route_scored(logits, sel_bias, T, E, K, rule, idx, w, counts, offsets, row_of, src_tok,
+                              at(L.route_ws), L.router_ws - L.route_ws, stream);
+    else
+        st = moe_route(logits, T, E, K, idx, w, counts, offsets, row_of, src_tok, at(L.route_ws),
+                       L.router_ws - L.route_ws, stream);
+    if (st != MOE_OK) return st;
     if (fuse_permute) {
         st = moe_grouped_gemm1_swiglu_gather(x, src_tok, offsets, T, E, TK, d, f, W1, h, stream);
     } else {
@@ -546,6 +723,17 @@ moe_status_t moe_forward(const uint16_t *x, const float *Wr, const float *bias, 
     MOE_RANGE();
     return forward_impl(x, Wr, bias, W1, W2, T, d, E, K, f, y, workspace, workspace_bytes, nullptr,
                         moe_forward_fuses_permute(T, d, E, K, f) != 0, stream);
+}
+
+moe_status_t moe_forward_scored(const uint16_t *x, const float *Wr, const float *bias, const float *sel_bias,
+                                const moe_route_rule_t *rule, const uint16_t *W1, const uint16_t *W2, int T, int d,
+                                int E, int K, int f, uint16_t *y, void *workspace, size_t workspace_bytes,
+                                uint16_t *preact, cudaStream_t stream) {
+    MOE_RANGE();
+    if (!rule) return MOE_ERR_INVALID_ARG;
+    const bool fuse = !preact && moe_forward_fuses_permute(T, d, E, K, f) != 0;
+    return forward_impl(x, Wr, bias, W1, W2, T, d, E, K, f, y, workspace, workspace_bytes, preact, fuse, stream, rule,
+                        sel_bias);
 }
 
 moe_status_t moe_forward_host(const uint16_t *x_host, const float *Wr, const float *bias, const uint16_t *W1,
@@ -791,13 +979,18 @@ moe_status_t moe_backward_views(int T, int d, int E, int K, int f, moe_backward_
     return MOE_OK;
 }
 
-moe_status_t moe_backward(const uint16_t *x, const float *Wr, const float *bias, const uint16_t *W1,
-                          const uint16_t *W2, int T, int d, int E, int K, int f, const uint16_t *dy,
-                          const void *fwd_workspace, size_t fwd_workspace_bytes, const uint16_t *preact,
-                          uint16_t *dx, float *dWr, float *dbias, float *dW1, float *dW2, void *workspace,
-                          size_t workspace_bytes, cudaStream_t stream) {
-    MOE_RANGE();
-    (void)bias;  // the bias enters the gradients only through the routing recorded by the forward
+}  // extern "C"
+
+namespace {
+
+// The backward of moe_backward and moe_backward_scored (`rule`: the gate
+// weights are moe_route_scored's, else the softmax over the K chosen logits).
+// The biases enter the gradients only through the routing recorded by the forward.
+moe_status_t backward_impl(const uint16_t *x, const float *Wr, const uint16_t *W1, const uint16_t *W2, int T, int d,
+                           int E, int K, int f, const uint16_t *dy, const void *fwd_workspace,
+                           size_t fwd_workspace_bytes, const uint16_t *preact, uint16_t *dx, float *dWr, float *dbias,
+                           float *dW1, float *dW2, void *workspace, size_t workspace_bytes, cudaStream_t stream,
+                           const moe_route_rule_t *rule = nullptr) {
     if (!x || !Wr || !W1 || !W2 || !dy || !fwd_workspace || !dx || !dWr || !dbias || !dW1 || !dW2 || !workspace)
         return MOE_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(W1, 16) || !aligned(W2, 16) || !aligned(dy, 16) || !aligned(dx, 16) ||
@@ -808,6 +1001,12 @@ moe_status_t moe_backward(const uint16_t *x, const float *Wr, const float *bias,
     if (st != MOE_OK) return st;
     moe_forward_layout_t F;
     forward_layout(T, d, E, K, f, &F);
+    moe::RouteRule scored;
+    if (rule) {
+        if ((st = check_rule(rule, E, K, &scored)) != MOE_OK) return st;
+        // raw softmax scores send a gradient to every expert's logit, which the row-wise sums below do not carry
+        if (scored.softmax && !scored.renorm) return MOE_ERR_UNSUPPORTED;
+    }
     moe_backward_layout_t B;
     backward_layout(T, d, E, K, f, &B);
     if (fwd_workspace_bytes < F.total || workspace_bytes < B.total) return MOE_ERR_WORKSPACE;
@@ -817,6 +1016,7 @@ moe_status_t moe_backward(const uint16_t *x, const float *Wr, const float *bias,
     uint8_t *bw = static_cast<uint8_t *>(workspace);
     auto fv = [&](size_t off) { return fw + off; };
     auto bv = [&](size_t off) { return bw + off; };
+    const float *logits = reinterpret_cast<const float *>(fv(F.logits));
     const int32_t *topk_idx = reinterpret_cast<const int32_t *>(fv(F.topk_idx));
     const float *topk_w = reinterpret_cast<const float *>(fv(F.topk_w));
     const int32_t *offsets = reinterpret_cast<const int32_t *>(fv(F.offsets));
@@ -846,7 +1046,12 @@ moe_status_t moe_backward(const uint16_t *x, const float *Wr, const float *bias,
     go(moe::launch_transpose_f32(Wr, 1, d, E, WrT, stream), 1);
     // combine and router
     go(moe::launch_combine_bwd(dy, y_perm, row_of, topk_w, T, K, d, dw, dy_perm, stream), 1);
-    go(moe::launch_router_bwd(topk_w, dw, row_of, T, K, dl, dl_row, stream), 1);
+    if (rule)
+        go(moe::launch_route_scored_bwd_rows(logits, topk_idx, topk_w, dw, row_of, T, E, K, scored, dl, dl_row,
+                                             stream),
+           1);
+    else
+        go(moe::launch_router_bwd(topk_w, dw, row_of, T, K, dl, dl_row, stream), 1);
     // GEMM2 dgrad: dh = dy_perm . W2[e]
     go(moe::launch_grouped_gemm(false, dy_perm, TK, d, W2, E, f, offsets, dh, g, ds->status, kWaitLimitNs, stream,
                                 nullptr, true),
@@ -869,6 +1074,32 @@ moe_status_t moe_backward(const uint16_t *x, const float *Wr, const float *bias,
     go(moe::launch_router_wgrad(x_perm, dl_row, offsets, E, TK, d, rw_part, dWr, dbias, stream), 2);
     go(moe::launch_dx(dx_perm, WrT, row_of, topk_idx, dl, T, K, E, d, dx, stream), 1);
     return cuda_status(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_backward(const uint16_t *x, const float *Wr, const float *bias, const uint16_t *W1,
+                          const uint16_t *W2, int T, int d, int E, int K, int f, const uint16_t *dy,
+                          const void *fwd_workspace, size_t fwd_workspace_bytes, const uint16_t *preact,
+                          uint16_t *dx, float *dWr, float *dbias, float *dW1, float *dW2, void *workspace,
+                          size_t workspace_bytes, cudaStream_t stream) {
+    MOE_RANGE();
+    (void)bias;
+    return backward_impl(x, Wr, W1, W2, T, d, E, K, f, dy, fwd_workspace, fwd_workspace_bytes, preact, dx, dWr, dbias,
+                         dW1, dW2, workspace, workspace_bytes, stream);
+}
+
+moe_status_t moe_backward_scored(const uint16_t *x, const float *Wr, const moe_route_rule_t *rule, const uint16_t *W1,
+                                 const uint16_t *W2, int T, int d, int E, int K, int f, const uint16_t *dy,
+                                 const void *fwd_workspace, size_t fwd_workspace_bytes, const uint16_t *preact,
+                                 uint16_t *dx, float *dWr, float *dbias, float *dW1, float *dW2, void *workspace,
+                                 size_t workspace_bytes, cudaStream_t stream) {
+    MOE_RANGE();
+    if (!rule) return MOE_ERR_INVALID_ARG;
+    return backward_impl(x, Wr, W1, W2, T, d, E, K, f, dy, fwd_workspace, fwd_workspace_bytes, preact, dx, dWr, dbias,
+                         dW1, dW2, workspace, workspace_bytes, stream, rule);
 }
 
 moe_status_t moe_check_bounded_wait(uint64_t limit_ns, cudaStream_t stream) {

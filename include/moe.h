@@ -1,7 +1,9 @@
 /*
  * moe.h -- C ABI of a dropless Mixture-of-Experts SwiGLU FFN layer on one
  * NVIDIA GB300 (sm_103a): the forward (bf16, and MXFP8 expert matmuls) and the
- * backward of a training step.
+ * backward of a training step; and of the operators around it in a model:
+ * routing by scores, the norms, gate and residual between two layers, and the
+ * clipping of a step's gradients.
  *
  * The operation follows "Accelerating dropless MoE training in JAX with NVIDIA
  * Transformer Engine":
@@ -144,6 +146,102 @@ moe_status_t moe_route_static(const float *logits, int T, int E, int K,
                               int32_t *topk_idx, float *topk_w, int32_t *counts, int32_t *offsets,
                               int32_t *row_of, int32_t *src_tok, cudaStream_t stream);
 
+/* Routing by scores of all experts, in place of moe_route: sigmoid or softmax
+ * scores, a bias for balance, groups of experts, renormalised weights.
+ *   s = sigmoid(logits) or softmax(logits) over the E experts; c = s + sel_bias
+ *   (fp32 [E], nullable: it enters the choice only, never the weights).
+ *   The experts form n_group runs of E / n_group; a run's score is the sum of
+ *   its group_top (1 or 2; at most the run's length) largest c; the topk_group
+ *   best runs stay open; topk_idx[t,:] are the K largest c of the open runs,
+ *   descending.  Every tie goes to the lower index.  Runs and experts are
+ *   ranked on 32-bit values with one definition (sigmoid 1 / (1 + exp(-l));
+ *   softmax exp(l - max) over a sum folded by halves, padded to 256).
+ *   topk_w[t,k] = scale * s_k / (sum_j s_j + 1e-20), or scale * s_k if
+ *   renorm is 0.
+ * The other outputs, the workspace, and determinism are moe_route's.  A
+ * sel_bias of -INFINITY closes an expert (it is chosen only where the open
+ * runs hold fewer than K others, the lowest indexes first).  NaN logits are
+ * outside the contract; the choice is then some K distinct experts.  Needs
+ * E % n_group == 0 and K <= topk_group * (E / n_group).  3 kernel launches. */
+enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };
+typedef struct {
+    int score;                           /* MOE_SCORE_* */
+    int n_group, topk_group, group_top;  /* 1, 1, 1: no groups */
+    int renorm;
+    float scale;
+} moe_route_rule_t;
+moe_status_t moe_route_scored(const float *logits, const float *sel_bias, int T, int E, int K,
+                              const moe_route_rule_t *rule, int32_t *topk_idx, float *topk_w, int32_t *counts,
+                              int32_t *offsets, int32_t *row_of, int32_t *src_tok, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+/* Its gradient: dlogits [T, E] fp32 (every entry written) of sum(dw * topk_w)
+ * for dw [T, K] and the choice topk_idx of the forward; none through the
+ * choice or to sel_bias.  With S = sum_j s_j + 1e-20,
+ *   ds_k = scale (dw_k - sum_j dw_j s_j / S) / S with renorm, else scale dw_k;
+ *   sigmoid: dl_k = ds_k s_k (1 - s_k) for the chosen, 0 for the others;
+ *   softmax: dl_e = s_e (ds_e - sum_j s_j ds_j) for every expert.
+ * One kernel launch.  */
+moe_status_t moe_route_scored_backward(const float *logits, const int32_t *topk_idx, const float *dw, int T, int E,
+                                       int K, const moe_route_rule_t *rule, float *dlogits, cudaStream_t stream);
+
+/* What stands between two layers, in one pass: the norm of a layer's output
+ * y, its gate, the residual's scale and sum, and the norm that the next layer
+ * reads.  All in fp32, rounded once where a row is stored:
+ *   u  = y * rstd_post * gamma_post,  rstd_post = 1 / sqrt(mean(y^2) + eps)
+ *   r_out = res_scale * r + gate * u
+ *   n     = r_out * rstd_pre * gamma_pre,  rstd_pre = 1 / sqrt(mean(r_out^2) + eps)
+ *                                          (of the fp32 r_out, before it is rounded)
+ * r, r_out [T, d] fp32 (residual_fp32 1) or bf16 (0); y, n [T, d] bf16;
+ * gamma_post, gamma_pre [d] fp32; gate fp32, [d] (MOE_GATE_CHANNEL) or [T]
+ * (MOE_GATE_TOKEN); rstd_post, rstd_pre [T] fp32, kept for the backward.
+ * Parts left out: gamma_post NULL: u = y; gate NULL (MOE_GATE_NONE): gate 1;
+ * gamma_pre NULL: no n, no rstd_pre; y NULL: n of r alone (r_out is not
+ * written, res_scale 1, no gamma_post, no gate).  r_out may be r itself.
+ * d a multiple of 64, at most 16384; matrices, gammas and a channel gate
+ * 16-byte aligned; eps > 0.  One kernel launch.  */
+enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 };
+moe_status_t moe_norm_residual(const void *r, int residual_fp32, const uint16_t *y, const float *gamma_post,
+                               const float *gate, int gate_kind, float res_scale, const float *gamma_pre, float eps,
+                               int T, int d, void *r_out, uint16_t *n, float *rstd_post, float *rstd_pre,
+                               cudaStream_t stream);
+/* Its gradients for dr_out [T, d] (the residual's type; nullable with
+ * gamma_pre: zero) and dn [T, d] bf16 (with gamma_pre), from the forward's
+ * r_out as it was stored (r where y is NULL; not read without gamma_pre), y
+ * and rstd rows: dr [T, d] (the residual's type; may be dr_out itself),
+ * dy [T, d] bf16, dgamma_pre, dgamma_post [d] fp32, dgate as gate.  Outputs of
+ * parts left out are not written and may be NULL.  The sums over the tokens
+ * have a fixed order: deterministic.  `workspace` (16-byte aligned) holds
+ * moe_norm_residual_backward_workspace_size(T, d) bytes.  2 kernel launches
+ * (1 when no gradient is summed over the tokens).  */
+size_t moe_norm_residual_backward_workspace_size(int T, int d);
+moe_status_t moe_norm_residual_backward(const void *r_out, int residual_fp32, const uint16_t *y,
+                                        const float *gamma_post, const float *gate, int gate_kind, float res_scale,
+                                        const float *gamma_pre, const float *rstd_post, const float *rstd_pre,
+                                        const void *dr_out, const uint16_t *dn, int T, int d, void *dr, uint16_t *dy,
+                                        float *dgamma_pre, float *dgamma_post, float *dgate, void *workspace,
+                                        size_t workspace_bytes, cudaStream_t stream);
+
+/* The global norm of a step's gradients and clipping by it, over many
+ * tensors, nothing read back to the host:
+ *   norm_out[0] = sqrt(sum over all tensors of |g|^2)          (fp32, device)
+ *   outs[i] = g_i * min(1, max_norm / (norm + 1e-6)), rounded once
+ * grads[i] (and outs[i], of the same type) are device pointers to sizes[i]
+ * (>= 0) contiguous elements, fp32 or bf16 by kinds[i], aligned to their type
+ * only; the four arrays themselves are HOST memory, read before the call
+ * returns.  outs NULL clips in place.  Squares are summed in fp32 per CTA, the
+ * CTAs' sums in fp64, in a fixed order: deterministic.  An infinite norm
+ * scales by 0 and a NaN by NaN, as the formula does.  max_norm > 0 (INFINITY
+ * allowed).  `workspace` (4-byte aligned) holds
+ * moe_grad_norm_workspace_size(n_tensors) bytes.  Two launches for every 512
+ * tensors (moe_grad_norm: one, and one more).  */
+enum { MOE_GRAD_FP32 = 0, MOE_GRAD_BF16 = 1 };
+size_t moe_grad_norm_workspace_size(int n_tensors);
+moe_status_t moe_grad_norm(const void *const *grads, const int64_t *sizes, const int32_t *kinds, int n_tensors,
+                           float *norm_out, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+moe_status_t moe_grad_norm_clip(const void *const *grads, void *const *outs, const int64_t *sizes,
+                                const int32_t *kinds, int n_tensors, float max_norm, float *norm_out, void *workspace,
+                                size_t workspace_bytes, cudaStream_t stream);
+
 /* Step a3 -- permute (local part of dispatch, Figure 3 caption):
  * x_perm[row_of[t,k], :] = x[t, :] for every (t, k).  */
 moe_status_t moe_permute(const uint16_t *x, const int32_t *row_of, int T, int K, int d,
@@ -245,6 +343,14 @@ moe_status_t moe_forward_train(const uint16_t *x, const float *Wr, const float *
                                const uint16_t *W1, const uint16_t *W2, int T, int d, int E, int K,
                                int f, uint16_t *y, void *workspace, size_t workspace_bytes,
                                uint16_t *preact, cudaStream_t stream);
+
+/* The layer routed by moe_route_scored: moe_forward, or with `preact`
+ * (nullable, [T*K, 2f] bf16) moe_forward_train, on the same workspace layout.
+ * Same number of launches.  */
+moe_status_t moe_forward_scored(const uint16_t *x, const float *Wr, const float *bias, const float *sel_bias,
+                                const moe_route_rule_t *rule, const uint16_t *W1, const uint16_t *W2, int T, int d,
+                                int E, int K, int f, uint16_t *y, void *workspace, size_t workspace_bytes,
+                                uint16_t *preact, cudaStream_t stream);
 
 /* moe_forward with the activations in HOST memory (pinned memory makes the
  * copies asynchronous): copies x_host [T, d] bf16 into the workspace,
@@ -380,6 +486,16 @@ moe_status_t moe_backward(const uint16_t *x, const float *Wr, const float *bias,
                           const uint16_t *preact, uint16_t *dx, float *dWr, float *dbias,
                           float *dW1, float *dW2, void *workspace,
                           size_t workspace_bytes, cudaStream_t stream);
+
+/* moe_backward for a layer routed by moe_route_scored with the same rule
+ * (same workspaces and launches).  Softmax scores need renorm: raw ones send a
+ * gradient to every logit, which returns MOE_ERR_UNSUPPORTED here (use
+ * moe_route_scored_backward).  */
+moe_status_t moe_backward_scored(const uint16_t *x, const float *Wr, const moe_route_rule_t *rule, const uint16_t *W1,
+                                 const uint16_t *W2, int T, int d, int E, int K, int f, const uint16_t *dy,
+                                 const void *fwd_workspace, size_t fwd_workspace_bytes, const uint16_t *preact,
+                                 uint16_t *dx, float *dWr, float *dbias, float *dW1, float *dW2, void *workspace,
+                                 size_t workspace_bytes, cudaStream_t stream);
 
 /* Reads and clears the device status word of the current device (0 = OK, or
  * a moe_status_t a kernel recorded).  Synchronous: call outside capture. */

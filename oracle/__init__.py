@@ -11,3 +11,4 @@ from .moe_oracle import (combine, dispatch_order, expert_counts, expert_ffn, for
 from .mxfp8 import (e4m3_decode, e4m3_encode, e4m3_round, expert_ffn_mxfp8, forward_mxfp8,  # noqa: F401
                     forward_mxfp8_tokens, mx_dequantize, mx_quantize, mx_scale_exponent)
 from .backward import backward, backward_sampled, forward_fp64  # noqa: F401
+from . import operators  # noqa: F401
