@@ -1,7 +1,7 @@
 // Internal launchers of the sm_103a kernels (not part of the C ABI).
 #pragma once
 
-#include <cuda_runtime_api.h>
+#include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -29,6 +29,23 @@ cudaError_t one_wave(Kernel kernel, int threads, std::atomic<int> (&cache)[64], 
     }
     *blocks = wave;
     return cudaSuccess;
+}
+
+// Launches `kernel` behind the last kernel of the stream without waiting for
+// it to end: the kernel's blocks may start as the others leave, and it calls
+// grid_dependency_wait() before it touches what they wrote.
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), int blocks, int threads, cudaStream_t stream, A... args) {
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
 // Tokens per routing chunk: the unit of the per-chunk histograms that make the
@@ -102,6 +119,8 @@ struct NormResidualGradArgs {
     void *dr;
     uint16_t *dy;
     float *dgamma_pre, *dgamma_post, *dgate;
+    int *status;
+    uint64_t wait_ns;
 };
 cudaError_t launch_norm_residual_bwd(const NormResidualArgs &a, const NormResidualGradArgs &g, float *part,
                                      int *launches, cudaStream_t stream);

@@ -448,7 +448,10 @@ moe_status_t moe_norm_residual_backward(const void *r_out, int residual_fp32, co
         return MOE_ERR_INVALID_ARG;
     if (gate && (!dgate || !aligned(dgate, 4))) return MOE_ERR_INVALID_ARG;
     if (workspace_bytes < moe::norm_residual_bwd_part_bytes(T, d)) return MOE_ERR_WORKSPACE;
-    const moe::NormResidualGradArgs g{r_out, dr_out, dn, rstd_post, rstd_pre, dr, dy, dgamma_pre, dgamma_post, dgate};
+    DeviceState *ds = nullptr;
+    if ((st = device_state(&ds)) != MOE_OK) return st;
+    const moe::NormResidualGradArgs g{r_out,      dr_out,      dn,    rstd_post,  rstd_pre,    dr, dy,
+                                      dgamma_pre, dgamma_post, dgate, ds->status, kWaitLimitNs};
     int launches = 0;
     const cudaError_t e = moe::launch_norm_residual_bwd(a, g, static_cast<float *>(workspace), &launches, stream);
     g_launches.fetch_add(launches, std::memory_order_relaxed);
