@@ -474,9 +474,11 @@ moe_status_t grad_clip_impl(const void *const *grads, void *const *outs, const i
         !aligned(workspace, 4))
         return MOE_ERR_INVALID_ARG;
     if (clip && !(max_norm > 0.0f)) return MOE_ERR_INVALID_ARG;
+    int64_t total = 0;
     for (int i = 0; i < n; ++i) {
         if (sizes[i] < 0 || (kinds[i] != MOE_GRAD_FP32 && kinds[i] != MOE_GRAD_BF16)) return MOE_ERR_INVALID_ARG;
-        if (sizes[i] > (int64_t(1) << 40)) return MOE_ERR_UNSUPPORTED;
+        if (sizes[i] > (int64_t(1) << 40) - total) return MOE_ERR_UNSUPPORTED;  // of all tensors together
+        total += sizes[i];
         const size_t a = kinds[i] == MOE_GRAD_BF16 ? 2 : 4;
         if (sizes[i] && (!grads[i] || !aligned(grads[i], a) || (outs && (!outs[i] || !aligned(outs[i], a)))))
             return MOE_ERR_INVALID_ARG;
