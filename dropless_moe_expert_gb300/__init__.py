@@ -72,7 +72,7 @@ def _load():
             "(python -c 'import __graft_entry__ as g; g.build()')")
     L = ctypes.CDLL(path)
     P, I, S, U64, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64, ctypes.c_float
-    RULE = ctypes.POINTER(_RouteRule)
+    RULE = P  # moe_route_rule_t *
     sig = {
         "moe_status_string": (ctypes.c_char_p, [I]),
         "moe_abi_version": (I, []),
@@ -112,6 +112,7 @@ def _load():
         "moe_backward": (I, [P, P, P, P, P, I, I, I, I, I, P, P, S, P, P, P, P, P, P, P, S, P]),
         "moe_combine_counters_size": (S, [I, I]),
         "moe_grouped_gemm2_combine": (I, [P, P, I, I, I, I, P, P, P, P, I, I, P, P, S, P, P]),
+        "moe_route_scored_workspace_size": (S, [I, I, I]),
         "moe_route_scored": (I, [P, P, I, I, I, RULE, P, P, P, P, P, P, P, S, P]),
         "moe_route_scored_backward": (I, [P, P, P, I, I, I, RULE, P, P]),
         "moe_forward_scored": (I, [P, P, P, P, RULE, P, P, I, I, I, I, I, P, P, S, P, P]),
@@ -144,6 +145,12 @@ def _stream(stream=None) -> int:
     return stream.cuda_stream
 
 
+def _stream_of(t, stream=None) -> int:
+    """The given stream, or the current one of the tensor's device (asked for
+    without building a torch.cuda.Stream: a microsecond per call)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+
+
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -154,6 +161,8 @@ def _check(code: int, where: str):
 
 
 def _need(t, dtype, shape, name):
+    if t is not None and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t
     if t is None:
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
@@ -243,8 +252,9 @@ class RouteRule:
     def __post_init__(self):
         if self.score not in ("sigmoid", "softmax"):
             raise ValueError(f"score must be 'sigmoid' or 'softmax', got {self.score!r}")
-        object.__setattr__(self, "_c", _RouteRule(int(self.score == "softmax"), self.n_group, self.topk_group,
-                                                  self.group_top, int(self.renorm), self.scale))
+        object.__setattr__(self, "_struct", _RouteRule(int(self.score == "softmax"), self.n_group, self.topk_group,
+                                                       self.group_top, int(self.renorm), self.scale))
+        object.__setattr__(self, "_c", ctypes.addressof(self._struct))
 
 
 class RouteBuffers:
@@ -252,9 +262,9 @@ class RouteBuffers:
     again from call to call."""
 
     def __init__(self, T: int, E: int, K: int, device="cuda"):
-        i32, n = torch.int32, route_workspace_size(T, E, K)
+        i32, n = torch.int32, int(lib.moe_route_scored_workspace_size(T, E, K))
         if n == 0:
-            raise MoEError(1, "moe_route_workspace_size")
+            raise MoEError(2, "moe_route_scored_workspace_size")
 
         def make(dtype, *shape):
             return torch.empty(shape, dtype=dtype, device=device)
@@ -281,7 +291,7 @@ def route_scored(logits, K: int, rule: RouteRule, sel_bias=None, buffers: RouteB
         buffers = RouteBuffers(T, E, K, logits.device)
     elif buffers.size != (T, E, K):
         raise ValueError(f"buffers are for (T, E, K) = {buffers.size}, not {(T, E, K)}")
-    _check(lib.moe_route_scored(_ptr(logits), _ptr(sel_bias), T, E, K, rule._c, *buffers._args, _stream(stream)),
+    _check(lib.moe_route_scored(_ptr(logits), _ptr(sel_bias), T, E, K, rule._c, *buffers._args, _stream_of(logits, stream)),
            "moe_route_scored")
     return buffers.routing
 
@@ -295,7 +305,7 @@ def route_scored_backward(logits, topk_idx, dw, rule: RouteRule, out=None, strea
     _need(dw, torch.float32, (T, K), "dw")
     out = _empty((T, E), torch.float32, logits) if out is None else _need(out, torch.float32, (T, E), "dlogits")
     _check(lib.moe_route_scored_backward(_ptr(logits), _ptr(topk_idx), _ptr(dw), T, E, K, rule._c, _ptr(out),
-                                         _stream(stream)), "moe_route_scored_backward")
+                                         _stream_of(logits, stream)), "moe_route_scored_backward")
     return out
 
 
@@ -384,7 +394,8 @@ def norm_residual(r, y=None, *, gamma_post=None, gate=None, gamma_pre=None, res_
             _need(out.rstd_post, torch.float32, (T,), "out.rstd_post")
     _check(lib.moe_norm_residual(_ptr(r), f32, _ptr(y), _ptr(gamma_post), _ptr(gate), kind, res_scale,
                                  _ptr(gamma_pre), eps, T, d, _ptr(out.r) if y is not None else None, _ptr(out.n),
-                                 _ptr(out.rstd_post), _ptr(out.rstd_pre), _stream(stream)), "moe_norm_residual")
+                                 _ptr(out.rstd_post), _ptr(out.rstd_pre), _stream_of(r, stream)),
+           "moe_norm_residual")
     if y is None:
         out.r = r
     return out
@@ -422,7 +433,7 @@ def norm_residual_backward(r, dr, dn=None, y=None, *, gamma_post=None, gate=None
     _check(lib.moe_norm_residual_backward(
         _ptr(r), f32, _ptr(y), _ptr(gamma_post), _ptr(gate), kind, res_scale, _ptr(gamma_pre), _ptr(rstd_post),
         _ptr(rstd_pre), _ptr(dr), _ptr(dn), T, d, _ptr(out.dr), _ptr(out.dy), _ptr(out.dgamma_pre),
-        _ptr(out.dgamma_post), _ptr(out.dgate), _ptr(out.workspace), out.workspace.numel(), _stream(stream)),
+        _ptr(out.dgamma_post), _ptr(out.dgate), _ptr(out.workspace), out.workspace.numel(), _stream_of(r, stream)),
         "moe_norm_residual_backward")
     return out
 
@@ -456,9 +467,10 @@ class GradClipper:
         self._kinds = (ctypes.c_int32 * n)(*[int(g.dtype == torch.bfloat16) for g in self.grads])
         self.norm = torch.empty((1,), dtype=torch.float32, device=device)
         self.workspace = torch.empty((int(lib.moe_grad_norm_workspace_size(n)),), dtype=torch.uint8, device=device)
+        self._ws = (_ptr(self.norm), _ptr(self.workspace), self.workspace.numel())
 
     def __call__(self, max_norm: float | None = None, stream=None):
-        ws = (_ptr(self.norm), _ptr(self.workspace), self.workspace.numel(), _stream(stream))
+        ws = (*self._ws, _stream_of(self.norm, stream))
         if max_norm is None:
             _check(lib.moe_grad_norm(self._ptrs, self._sizes, self._kinds, len(self.grads), *ws), "moe_grad_norm")
         else:

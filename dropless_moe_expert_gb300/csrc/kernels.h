@@ -73,11 +73,6 @@ cudaError_t launch_route(const float *logits, int T, int E, int K, int32_t *topk
                          int32_t *counts, int32_t *offsets, int32_t *row_of, int32_t *src_tok, int32_t *workspace,
                          cudaStream_t stream);
 
-// The scan and scatter of a routing whose top-K kernel has written topk_idx,
-// each pair's rank inside its chunk (row_of) and the per-chunk counts (workspace).
-cudaError_t launch_route_dispatch(const int32_t *topk_idx, int T, int E, int K, int32_t *counts, int32_t *offsets,
-                                  int32_t *row_of, int32_t *src_tok, int32_t *workspace, cudaStream_t stream);
-
 // Routing by scores of all experts (route_scored.cu): the moe_route_rule_t of the C ABI, checked.
 constexpr float kRouteEps = 1e-20f;  // beside the sum of the chosen scores
 struct RouteRule {
@@ -88,7 +83,8 @@ struct RouteRule {
 };
 cudaError_t launch_route_scored(const float *logits, const float *sel_bias, int T, int E, int K, const RouteRule &rule,
                                 int32_t *topk_idx, float *topk_w, int32_t *counts, int32_t *offsets, int32_t *row_of,
-                                int32_t *src_tok, int32_t *workspace, cudaStream_t stream);
+                                int32_t *src_tok, uint8_t *workspace, int *launches, cudaStream_t stream);
+size_t route_scored_workspace_bytes(int T, int E);
 cudaError_t launch_route_scored_bwd(const float *logits, const int32_t *topk_idx, const float *dw, int T, int E, int K,
                                     const RouteRule &rule, float *dlogits, cudaStream_t stream);
 // dl [T, K] and dl_row [TK] (by row_of), as launch_router_bwd for the layer's own softmax

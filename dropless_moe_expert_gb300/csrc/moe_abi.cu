@@ -8,6 +8,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <mutex>
@@ -186,7 +187,7 @@ bool forward_layout(int T, int d, int E, int K, int f, moe_forward_layout_t *L) 
     L->offsets = take(static_cast<size_t>(E + 1) * 4);
     L->row_of = take(TK * 4);
     L->src_tok = take(TK * 4);
-    L->route_ws = take(moe::route_workspace_bytes(T, E));
+    L->route_ws = take(std::max(moe::route_workspace_bytes(T, E), moe::route_scored_workspace_bytes(T, E)));
     L->router_ws = take(moe::router_workspace_bytes(d, E));
     L->x_perm = take(TK * d * 2);
     L->h = take(TK * f * 2);
@@ -372,6 +373,11 @@ moe_status_t moe_route(const float *logits, int T, int E, int K, int32_t *topk_i
                                          static_cast<int32_t *>(workspace), stream));
 }
 
+size_t moe_route_scored_workspace_size(int T, int E, int K) {
+    if (T < 1 || E < 1 || E > kMaxE || K < 1) return 0;
+    return moe::route_scored_workspace_bytes(T, E);
+}
+
 moe_status_t moe_route_scored(const float *logits, const float *sel_bias, int T, int E, int K,
                               const moe_route_rule_t *rule, int32_t *topk_idx, float *topk_w, int32_t *counts,
                               int32_t *offsets, int32_t *row_of, int32_t *src_tok, void *workspace,
@@ -381,16 +387,18 @@ moe_status_t moe_route_scored(const float *logits, const float *sel_bias, int T,
         return MOE_ERR_INVALID_ARG;
     if (!aligned(logits, 4) || (sel_bias && !aligned(sel_bias, 4)) || !aligned(topk_idx, 4) || !aligned(topk_w, 4) ||
         !aligned(counts, 4) || !aligned(offsets, 4) || !aligned(row_of, 4) || !aligned(src_tok, 4) ||
-        !aligned(workspace, 4))
+        !aligned(workspace, 16))
         return MOE_ERR_INVALID_ARG;
     moe_status_t st = check_shape(T, 64, E, K, 64, false, false);
     if (st != MOE_OK) return st;
     moe::RouteRule r;
     if ((st = check_rule(rule, E, K, &r)) != MOE_OK) return st;
-    if (workspace_bytes < moe::route_workspace_bytes(T, E)) return MOE_ERR_WORKSPACE;
-    g_launches.fetch_add(3, std::memory_order_relaxed);
-    return cuda_status(moe::launch_route_scored(logits, sel_bias, T, E, K, r, topk_idx, topk_w, counts, offsets,
-                                                row_of, src_tok, static_cast<int32_t *>(workspace), stream));
+    if (workspace_bytes < moe::route_scored_workspace_bytes(T, E)) return MOE_ERR_WORKSPACE;
+    int launches = 0;
+    const cudaError_t e = moe::launch_route_scored(logits, sel_bias, T, E, K, r, topk_idx, topk_w, counts, offsets,
+                                                   row_of, src_tok, static_cast<uint8_t *>(workspace), &launches, stream);
+    g_launches.fetch_add(launches, std::memory_order_relaxed);
+    return cuda_status(e);
 }
 
 moe_status_t moe_route_scored_backward(const float *logits, const int32_t *topk_idx, const float *dw, int T, int E,

@@ -19,18 +19,26 @@
 //   sigmoid: dl_k = ds_k s_k (1 - s_k) for the chosen, 0 for the others;
 //   softmax: dl_e = s_e (ds_e - sum_j s_j ds_j) for every expert.
 #include "kernels.h"
+#include "ptx.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace moe {
 namespace rs {
 
-constexpr int CH = kRouteChunk;  // tokens per CTA
 constexpr int MAX_E = 256;
-constexpr int MAX_K = 16;
-constexpr int WARPS = 16;
-constexpr int THREADS = WARPS * 32;
+constexpr int CH = 16;             // tokens per chunk: a CTA of the top-K kernel, a warp per token
+constexpr int FEW = 32;            // tokens that one CTA routes alone
+constexpr int SPANS = 152;         // CTAs of the dispatch kernel, each a run of chunks
+constexpr int DISPATCH_THREADS = 1024;
+constexpr size_t SELF_SUM_BYTES = 256 * 1024;  // of counts that every dispatch CTA adds up itself
 constexpr unsigned FULL = 0xffffffffu;
+
+// Bytes of a chunk's row of counts (one byte per expert, whole 16-byte words).
+__host__ __device__ constexpr int count_pitch(int E) { return (E + 15) / 16 * 16; }
+int num_chunks(int T) { return (T + CH - 1) / CH; }
+int span_chunks(int chunks) { return (chunks + SPANS - 1) / SPANS; }
 
 // Keys that order as the values do, -0.0 as +0.0; 0 is kept for "not there".
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -82,27 +90,62 @@ __device__ __forceinline__ void scores(float *v, int E, int lane, bool softmax) 
     for (int j = 0; j < EPL; ++j) v[j] = v[j] / sum;
 }
 
-// One CTA per chunk of CH tokens, one warp per token at a time.
-template <int EPL>
-__global__ void __launch_bounds__(THREADS)
+// The runs that stay open, as a bit mask per 32 runs (`open`, filled by the
+// warp).  `keys`: the experts' keys in shared memory; `score`: room for a key
+// per run.  Lanes share a run's experts; each keeps its two largest.
+__device__ __forceinline__ void open_runs(const uint32_t *keys, uint32_t *score, uint32_t *open, int per,
+                                          const RouteRule &rule, int lane) {
+    const int G = rule.n_group;
+    int share = 1;  // lanes per run: the largest power of two that leaves every run its own
+    while (2 * share * G <= 32 && share < per) share *= 2;
+    const int at_once = 32 / share;
+    for (int g0 = 0; g0 < G; g0 += at_once) {
+        const int g = g0 + lane / share;
+        uint32_t a = 0, b = 0;
+        if (g < G)
+            for (int i = lane % share; i < per; i += share) {
+                const uint32_t k = keys[g * per + i];
+                b = max(b, min(a, k));
+                a = max(a, k);
+            }
+        for (int o = share / 2; o; o >>= 1) {
+            const uint32_t c = __shfl_xor_sync(FULL, a, o), d = __shfl_xor_sync(FULL, b, o);
+            b = max(max(b, d), min(a, c));
+            a = max(a, c);
+        }
+        if (g < G && lane % share == 0)
+            score[g] = rule.group_top == 2 && b ? order_key(key_value(a) + key_value(b)) : a;
+    }
+    __syncwarp();
+    for (int g0 = 0; g0 < G; g0 += 32) {
+        const int g = g0 + lane;
+        const uint32_t mine = g < G ? score[g] : 0u;
+        int above = 0;  // runs that come before this one
+        for (int o = 0; o < G; ++o) above += score[o] > mine || (score[o] == mine && o < g);
+        const uint32_t bits = __ballot_sync(FULL, g < G && above < rule.topk_group);
+        if (lane == 0) open[g0 >> 5] = bits;
+    }
+    __syncwarp();
+}
+
+// A warp per token, TOK tokens per CTA.  FINAL: the CTA holds every token and
+// writes the dispatch order too; else it writes its chunk's counts and each
+// pair's rank inside the chunk (in row_of) for the dispatch kernel.
+template <int EPL, int TOK, bool FINAL>
+__global__ void __launch_bounds__(TOK * 32)
 route_scored_topk_kernel(const float *__restrict__ L, const float *__restrict__ bias, int T, int E, int K,
                          RouteRule rule, int32_t *__restrict__ topk_idx, float *__restrict__ topk_w,
-                         int32_t *__restrict__ row_rank, int32_t *__restrict__ chunk_counts) {
-    __shared__ uint32_t bits[MAX_E][CH / 32];
-    __shared__ int32_t s_idx[CH * MAX_K];
-    __shared__ uint32_t s_key[WARPS][MAX_E], s_group[WARPS][MAX_E];
+                         int32_t *__restrict__ row_of, uint8_t *__restrict__ chunk_counts,
+                         int32_t *__restrict__ counts, int32_t *__restrict__ offsets, int32_t *__restrict__ src_tok) {
+    __shared__ uint32_t chose[MAX_E];  // bit i: token i of the CTA chose the expert
+    __shared__ int32_t s_off[MAX_E];
+    extern __shared__ uint32_t s_groups[];  // with groups: keys [TOK][E], scores [TOK][n_group], open [TOK][8]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t0 = blockIdx.x * CH;
-    const int nt = min(CH, T - t0);
-    const int per = E / rule.n_group;
-    for (int i = threadIdx.x; i < E * (CH / 32); i += THREADS) (&bits[0][0])[i] = 0u;
+    const int t = blockIdx.x * TOK + warp;
+    for (int e = threadIdx.x; e < MAX_E; e += TOK * 32) chose[e] = 0u;
     __syncthreads();
-    float b[EPL];
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) b[j] = bias && lane + 32 * j < E ? bias[lane + 32 * j] : 0.0f;
-
-    for (int tl = warp; tl < nt; tl += WARPS) {
-        const int t = t0 + tl;
+    int my_e = 0;
+    if (t < T) {
         const float *row = L + static_cast<size_t>(t) * E;
         float s[EPL];
         uint32_t key[EPL];
@@ -110,37 +153,25 @@ route_scored_topk_kernel(const float *__restrict__ L, const float *__restrict__ 
         for (int j = 0; j < EPL; ++j) s[j] = lane + 32 * j < E ? row[lane + 32 * j] : 0.0f;
         scores<EPL>(s, E, lane, rule.softmax);
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) key[j] = lane + 32 * j < E ? order_key(bias ? s[j] + b[j] : s[j]) : 0u;
+        for (int j = 0; j < EPL; ++j) {
+            const int e = lane + 32 * j;
+            key[j] = e < E ? order_key(bias ? s[j] + bias[e] : s[j]) : 0u;
+        }
         if (rule.topk_group < rule.n_group) {
-            uint32_t *sk = s_key[warp], *sg = s_group[warp];
-            __syncwarp();
+            uint32_t *keys = s_groups + warp * E;
+            uint32_t *score = s_groups + TOK * E + warp * rule.n_group;
+            uint32_t *open = s_groups + TOK * (E + rule.n_group) + warp * (MAX_E / 32);
+            const int per = E / rule.n_group;
 #pragma unroll
             for (int j = 0; j < EPL; ++j)
-                if (lane + 32 * j < E) sk[lane + 32 * j] = key[j];
+                if (lane + 32 * j < E) keys[lane + 32 * j] = key[j];
             __syncwarp();
-            for (int g = lane; g < rule.n_group; g += 32) {
-                uint32_t a = 0, c = 0;  // the two largest
-                for (int i = 0; i < per; ++i) {
-                    const uint32_t k = sk[g * per + i];
-                    c = max(c, min(a, k));
-                    a = max(a, k);
-                }
-                sg[g] = rule.group_top == 2 && c ? order_key(key_value(a) + key_value(c)) : a;
-            }
-            __syncwarp();
-            uint32_t open = 0;  // bit i: run lane + 32 i stays open
-            for (int g = lane, i = 0; g < rule.n_group; g += 32, ++i) {
-                const uint32_t mine = sg[g];
-                int above = 0;
-                for (int o = 0; o < rule.n_group; ++o) above += sg[o] > mine || (sg[o] == mine && o < g);
-                if (above < rule.topk_group) open |= 1u << i;
-            }
-            __syncwarp();
-            for (int g = lane, i = 0; g < rule.n_group; g += 32, ++i) sg[g] = (open >> i) & 1u;
-            __syncwarp();
+            open_runs(keys, score, open, per, rule, lane);
 #pragma unroll
-            for (int j = 0; j < EPL; ++j)
-                if (lane + 32 * j < E && !sg[(lane + 32 * j) / per]) key[j] = 0u;
+            for (int j = 0; j < EPL; ++j) {
+                const int g = (lane + 32 * j) / per;
+                if (lane + 32 * j < E && !((open[g >> 5] >> (g & 31)) & 1u)) key[j] = 0u;
+            }
         }
         uint32_t best = 0;
         int bj = 0;
@@ -152,7 +183,6 @@ route_scored_topk_kernel(const float *__restrict__ L, const float *__restrict__ 
                 if (key[j] > best) best = key[j], bj = j, bs = s[j];
         };
         find();
-        int my_e = 0;
         float my_s = 0.0f, sum = 0.0f;
         for (int k = 0; k < K; ++k) {
             const uint32_t top = __reduce_max_sync(FULL, best);
@@ -171,22 +201,202 @@ route_scored_topk_kernel(const float *__restrict__ L, const float *__restrict__ 
             const size_t p = static_cast<size_t>(t) * K + lane;
             topk_idx[p] = my_e;
             topk_w[p] = rule.renorm ? rule.scale * my_s / (sum + kRouteEps) : rule.scale * my_s;
-            s_idx[tl * K + lane] = my_e;
-            atomicOr(&bits[my_e][tl >> 5], 1u << (tl & 31));
+            atomicOr(&chose[my_e], 1u << warp);  // the final mask does not depend on the order
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += THREADS) {
-        int c = 0;
+    if constexpr (FINAL) {
+        if (warp == 0) {
+            int carry = 0;
+            for (int base = 0; base < E; base += 32) {
+                const int e = base + lane;
+                const int c = e < E ? __popc(chose[e]) : 0;
+                int incl = c;
 #pragma unroll
-        for (int w = 0; w < CH / 32; ++w) c += __popc(bits[e][w]);
-        chunk_counts[static_cast<size_t>(blockIdx.x) * E + e] = c;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(FULL, incl, o);
+                    if (lane >= o) incl += v;
+                }
+                if (e < E) {
+                    s_off[e] = offsets[e] = carry + incl - c;
+                    counts[e] = c;
+                }
+                carry += __shfl_sync(FULL, incl, 31);
+            }
+            if (lane == 0) offsets[E] = carry;
+        }
+        __syncthreads();
+    } else {
+        uint8_t *mine = chunk_counts + static_cast<size_t>(blockIdx.x) * count_pitch(E);
+        for (int e = threadIdx.x; e < count_pitch(E); e += TOK * 32)
+            mine[e] = static_cast<uint8_t>(e < E ? __popc(chose[e]) : 0);
     }
-    for (int p = threadIdx.x; p < nt * K; p += THREADS) {
-        const int tl = p / K, e = s_idx[p];
-        int r = __popc(bits[e][tl >> 5] & ((1u << (tl & 31)) - 1u));
-        for (int w = 0; w < (tl >> 5); ++w) r += __popc(bits[e][w]);
-        row_rank[static_cast<size_t>(t0) * K + p] = r;
+    if (t < T && lane < K) {
+        int r = __popc(chose[my_e] & ((1u << warp) - 1u));
+        if constexpr (FINAL) {
+            r += s_off[my_e];
+            src_tok[r] = t;
+        }
+        row_of[static_cast<size_t>(t) * K + lane] = r;
+    }
+}
+
+// Sums of the rows [from, to) of byte counts: thread (word, slice) of the
+// block adds 16 experts' bytes of every slice-th row, as sixteen 16-bit sums.
+struct Sums16 {
+    uint32_t even[4], odd[4];
+    __device__ __forceinline__ void add(const uint4 &v) {
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            even[i] += x[i] & 0x00ff00ffu;
+            odd[i] += (x[i] >> 8) & 0x00ff00ffu;
+        }
+    }
+};
+
+// span_counts[s][e]: the pairs of expert e in span s.
+__global__ void __launch_bounds__(256)
+route_scored_span_kernel(const uint8_t *__restrict__ chunk_counts, int chunks, int per_span, int E,
+                         int32_t *__restrict__ span_counts) {
+    grid_dependency_wait();  // launched early: the counts
+    const int c0 = blockIdx.x * per_span, c1 = min(chunks, c0 + per_span);
+    for (int e = threadIdx.x; e < E; e += 256) {
+        int sum = 0;
+#pragma unroll 8
+        for (int c = c0; c < c1; ++c) sum += chunk_counts[static_cast<size_t>(c) * count_pitch(E) + e];
+        span_counts[static_cast<size_t>(blockIdx.x) * E + e] = sum;
+    }
+}
+
+// Counts, offsets and the dispatch order from the chunks' counts and the
+// pairs' ranks.  CTA s takes the chunks of span s.  It needs the experts'
+// totals and what the spans before it hold: summed from the chunks' bytes by
+// every CTA itself, or from the spans' sums (SPANNED) where the bytes are many.
+template <bool SPANNED>
+__global__ void __launch_bounds__(DISPATCH_THREADS)
+route_scored_dispatch_kernel(const int32_t *__restrict__ topk_idx, const uint8_t *__restrict__ chunk_counts,
+                             const int32_t *__restrict__ span_counts, int T, int E, int K, int chunks, int per_span,
+                             int32_t *__restrict__ counts, int32_t *__restrict__ offsets,
+                             int32_t *__restrict__ row_of, int32_t *__restrict__ src_tok) {
+    constexpr int WARPS = DISPATCH_THREADS / 32;
+    constexpr int BLOCK = 16;  // chunks whose first rows are held at a time
+    __shared__ union {
+        uint16_t part[2][WARPS][MAX_E];  // the warps' sums: all chunks, those before the span
+        int32_t base[BLOCK][MAX_E];      // then the chunks' first rows
+    } sh;
+    __shared__ int32_t s_total[MAX_E], s_next[MAX_E];  // totals, then offsets; the experts' next rows
+    grid_dependency_wait();  // launched early: the choices, ranks and counts
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int pitch = count_pitch(E);
+    const int c0 = blockIdx.x * per_span, c1 = min(chunks, c0 + per_span);
+    if constexpr (SPANNED) {
+        const int e = threadIdx.x;
+        if (e < E) {
+            int total = 0, before = 0;
+#pragma unroll 8
+            for (int s = 0; s < static_cast<int>(gridDim.x); ++s) {
+                const int v = span_counts[static_cast<size_t>(s) * E + e];
+                total += v;
+                before += s < static_cast<int>(blockIdx.x) ? v : 0;
+            }
+            s_total[e] = total;
+            s_next[e] = before;
+        }
+    } else {
+        const int words = pitch / 16;  // at most 16; the words of a row lie in neighbouring lanes
+        int lanes = 1;
+        while (lanes < words) lanes *= 2;
+        const int word = lane % lanes, slices = DISPATCH_THREADS / lanes;
+        Sums16 all = {}, before = {};
+        if (word < words) {
+#pragma unroll 4
+            for (int c = threadIdx.x / lanes; c < chunks; c += slices) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(chunk_counts + static_cast<size_t>(c) * pitch + word * 16);
+                all.add(v);
+                if (c < c0) before.add(v);
+            }
+        }
+        for (int o = lanes; o < 32; o <<= 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                all.even[i] += __shfl_xor_sync(FULL, all.even[i], o);
+                all.odd[i] += __shfl_xor_sync(FULL, all.odd[i], o);
+                before.even[i] += __shfl_xor_sync(FULL, before.even[i], o);
+                before.odd[i] += __shfl_xor_sync(FULL, before.odd[i], o);
+            }
+        }
+        if (lane < words) {
+            uint16_t *a = &sh.part[0][warp][word * 16], *b = &sh.part[1][warp][word * 16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // byte order: even 0, odd 0, even 1, odd 1 of each 32-bit word
+                a[4 * i] = all.even[i] & 0xffffu, a[4 * i + 1] = all.odd[i] & 0xffffu;
+                a[4 * i + 2] = all.even[i] >> 16, a[4 * i + 3] = all.odd[i] >> 16;
+                b[4 * i] = before.even[i] & 0xffffu, b[4 * i + 1] = before.odd[i] & 0xffffu;
+                b[4 * i + 2] = before.even[i] >> 16, b[4 * i + 3] = before.odd[i] >> 16;
+            }
+        }
+        __syncthreads();
+        if (threadIdx.x < 2 * MAX_E) {
+            const int set = threadIdx.x / MAX_E, e = threadIdx.x % MAX_E;
+            if (e < E) {
+                int sum = 0;
+#pragma unroll 8
+                for (int w = 0; w < WARPS; ++w) sum += sh.part[set][w][e];
+                (set ? s_next : s_total)[e] = sum;
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {  // offsets, and the span's first rows
+        int carry = 0;
+        for (int base = 0; base < E; base += 32) {
+            const int e = base + lane;
+            const int c = e < E ? s_total[e] : 0;
+            int incl = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(FULL, incl, o);
+                if (lane >= o) incl += v;
+            }
+            if (e < E) {
+                s_next[e] += carry + incl - c;
+                if (blockIdx.x == 0) {
+                    counts[e] = c;
+                    offsets[e] = carry + incl - c;
+                }
+            }
+            carry += __shfl_sync(FULL, incl, 31);
+        }
+        if (blockIdx.x == 0 && lane == 0) offsets[E] = carry;
+    }
+    __syncthreads();
+    for (int b0 = c0; b0 < c1; b0 += BLOCK) {
+        const int nb = min(BLOCK, c1 - b0);
+        if (threadIdx.x < E) {
+            const int e = threadIdx.x;
+            int run = s_next[e];
+            uint8_t n[BLOCK];
+#pragma unroll
+            for (int i = 0; i < BLOCK; ++i) n[i] = i < nb ? chunk_counts[static_cast<size_t>(b0 + i) * pitch + e] : 0;
+#pragma unroll
+            for (int i = 0; i < BLOCK; ++i) {
+                sh.base[i][e] = run;
+                run += n[i];
+            }
+            s_next[e] = run;
+        }
+        __syncthreads();
+        const int64_t first = static_cast<int64_t>(b0) * CH * K;
+        const int64_t last = min(static_cast<int64_t>(T), static_cast<int64_t>(b0 + nb) * CH) * K;
+        for (int64_t p = first + threadIdx.x; p < last; p += DISPATCH_THREADS) {
+            const int e = topk_idx[p], rank = row_of[p];
+            const int i = static_cast<int>(p - first) / (CH * K);
+            const int r = sh.base[i][e] + rank;
+            row_of[p] = r;
+            src_tok[r] = static_cast<int32_t>(p / K);
+        }
+        __syncthreads();
     }
 }
 
@@ -280,21 +490,54 @@ route_scored_bwd_rows_kernel(const float *__restrict__ L, const int32_t *__restr
 
 }  // namespace rs
 
+size_t route_scored_workspace_bytes(int T, int E) {
+    return static_cast<size_t>(rs::num_chunks(T)) * rs::count_pitch(E) + sizeof(int32_t) * rs::SPANS * E;
+}
+
 cudaError_t launch_route_scored(const float *logits, const float *sel_bias, int T, int E, int K, const RouteRule &rule,
                                 int32_t *topk_idx, float *topk_w, int32_t *counts, int32_t *offsets, int32_t *row_of,
-                                int32_t *src_tok, int32_t *workspace, cudaStream_t stream) {
-    const int C = route_num_chunks(T);
-#define ROUTE_SCORED(EPL)                                                                                       \
-    rs::route_scored_topk_kernel<EPL><<<C, rs::THREADS, 0, stream>>>(logits, sel_bias, T, E, K, rule, topk_idx, \
-                                                                     topk_w, row_of, workspace)
-    if (E <= 32) ROUTE_SCORED(1);
-    else if (E <= 64) ROUTE_SCORED(2);
-    else if (E <= 128) ROUTE_SCORED(4);
-    else ROUTE_SCORED(8);
-#undef ROUTE_SCORED
-    const cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-    return launch_route_dispatch(topk_idx, T, E, K, counts, offsets, row_of, src_tok, workspace, stream);
+                                int32_t *src_tok, uint8_t *workspace, int *launches, cudaStream_t stream) {
+    const int chunks = rs::num_chunks(T);
+    const bool few = T <= rs::FEW;
+    const int tok = few ? rs::FEW : rs::CH;
+    const size_t smem =
+        rule.topk_group < rule.n_group ? static_cast<size_t>(tok) * (E + rule.n_group + rs::MAX_E / 32) * 4 : 0;
+    auto topk = [&](auto kernel) {
+        static_assert(rs::FEW * (2 * rs::MAX_E + rs::MAX_E / 32) * 4 < 227 * 1024, "keys and scores fit a CTA");
+        if (smem > 40 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+            if (e != cudaSuccess) return e;
+        }
+        kernel<<<few ? 1 : chunks, tok * 32, smem, stream>>>(logits, sel_bias, T, E, K, rule, topk_idx, topk_w, row_of,
+                                                             workspace, counts, offsets, src_tok);
+        return cudaGetLastError();
+    };
+    auto by_experts = [&](auto lanes) {
+        constexpr int EPL = decltype(lanes)::value;
+        return few ? topk(rs::route_scored_topk_kernel<EPL, rs::FEW, true>)
+                   : topk(rs::route_scored_topk_kernel<EPL, rs::CH, false>);
+    };
+    cudaError_t err = E <= 32    ? by_experts(std::integral_constant<int, 1>{})
+                      : E <= 64  ? by_experts(std::integral_constant<int, 2>{})
+                      : E <= 128 ? by_experts(std::integral_constant<int, 4>{})
+                                 : by_experts(std::integral_constant<int, 8>{});
+    *launches = 1;
+    if (err != cudaSuccess || few) return err;
+    const int per_span = rs::span_chunks(chunks), spans = (chunks + per_span - 1) / per_span;
+    const size_t count_bytes = static_cast<size_t>(chunks) * rs::count_pitch(E);
+    int32_t *span_counts = reinterpret_cast<int32_t *>(workspace + count_bytes);
+    const bool spanned = count_bytes > rs::SELF_SUM_BYTES;
+    if (spanned) {
+        err = launch_dependent(rs::route_scored_span_kernel, spans, 256, stream,
+                               static_cast<const uint8_t *>(workspace), chunks, per_span, E, span_counts);
+        if (err != cudaSuccess) return err;
+        ++*launches;
+    }
+    ++*launches;
+    return launch_dependent(spanned ? rs::route_scored_dispatch_kernel<true> : rs::route_scored_dispatch_kernel<false>,
+                            spans, rs::DISPATCH_THREADS, stream, static_cast<const int32_t *>(topk_idx),
+                            static_cast<const uint8_t *>(workspace), static_cast<const int32_t *>(span_counts), T, E,
+                            K, chunks, per_span, counts, offsets, row_of, src_tok);
 }
 
 cudaError_t launch_route_scored_bwd(const float *logits, const int32_t *topk_idx, const float *dw, int T, int E, int K,

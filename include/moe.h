@@ -158,11 +158,13 @@ moe_status_t moe_route_static(const float *logits, int T, int E, int K,
  *   softmax exp(l - max) over a sum folded by halves, padded to 256).
  *   topk_w[t,k] = scale * s_k / (sum_j s_j + 1e-20), or scale * s_k if
  *   renorm is 0.
- * The other outputs, the workspace, and determinism are moe_route's.  A
+ * The other outputs and determinism are moe_route's; `workspace` (16-byte
+ * aligned) holds moe_route_scored_workspace_size(T, E, K) bytes.  A
  * sel_bias of -INFINITY closes an expert (it is chosen only where the open
  * runs hold fewer than K others, the lowest indexes first).  NaN logits are
  * outside the contract; the choice is then some K distinct experts.  Needs
- * E % n_group == 0 and K <= topk_group * (E / n_group).  3 kernel launches. */
+ * E % n_group == 0 and K <= topk_group * (E / n_group).  One kernel launch up to 32 tokens, else two,
+ * or three where the tokens and experts are many. */
 enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };
 typedef struct {
     int score;                           /* MOE_SCORE_* */
@@ -170,6 +172,7 @@ typedef struct {
     int renorm;
     float scale;
 } moe_route_rule_t;
+size_t moe_route_scored_workspace_size(int T, int E, int K);
 moe_status_t moe_route_scored(const float *logits, const float *sel_bias, int T, int E, int K,
                               const moe_route_rule_t *rule, int32_t *topk_idx, float *topk_w, int32_t *counts,
                               int32_t *offsets, int32_t *row_of, int32_t *src_tok, void *workspace,
@@ -345,8 +348,7 @@ moe_status_t moe_forward_train(const uint16_t *x, const float *Wr, const float *
                                uint16_t *preact, cudaStream_t stream);
 
 /* The layer routed by moe_route_scored: moe_forward, or with `preact`
- * (nullable, [T*K, 2f] bf16) moe_forward_train, on the same workspace layout.
- * Same number of launches.  */
+ * (nullable, [T*K, 2f] bf16) moe_forward_train, on the same workspace layout.  */
 moe_status_t moe_forward_scored(const uint16_t *x, const float *Wr, const float *bias, const float *sel_bias,
                                 const moe_route_rule_t *rule, const uint16_t *W1, const uint16_t *W2, int T, int d,
                                 int E, int K, int f, uint16_t *y, void *workspace, size_t workspace_bytes,

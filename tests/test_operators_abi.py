@@ -19,7 +19,7 @@ def moe():
 
 def _rule(moe, **kw):
     base = dict(score=0, n_group=4, topk_group=2, group_top=2, renorm=1, scale=1.0)
-    return moe._RouteRule(*{**base, **kw}.values())
+    return ctypes.byref(moe._RouteRule(*{**base, **kw}.values()))
 
 
 def _route(moe, rule, T=8, E=64, K=4, at={}, ws=BIG):
@@ -40,8 +40,10 @@ def test_route_scored_refusals(moe):
     assert _route(moe, r, E=512) == 2 and _route(moe, _rule(moe, n_group=1, topk_group=1), K=17) == 2
     for name in ("l", "i", "w", "c", "o", "r", "s", "ws"):
         assert _route(moe, r, at={name: None}) == 1 and _route(moe, r, at={name: FAKE + 2}) == 1
-    assert _route(moe, r, at={"b": FAKE + 1}) == 1
-    assert _route(moe, r, T=1000, ws=moe.route_workspace_size(1000, 64, 4) - 4) == 3
+    assert _route(moe, r, at={"b": FAKE + 1}) == 1 and _route(moe, r, at={"ws": FAKE + 8}) == 1
+    assert moe.lib.moe_route_scored_workspace_size(0, 64, 4) == 0
+    assert moe.lib.moe_route_scored_workspace_size(8, 512, 4) == 0
+    assert _route(moe, r, T=1000, ws=moe.lib.moe_route_scored_workspace_size(1000, 64, 4) - 16) == 3
     for args in ((None, FAKE, FAKE), (FAKE, None, FAKE), (FAKE, FAKE, None), (FAKE, FAKE + 2, FAKE)):
         assert moe.lib.moe_route_scored_backward(*args, 8, 64, 4, r, FAKE, None) == 1
     assert moe.lib.moe_route_scored_backward(FAKE, FAKE, FAKE, 8, 64, 4, r, None, None) == 1
