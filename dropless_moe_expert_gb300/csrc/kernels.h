@@ -80,6 +80,7 @@ struct RouteRule {
     int n_group, topk_group, group_top;
     bool renorm;
     float scale;
+    int run_of;  // e * run_of >> 20 is expert e's run (e < 256)
 };
 cudaError_t launch_route_scored(const float *logits, const float *sel_bias, int T, int E, int K, const RouteRule &rule,
                                 int32_t *topk_idx, float *topk_w, int32_t *counts, int32_t *offsets, int32_t *row_of,

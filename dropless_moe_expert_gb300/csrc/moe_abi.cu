@@ -145,7 +145,7 @@ moe_status_t check_rule(const moe_route_rule_t *rule, int E, int K, moe::RouteRu
     if (K > rule->topk_group * (E / rule->n_group)) return MOE_ERR_INVALID_ARG;
     if (!std::isfinite(rule->scale)) return MOE_ERR_INVALID_ARG;
     *out = moe::RouteRule{rule->score == MOE_SCORE_SOFTMAX, rule->n_group, rule->topk_group, rule->group_top,
-                          rule->renorm != 0, rule->scale};
+                          rule->renorm != 0, rule->scale, (1 << 20) / (E / rule->n_group) + 1};
     return MOE_OK;
 }
 

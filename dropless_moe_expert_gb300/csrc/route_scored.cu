@@ -53,11 +53,6 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL, v, o));
-    return v;
-}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
@@ -72,11 +67,11 @@ __device__ __forceinline__ void scores(float *v, int E, int lane, bool softmax) 
         for (int j = 0; j < EPL; ++j) v[j] = sigmoid(v[j]);
         return;
     }
-    float m = -INFINITY;
+    uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < EPL; ++j)
-        if (lane + 32 * j < E) m = fmaxf(m, v[j]);
-    m = warp_max(m);
+        if (lane + 32 * j < E) top = max(top, order_key(v[j]));
+    const float m = key_value(__reduce_max_sync(FULL, top));
     float t[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) t[j] = v[j] = lane + 32 * j < E ? expf(v[j] - m) : 0.0f;
@@ -102,12 +97,14 @@ __device__ __forceinline__ void open_runs(const uint32_t *keys, uint32_t *score,
     for (int g0 = 0; g0 < G; g0 += at_once) {
         const int g = g0 + lane / share;
         uint32_t a = 0, b = 0;
-        if (g < G)
+        if (g < G) {
+#pragma unroll 4
             for (int i = lane % share; i < per; i += share) {
                 const uint32_t k = keys[g * per + i];
                 b = max(b, min(a, k));
                 a = max(a, k);
             }
+        }
         for (int o = share / 2; o; o >>= 1) {
             const uint32_t c = __shfl_xor_sync(FULL, a, o), d = __shfl_xor_sync(FULL, b, o);
             b = max(max(b, d), min(a, c));
@@ -121,6 +118,7 @@ __device__ __forceinline__ void open_runs(const uint32_t *keys, uint32_t *score,
         const int g = g0 + lane;
         const uint32_t mine = g < G ? score[g] : 0u;
         int above = 0;  // runs that come before this one
+#pragma unroll 4
         for (int o = 0; o < G; ++o) above += score[o] > mine || (score[o] == mine && o < g);
         const uint32_t bits = __ballot_sync(FULL, g < G && above < rule.topk_group);
         if (lane == 0) open[g0 >> 5] = bits;
@@ -169,34 +167,56 @@ route_scored_topk_kernel(const float *__restrict__ L, const float *__restrict__ 
             open_runs(keys, score, open, per, rule, lane);
 #pragma unroll
             for (int j = 0; j < EPL; ++j) {
-                const int g = (lane + 32 * j) / per;
+                const int g = ((lane + 32 * j) * rule.run_of) >> 20;
                 if (lane + 32 * j < E && !((open[g >> 5] >> (g & 31)) & 1u)) key[j] = 0u;
             }
         }
-        uint32_t best = 0;
-        int bj = 0;
-        float bs = 0.0f;
-        auto find = [&]() {  // this lane's largest key, the lowest expert on ties
-            best = key[0], bj = 0, bs = s[0];
+        // this lane's largest key, the lowest expert on ties, kept as the largest of two halves
+        constexpr int HALF = (EPL + 1) / 2;
+        uint32_t lo, hi = 0u;
+        int lo_j, hi_j = HALF;
+        auto find_lo = [&]() {
+            lo = key[0], lo_j = 0;
 #pragma unroll
-            for (int j = 1; j < EPL; ++j)
-                if (key[j] > best) best = key[j], bj = j, bs = s[j];
+            for (int j = 1; j < HALF; ++j)
+                if (key[j] > lo) lo = key[j], lo_j = j;
         };
-        find();
-        float my_s = 0.0f, sum = 0.0f;
-        for (int k = 0; k < K; ++k) {
-            const uint32_t top = __reduce_max_sync(FULL, best);
-            const int e = static_cast<int>(
-                __reduce_min_sync(FULL, best == top ? static_cast<uint32_t>(lane + 32 * bj) : FULL));
-            const float se = __shfl_sync(FULL, bs, e & 31);
-            if ((e & 31) == lane) {
+        auto find_hi = [&]() {
+            if constexpr (EPL > 1) {
+                hi = key[HALF], hi_j = HALF;
 #pragma unroll
-                for (int j = 0; j < EPL; ++j) key[j] = j == bj ? 0u : key[j];
-                find();
+                for (int j = HALF + 1; j < EPL; ++j)
+                    if (key[j] > hi) hi = key[j], hi_j = j;
             }
-            sum += se;
-            if (lane == k) my_e = e, my_s = se;
+        };
+        find_lo();
+        find_hi();
+        for (int k = 0; k < K; ++k) {
+            const uint32_t best = max(lo, hi);
+            const int mine = lane + 32 * (lo >= hi ? lo_j : hi_j);
+            const uint32_t top = __reduce_max_sync(FULL, best);
+            const int e = static_cast<int>(__reduce_min_sync(FULL, best == top ? static_cast<uint32_t>(mine) : FULL));
+            if (lane == k) my_e = e;
+            if (e == mine) {  // taken: the half that held it is searched again
+                const int taken = e >> 5;
+                if (taken < HALF) {
+#pragma unroll
+                    for (int j = 0; j < HALF; ++j) key[j] = j == taken ? 0u : key[j];
+                    find_lo();
+                } else {
+#pragma unroll
+                    for (int j = HALF; j < EPL; ++j) key[j] = j == taken ? 0u : key[j];
+                    find_hi();
+                }
+            }
         }
+        float my_s = 0.0f;  // lane k: the score of the k-th choice
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            const float v = __shfl_sync(FULL, s[j], my_e & 31);
+            my_s = my_e >> 5 == j ? v : my_s;
+        }
+        const float sum = rule.renorm ? warp_sum(lane < K ? my_s : 0.0f) : 0.0f;
         if (lane < K) {
             const size_t p = static_cast<size_t>(t) * K + lane;
             topk_idx[p] = my_e;
@@ -285,11 +305,24 @@ route_scored_dispatch_kernel(const int32_t *__restrict__ topk_idx, const uint8_t
         uint16_t part[2][WARPS][MAX_E];  // the warps' sums: all chunks, those before the span
         int32_t base[BLOCK][MAX_E];      // then the chunks' first rows
     } sh;
-    __shared__ int32_t s_total[MAX_E], s_next[MAX_E];  // totals, then offsets; the experts' next rows
+    __shared__ int32_t s_total[MAX_E], s_next[MAX_E], s_warp[MAX_E / 32];  // totals; the experts' next rows
     grid_dependency_wait();  // launched early: the choices, ranks and counts
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int pitch = count_pitch(E);
     const int c0 = blockIdx.x * per_span, c1 = min(chunks, c0 + per_span);
+    // of the first block of chunks: the counts and this thread's first pair, ahead of the sums
+    uint8_t n[BLOCK];
+    auto load_counts = [&](int b0) {
+#pragma unroll
+        for (int i = 0; i < BLOCK; ++i)
+            n[i] = static_cast<int>(threadIdx.x) < E && b0 + i < c1
+                       ? chunk_counts[static_cast<size_t>(b0 + i) * pitch + threadIdx.x] : 0;
+    };
+    load_counts(c0);
+    const int64_t pairs = min(static_cast<int64_t>(T), static_cast<int64_t>(c1) * CH) * K;  // up to the span's end
+    int64_t p = static_cast<int64_t>(c0) * CH * K + threadIdx.x;
+    int next_e = 0, next_rank = 0;
+    if (p < pairs) next_e = topk_idx[p], next_rank = row_of[p];
     if constexpr (SPANNED) {
         const int e = threadIdx.x;
         if (e < E) {
@@ -348,37 +381,35 @@ route_scored_dispatch_kernel(const int32_t *__restrict__ topk_idx, const uint8_t
         }
     }
     __syncthreads();
-    if (warp == 0) {  // offsets, and the span's first rows
-        int carry = 0;
-        for (int base = 0; base < E; base += 32) {
-            const int e = base + lane;
-            const int c = e < E ? s_total[e] : 0;
-            int incl = c;
+    // offsets, and the span's first rows: the warps scan 32 experts each
+    {
+        const int e = threadIdx.x;
+        int c = 0, incl = 0;
+        if (warp < MAX_E / 32) {
+            incl = c = e < E ? s_total[e] : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(FULL, incl, o);
                 if (lane >= o) incl += v;
             }
-            if (e < E) {
-                s_next[e] += carry + incl - c;
-                if (blockIdx.x == 0) {
-                    counts[e] = c;
-                    offsets[e] = carry + incl - c;
-                }
-            }
-            carry += __shfl_sync(FULL, incl, 31);
+            if (lane == 31) s_warp[warp] = incl;
         }
-        if (blockIdx.x == 0 && lane == 0) offsets[E] = carry;
+        __syncthreads();
+        if (e < E) {
+            int off = incl - c;
+            for (int w = 0; w < warp; ++w) off += s_warp[w];
+            s_next[e] += off;
+            if (blockIdx.x == 0) {
+                counts[e] = c;
+                offsets[e] = off;
+                if (e == E - 1) offsets[E] = off + c;
+            }
+        }
     }
-    __syncthreads();
     for (int b0 = c0; b0 < c1; b0 += BLOCK) {
-        const int nb = min(BLOCK, c1 - b0);
         if (threadIdx.x < E) {
             const int e = threadIdx.x;
             int run = s_next[e];
-            uint8_t n[BLOCK];
-#pragma unroll
-            for (int i = 0; i < BLOCK; ++i) n[i] = i < nb ? chunk_counts[static_cast<size_t>(b0 + i) * pitch + e] : 0;
 #pragma unroll
             for (int i = 0; i < BLOCK; ++i) {
                 sh.base[i][e] = run;
@@ -388,15 +419,19 @@ route_scored_dispatch_kernel(const int32_t *__restrict__ topk_idx, const uint8_t
         }
         __syncthreads();
         const int64_t first = static_cast<int64_t>(b0) * CH * K;
-        const int64_t last = min(static_cast<int64_t>(T), static_cast<int64_t>(b0 + nb) * CH) * K;
-        for (int64_t p = first + threadIdx.x; p < last; p += DISPATCH_THREADS) {
-            const int e = topk_idx[p], rank = row_of[p];
+        const int64_t last = min(pairs, static_cast<int64_t>(min(b0 + BLOCK, c1)) * CH * K);
+        while (p < last) {
             const int i = static_cast<int>(p - first) / (CH * K);
-            const int r = sh.base[i][e] + rank;
+            const int r = sh.base[i][next_e] + next_rank;
             row_of[p] = r;
             src_tok[r] = static_cast<int32_t>(p / K);
+            p += DISPATCH_THREADS;
+            if (p < pairs) next_e = topk_idx[p], next_rank = row_of[p];
         }
-        __syncthreads();
+        if (b0 + BLOCK < c1) {
+            load_counts(b0 + BLOCK);
+            __syncthreads();
+        }
     }
 }
 
