@@ -37,6 +37,10 @@ struct Table {
     int64_t size[GROUP];
     int32_t first[GROUP + 1];  // the tensor's first chunk
     uint8_t bf16[GROUP];
+    // The tensors of each CTA's first and last chunk: looked up in the table,
+    // whose every cold read costs a constant-cache miss, they took two thirds
+    // of a launch over small tensors.
+    uint16_t begin[CTAS], end[CTAS];
     int n;
 };
 
@@ -148,7 +152,7 @@ __global__ void __launch_bounds__(THREADS, 2) grad_squares_kernel(const __grid_c
     __shared__ float red[THREADS / 32];
     float s = 0.0f;
     int64_t at;
-    for (int c = blockIdx.x, i = 0; c < t.first[t.n]; c += gridDim.x) {
+    for (int c = blockIdx.x, i = t.begin[blockIdx.x]; c < t.first[t.n]; c += gridDim.x) {
         if (c >= t.first[i + 1]) i = tensor_of(t, c);
         if (t.bf16[i]) {
             const int n = chunk_of<uint16_t>(t, i, c, &at);
@@ -172,7 +176,18 @@ __global__ void __launch_bounds__(THREADS, 2) grad_squares_kernel(const __grid_c
 // The norm from all partial sums; one warp.
 __device__ __forceinline__ float total_norm(const float *part, int parts) {
     double s = 0.0;
-    for (int i = threadIdx.x & 31; i < parts; i += 32) s += part[i];
+    for (int i = threadIdx.x & 31; i < parts; i += 32 * 10) {
+        float v[10];
+#pragma unroll
+        for (int q = 0; q < 10; ++q) v[q] = i + 32 * q < parts ? part[i + 32 * q] : 0.0f;
+#pragma unroll
+        for (int w = 5; w; w /= 2) {  // 10 -> 5 -> 4 -> 2 -> 1
+#pragma unroll
+            for (int q = 0; q < w; ++q) v[q] += v[q + w];
+            if (w == 5) v[0] += v[4];
+        }
+        s += v[0];
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
     return sqrtf(static_cast<float>(s));
@@ -191,7 +206,7 @@ grad_scale_kernel(const __grid_constant__ Table t, const float *__restrict__ par
     __shared__ float factor;
     const int chunks = t.first[t.n], begin = blockIdx.x, step = gridDim.x;
     const int last = begin < chunks ? begin + (chunks - 1 - begin) / step * step : -1;
-    int i = last >= 0 ? tensor_of(t, last) : 0;
+    int i = t.end[blockIdx.x];
     grid_dependency_wait();  // launched early: the partial sums
     if (threadIdx.x < 32) {
         const float norm = total_norm(part, parts);
@@ -241,7 +256,18 @@ cudaError_t launch_grad_clip(const void *const *grads, void *const *outs, const 
             t.bf16[i] = bf16;
             t.first[i + 1] = t.first[i] + static_cast<int32_t>((sizes[first + i] + chunk - 1) / chunk);
         }
-        return std::max(1, std::min(gc::CTAS, t.first[t.n]));
+        const int chunks = t.first[t.n], ctas = std::max(1, std::min(gc::CTAS, chunks));
+        for (int b = 0, i = 0; b < ctas; ++b) {
+            while (i + 1 < t.n && b >= t.first[i + 1]) ++i;
+            t.begin[b] = static_cast<uint16_t>(i);
+        }
+        // the last chunks of the CTAs are the last `ctas` chunks
+        for (int q = 0, i = t.n - 1; q < ctas; ++q) {
+            const int c = chunks - 1 - q;
+            while (i > 0 && c < t.first[i]) --i;
+            t.end[c >= 0 ? c % ctas : 0] = static_cast<uint16_t>(std::max(i, 0));
+        }
+        return ctas;
     };
     *launches = 0;
     int parts = 0, ctas = 0;

@@ -30,6 +30,7 @@ namespace rs {
 constexpr int MAX_E = 256;
 constexpr int CH = 16;             // tokens per chunk: a CTA of the top-K kernel, a warp per token
 constexpr int FEW = 32;            // tokens that one CTA routes alone
+constexpr int OPEN = MAX_E / 16;   // words of a token's open runs
 constexpr int SPANS = 152;         // CTAs of the dispatch kernel, each a run of chunks
 constexpr int DISPATCH_THREADS = 1024;
 constexpr size_t SELF_SUM_BYTES = 256 * 1024;  // of counts that every dispatch CTA adds up itself
@@ -42,10 +43,8 @@ int span_chunks(int chunks) { return (chunks + SPANS - 1) / SPANS; }
 
 // Keys that order as the values do, -0.0 as +0.0; 0 is kept for "not there".
 __device__ __forceinline__ uint32_t order_key(float v) {
-    if (v == 0.0f) v = 0.0f;
-    const uint32_t u = __float_as_uint(v);
-    const uint32_t k = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return k ? k : 1u;
+    const uint32_t u = __float_as_uint(v + 0.0f);  // -0.0 becomes +0.0
+    return max(u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u), 1u);
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
@@ -53,14 +52,36 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Over the LANES lanes (32, or a half of the warp) that hold a token.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+    for (int o = LANES / 2; o; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
     return v;
 }
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+    if constexpr (LANES == 32) {
+        return __reduce_max_sync(FULL, v);
+    } else {
+#pragma unroll
+        for (int o = LANES / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(FULL, v, o));
+        return v;
+    }
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_min(uint32_t v) {
+    if constexpr (LANES == 32) {
+        return __reduce_min_sync(FULL, v);
+    } else {
+#pragma unroll
+        for (int o = LANES / 2; o; o >>= 1) v = min(v, __shfl_xor_sync(FULL, v, o));
+        return v;
+    }
+}
 
-// Scores of one token: lane holds experts lane + 32 j in v (logits in, scores out).
-template <int EPL>
+// Scores of one token: lane holds experts lane + LANES j in v (logits in, scores out).
+template <int LANES, int EPL>
 __device__ __forceinline__ void scores(float *v, int E, int lane, bool softmax) {
     if (!softmax) {
 #pragma unroll
@@ -70,30 +91,31 @@ __device__ __forceinline__ void scores(float *v, int E, int lane, bool softmax) 
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < EPL; ++j)
-        if (lane + 32 * j < E) top = max(top, order_key(v[j]));
-    const float m = key_value(__reduce_max_sync(FULL, top));
+        if (lane + LANES * j < E) top = max(top, order_key(v[j]));
+    const float m = key_value(lanes_max<LANES>(top));
     float t[EPL];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) t[j] = v[j] = lane + 32 * j < E ? expf(v[j] - m) : 0.0f;
+    for (int j = 0; j < EPL; ++j) t[j] = v[j] = lane + LANES * j < E ? expf(v[j] - m) : 0.0f;
 #pragma unroll
     for (int h = EPL / 2; h; h >>= 1) {
 #pragma unroll
         for (int j = 0; j < h; ++j) t[j] += t[j + h];
     }
-    const float sum = warp_sum(t[0]);
+    const float sum = lanes_sum<LANES>(t[0]);
 #pragma unroll
     for (int j = 0; j < EPL; ++j) v[j] = v[j] / sum;
 }
 
-// The runs that stay open, as a bit mask per 32 runs (`open`, filled by the
-// warp).  `keys`: the experts' keys in shared memory; `score`: room for a key
+// The runs that stay open, as a bit mask per LANES runs: `open`, filled by the
+// token's lanes, and the first mask returned to all of them.  `keys`: the experts' keys in shared memory; `score`: room for a key
 // per run.  Lanes share a run's experts; each keeps its two largest.
-__device__ __forceinline__ void open_runs(const uint32_t *keys, uint32_t *score, uint32_t *open, int per,
+template <int LANES>
+__device__ __forceinline__ uint32_t open_runs(const uint32_t *keys, uint32_t *score, uint32_t *open, int per,
                                           const RouteRule &rule, int lane) {
     const int G = rule.n_group;
     int share = 1;  // lanes per run: the largest power of two that leaves every run its own
-    while (2 * share * G <= 32 && share < per) share *= 2;
-    const int at_once = 32 / share;
+    while (2 * share * G <= LANES && share < per) share *= 2;
+    const int at_once = LANES / share;
     for (int g0 = 0; g0 < G; g0 += at_once) {
         const int g = g0 + lane / share;
         uint32_t a = 0, b = 0;
@@ -114,61 +136,69 @@ __device__ __forceinline__ void open_runs(const uint32_t *keys, uint32_t *score,
             score[g] = rule.group_top == 2 && b ? order_key(key_value(a) + key_value(b)) : a;
     }
     __syncwarp();
-    for (int g0 = 0; g0 < G; g0 += 32) {
+    uint32_t first = 0;
+    for (int g0 = 0; g0 < G; g0 += LANES) {
         const int g = g0 + lane;
         const uint32_t mine = g < G ? score[g] : 0u;
         int above = 0;  // runs that come before this one
 #pragma unroll 4
         for (int o = 0; o < G; ++o) above += score[o] > mine || (score[o] == mine && o < g);
-        const uint32_t bits = __ballot_sync(FULL, g < G && above < rule.topk_group);
-        if (lane == 0) open[g0 >> 5] = bits;
+        uint32_t bits = __ballot_sync(FULL, g < G && above < rule.topk_group);
+        if (LANES < 32) bits = bits >> (threadIdx.x & 16) & 0xffffu;
+        if (g0 == 0) first = bits;
+        if (lane == 0) open[g0 / LANES] = bits;
     }
     __syncwarp();
+    return first;
 }
 
-// A warp per token, TOK tokens per CTA.  FINAL: the CTA holds every token and
-// writes the dispatch order too; else it writes its chunk's counts and each
+// LANES lanes per token, TOK tokens per CTA.  FINAL: the CTA holds every token
+// and writes the dispatch order too; else it writes its chunk's counts and each
 // pair's rank inside the chunk (in row_of) for the dispatch kernel.
-template <int EPL, int TOK, bool FINAL>
-__global__ void __launch_bounds__(TOK * 32)
+// The instructions of a token bound it: half a warp per token up to 64 experts
+// (32768 tokens, 64 experts: 19.5 us for the whole routing, 20.9 with a warp;
+// 128 experts the other way round, 17.7 and 18.8 for 16384 tokens).
+template <int LANES, int EPL, int TOK, bool FINAL>
+__global__ void __launch_bounds__(TOK *LANES)
 route_scored_topk_kernel(const float *__restrict__ L, const float *__restrict__ bias, int T, int E, int K,
                          RouteRule rule, int32_t *__restrict__ topk_idx, float *__restrict__ topk_w,
                          int32_t *__restrict__ row_of, uint8_t *__restrict__ chunk_counts,
                          int32_t *__restrict__ counts, int32_t *__restrict__ offsets, int32_t *__restrict__ src_tok) {
+    constexpr int THREADS = TOK * LANES;
     __shared__ uint32_t chose[MAX_E];  // bit i: token i of the CTA chose the expert
     __shared__ int32_t s_off[MAX_E];
-    extern __shared__ uint32_t s_groups[];  // with groups: keys [TOK][E], scores [TOK][n_group], open [TOK][8]
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = blockIdx.x * TOK + warp;
-    for (int e = threadIdx.x; e < MAX_E; e += TOK * 32) chose[e] = 0u;
-    __syncthreads();
+    extern __shared__ uint32_t s_groups[];  // with groups: keys [TOK][E], scores [TOK][n_group], open [TOK][OPEN]
+    const int tok = threadIdx.x / LANES, lane = threadIdx.x % LANES;
+    const int t = blockIdx.x * TOK + tok;
+    for (int e = threadIdx.x; e < E; e += THREADS) chose[e] = 0u;
     int my_e = 0;
-    if (t < T) {
-        const float *row = L + static_cast<size_t>(t) * E;
+    float w = 0.0f;  // lane k: the k-th choice and its weight
+    if (t - (LANES < 32 ? tok & 1 : 0) < T) {  // the whole warp; a second token beyond the last is routed as the last
+        const float *row = L + static_cast<size_t>(min(t, T - 1)) * E;
         float s[EPL];
         uint32_t key[EPL];
 #pragma unroll
-        for (int j = 0; j < EPL; ++j) s[j] = lane + 32 * j < E ? row[lane + 32 * j] : 0.0f;
-        scores<EPL>(s, E, lane, rule.softmax);
+        for (int j = 0; j < EPL; ++j) s[j] = lane + LANES * j < E ? row[lane + LANES * j] : 0.0f;
+        scores<LANES, EPL>(s, E, lane, rule.softmax);
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            const int e = lane + 32 * j;
+            const int e = lane + LANES * j;
             key[j] = e < E ? order_key(bias ? s[j] + bias[e] : s[j]) : 0u;
         }
         if (rule.topk_group < rule.n_group) {
-            uint32_t *keys = s_groups + warp * E;
-            uint32_t *score = s_groups + TOK * E + warp * rule.n_group;
-            uint32_t *open = s_groups + TOK * (E + rule.n_group) + warp * (MAX_E / 32);
-            const int per = E / rule.n_group;
+            uint32_t *keys = s_groups + tok * E;
+            uint32_t *score = s_groups + TOK * E + tok * rule.n_group;
+            uint32_t *open = s_groups + TOK * (E + rule.n_group) + tok * OPEN;
 #pragma unroll
             for (int j = 0; j < EPL; ++j)
-                if (lane + 32 * j < E) keys[lane + 32 * j] = key[j];
+                if (lane + LANES * j < E) keys[lane + LANES * j] = key[j];
             __syncwarp();
-            open_runs(keys, score, open, per, rule, lane);
+            const uint32_t first = open_runs<LANES>(keys, score, open, E / rule.n_group, rule, lane);
 #pragma unroll
             for (int j = 0; j < EPL; ++j) {
-                const int g = ((lane + 32 * j) * rule.run_of) >> 20;
-                if (lane + 32 * j < E && !((open[g >> 5] >> (g & 31)) & 1u)) key[j] = 0u;
+                const int g = ((lane + LANES * j) * rule.run_of) >> 20;
+                const uint32_t bits = rule.n_group <= LANES ? first : lane + LANES * j < E ? open[g / LANES] : 0u;
+                if (!((bits >> (g % LANES)) & 1u)) key[j] = 0u;
             }
         }
         // this lane's largest key, the lowest expert on ties, kept as the largest of two halves
@@ -193,12 +223,12 @@ route_scored_topk_kernel(const float *__restrict__ L, const float *__restrict__ 
         find_hi();
         for (int k = 0; k < K; ++k) {
             const uint32_t best = max(lo, hi);
-            const int mine = lane + 32 * (lo >= hi ? lo_j : hi_j);
-            const uint32_t top = __reduce_max_sync(FULL, best);
-            const int e = static_cast<int>(__reduce_min_sync(FULL, best == top ? static_cast<uint32_t>(mine) : FULL));
+            const int mine = lane + LANES * (lo >= hi ? lo_j : hi_j);
+            const uint32_t top = lanes_max<LANES>(best);
+            const int e = static_cast<int>(lanes_min<LANES>(best == top ? static_cast<uint32_t>(mine) : FULL));
             if (lane == k) my_e = e;
             if (e == mine) {  // taken: the half that held it is searched again
-                const int taken = e >> 5;
+                const int taken = e / LANES;
                 if (taken < HALF) {
 #pragma unroll
                     for (int j = 0; j < HALF; ++j) key[j] = j == taken ? 0u : key[j];
@@ -209,33 +239,37 @@ route_scored_topk_kernel(const float *__restrict__ L, const float *__restrict__ 
                     find_hi();
                 }
             }
+            if (LANES < 32) __syncwarp();  // the halves of a warp take different experts
         }
-        float my_s = 0.0f;  // lane k: the score of the k-th choice
+        float my_s = 0.0f;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
-            const float v = __shfl_sync(FULL, s[j], my_e & 31);
-            my_s = my_e >> 5 == j ? v : my_s;
+            const float v = __shfl_sync(FULL, s[j], my_e % LANES, LANES);
+            my_s = my_e / LANES == j ? v : my_s;
         }
-        const float sum = rule.renorm ? warp_sum(lane < K ? my_s : 0.0f) : 0.0f;
-        if (lane < K) {
-            const size_t p = static_cast<size_t>(t) * K + lane;
-            topk_idx[p] = my_e;
-            topk_w[p] = rule.renorm ? rule.scale * my_s / (sum + kRouteEps) : rule.scale * my_s;
-            atomicOr(&chose[my_e], 1u << warp);  // the final mask does not depend on the order
-        }
+        w = rule.scale * my_s;
+        if (rule.renorm) w /= lanes_sum<LANES>(lane < K ? my_s : 0.0f) + kRouteEps;
+    }
+    const bool write = t < T && lane < K;
+    __syncthreads();  // `chose` is zero
+    if (write) {
+        const size_t p = static_cast<size_t>(t) * K + lane;
+        topk_idx[p] = my_e;
+        topk_w[p] = w;
+        atomicOr(&chose[my_e], 1u << tok);  // the final mask does not depend on the order
     }
     __syncthreads();
     if constexpr (FINAL) {
-        if (warp == 0) {
+        if (threadIdx.x < 32) {
             int carry = 0;
             for (int base = 0; base < E; base += 32) {
-                const int e = base + lane;
+                const int e = base + static_cast<int>(threadIdx.x);
                 const int c = e < E ? __popc(chose[e]) : 0;
                 int incl = c;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int v = __shfl_up_sync(FULL, incl, o);
-                    if (lane >= o) incl += v;
+                    if (static_cast<int>(threadIdx.x) >= o) incl += v;
                 }
                 if (e < E) {
                     s_off[e] = offsets[e] = carry + incl - c;
@@ -243,16 +277,16 @@ route_scored_topk_kernel(const float *__restrict__ L, const float *__restrict__ 
                 }
                 carry += __shfl_sync(FULL, incl, 31);
             }
-            if (lane == 0) offsets[E] = carry;
+            if (threadIdx.x == 0) offsets[E] = carry;
         }
         __syncthreads();
     } else {
         uint8_t *mine = chunk_counts + static_cast<size_t>(blockIdx.x) * count_pitch(E);
-        for (int e = threadIdx.x; e < count_pitch(E); e += TOK * 32)
+        for (int e = threadIdx.x; e < count_pitch(E); e += THREADS)
             mine[e] = static_cast<uint8_t>(e < E ? __popc(chose[e]) : 0);
     }
-    if (t < T && lane < K) {
-        int r = __popc(chose[my_e] & ((1u << warp) - 1u));
+    if (write) {
+        int r = __popc(chose[my_e] & ((1u << tok) - 1u));
         if constexpr (FINAL) {
             r += s_off[my_e];
             src_tok[r] = t;
@@ -456,42 +490,35 @@ route_scored_bwd_kernel(const float *__restrict__ L, const int32_t *__restrict__
         if (rule.softmax) {
 #pragma unroll
             for (int j = 0; j < EPL; ++j) s[j] = lane + 32 * j < E ? row[lane + 32 * j] : 0.0f;
-            scores<EPL>(s, E, lane, true);
+            scores<32, EPL>(s, E, lane, true);
 #pragma unroll
             for (int j = 0; j < EPL; ++j) {
                 const float v = __shfl_sync(FULL, s[j], e & 31);
-                if (e >= 0 && (e >> 5) == j) se = v;
+                if ((e >> 5) == j) se = v;  // -1 >> 5 is no j
             }
         } else if (e >= 0) {
             se = sigmoid(row[e]);
         }
         float ds = e >= 0 ? rule.scale * g : 0.0f;
         if (rule.renorm) {
-            const float inv = 1.0f / (warp_sum(se) + kRouteEps);
-            const float mean = warp_sum(e >= 0 ? g * (se * inv) : 0.0f);
+            const float inv = 1.0f / (lanes_sum<32>(se) + kRouteEps);
+            const float mean = lanes_sum<32>(e >= 0 ? g * (se * inv) : 0.0f);
             ds = e >= 0 ? rule.scale * (g - mean) * inv : 0.0f;
         }
-        // what this lane's choice adds to its expert's entry
-        const float mine = rule.softmax ? ds : e >= 0 ? ds * se / (1.0f + expf(row[e])) : 0.0f;
-        float o[EPL];
-#pragma unroll
-        for (int j = 0; j < EPL; ++j) o[j] = 0.0f;
-        for (int k = 0; k < K; ++k) {
-            const int ek = __shfl_sync(FULL, e, k);
-            const float v = __shfl_sync(FULL, mine, k);
-#pragma unroll
-            for (int j = 0; j < EPL; ++j)
-                if (ek == lane + 32 * j) o[j] = v;
-        }
+        // every expert's entry as if it were not chosen, then the chosen ones over them
+        float mean = 0.0f, mine;
         if (rule.softmax) {
-            const float mean = warp_sum(se * ds);
-#pragma unroll
-            for (int j = 0; j < EPL; ++j) o[j] = s[j] * (o[j] - mean);
+            mean = lanes_sum<32>(se * ds);
+            mine = se * (ds - mean);
+        } else {
+            mine = e >= 0 ? ds * se / (1.0f + expf(row[e])) : 0.0f;
         }
         float *out = dL + static_cast<size_t>(t) * E;
 #pragma unroll
         for (int j = 0; j < EPL; ++j)
-            if (lane + 32 * j < E) out[lane + 32 * j] = o[j];
+            if (lane + 32 * j < E) out[lane + 32 * j] = rule.softmax ? s[j] * -mean : 0.0f;
+        __syncwarp();  // orders the warp's stores
+        if (e >= 0) out[e] = mine;
     }
 }
 
@@ -536,26 +563,30 @@ cudaError_t launch_route_scored(const float *logits, const float *sel_bias, int 
     const bool few = T <= rs::FEW;
     const int tok = few ? rs::FEW : rs::CH;
     const size_t smem =
-        rule.topk_group < rule.n_group ? static_cast<size_t>(tok) * (E + rule.n_group + rs::MAX_E / 32) * 4 : 0;
-    auto topk = [&](auto kernel) {
-        static_assert(rs::FEW * (2 * rs::MAX_E + rs::MAX_E / 32) * 4 < 227 * 1024, "keys and scores fit a CTA");
+        rule.topk_group < rule.n_group ? static_cast<size_t>(tok) * (E + rule.n_group + rs::OPEN) * 4 : 0;
+    auto topk = [&](auto kernel, int lanes) {
+        static_assert(rs::FEW * (2 * rs::MAX_E + rs::OPEN) * 4 < 227 * 1024, "keys and scores fit a CTA");
         if (smem > 40 * 1024) {
             const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
             if (e != cudaSuccess) return e;
         }
-        kernel<<<few ? 1 : chunks, tok * 32, smem, stream>>>(logits, sel_bias, T, E, K, rule, topk_idx, topk_w, row_of,
+        kernel<<<few ? 1 : chunks, tok * lanes, smem, stream>>>(logits, sel_bias, T, E, K, rule, topk_idx, topk_w, row_of,
                                                              workspace, counts, offsets, src_tok);
         return cudaGetLastError();
     };
-    auto by_experts = [&](auto lanes) {
-        constexpr int EPL = decltype(lanes)::value;
-        return few ? topk(rs::route_scored_topk_kernel<EPL, rs::FEW, true>)
-                   : topk(rs::route_scored_topk_kernel<EPL, rs::CH, false>);
+    auto by_experts = [&](auto lanes, auto each) {
+        constexpr int LANES = decltype(lanes)::value, EPL = decltype(each)::value;
+        return few ? topk(rs::route_scored_topk_kernel<LANES, EPL, rs::FEW, true>, LANES)
+                   : topk(rs::route_scored_topk_kernel<LANES, EPL, rs::CH, false>, LANES);
     };
-    cudaError_t err = E <= 32    ? by_experts(std::integral_constant<int, 1>{})
-                      : E <= 64  ? by_experts(std::integral_constant<int, 2>{})
-                      : E <= 128 ? by_experts(std::integral_constant<int, 4>{})
-                                 : by_experts(std::integral_constant<int, 8>{});
+    using std::integral_constant;
+    const integral_constant<int, 16> half;
+    const integral_constant<int, 32> whole;
+    cudaError_t err = E <= 16    ? by_experts(half, integral_constant<int, 1>{})
+                      : E <= 32  ? by_experts(half, integral_constant<int, 2>{})
+                      : E <= 64  ? by_experts(half, integral_constant<int, 4>{})
+                      : E <= 128 ? by_experts(whole, integral_constant<int, 4>{})
+                                 : by_experts(whole, integral_constant<int, 8>{});
     *launches = 1;
     if (err != cudaSuccess || few) return err;
     const int per_span = rs::span_chunks(chunks), spans = (chunks + per_span - 1) / per_span;
