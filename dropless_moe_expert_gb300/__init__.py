@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, field
 
 import torch
 
@@ -176,6 +176,13 @@ def _need(t, dtype, shape, name):
     return t
 
 
+def _in(t, dtype, shape, name) -> int:
+    """The address of a tensor that _need() accepts, in one step."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _need(t, dtype, shape, name).data_ptr()
+
+
 def _empty(shape, dtype, like):
     return torch.empty(shape, dtype=dtype, device=like.device)
 
@@ -284,14 +291,13 @@ def route_scored(logits, K: int, rule: RouteRule, sel_bias=None, buffers: RouteB
     is added to the scores for the choice only.  Ties go to the lower expert.
     ``buffers`` holds the outputs (then reused) and the workspace."""
     T, E = logits.shape
-    _need(logits, torch.float32, (T, E), "logits")
-    if sel_bias is not None:
-        _need(sel_bias, torch.float32, (E,), "sel_bias")
+    lp = _in(logits, torch.float32, (T, E), "logits")
+    bp = None if sel_bias is None else _in(sel_bias, torch.float32, (E,), "sel_bias")
     if buffers is None:
         buffers = RouteBuffers(T, E, K, logits.device)
     elif buffers.size != (T, E, K):
         raise ValueError(f"buffers are for (T, E, K) = {buffers.size}, not {(T, E, K)}")
-    _check(lib.moe_route_scored(_ptr(logits), _ptr(sel_bias), T, E, K, rule._c, *buffers._args, _stream_of(logits, stream)),
+    _check(lib.moe_route_scored(lp, bp, T, E, K, rule._c, *buffers._args, _stream_of(logits, stream)),
            "moe_route_scored")
     return buffers.routing
 
@@ -300,11 +306,11 @@ def route_scored_backward(logits, topk_idx, dw, rule: RouteRule, out=None, strea
     """dlogits [T, E] fp32 of sum(dw * topk_w) for the forward's choice."""
     T, E = logits.shape
     K = topk_idx.shape[1]
-    _need(logits, torch.float32, (T, E), "logits")
-    _need(topk_idx, torch.int32, (T, K), "topk_idx")
-    _need(dw, torch.float32, (T, K), "dw")
-    out = _empty((T, E), torch.float32, logits) if out is None else _need(out, torch.float32, (T, E), "dlogits")
-    _check(lib.moe_route_scored_backward(_ptr(logits), _ptr(topk_idx), _ptr(dw), T, E, K, rule._c, _ptr(out),
+    args = (_in(logits, torch.float32, (T, E), "logits"), _in(topk_idx, torch.int32, (T, K), "topk_idx"),
+            _in(dw, torch.float32, (T, K), "dw"))
+    if out is None:
+        out = _empty((T, E), torch.float32, logits)
+    _check(lib.moe_route_scored_backward(*args, T, E, K, rule._c, _in(out, torch.float32, (T, E), "dlogits"),
                                          _stream_of(logits, stream)), "moe_route_scored_backward")
     return out
 
@@ -316,6 +322,7 @@ class NormResidual:
     n: torch.Tensor | None = None        # [T, d] bf16, what the next layer reads
     rstd_post: torch.Tensor | None = None   # [T] fp32
     rstd_pre: torch.Tensor | None = None    # [T] fp32
+    _made: tuple | None = field(default=None, repr=False, compare=False)  # by empty(): its arguments and tensors
 
     @classmethod
     def empty(cls, T: int, d: int, dtype=torch.bfloat16, y=True, post=True, pre=True, device="cuda"):
@@ -324,8 +331,25 @@ class NormResidual:
         def make(on, dt, *shape):
             return torch.empty(shape, dtype=dt, device=device) if on else None
 
-        return cls(make(y, dtype, T, d), make(pre, torch.bfloat16, T, d), make(post, torch.float32, T),
-                   make(pre, torch.float32, T))
+        out = cls(make(y, dtype, T, d), make(pre, torch.bfloat16, T, d), make(post, torch.float32, T),
+                  make(pre, torch.float32, T))
+        out._made = ((T, d, dtype, y, post, pre), out.r, out.n, out.rstd_post, out.rstd_pre)
+        return out
+
+    def _pointers(self, key):
+        """Addresses of the buffers; those that empty() made for the same arguments need no check."""
+        m = self._made
+        if m is None or m[0] != key or m[1] is not self.r or m[2] is not self.n or m[3] is not self.rstd_post \
+                or m[4] is not self.rstd_pre:
+            T, d, dtype, y, post, pre = key
+            if y:
+                _need(self.r, dtype, (T, d), "out.r")
+            if pre:
+                _need(self.n, torch.bfloat16, (T, d), "out.n")
+                _need(self.rstd_pre, torch.float32, (T,), "out.rstd_pre")
+            if post:
+                _need(self.rstd_post, torch.float32, (T,), "out.rstd_post")
+        return (_ptr(self.r) if key[3] else None, _ptr(self.n), _ptr(self.rstd_post), _ptr(self.rstd_pre))
 
 
 @dataclass
@@ -336,6 +360,7 @@ class NormResidualGrads:
     dgamma_post: torch.Tensor | None = None
     dgate: torch.Tensor | None = None       # shaped like the gate
     workspace: torch.Tensor | None = None
+    _made: tuple | None = field(default=None, repr=False, compare=False)  # by empty(): its arguments and tensors
 
     @classmethod
     def empty(cls, T: int, d: int, dtype=torch.bfloat16, y=True, post=True, pre=True, gate="none", device="cuda"):
@@ -346,30 +371,51 @@ class NormResidualGrads:
         f32, n = torch.float32, int(lib.moe_norm_residual_backward_workspace_size(T, d))
         if n == 0:
             raise MoEError(2, "moe_norm_residual_backward_workspace_size")
-        return cls(make(True, dtype, T, d), make(y, torch.bfloat16, T, d), make(pre, f32, d), make(post, f32, d),
-                   make(gate != "none", f32, *((d,) if gate == "channel" else (T, 1))), make(True, torch.uint8, n))
+        out = cls(make(True, dtype, T, d), make(y, torch.bfloat16, T, d), make(pre, f32, d), make(post, f32, d),
+                  make(gate != "none", f32, *((d,) if gate == "channel" else (T, 1))), make(True, torch.uint8, n))
+        out._made = ((T, d, dtype, y, post, pre, gate), out.dr, out.dy, out.dgamma_pre, out.dgamma_post, out.dgate,
+                     out.workspace)
+        return out
+
+    def _pointers(self, key):
+        m = self._made
+        if m is None or m[0] != key or m[1] is not self.dr or m[2] is not self.dy or m[3] is not self.dgamma_pre \
+                or m[4] is not self.dgamma_post or m[5] is not self.dgate or m[6] is not self.workspace:
+            T, d, dtype, y, post, pre, gate = key
+            _need(self.dr, dtype, (T, d), "out.dr")
+            if y:
+                _need(self.dy, torch.bfloat16, (T, d), "out.dy")
+            if pre:
+                _need(self.dgamma_pre, torch.float32, (d,), "out.dgamma_pre")
+            if post:
+                _need(self.dgamma_post, torch.float32, (d,), "out.dgamma_post")
+            if gate != "none":
+                _need(self.dgate, torch.float32, (d,) if gate == "channel" else (T, 1), "out.dgate")
+            if self.workspace is None:
+                n = int(lib.moe_norm_residual_backward_workspace_size(T, d))
+                self.workspace = _empty((n,), torch.uint8, self.dr)
+        ws = self.workspace
+        return (_ptr(self.dr), _ptr(self.dy), _ptr(self.dgamma_pre), _ptr(self.dgamma_post), _ptr(self.dgate),
+                ws.data_ptr(), ws.numel())
 
 
 _GATES = ("none", "channel", "token")
 
 
 def _norm_args(r, y, gamma_post, gate, gamma_pre):
-    """T, d, whether the residual is fp32, the kind of gate; checked."""
+    """T, d, the kind of gate, and the addresses of r, y, gamma_post, gate and gamma_pre; checked."""
     T, d = r.shape
-    if r.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"the residual stream must be bfloat16 or float32, got {r.dtype}")
-    _need(r, r.dtype, (T, d), "r")
-    if y is not None:
-        _need(y, torch.bfloat16, (T, d), "y")
-    if gamma_post is not None:
-        _need(gamma_post, torch.float32, (d,), "gamma_post")
-    if gamma_pre is not None:
-        _need(gamma_pre, torch.float32, (d,), "gamma_pre")
-    kind = 0
+    dtype = r.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError(f"the residual stream must be bfloat16 or float32, got {dtype}")
+    f32, cols = torch.float32, (d,)
+    kind, gp = 0, None
     if gate is not None:
         kind = 1 if gate.dim() == 1 else 2
-        _need(gate, torch.float32, (d,) if kind == 1 else (T, 1), "gate")
-    return T, d, int(r.dtype == torch.float32), kind
+        gp = _in(gate, f32, cols if kind == 1 else (T, 1), "gate")
+    return (T, d, kind, _in(r, dtype, (T, d), "r"), None if y is None else _in(y, torch.bfloat16, (T, d), "y"),
+            None if gamma_post is None else _in(gamma_post, f32, cols, "gamma_post"), gp,
+            None if gamma_pre is None else _in(gamma_pre, f32, cols, "gamma_pre"))
 
 
 def norm_residual(r, y=None, *, gamma_post=None, gate=None, gamma_pre=None, res_scale: float = 1.0,
@@ -380,22 +426,12 @@ def norm_residual(r, y=None, *, gamma_post=None, gate=None, gamma_pre=None, res_
     gammas [d] fp32, gate fp32 [d] (per channel) or [T, 1] (per token).
     Without y: n = norm(r) * gamma_pre, and the result's r is r itself.
     ``out.r`` may be r (updated in place)."""
-    T, d, f32, kind = _norm_args(r, y, gamma_post, gate, gamma_pre)
-    post, pre = gamma_post is not None, gamma_pre is not None
+    T, d, kind, rp, yp, postp, gatep, prep = _norm_args(r, y, gamma_post, gate, gamma_pre)
+    key = (T, d, r.dtype, yp is not None, postp is not None, prep is not None)
     if out is None:
-        out = NormResidual.empty(T, d, r.dtype, y is not None, post, pre, r.device)
-    else:
-        if y is not None:
-            _need(out.r, r.dtype, (T, d), "out.r")
-        if pre:
-            _need(out.n, torch.bfloat16, (T, d), "out.n")
-            _need(out.rstd_pre, torch.float32, (T,), "out.rstd_pre")
-        if post:
-            _need(out.rstd_post, torch.float32, (T,), "out.rstd_post")
-    _check(lib.moe_norm_residual(_ptr(r), f32, _ptr(y), _ptr(gamma_post), _ptr(gate), kind, res_scale,
-                                 _ptr(gamma_pre), eps, T, d, _ptr(out.r) if y is not None else None, _ptr(out.n),
-                                 _ptr(out.rstd_post), _ptr(out.rstd_pre), _stream_of(r, stream)),
-           "moe_norm_residual")
+        out = NormResidual.empty(*key, r.device)
+    _check(lib.moe_norm_residual(rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep, eps, T, d,
+                                 *out._pointers(key), _stream_of(r, stream)), "moe_norm_residual")
     if y is None:
         out.r = r
     return out
@@ -407,34 +443,17 @@ def norm_residual_backward(r, dr, dn=None, y=None, *, gamma_post=None, gate=None
     """Gradients of norm_residual for ``dr`` (of its output stream, the
     residual's type; None: zero, with gamma_pre) and ``dn`` (with gamma_pre),
     from its output stream ``r`` as stored, y and the factors it returned."""
-    T, d, f32, kind = _norm_args(r, y, gamma_post, gate, gamma_pre)
-    post, pre = gamma_post is not None, gamma_pre is not None
-    if dr is not None:
-        _need(dr, r.dtype, (T, d), "dr")
-    if pre:
-        _need(dn, torch.bfloat16, (T, d), "dn")
-        _need(rstd_pre, torch.float32, (T,), "rstd_pre")
-    if post:
-        _need(rstd_post, torch.float32, (T,), "rstd_post")
+    T, d, kind, rp, yp, postp, gatep, prep = _norm_args(r, y, gamma_post, gate, gamma_pre)
+    drp = None if dr is None else _in(dr, r.dtype, (T, d), "dr")
+    dnp = _in(dn, torch.bfloat16, (T, d), "dn") if prep is not None else None
+    rqp = _in(rstd_pre, torch.float32, (T,), "rstd_pre") if prep is not None else None
+    rpp = _in(rstd_post, torch.float32, (T,), "rstd_post") if postp is not None else None
+    key = (T, d, r.dtype, yp is not None, postp is not None, prep is not None, _GATES[kind])
     if out is None:
-        out = NormResidualGrads.empty(T, d, r.dtype, y is not None, post, pre, _GATES[kind], r.device)
-    else:
-        _need(out.dr, r.dtype, (T, d), "out.dr")
-        if y is not None:
-            _need(out.dy, torch.bfloat16, (T, d), "out.dy")
-        if pre:
-            _need(out.dgamma_pre, torch.float32, (d,), "out.dgamma_pre")
-        if post:
-            _need(out.dgamma_post, torch.float32, (d,), "out.dgamma_post")
-        if kind:
-            _need(out.dgate, torch.float32, gate.shape, "out.dgate")
-        if out.workspace is None:
-            out.workspace = _empty((int(lib.moe_norm_residual_backward_workspace_size(T, d)),), torch.uint8, r)
+        out = NormResidualGrads.empty(*key, r.device)
     _check(lib.moe_norm_residual_backward(
-        _ptr(r), f32, _ptr(y), _ptr(gamma_post), _ptr(gate), kind, res_scale, _ptr(gamma_pre), _ptr(rstd_post),
-        _ptr(rstd_pre), _ptr(dr), _ptr(dn), T, d, _ptr(out.dr), _ptr(out.dy), _ptr(out.dgamma_pre),
-        _ptr(out.dgamma_post), _ptr(out.dgate), _ptr(out.workspace), out.workspace.numel(), _stream_of(r, stream)),
-        "moe_norm_residual_backward")
+        rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep, rpp, rqp, drp, dnp, T, d,
+        *out._pointers(key), _stream_of(r, stream)), "moe_norm_residual_backward")
     return out
 
 

@@ -109,7 +109,7 @@ def test_forward_and_backward(c):
     _check_backward(got, out.r, y, dr, dn, args)
     again = moe.norm_residual_backward(out.r, dr, dn, y, **args)
     for k, v in vars(got).items():
-        if v is not None and k != "workspace":
+        if v is not None and k != "workspace" and not k.startswith("_"):
             assert torch.equal(v, vars(again)[k]), k      # a fixed order of addition
 
 
