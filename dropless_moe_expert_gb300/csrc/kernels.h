@@ -104,6 +104,8 @@ struct NormResidualArgs {
     float res_scale, eps;
     int T, d;
     bool res_f32;
+    int *status;  // of the bounded waits
+    uint64_t wait_ns;
 };
 cudaError_t launch_norm_residual(const NormResidualArgs &a, const void *r, void *r_out, uint16_t *n, float *rstd_post,
                                  float *rstd_pre, cudaStream_t stream);
@@ -116,8 +118,6 @@ struct NormResidualGradArgs {
     void *dr;
     uint16_t *dy;
     float *dgamma_pre, *dgamma_post, *dgate;
-    int *status;
-    uint64_t wait_ns;
 };
 cudaError_t launch_norm_residual_bwd(const NormResidualArgs &a, const NormResidualGradArgs &g, float *part,
                                      int *launches, cudaStream_t stream);

@@ -166,7 +166,7 @@ moe_status_t check_norm(int residual_fp32, const uint16_t *y, const float *gamma
         (gate && !aligned(gate, gate_kind == MOE_GATE_CHANNEL ? 16 : 4)))
         return MOE_ERR_INVALID_ARG;
     *out = moe::NormResidualArgs{y, gamma_post, gate, gamma_pre, gate_kind == MOE_GATE_TOKEN, res_scale, eps, T, d,
-                                 residual_fp32 == 1};
+                                 residual_fp32 == 1, nullptr, kWaitLimitNs};
     return MOE_OK;
 }
 
@@ -427,6 +427,9 @@ moe_status_t moe_norm_residual(const void *r, int residual_fp32, const uint16_t 
     if (y && (!r_out || !aligned(r_out, 16))) return MOE_ERR_INVALID_ARG;
     if (gamma_pre && (!n || !rstd_pre || !aligned(n, 16) || !aligned(rstd_pre, 4))) return MOE_ERR_INVALID_ARG;
     if (gamma_post && (!rstd_post || !aligned(rstd_post, 4))) return MOE_ERR_INVALID_ARG;
+    DeviceState *ds = nullptr;
+    if ((st = device_state(&ds)) != MOE_OK) return st;
+    a.status = ds->status;
     g_launches.fetch_add(1, std::memory_order_relaxed);
     return cuda_status(moe::launch_norm_residual(a, r, r_out, n, rstd_post, rstd_pre, stream));
 }
@@ -458,8 +461,8 @@ moe_status_t moe_norm_residual_backward(const void *r_out, int residual_fp32, co
     if (workspace_bytes < moe::norm_residual_bwd_part_bytes(T, d)) return MOE_ERR_WORKSPACE;
     DeviceState *ds = nullptr;
     if ((st = device_state(&ds)) != MOE_OK) return st;
-    const moe::NormResidualGradArgs g{r_out,      dr_out,      dn,    rstd_post,  rstd_pre,    dr, dy,
-                                      dgamma_pre, dgamma_post, dgate, ds->status, kWaitLimitNs};
+    a.status = ds->status;
+    const moe::NormResidualGradArgs g{r_out, dr_out, dn, rstd_post, rstd_pre, dr, dy, dgamma_pre, dgamma_post, dgate};
     int launches = 0;
     const cudaError_t e = moe::launch_norm_residual_bwd(a, g, static_cast<float *>(workspace), &launches, stream);
     g_launches.fetch_add(launches, std::memory_order_relaxed);

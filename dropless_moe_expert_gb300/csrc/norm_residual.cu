@@ -25,53 +25,31 @@ namespace nr {
 
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int SMS = 152;
-constexpr int MAX_THREADS = 512;       // of an SM, 128 registers each (the narrow forward: twice as many, 64 each)
+constexpr int MAX_THREADS = 512;       // of an SM, 128 registers each
 constexpr int RING_BYTES = 208 * 1024; // the rings of an SM's CTAs
-constexpr int MAX_STAGES = 4;
+// Rows in the ring.  More of them ahead made the forward slower (8192 x 4096
+// bf16, us: 46.5 with two rows, 50.4 with three, 52.5 with four); the backward,
+// which reads a row twice, needs a third one to run ahead.
+constexpr int FWD_STAGES = 2;
+constexpr int BWD_STAGES = 4;
 
-// Which backward kernels read a row ahead: those whose ring always holds three rows.
+// Which backward kernels read a row ahead: of those whose ring always holds three rows, the one it makes faster.
 template <typename R>
-__host__ __device__ constexpr bool pipelined(int vpt) { return vpt == 1 || (vpt == 2 && sizeof(R) == 2); }
+__host__ __device__ constexpr bool pipelined(int vpt, bool full) { return full && vpt == 2 && sizeof(R) == 2; }
 
 // With what the launch adds to the caller's arguments.
 struct Args : NormResidualArgs {
     int stages;  // rows in the ring
     bool wide;   // the fp32 rows that are written begin on 32-byte boundaries
-    int *status;       // of the bounded waits
-    uint64_t wait_ns;
 };
 
 
-// A row lies in shared memory in pieces of 32 vectors of eight elements, one
-// vector per lane of the warp that copies and reads the piece, in the order of
-// global memory: with the 16-byte halves of fp32 vectors in two planes the reads
-// had no bank conflicts, but the copies no longer went as whole sectors (backward
-// of 4093 x 7168 fp32: 127 us, 103 in order).
+// A row is cut into pieces of 32 vectors of eight elements, one vector per lane.
 template <typename T>
-__host__ __device__ constexpr int piece_bytes() { return sizeof(T) == 4 ? 1024 : 512; }
-
-// A lane's part of copying piece `piece`: where in the row, where in the piece, and which of its copies exist.
-template <typename T>
-struct Copy {
-    static constexpr int N = sizeof(T) / 2;
-    int from, to;
-    bool on[N];
-    __device__ __forceinline__ Copy(int piece, int lane, int nvec) {
-        from = piece * 256 + lane * (16 / static_cast<int>(sizeof(T)));
-        to = piece * piece_bytes<T>() + lane * 16;
-#pragma unroll
-        for (int q = 0; q < N; ++q) on[q] = from + q * 128 < 8 * nvec;
-    }
-    __device__ __forceinline__ void go(uint8_t *dst, const T *row) const {
-#pragma unroll
-        for (int q = 0; q < N; ++q)
-            if (on[q]) cp_async_16(dst + to + q * 512, row + from + q * 128);
-    }
-};
+__host__ __device__ constexpr int piece_bytes() { return 256 * static_cast<int>(sizeof(T)); }
 
 template <typename T>
-__device__ __forceinline__ void read8(const uint8_t *src, int piece, int lane, float2 (&o)[4]) {
-    src += piece * piece_bytes<T>() + lane * 8 * static_cast<int>(sizeof(T));
+__device__ __forceinline__ void read8(const uint8_t *src, float2 (&o)[4]) {
     if constexpr (sizeof(T) == 2) {
         bf16x8_to_f32(*reinterpret_cast<const uint4 *>(src), &o[0].x);
     } else {
@@ -81,20 +59,43 @@ __device__ __forceinline__ void read8(const uint8_t *src, int piece, int lane, f
     }
 }
 
-// Until the oldest of the ring's rows is there (one group of copies per row).
-__device__ __forceinline__ void wait_oldest(int stages) {
-    switch (stages) {
-        case 1: cp_async_wait_group<0>(); break;
-        case 2: cp_async_wait_group<1>(); break;
-        case 3: cp_async_wait_group<2>(); break;
-        default: cp_async_wait_group<3>();
-    }
+// A vector to column `col` of a row.
+__device__ __forceinline__ void store(uint16_t *row, uint32_t col, const float2 (&x)[4], bool) {
+    store8(row + col, 0, &x[0].x);
+}
+__device__ __forceinline__ void store(float *row, uint32_t col, const float2 (&x)[4], bool wide) {
+    wide ? store8_wide(row + col, 0, &x[0].x) : store8(row + col, 0, &x[0].x);
 }
 
-__device__ __forceinline__ void store(uint16_t *row, int v, const float2 (&x)[4], bool) { store8(row, v, &x[0].x); }
-__device__ __forceinline__ void store(float *row, int v, const float2 (&x)[4], bool wide) {
-    wide ? store8_wide(row, v, &x[0].x) : store8(row, v, &x[0].x);
-}
+// What a thread owns: VPT neighbouring pieces per warp, a vector of each.
+template <int VPT>
+struct Owned {
+    uint32_t col;  // of the first vector (the j-th: + 256 j)
+    bool on[VPT];  // whether the row has them
+    int first, cols;  // the warp's columns
+    __device__ __forceinline__ Owned(int warp, int lane, int nvec) {
+        col = (warp * VPT * 32 + lane) * 8;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) on[j] = (warp * VPT + j) * 32 + lane < nvec;
+        first = warp * VPT * 256;
+        cols = max(0, min(VPT * 32, nvec - warp * VPT * 32)) * 8;
+    }
+};
+
+// The barriers of a warp's slots in the ring: each counts the bytes of a row's copies.
+struct Ring {
+    uint64_t *full;
+    int *abort, *status;
+    uint64_t wait_ns;
+    bool used;  // the warp has columns
+    // Until the row in a slot is there.  After another wait ran out this one
+    // still waits (as long again) for its own copies.
+    __device__ __forceinline__ void wait(int slot, int phase) const {
+        int again = 0;
+        if (used && !mbar_wait(&full[slot], phase, abort, status, wait_ns))
+            mbar_wait(&full[slot], phase, &again, status, wait_ns);
+    }
+};
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -140,85 +141,95 @@ __device__ __forceinline__ float4 collect_sums4(const float4 *red) {
     return make_float4(a.x, a.y, b.x, b.y);
 }
 
-// Weights of eight columns (vector v of nvec): c of y (gamma_post times a
-// channel gate) and w of n; 1 for those left out.
-__device__ __forceinline__ void weights(const NormResidualArgs &a, int v, int nvec, float2 (&c)[4], float2 (&w)[4]) {
+// Weights of the eight columns from `col` (where the row has them): c of y
+// (gamma_post times a channel gate) and w of n; 1 for those left out.
+__device__ __forceinline__ void weights(const NormResidualArgs &a, uint32_t col, bool on, float2 (&c)[4], float2 (&w)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[i] = w[i] = both(1.0f);
-    if (v >= nvec) return;
-    if (a.gamma_post) load8(a.gamma_post, v, &c[0].x);
+    if (!on) return;
+    if (a.gamma_post) load8(a.gamma_post + col, 0, &c[0].x);
     if (a.gate && !a.gate_per_token) {
         float2 g[4];
-        load8(a.gate, v, &g[0].x);
+        load8(a.gate + col, 0, &g[0].x);
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[i] = mul2(c[i], g[i]);
     }
-    if (a.gamma_pre) load8(a.gamma_pre, v, &w[0].x);
+    if (a.gamma_pre) load8(a.gamma_pre + col, 0, &w[0].x);
 }
 
 // Row r of CTA blockIdx.x is blockIdx.x + r gridDim.x.  A thread owns VPT
-// vectors of eight columns; each warp copies the pieces that it reads, so its
-// rows come ahead of their use through a ring in shared memory without
-// barriers.  A row's slot is refilled as soon as the row is in registers, so
+// vectors of eight columns; each warp fetches the columns that it reads with
+// bulk copies of its own, so its rows come ahead of their use through a ring in
+// shared memory and wait for no other warp.  (With 16-byte copies by every lane
+// the backward of 8192 x 4096 took 78.3 us, 72.1 with bulk copies: the lanes'
+// requests, not the memory, were the limit.)  A row's slot is refilled as soon as the row is in registers, so
 // the ring's copies stay in flight through the row's sums and stores.
 template <typename R, int VPT>
-__global__ void __launch_bounds__(VPT == 1 ? 2 * MAX_THREADS : MAX_THREADS)
+__global__ void __launch_bounds__(MAX_THREADS)
 norm_residual_kernel(Args a, float inv_d, const R *r, R *r_out, uint16_t *__restrict__ n,
                      float *__restrict__ rstd_post, float *__restrict__ rstd_pre) {
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float red[2][32];
+    __shared__ uint64_t landed[MAX_THREADS / 32][FWD_STAGES];
+    __shared__ int abort;
     const int stages = a.stages;
     constexpr bool HOLD = VPT <= 2;  // the weights stay in registers
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int nvec = a.d / 8;
     const bool has_y = a.y != nullptr, post = a.gamma_post != nullptr, pre = a.gamma_pre != nullptr;
-    const int y_bytes = VPT * warps * piece_bytes<uint16_t>();
-    const int stage = y_bytes + VPT * warps * piece_bytes<R>();
+    const Owned<VPT> own(warp, lane, a.d / 8);
+    constexpr int AT_R = VPT * piece_bytes<uint16_t>(), PART = AT_R + VPT * piece_bytes<R>();
+    const int stage = warps * PART;
+    uint8_t *const mine = ring + warp * PART;
     float2 c[VPT][4], w[VPT][4];
     if (HOLD) {
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) weights(a, (warp + j * warps) * 32 + lane, nvec, c[j], w[j]);
+        for (int j = 0; j < VPT; ++j) weights(a, own.col + 256 * j, own.on[j], c[j], w[j]);
     }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < warps; ++i)
+            for (int q = 0; q < FWD_STAGES; ++q) mbar_init(&landed[i][q], 1);
+        abort = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    const Ring rows{landed[warp], &abort, a.status, a.wait_ns, own.cols > 0};
     auto issue = [&](int64_t t, int slot) {
-        if (t < a.T) {
-            uint8_t *at = ring + slot * stage;
-            const int64_t from = t * a.d;
-#pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                if (has_y) Copy<uint16_t>(warp + j * warps, lane, nvec).go(at, a.y + from);
-                Copy<R>(warp + j * warps, lane, nvec).go(at + y_bytes, r + from);
-            }
+        if (lane == 0 && t < a.T && own.cols > 0) {
+            uint8_t *to = mine + slot * stage;
+            const int64_t from = t * a.d + own.first;
+            const uint32_t nb = own.cols * 2, nr = own.cols * static_cast<int>(sizeof(R));
+            mbar_arrive_expect_tx(&rows.full[slot], (has_y ? nb : 0) + nr);
+            if (has_y) bulk_load(to, a.y + from, nb, &rows.full[slot]);
+            bulk_load(to + AT_R, r + from, nr, &rows.full[slot]);
         }
-        cp_async_commit();
     };
     const int64_t step = gridDim.x;
     for (int s = 0; s < stages; ++s) issue(blockIdx.x + s * step, s);
     const bool token_gate = a.gate && a.gate_per_token;
     float gt = token_gate ? a.gate[blockIdx.x] : 1.0f;
-    int slot = 0, turn = 0;
+    int slot = 0, turn = 0, phase = 0;
     for (int64_t t = blockIdx.x; t < a.T; t += step) {
         const float gt_next = token_gate && t + step < a.T ? a.gate[t + step] : 1.0f;
-        wait_oldest(stages);
-        __syncwarp();  // what the warp's other lanes copied
-        const uint8_t *at = ring + slot * stage;
+        rows.wait(slot, phase);
+        const uint8_t *at = mine + slot * stage;
         float2 x[VPT][4], y[VPT][4];
         float2 ss = both(0.0f);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int piece = warp + j * warps;
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[j][i] = y[j][i] = both(0.0f);
-            if (piece * 32 + lane >= nvec) continue;
-            read8<R>(at + y_bytes, piece, lane, x[j]);
+            if (!own.on[j]) continue;
+            read8<R>(at + AT_R + j * piece_bytes<R>() + lane * (8 * sizeof(R)), x[j]);
             if (has_y) {
-                read8<uint16_t>(at, piece, lane, y[j]);
+                read8<uint16_t>(at + j * 512 + lane * 16, y[j]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) ss = fma2(y[j][i], y[j][i], ss);
             }
         }
-        __syncwarp();
+        __syncwarp();  // the warp has read the row
         issue(t + stages * step, slot);
         slot = slot + 1 == stages ? 0 : slot + 1;
+        if (slot == 0) phase ^= 1;
         if (has_y) {
             float f = gt;
             if (post) {
@@ -230,12 +241,11 @@ norm_residual_kernel(Args a, float inv_d, const R *r, R *r_out, uint16_t *__rest
             R *out = r_out + t * a.d;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int v = (warp + j * warps) * 32 + lane;
-                if (!HOLD) weights(a, v, nvec, c[j], w[j]);
+                if (!HOLD) weights(a, own.col + 256 * j, own.on[j], c[j], w[j]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     x[j][i] = fma2(mul2(both(f), c[j][i]), y[j][i], mul2(both(a.res_scale), x[j][i]));
-                if (v < nvec) store(out, v, x[j], a.wide);
+                if (own.on[j]) store(out, own.col + 256 * j, x[j], a.wide);
             }
         }
         if (pre) {
@@ -250,11 +260,11 @@ norm_residual_kernel(Args a, float inv_d, const R *r, R *r_out, uint16_t *__rest
             uint16_t *out = n + t * a.d;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int v = (warp + j * warps) * 32 + lane;
-                if (!HOLD && v < nvec) load8(a.gamma_pre, v, &w[j][0].x);
+                if (!own.on[j]) continue;
+                if (!HOLD) load8(a.gamma_pre + own.col + 256 * j, 0, &w[j][0].x);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[j][i] = mul2(x[j][i], mul2(both(rq), w[j][i]));
-                if (v < nvec) store8(out, v, &x[j][0].x);
+                store(out, own.col + 256 * j, x[j], true);
             }
         }
         gt = gt_next;
@@ -262,11 +272,11 @@ norm_residual_kernel(Args a, float inv_d, const R *r, R *r_out, uint16_t *__rest
 }
 
 // Rows and ring as above, but the row is read from its slot twice, before and
-// after the sums, and each piece refilled once it has been read the second time.
+// after the sums, and the slot refilled after the second time.
 // PIPE: the first reading of row r + 1 stands between the sums of row r and
-// their use, so one barrier per row remains and nothing waits for the sums'
-// exchanges (8192 x 4096 bf16: 84.6 us, 79.7 with it); it needs a third row in the ring, which
-// fp32 rows do not leave room for.
+// their use, so that no warp waits for the others' sums (8192 x 4096 bf16:
+// 77.2 us, 72.3 with it).  It needs a third row in the ring, which fp32 rows do
+// not leave room for.
 // One reduction gives both means of a row: with z = r' rq, m1 = rq mean(h z)
 // and c the weight of y without a token gate g,
 //   D = dr' + rq h - m1 z,   sum(c y D) = sum(c y dr') + rq sum(c y h) - m1 sum(c y z),
@@ -282,34 +292,48 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
                          float *__restrict__ dgate, float *__restrict__ part) {
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float4 red[2][MAX_THREADS / 32];
+    __shared__ uint64_t landed[MAX_THREADS / 32][BWD_STAGES];
     __shared__ uint64_t posted;  // a phase per row, an arrival per warp
     __shared__ int abort;
-    constexpr bool PIPE = pipelined<R>(VPT);
+    constexpr bool PIPE = pipelined<R>(VPT, FULL);
     const int stages = a.stages;
     constexpr bool HOLD = VPT <= 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int nvec = a.d / 8;
     const bool has_y = FULL || a.y, has_dr = FULL || dr_out, pre = FULL || a.gamma_pre, post = a.gamma_post != nullptr;
-    const int b_bytes = VPT * warps * piece_bytes<uint16_t>(), r_bytes = VPT * warps * piece_bytes<R>();
-    const int at_dn = b_bytes, at_x = 2 * b_bytes, at_dr = at_x + r_bytes, stage = at_dr + r_bytes;
+    const Owned<VPT> own(warp, lane, a.d / 8);
+    // a warp's part of a row in the ring: its columns of y, dn, r' and dr'
+    constexpr int B = VPT * piece_bytes<uint16_t>(), AT_DN = B, AT_X = 2 * B, AT_DR = AT_X + VPT * piece_bytes<R>();
+    constexpr int PART = AT_DR + VPT * piece_bytes<R>();
+    const int stage = warps * PART;
+    uint8_t *const mine = ring + warp * PART;
     float2 c[VPT][4], w[VPT][4], accq[VPT][4], accp[VPT][4];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        if (HOLD) weights(a, (warp + j * warps) * 32 + lane, nvec, c[j], w[j]);
+        if (HOLD) weights(a, own.col + 256 * j, own.on[j], c[j], w[j]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) accq[j][i] = accp[j][i] = both(0.0f);
     }
-    auto issue = [&](int64_t t, int slot, int piece) {
-        if (t < a.T) {
-            uint8_t *at = ring + slot * stage;
-            const int64_t from = t * a.d;
-            const Copy<uint16_t> b(piece, lane, nvec);
-            const Copy<R> x(piece, lane, nvec);
-            if (has_y) b.go(at, a.y + from);
-            if (has_dr) x.go(at + at_dr, dr_out + from);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < warps; ++i)
+            for (int q = 0; q < BWD_STAGES; ++q) mbar_init(&landed[i][q], 1);
+        mbar_init(&posted, warps);
+        abort = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    const Ring rows{landed[warp], &abort, a.status, a.wait_ns, own.cols > 0};
+    auto issue = [&](int64_t t, int slot) {
+        if (lane == 0 && t < a.T && own.cols > 0) {
+            uint8_t *to = mine + slot * stage;
+            const int64_t from = t * a.d + own.first;
+            const uint32_t nb = own.cols * 2, nr = own.cols * static_cast<int>(sizeof(R));
+            uint64_t *full = rows.full;
+            mbar_arrive_expect_tx(&full[slot], (has_y ? nb : 0) + (has_dr ? nr : 0) + (pre ? nb + nr : 0));
+            if (has_y) bulk_load(to, a.y + from, nb, &full[slot]);
+            if (has_dr) bulk_load(to + AT_DR, dr_out + from, nr, &full[slot]);
             if (pre) {
-                b.go(at + at_dn, dn + from);
-                x.go(at + at_x, r_out + from);
+                bulk_load(to + AT_DN, dn + from, nb, &full[slot]);
+                bulk_load(to + AT_X, r_out + from, nr, &full[slot]);
             }
         }
     };
@@ -326,37 +350,32 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
         return f;
     };
     const int64_t step = gridDim.x;
-    for (int s = 0; s < stages; ++s) {
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) issue(blockIdx.x + s * step, s, warp + j * warps);
-        cp_async_commit();
-    }
+    for (int s = 0; s < stages; ++s) issue(blockIdx.x + s * step, s);
     // The first reading of the row in slot `slot`: the four sums (of h z,
     // c y dr', c y h, c y z) of the warp go to `sums`.
     auto first_pass = [&](int slot, float rq, float4 *sums) {
-        const uint8_t *at = ring + slot * stage;
+        const uint8_t *at16 = mine + slot * stage + lane * 16, *at_r = mine + slot * stage + lane * (8 * sizeof(R));
         float2 s0 = both(0.0f), s1 = s0, s2 = s0, s3 = s0;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int piece = warp + j * warps, v = piece * 32 + lane;
-            if (v >= nvec) continue;
-            if (!HOLD) weights(a, v, nvec, c[j], w[j]);
+            if (!own.on[j]) continue;
+            if (!HOLD) weights(a, own.col + 256 * j, true, c[j], w[j]);
             float2 cy[4];
             if (has_y) {
-                read8<uint16_t>(at, piece, lane, cy);
+                read8<uint16_t>(at16 + j * 512, cy);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) cy[i] = mul2(cy[i], c[j][i]);
                 if (has_dr) {
                     float2 g[4];
-                    read8<R>(at + at_dr, piece, lane, g);
+                    read8<R>(at_r + j * piece_bytes<R>() + AT_DR, g);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s1 = fma2(cy[i], g[i], s1);
                 }
             }
             if (pre) {
                 float2 z[4], g[4];
-                read8<R>(at + at_x, piece, lane, z);
-                read8<uint16_t>(at + at_dn, piece, lane, g);
+                read8<R>(at_r + j * piece_bytes<R>() + AT_X, z);
+                read8<uint16_t>(at16 + j * 512 + AT_DN, g);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     z[i] = mul2(z[i], both(rq));
@@ -391,19 +410,11 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
         }
         return collect_sums4(sums);
     };
-    if (PIPE) {
-        if (threadIdx.x == 0) {
-            mbar_init(&posted, warps);
-            abort = 0;
-            fence_mbar_init();
-        }
-        __syncthreads();
-    }
     Row f = factors(blockIdx.x), next = factors(blockIdx.x + step);
     int slot = 0, turn = 0;
+    int phase = 0;  // of the slot that first_pass reads next
     if (PIPE) {
-        wait_oldest(stages);
-        __syncwarp();  // what the warp's other lanes copied
+        rows.wait(0, 0);
         first_pass(0, f.rq, red[0]);
     }
     for (int64_t t = blockIdx.x; t < a.T; t += step) {
@@ -412,17 +423,19 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
         float4 s;
         if (PIPE) {
             s = collect(red[turn]);
-            wait_oldest(stages - 1);  // the newest `stages - 2` rows may still be on their way
-            __syncwarp();
-            if (t + step < a.T) first_pass(ahead, next.rq, red[turn ^ 1]);
+            if (ahead == 0) phase ^= 1;
+            if (t + step < a.T) {
+                rows.wait(ahead, phase);
+                first_pass(ahead, next.rq, red[turn ^ 1]);
+            }
         } else {
-            wait_oldest(stages);
-            __syncwarp();
+            rows.wait(slot, phase);
             first_pass(slot, f.rq, red[turn]);
             s = collect(red[turn]);
+            if (ahead == 0) phase ^= 1;
         }
         turn ^= 1;
-        const uint8_t *at = ring + slot * stage;
+        const uint8_t *at16 = mine + slot * stage + lane * 16, *at_r = mine + slot * stage + lane * (8 * sizeof(R));
         const float m1 = f.rq * s.x * inv_d;
         const float cyD = s.y + f.rq * s.z - m1 * s.w;
         const float m2 = post ? f.gt * cyD * inv_d * f.rp * f.rp * f.rp : 0.0f;
@@ -432,29 +445,31 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
         uint16_t *to_y = dy + t * a.d;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int piece = warp + j * warps, v = piece * 32 + lane;
+            const uint32_t col = own.col + 256 * j;
             float2 D[4], y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) D[i] = both(0.0f);
-            if (v < nvec) {
-                if (!HOLD) weights(a, v, nvec, c[j], w[j]);
-                if (has_dr) read8<R>(at + at_dr, piece, lane, D);
+            if (own.on[j]) {
+                if (!HOLD) weights(a, col, true, c[j], w[j]);
+                if (has_dr) read8<R>(at_r + j * piece_bytes<R>() + AT_DR, D);
                 if (pre) {
                     float2 x[4], g[4];
-                    read8<R>(at + at_x, piece, lane, x);
-                    read8<uint16_t>(at + at_dn, piece, lane, g);
+                    read8<R>(at_r + j * piece_bytes<R>() + AT_X, x);
+                    read8<uint16_t>(at16 + j * 512 + AT_DN, g);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) D[i] = fma2(mz, x[i], fma2(mul2(rq, g[i]), w[j][i], D[i]));
                 }
-                if (has_y) read8<uint16_t>(at, piece, lane, y);
+                if (has_y) read8<uint16_t>(at16 + j * 512, y);
             }
-            __syncwarp();
-            issue(t + stages * step, slot, piece);
-            if (v >= nvec) continue;
+            if (j == VPT - 1) {
+                __syncwarp();  // the warp has read the row
+                issue(t + stages * step, slot);
+            }
+            if (!own.on[j]) continue;
             float2 o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = mul2(both(a.res_scale), D[i]);  // res_scale is 1 without y
-            store(to_r, v, o, a.wide);
+            store(to_r, col, o, a.wide);
             if (!has_y) continue;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -462,20 +477,18 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
                 accp[j][i] = fma2(y[i], D[i], accp[j][i]);
                 o[i] = fma2(my, y[i], mul2(D[i], c[j][i]));
             }
-            store8(to_y, v, &o[0].x);
+            store(to_y, col, o, true);
         }
-        cp_async_commit();
         slot = ahead;
         f = next;
         next = after;
     }
-    float *mine = part + static_cast<size_t>(blockIdx.x) * 2 * a.d;
+    float *sums = part + static_cast<size_t>(blockIdx.x) * 2 * a.d;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int v = (warp + j * warps) * 32 + lane;
-        if (v >= nvec) break;
-        store8(mine, v, &accq[j][0].x);
-        store8(mine + a.d, v, &accp[j][0].x);
+        if (!own.on[j]) break;
+        store8(sums + own.col + 256 * j, 0, &accq[j][0].x);
+        store8(sums + a.d + own.col + 256 * j, 0, &accp[j][0].x);
     }
 }
 
@@ -520,33 +533,28 @@ struct Shape {
     int vpt, threads, ctas, stages;
     size_t smem;
 };
-// `piece`: bytes of one piece of all the arrays that a row is read from;
-// `threads`: of an SM.
-Shape shape(int T, int d, int vpt, int piece, int threads) {
+// `piece`: bytes of one piece of all the arrays that a row is read from.
+Shape shape(int T, int d, int stages, int piece) {
     Shape s;
-    s.vpt = vpt;
-    s.threads = (d / 8 + 32 * vpt - 1) / (32 * vpt) * 32;
-    const int per_sm = std::min(16, threads / s.threads);
+    // Two vectors per thread: the work of a warp per row is what bounds these
+    // kernels next to memory (one vector and twice the threads, us: forward of
+    // 8192 x 4096 bf16 56.5, 46.5 with two; backward 86.7 and 72.3).
+    s.vpt = d <= 256 ? 1 : d <= 16 * MAX_THREADS ? 2 : 4;
+    s.threads = (d / 8 + 32 * s.vpt - 1) / (32 * s.vpt) * 32;
+    const int per_sm = std::min(16, MAX_THREADS / s.threads);
     s.ctas = std::min(T, SMS * per_sm);
-    const int row = vpt * (s.threads / 32) * piece;
-    s.stages = std::max(1, std::min(MAX_STAGES, RING_BYTES / per_sm / row));
+    const int row = s.vpt * (s.threads / 32) * piece;
+    s.stages = std::max(1, std::min(stages, RING_BYTES / per_sm / row));
     s.smem = static_cast<size_t>(s.stages) * row;
     return s;
 }
-// One vector per thread and twice the threads, but two vectors for bf16 rows
-// of more than 4096 columns, and four beyond 8192 (us, one vector / two:
-// 8192 x 4096 bf16 47.0 / 50.9, 4093 x 7168 fp32 58.8 / 65.9, bf16 45.5 / 43.0).
-Shape fwd_shape(int T, int d, bool res_f32) {
-    const int vpt = d > 16 * MAX_THREADS ? 4 : d > 8 * MAX_THREADS && !res_f32 ? 2 : 1;
-    return shape(T, d, vpt, piece_bytes<uint16_t>() + (res_f32 ? piece_bytes<float>() : piece_bytes<uint16_t>()),
-                 vpt == 1 ? 2 * MAX_THREADS : MAX_THREADS);
+template <typename R>
+Shape fwd_shape(int T, int d) {
+    return shape(T, d, FWD_STAGES, piece_bytes<uint16_t>() + piece_bytes<R>());
 }
-// Two vectors per thread: the per-row work of a warp is what bounds the
-// backward (4096 columns, bf16: 80.1 us; one vector and twice the threads 94.9).
-Shape bwd_shape(int T, int d, bool res_f32) {
-    return shape(T, d, d <= 512 ? 1 : d <= 16 * MAX_THREADS ? 2 : 4,
-                 2 * piece_bytes<uint16_t>() + 2 * (res_f32 ? piece_bytes<float>() : piece_bytes<uint16_t>()),
-                 MAX_THREADS);
+template <typename R>
+Shape bwd_shape(int T, int d) {
+    return shape(T, d, BWD_STAGES, 2 * piece_bytes<uint16_t>() + 2 * piece_bytes<R>());
 }
 
 // Raises the kernel's limit of dynamic shared memory, once per device.
@@ -566,7 +574,7 @@ cudaError_t forward(const Shape &s, const NormResidualArgs &a, const void *r, vo
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_ring(norm_residual_kernel<R, VPT>, done);
     if (e != cudaSuccess) return e;
-    const Args args{a, s.stages, reinterpret_cast<uintptr_t>(r_out) % 32 == 0, nullptr, 0};
+    const Args args{a, s.stages, reinterpret_cast<uintptr_t>(r_out) % 32 == 0};
     norm_residual_kernel<R, VPT><<<s.ctas, s.threads, s.smem, stream>>>(
         args, 1.0f / a.d, static_cast<const R *>(r), static_cast<R *>(r_out), n, rstd_post, rstd_pre);
     return cudaGetLastError();
@@ -578,7 +586,7 @@ cudaError_t backward(const Shape &s, const NormResidualArgs &a, const NormResidu
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_ring(norm_residual_bwd_kernel<R, VPT, FULL>, done);
     if (e != cudaSuccess) return e;
-    const Args args{a, s.stages, reinterpret_cast<uintptr_t>(g.dr) % 32 == 0, g.status, g.wait_ns};
+    const Args args{a, s.stages, reinterpret_cast<uintptr_t>(g.dr) % 32 == 0};
     norm_residual_bwd_kernel<R, VPT, FULL><<<s.ctas, s.threads, s.smem, stream>>>(
         args, 1.0f / a.d, static_cast<const R *>(g.r_out), static_cast<const R *>(g.dr_out), g.dn, g.rstd_post,
         g.rstd_pre, static_cast<R *>(g.dr), g.dy, g.dgate, part);
@@ -589,27 +597,27 @@ cudaError_t backward(const Shape &s, const NormResidualArgs &a, const NormResidu
 
 cudaError_t launch_norm_residual(const NormResidualArgs &a, const void *r, void *r_out, uint16_t *n, float *rstd_post,
                                  float *rstd_pre, cudaStream_t stream) {
-    const nr::Shape s = nr::fwd_shape(a.T, a.d, a.res_f32);
     auto go = [&](auto type) {
         using R = decltype(type);
+        const nr::Shape s = nr::fwd_shape<R>(a.T, a.d);
         if (s.vpt == 1) return nr::forward<R, 1>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
-        if constexpr (sizeof(R) == 2) {
-            if (s.vpt == 2) return nr::forward<R, 2>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
-        }
+        if (s.vpt == 2) return nr::forward<R, 2>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
         return nr::forward<R, 4>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
     };
     return a.res_f32 ? go(float{}) : go(uint16_t{});
 }
 
 size_t norm_residual_bwd_part_bytes(int T, int d) {
-    return static_cast<size_t>(nr::bwd_shape(T, d, false).ctas) * 2 * d * 4;
+    return static_cast<size_t>(nr::bwd_shape<float>(T, d).ctas) * 2 * d * 4;
 }
 
 cudaError_t launch_norm_residual_bwd(const NormResidualArgs &a, const NormResidualGradArgs &g, float *part,
                                      int *launches, cudaStream_t stream) {
-    const nr::Shape s = nr::bwd_shape(a.T, a.d, a.res_f32);
+    int ctas = 0;
     auto go = [&](auto type) {
         using R = decltype(type);
+        const nr::Shape s = nr::bwd_shape<R>(a.T, a.d);
+        ctas = s.ctas;
         if (a.y && g.dr_out && a.gamma_pre) {
             if (s.vpt == 1) return nr::backward<R, 1, true>(s, a, g, part, stream);
             return s.vpt == 2 ? nr::backward<R, 2, true>(s, a, g, part, stream)
@@ -624,7 +632,7 @@ cudaError_t launch_norm_residual_bwd(const NormResidualArgs &a, const NormResidu
     if (err != cudaSuccess || !(a.gamma_pre || a.gamma_post || (a.gate && !a.gate_per_token))) return err;
     *launches = 2;
     return launch_dependent(nr::norm_residual_bwd_columns_kernel, a.d / 32, 32 * nr::RUNS, stream,
-                            static_cast<const NormResidualArgs &>(a), static_cast<const float *>(part), s.ctas,
+                            static_cast<const NormResidualArgs &>(a), static_cast<const float *>(part), ctas,
                             g.dgamma_pre, g.dgamma_post, g.dgate);
 }
 
