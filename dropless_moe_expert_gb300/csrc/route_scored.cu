@@ -28,13 +28,18 @@ namespace moe {
 namespace rs {
 
 constexpr int MAX_E = 256;
-constexpr int CH = 16;             // tokens per chunk: a CTA of the top-K kernel, a warp per token
-constexpr int FEW = 32;            // tokens that one CTA routes alone
+constexpr int CH = 16;             // tokens of a chunk, which a CTA of the top-K kernel takes
 constexpr int OPEN = MAX_E / 16;   // words of a token's open runs
 constexpr int SPANS = 152;         // CTAs of the dispatch kernel, each a run of chunks
-constexpr int DISPATCH_THREADS = 1024;
-constexpr size_t SELF_SUM_BYTES = 256 * 1024;  // of counts that every dispatch CTA adds up itself
+// Of counts that every dispatch CTA adds up itself, not another launch before
+// it (32768 x 64, 128 KB: 19.2 us, 24.2 with the launch; 131072 x 64, 512 KB:
+// 68.0 and 61.5).
+constexpr size_t SELF_SUM_BYTES = 256 * 1024;
 constexpr unsigned FULL = 0xffffffffu;
+
+// Of a dispatch CTA: 512 while it adds the counts up itself (4096 x 256: 11.8 us,
+// 12.3 with 1024), 1024 where its span is long (131072 x 64: 61.5 us, 65.5 with 512).
+__host__ __device__ constexpr int dispatch_threads(bool spanned) { return spanned ? 1024 : 512; }
 
 // Bytes of a chunk's row of counts (one byte per expert, whole 16-byte words).
 __host__ __device__ constexpr int count_pitch(int E) { return (E + 15) / 16 * 16; }
@@ -152,24 +157,24 @@ __device__ __forceinline__ uint32_t open_runs(const uint32_t *keys, uint32_t *sc
     return first;
 }
 
-// LANES lanes per token, TOK tokens per CTA.  FINAL: the CTA holds every token
-// and writes the dispatch order too; else it writes its chunk's counts and each
-// pair's rank inside the chunk (in row_of) for the dispatch kernel.
+// LANES lanes per token, a chunk per CTA.  FINAL: the chunk holds every token
+// and the CTA writes the dispatch order too; else it writes its chunk's counts
+// and each pair's rank inside the chunk (in row_of) for the dispatch kernel.
 // The instructions of a token bound it: half a warp per token up to 64 experts
 // (32768 tokens, 64 experts: 19.5 us for the whole routing, 20.9 with a warp;
 // 128 experts the other way round, 17.7 and 18.8 for 16384 tokens).
-template <int LANES, int EPL, int TOK, bool FINAL>
-__global__ void __launch_bounds__(TOK *LANES)
+template <int LANES, int EPL, bool FINAL>
+__global__ void __launch_bounds__(CH *LANES, !FINAL && LANES == 32 ? 3 : 1)
 route_scored_topk_kernel(const float *__restrict__ L, const float *__restrict__ bias, int T, int E, int K,
                          RouteRule rule, int32_t *__restrict__ topk_idx, float *__restrict__ topk_w,
                          int32_t *__restrict__ row_of, uint8_t *__restrict__ chunk_counts,
                          int32_t *__restrict__ counts, int32_t *__restrict__ offsets, int32_t *__restrict__ src_tok) {
-    constexpr int THREADS = TOK * LANES;
+    constexpr int THREADS = CH * LANES;
     __shared__ uint32_t chose[MAX_E];  // bit i: token i of the CTA chose the expert
     __shared__ int32_t s_off[MAX_E];
-    extern __shared__ uint32_t s_groups[];  // with groups: keys [TOK][E], scores [TOK][n_group], open [TOK][OPEN]
+    extern __shared__ uint32_t s_groups[];  // with groups: keys [CH][E], scores [CH][n_group], open [CH][OPEN]
     const int tok = threadIdx.x / LANES, lane = threadIdx.x % LANES;
-    const int t = blockIdx.x * TOK + tok;
+    const int t = blockIdx.x * CH + tok;
     for (int e = threadIdx.x; e < E; e += THREADS) chose[e] = 0u;
     int my_e = 0;
     float w = 0.0f;  // lane k: the k-th choice and its weight
@@ -187,8 +192,8 @@ route_scored_topk_kernel(const float *__restrict__ L, const float *__restrict__ 
         }
         if (rule.topk_group < rule.n_group) {
             uint32_t *keys = s_groups + tok * E;
-            uint32_t *score = s_groups + TOK * E + tok * rule.n_group;
-            uint32_t *open = s_groups + TOK * (E + rule.n_group) + tok * OPEN;
+            uint32_t *score = s_groups + CH * E + tok * rule.n_group;
+            uint32_t *open = s_groups + CH * (E + rule.n_group) + tok * OPEN;
 #pragma unroll
             for (int j = 0; j < EPL; ++j)
                 if (lane + LANES * j < E) keys[lane + LANES * j] = key[j];
@@ -328,12 +333,12 @@ route_scored_span_kernel(const uint8_t *__restrict__ chunk_counts, int chunks, i
 // totals and what the spans before it hold: summed from the chunks' bytes by
 // every CTA itself, or from the spans' sums (SPANNED) where the bytes are many.
 template <bool SPANNED>
-__global__ void __launch_bounds__(DISPATCH_THREADS)
+__global__ void __launch_bounds__(dispatch_threads(SPANNED))
 route_scored_dispatch_kernel(const int32_t *__restrict__ topk_idx, const uint8_t *__restrict__ chunk_counts,
                              const int32_t *__restrict__ span_counts, int T, int E, int K, int chunks, int per_span,
                              int32_t *__restrict__ counts, int32_t *__restrict__ offsets,
                              int32_t *__restrict__ row_of, int32_t *__restrict__ src_tok) {
-    constexpr int WARPS = DISPATCH_THREADS / 32;
+    constexpr int THREADS = dispatch_threads(SPANNED), WARPS = THREADS / 32;
     constexpr int BLOCK = 16;  // chunks whose first rows are held at a time
     __shared__ union {
         uint16_t part[2][WARPS][MAX_E];  // the warps' sums: all chunks, those before the span
@@ -345,8 +350,9 @@ route_scored_dispatch_kernel(const int32_t *__restrict__ topk_idx, const uint8_t
     const int pitch = count_pitch(E);
     const int c0 = blockIdx.x * per_span, c1 = min(chunks, c0 + per_span);
     // of the first block of chunks: the counts and this thread's first pair, ahead of the sums
-    uint8_t n[BLOCK];
+    uint8_t n[BLOCK] = {};
     auto load_counts = [&](int b0) {
+        if (warp * 32 >= E) return;
 #pragma unroll
         for (int i = 0; i < BLOCK; ++i)
             n[i] = static_cast<int>(threadIdx.x) < E && b0 + i < c1
@@ -374,7 +380,7 @@ route_scored_dispatch_kernel(const int32_t *__restrict__ topk_idx, const uint8_t
         const int words = pitch / 16;  // at most 16; the words of a row lie in neighbouring lanes
         int lanes = 1;
         while (lanes < words) lanes *= 2;
-        const int word = lane % lanes, slices = DISPATCH_THREADS / lanes;
+        const int word = lane % lanes, slices = THREADS / lanes;
         Sums16 all = {}, before = {};
         if (word < words) {
 #pragma unroll 4
@@ -459,7 +465,7 @@ route_scored_dispatch_kernel(const int32_t *__restrict__ topk_idx, const uint8_t
             const int r = sh.base[i][next_e] + next_rank;
             row_of[p] = r;
             src_tok[r] = static_cast<int32_t>(p / K);
-            p += DISPATCH_THREADS;
+            p += THREADS;
             if (p < pairs) next_e = topk_idx[p], next_rank = row_of[p];
         }
         if (b0 + BLOCK < c1) {
@@ -560,24 +566,19 @@ cudaError_t launch_route_scored(const float *logits, const float *sel_bias, int 
                                 int32_t *topk_idx, float *topk_w, int32_t *counts, int32_t *offsets, int32_t *row_of,
                                 int32_t *src_tok, uint8_t *workspace, int *launches, cudaStream_t stream) {
     const int chunks = rs::num_chunks(T);
-    const bool few = T <= rs::FEW;
-    const int tok = few ? rs::FEW : rs::CH;
+    const bool few = T <= rs::CH;
     const size_t smem =
-        rule.topk_group < rule.n_group ? static_cast<size_t>(tok) * (E + rule.n_group + rs::OPEN) * 4 : 0;
+        rule.topk_group < rule.n_group ? static_cast<size_t>(rs::CH) * (E + rule.n_group + rs::OPEN) * 4 : 0;
     auto topk = [&](auto kernel, int lanes) {
-        static_assert(rs::FEW * (2 * rs::MAX_E + rs::OPEN) * 4 < 227 * 1024, "keys and scores fit a CTA");
-        if (smem > 40 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-            if (e != cudaSuccess) return e;
-        }
-        kernel<<<few ? 1 : chunks, tok * lanes, smem, stream>>>(logits, sel_bias, T, E, K, rule, topk_idx, topk_w, row_of,
+        static_assert(rs::CH * (2 * rs::MAX_E + rs::OPEN) * 4 < 40 * 1024, "the groups' keys fit without an attribute");
+        kernel<<<few ? 1 : chunks, rs::CH * lanes, smem, stream>>>(logits, sel_bias, T, E, K, rule, topk_idx, topk_w, row_of,
                                                              workspace, counts, offsets, src_tok);
         return cudaGetLastError();
     };
     auto by_experts = [&](auto lanes, auto each) {
         constexpr int LANES = decltype(lanes)::value, EPL = decltype(each)::value;
-        return few ? topk(rs::route_scored_topk_kernel<LANES, EPL, rs::FEW, true>, LANES)
-                   : topk(rs::route_scored_topk_kernel<LANES, EPL, rs::CH, false>, LANES);
+        return few ? topk(rs::route_scored_topk_kernel<LANES, EPL, true>, LANES)
+                   : topk(rs::route_scored_topk_kernel<LANES, EPL, false>, LANES);
     };
     using std::integral_constant;
     const integral_constant<int, 16> half;
@@ -601,7 +602,7 @@ cudaError_t launch_route_scored(const float *logits, const float *sel_bias, int 
     }
     ++*launches;
     return launch_dependent(spanned ? rs::route_scored_dispatch_kernel<true> : rs::route_scored_dispatch_kernel<false>,
-                            spans, rs::DISPATCH_THREADS, stream, static_cast<const int32_t *>(topk_idx),
+                            spans, rs::dispatch_threads(spanned), stream, static_cast<const int32_t *>(topk_idx),
                             static_cast<const uint8_t *>(workspace), static_cast<const int32_t *>(span_counts), T, E,
                             K, chunks, per_span, counts, offsets, row_of, src_tok);
 }

@@ -163,7 +163,7 @@ moe_status_t moe_route_static(const float *logits, int T, int E, int K,
  * sel_bias of -INFINITY closes an expert (it is chosen only where the open
  * runs hold fewer than K others, the lowest indexes first).  NaN logits are
  * outside the contract; the choice is then some K distinct experts.  Needs
- * E % n_group == 0 and K <= topk_group * (E / n_group).  One kernel launch up to 32 tokens, else two,
+ * E % n_group == 0 and K <= topk_group * (E / n_group).  One kernel launch up to 16 tokens, else two,
  * or three where the tokens and experts are many. */
 enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };
 typedef struct {

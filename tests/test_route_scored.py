@@ -27,6 +27,9 @@ ULP = 2.0 ** -24
 # T, E, K, score, n_group, topk_group, group_top, renorm, scale, bias
 CASES = [
     (1, 256, 8, "sigmoid", 8, 4, 2, True, 2.5, True),
+    (16, 256, 8, "sigmoid", 8, 4, 2, True, 2.5, True),       # the most tokens of one CTA, and one more
+    (17, 48, 5, "softmax", 4, 3, 2, True, 1.0, True),
+    (15, 31, 16, "sigmoid", 1, 1, 1, False, 1.0, False),
     (64, 256, 8, "sigmoid", 8, 4, 2, True, 2.5, True),
     (65, 256, 8, "softmax", 8, 3, 1, False, 16.0, False),
     (1000, 256, 8, "sigmoid", 8, 4, 2, True, 2.5, True),
