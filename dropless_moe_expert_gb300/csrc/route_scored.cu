@@ -252,8 +252,8 @@ route_scored_topk_kernel(const float *__restrict__ L, const float *__restrict__ 
             const float v = __shfl_sync(FULL, s[j], my_e % LANES, LANES);
             my_s = my_e / LANES == j ? v : my_s;
         }
-        w = rule.scale * my_s;
-        if (rule.renorm) w /= lanes_sum<LANES>(lane < K ? my_s : 0.0f) + kRouteEps;
+        // the share first: that of a single choice is 1 to the last bit
+        w = rule.scale * (rule.renorm ? my_s / (lanes_sum<LANES>(lane < K ? my_s : 0.0f) + kRouteEps) : my_s);
     }
     const bool write = t < T && lane < K;
     __syncthreads();  // `chose` is zero
@@ -507,9 +507,11 @@ route_scored_bwd_kernel(const float *__restrict__ L, const int32_t *__restrict__
         }
         float ds = e >= 0 ? rule.scale * g : 0.0f;
         if (rule.renorm) {
-            const float inv = 1.0f / (lanes_sum<32>(se) + kRouteEps);
-            const float mean = lanes_sum<32>(e >= 0 ? g * (se * inv) : 0.0f);
-            ds = e >= 0 ? rule.scale * (g - mean) * inv : 0.0f;
+            // a division, not a product with 1 / total: the share of a single choice
+            // is 1 to the last bit, and its gradient zero
+            const float total = lanes_sum<32>(se) + kRouteEps;
+            const float mean = lanes_sum<32>(e >= 0 ? g * (se / total) : 0.0f);
+            ds = e >= 0 ? rule.scale * (g - mean) / total : 0.0f;
         }
         // every expert's entry as if it were not chosen, then the chosen ones over them
         float mean = 0.0f, mine;
@@ -529,7 +531,7 @@ route_scored_bwd_kernel(const float *__restrict__ L, const int32_t *__restrict__
 }
 
 // The chosen experts' entries alone, for a layer's backward: with w saved by
-// the forward, dl_k = w_k (dw_k - sum_j dw_j w_j / scale [renorm]), times
+// the forward, dl_k = w_k (dw_k - sum_j dw_j (w_j / scale) [renorm]), times
 // 1 - s_k for sigmoid scores.  Softmax scores only with renorm: there the
 // entries of the experts that were not chosen are zero (up to the 1e-20).
 __global__ void __launch_bounds__(256)
@@ -540,11 +542,11 @@ route_scored_bwd_rows_kernel(const float *__restrict__ L, const int32_t *__restr
     const int t = blockIdx.x * blockDim.x + threadIdx.x;
     if (t >= T) return;
     float mean = 0.0f;
-    if (rule.renorm && rule.scale != 0.0f) {
-        for (int k = 0; k < K; ++k)
-            mean = __fmaf_rn(topk_w[static_cast<size_t>(t) * K + k], dw[static_cast<size_t>(t) * K + k], mean);
-        mean /= rule.scale;
-    }
+    if (rule.renorm && rule.scale != 0.0f)
+        for (int k = 0; k < K; ++k) {
+            const size_t i = static_cast<size_t>(t) * K + k;
+            mean = __fmaf_rn(topk_w[i] / rule.scale, dw[i], mean);  // the share of a single choice is 1 to the last bit
+        }
     for (int k = 0; k < K; ++k) {
         const size_t i = static_cast<size_t>(t) * K + k;
         const int e = topk_idx[i];

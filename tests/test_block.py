@@ -69,6 +69,17 @@ def test_layer_routed_by_scores(s, rule, bias):
     assert np.all(np.abs(to_np(g["dWr"]) - xs.astype(np.float64).T @ dL) <= 2.0 ** -5 * S + 1e-6 * S.max())
 
 
+def test_layer_with_one_renormalised_choice():
+    """K = 1 with renorm: the router gets no gradient, and dx only that of the expert."""
+    s = Shape(T=200, d=128, E=8, K=1, f=64)
+    w, layer, _ = _layer(s, moe.RouteRule("sigmoid", 2, 1, 2, True, 1.7), True)
+    x = make_tokens(s, seed=1, device="cpu").cuda()
+    y = layer(x, save_preact=True)
+    assert bool((layer.views(s.T)["topk_w"] == 1.7).all())
+    g = layer.backward(x, y)
+    assert not bool(g["dWr"].any()) and not bool(g["dbias"].any()) and bool(g["dx"].any())
+
+
 def test_raw_softmax_layer_has_no_backward():
     s = Shape(T=64, d=128, E=8, K=2, f=64)
     _, layer, _ = _layer(s, moe.RouteRule("softmax", renorm=False), False)

@@ -31,6 +31,9 @@ CASES = [
     (17, 48, 5, "softmax", 4, 3, 2, True, 1.0, True),
     (15, 31, 16, "sigmoid", 1, 1, 1, False, 1.0, False),
     (64, 256, 8, "sigmoid", 8, 4, 2, True, 2.5, True),
+    (200, 192, 7, "softmax", 6, 3, 1, True, 1.0, True),      # runs of 32, one or two of their experts
+    (77, 192, 7, "sigmoid", 6, 2, 2, False, 1.0, False),
+    (90, 128, 4, "sigmoid", 4, 1, 2, True, 1.0, True),
     (65, 256, 8, "softmax", 8, 3, 1, False, 16.0, False),
     (1000, 256, 8, "sigmoid", 8, 4, 2, True, 2.5, True),
     (4097, 64, 6, "softmax", 1, 1, 1, False, 1.0, True),
@@ -106,6 +109,16 @@ def test_backward(c):
     assert np.all(np.abs(to_np(out) - ref) <= (64 + 8 * D) * ULP * mag)
 
 
+def test_one_renormalised_choice_has_no_gradient():
+    """K = 1 with renorm: the weight is scale whatever the logits, so every entry is zero, not nearly zero."""
+    L, dw = torch.randn(300, 64).cuda(), torch.randn(300, 1).cuda()
+    for score in ("sigmoid", "softmax"):
+        rule = moe.RouteRule(score, 4, 2, 2, True, 2.5)
+        r = moe.route_scored(L, 1, rule)
+        assert bool((r.topk_w == 2.5).all())
+        assert not bool(moe.route_scored_backward(L, r.topk_idx, dw, rule).any())
+
+
 def test_ties_and_signed_zeros():
     for score in ("sigmoid", "softmax"):
         for L in (torch.zeros(70, 256), -torch.zeros(70, 256)):
@@ -113,6 +126,14 @@ def test_ties_and_signed_zeros():
             r = moe.route_scored(L.cuda(), 8, moe.RouteRule(score, 8, 4, 2))
             assert to_np(r.topk_idx).tolist() == [list(range(8))] * 70
             assert np.allclose(to_np(r.topk_w), 0.125, rtol=1e-6)
+    # runs of 32 of equal experts; one run ahead by one expert, one by two equal ones
+    L = torch.zeros(5, 256)
+    L[:, 96] = 1.0
+    L[:, [160, 191]] = 0.75
+    r = moe.route_scored(L.cuda(), 6, moe.RouteRule("sigmoid", 8, 2, 2))
+    assert to_np(r.topk_idx).tolist() == [[96, 160, 191, 97, 98, 99]] * 5
+    r = moe.route_scored(L.cuda(), 4, moe.RouteRule("sigmoid", 8, 3, 1))
+    assert to_np(r.topk_idx).tolist() == [[96, 160, 191, 0]] * 5
     # equal runs: the lower ones stay open; equal experts inside: the lower ones
     L = torch.zeros(3, 64)
     L[:, 32:] = 1.0
@@ -166,6 +187,21 @@ def test_extreme_logits():
     assert np.all(np.abs(to_np(r.topk_w)[0] - [1.0, 0.0]) <= 1e-30)
     d = moe.route_scored_backward(L.cuda(), r.topk_idx, torch.ones(3, 2).cuda(), moe.RouteRule())
     assert np.all(np.isfinite(to_np(d)))
+
+
+def test_masked_logits():
+    """A logit of -inf is a score of zero; the others are as if it were not there."""
+    g = torch.Generator().manual_seed(1)
+    L = torch.randn(70, 64, generator=g)
+    M = L.clone()
+    M[:, 40:] = -float("inf")
+    for score in ("sigmoid", "softmax"):
+        rule = moe.RouteRule(score, renorm=False)
+        a = moe.route_scored(M.cuda(), 5, rule)
+        b = moe.route_scored(L[:, :40].contiguous().cuda(), 5, rule)
+        assert torch.equal(a.topk_idx, b.topk_idx) and torch.equal(a.topk_w, b.topk_w)
+        d = moe.route_scored_backward(M.cuda(), a.topk_idx, torch.ones(70, 5).cuda(), rule)
+        assert bool(torch.isfinite(d).all()) and not bool(d[:, 40:].any())
 
 
 def test_buffers_streams_and_bits():
