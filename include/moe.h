@@ -161,7 +161,9 @@ moe_status_t moe_route_static(const float *logits, int T, int E, int K,
  * The other outputs and determinism are moe_route's; `workspace` (16-byte
  * aligned) holds moe_route_scored_workspace_size(T, E, K) bytes.  A
  * sel_bias of -INFINITY closes an expert (it is chosen only where the open
- * runs hold fewer than K others, the lowest indexes first).  NaN logits are
+ * runs hold fewer than K others, the lowest indexes first).  A logit of
+ * -INFINITY is a score of 0 (softmax needs a finite one in the row).  NaN
+ * logits are
  * outside the contract; the choice is then some K distinct experts.  Needs
  * E % n_group == 0 and K <= topk_group * (E / n_group).  One kernel launch up to 16 tokens, else two,
  * or three where the tokens and experts are many. */
@@ -232,7 +234,8 @@ moe_status_t moe_norm_residual_backward(const void *r_out, int residual_fp32, co
  * (>= 0) contiguous elements, fp32 or bf16 by kinds[i], aligned to their type
  * only; the four arrays themselves are HOST memory, read before the call
  * returns.  outs NULL clips in place.  Squares are summed in fp32 per CTA, the
- * CTAs' sums in fp64, in a fixed order: deterministic.  An infinite norm
+ * CTAs' sums in fp64, in a fixed order: deterministic (entries beyond 1.8e19
+ * give an infinite norm).  An infinite norm
  * scales by 0 and a NaN by NaN, as the formula does.  max_norm > 0 (INFINITY
  * allowed).  `workspace` (4-byte aligned) holds
  * moe_grad_norm_workspace_size(n_tensors) bytes.  Two launches for every 512
