@@ -24,6 +24,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 namespace moe {
 namespace nr {
@@ -288,8 +289,13 @@ norm_residual_kernel(Args a, float inv_d, const R *r, R *r_out, uint16_t *__rest
 // g times which is sum(k y), and rp times which is the token gate's gradient.
 // Each thread keeps its columns' two sums over the rows (of dn z, and of
 // g y rp D, from which both dgp and a channel gate's dg follow).
-// FULL: y, dr' and gamma_pre are all there (fewer branches in the inner loops).
-template <typename R, int VPT, bool FULL>
+// Y, PRE, DR: whether there is a y, a gamma_pre and a dr' (y or gamma_pre is,
+// dn or dr' is).  A kernel of its own for each form has no branches in the inner
+// loops, and a ring of the arrays that it reads only.  8192 x 4096 bf16 with one
+// kernel for all that lack one: 66.3 us without y, 57.3 without gamma_pre; with
+// their own 48.9 and 51.3.  A higher share of the SM's threads for these lighter
+// forms was slower: 768 of 80 registers 53.1 and 56.5, 1024 of 64 55.2 and 58.0.
+template <typename R, int VPT, bool Y, bool PRE, bool DR>
 __global__ void __launch_bounds__(MAX_THREADS)
 norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const R *dr_out,
                          const uint16_t *__restrict__ dn, const float *__restrict__ rstd_post,
@@ -300,15 +306,16 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
     __shared__ uint64_t landed[MAX_THREADS / 32][BWD_STAGES];
     __shared__ uint64_t posted;  // a phase per row, an arrival per warp
     __shared__ int abort;
-    constexpr bool PIPE = pipelined<R>(VPT, FULL);
+    constexpr bool PIPE = pipelined<R>(VPT, Y && PRE);
     const int stages = a.stages;
     constexpr bool HOLD = VPT <= 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const bool has_y = FULL || a.y, has_dr = FULL || dr_out, pre = FULL || a.gamma_pre, post = a.gamma_post != nullptr;
+    constexpr bool has_y = Y, pre = PRE;
+    const bool post = a.gamma_post != nullptr;
     const Owned<VPT> own(warp, lane, a.d / 8);
     // a warp's part of a row in the ring: its columns of y, dn, r' and dr'
-    constexpr int B = VPT * piece_bytes<uint16_t>(), AT_DN = B, AT_X = 2 * B, AT_DR = AT_X + VPT * piece_bytes<R>();
-    constexpr int PART = AT_DR + VPT * piece_bytes<R>();
+    constexpr int B = VPT * piece_bytes<uint16_t>(), AT_DN = Y ? B : 0, AT_X = AT_DN + (PRE ? B : 0);
+    constexpr int AT_DR = AT_X + (PRE ? VPT * piece_bytes<R>() : 0), PART = AT_DR + VPT * piece_bytes<R>();
     const int stage = warps * PART;
     uint8_t *const mine = ring + warp * PART;
     float2 c[VPT][4], w[VPT][4], accq[VPT][4], accp[VPT][4];
@@ -333,9 +340,9 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
             const int64_t from = t * a.d + own.first;
             const uint32_t nb = own.cols * 2, nr = own.cols * static_cast<int>(sizeof(R));
             uint64_t *full = rows.full;
-            mbar_arrive_expect_tx(&full[slot], (has_y ? nb : 0) + (has_dr ? nr : 0) + (pre ? nb + nr : 0));
+            mbar_arrive_expect_tx(&full[slot], (has_y ? nb : 0) + (DR ? nr : 0) + (pre ? nb + nr : 0));
             if (has_y) bulk_load(to, a.y + from, nb, &full[slot]);
-            if (has_dr) bulk_load(to + AT_DR, dr_out + from, nr, &full[slot]);
+            if (DR) bulk_load(to + AT_DR, dr_out + from, nr, &full[slot]);
             if (pre) {
                 bulk_load(to + AT_DN, dn + from, nb, &full[slot]);
                 bulk_load(to + AT_X, r_out + from, nr, &full[slot]);
@@ -370,7 +377,7 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
                 read8<uint16_t>(at16 + j * 512, cy);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) cy[i] = mul2(cy[i], c[j][i]);
-                if (has_dr) {
+                if (DR) {
                     float2 g[4];
                     read8<R>(at_r + j * piece_bytes<R>() + AT_DR, g);
 #pragma unroll
@@ -456,7 +463,7 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
             for (int i = 0; i < 4; ++i) D[i] = both(0.0f);
             if (own.on[j]) {
                 if (!HOLD) weights(a, col, true, c[j], w[j]);
-                if (has_dr) read8<R>(at_r + j * piece_bytes<R>() + AT_DR, D);
+                if (DR) read8<R>(at_r + j * piece_bytes<R>() + AT_DR, D);
                 if (pre) {
                     float2 x[4], g[4];
                     read8<R>(at_r + j * piece_bytes<R>() + AT_X, x);
@@ -475,14 +482,15 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = mul2(both(a.res_scale), D[i]);  // res_scale is 1 without y
             store(to_r, col, o, a.wide);
-            if (!has_y) continue;
+            if constexpr (has_y) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                D[i] = mul2(D[i], q);
-                accp[j][i] = fma2(y[i], D[i], accp[j][i]);
-                o[i] = fma2(my, y[i], mul2(D[i], c[j][i]));
+                for (int i = 0; i < 4; ++i) {
+                    D[i] = mul2(D[i], q);
+                    accp[j][i] = fma2(y[i], D[i], accp[j][i]);
+                    o[i] = fma2(my, y[i], mul2(D[i], c[j][i]));
+                }
+                store(to_y, col, o, true);
             }
-            store(to_y, col, o, true);
         }
         slot = ahead;
         f = next;
@@ -558,8 +566,8 @@ Shape fwd_shape(int T, int d) {
     return shape(T, d, FWD_STAGES, piece_bytes<uint16_t>() + piece_bytes<R>());
 }
 template <typename R>
-Shape bwd_shape(int T, int d) {
-    return shape(T, d, BWD_STAGES, 2 * piece_bytes<uint16_t>() + 2 * piece_bytes<R>());
+Shape bwd_shape(int T, int d, bool y, bool pre) {
+    return shape(T, d, BWD_STAGES, (y + pre) * piece_bytes<uint16_t>() + (1 + pre) * piece_bytes<R>());
 }
 
 // Raises the kernel's limit of dynamic shared memory, once per device.
@@ -585,14 +593,14 @@ cudaError_t forward(const Shape &s, const NormResidualArgs &a, const void *r, vo
     return cudaGetLastError();
 }
 
-template <typename R, int VPT, bool FULL>
+template <typename R, int VPT, bool Y, bool PRE, bool DR>
 cudaError_t backward(const Shape &s, const NormResidualArgs &a, const NormResidualGradArgs &g, float *part,
                      cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_ring(norm_residual_bwd_kernel<R, VPT, FULL>, done);
+    const cudaError_t e = allow_ring(norm_residual_bwd_kernel<R, VPT, Y, PRE, DR>, done);
     if (e != cudaSuccess) return e;
     const Args args{a, s.stages, reinterpret_cast<uintptr_t>(g.dr) % 32 == 0};
-    norm_residual_bwd_kernel<R, VPT, FULL><<<s.ctas, s.threads, s.smem, stream>>>(
+    norm_residual_bwd_kernel<R, VPT, Y, PRE, DR><<<s.ctas, s.threads, s.smem, stream>>>(
         args, 1.0f / a.d, static_cast<const R *>(g.r_out), static_cast<const R *>(g.dr_out), g.dn, g.rstd_post,
         g.rstd_pre, static_cast<R *>(g.dr), g.dy, g.dgate, part);
     return cudaGetLastError();
@@ -613,7 +621,7 @@ cudaError_t launch_norm_residual(const NormResidualArgs &a, const void *r, void 
 }
 
 size_t norm_residual_bwd_part_bytes(int T, int d) {
-    return static_cast<size_t>(nr::bwd_shape<float>(T, d).ctas) * 2 * d * 4;
+    return static_cast<size_t>(nr::bwd_shape<float>(T, d, true, true).ctas) * 2 * d * 4;
 }
 
 cudaError_t launch_norm_residual_bwd(const NormResidualArgs &a, const NormResidualGradArgs &g, float *part,
@@ -621,16 +629,19 @@ cudaError_t launch_norm_residual_bwd(const NormResidualArgs &a, const NormResidu
     int ctas = 0;
     auto go = [&](auto type) {
         using R = decltype(type);
-        const nr::Shape s = nr::bwd_shape<R>(a.T, a.d);
+        const nr::Shape s = nr::bwd_shape<R>(a.T, a.d, a.y, a.gamma_pre);
         ctas = s.ctas;
-        if (a.y && g.dr_out && a.gamma_pre) {
-            if (s.vpt == 1) return nr::backward<R, 1, true>(s, a, g, part, stream);
-            return s.vpt == 2 ? nr::backward<R, 2, true>(s, a, g, part, stream)
-                              : nr::backward<R, 4, true>(s, a, g, part, stream);
-        }
-        if (s.vpt == 1) return nr::backward<R, 1, false>(s, a, g, part, stream);
-        return s.vpt == 2 ? nr::backward<R, 2, false>(s, a, g, part, stream)
-                          : nr::backward<R, 4, false>(s, a, g, part, stream);
+        auto form = [&](auto y, auto pre, auto dr) {
+            constexpr bool Y = decltype(y)::value, PRE = decltype(pre)::value, DR = decltype(dr)::value;
+            if (s.vpt == 1) return nr::backward<R, 1, Y, PRE, DR>(s, a, g, part, stream);
+            return s.vpt == 2 ? nr::backward<R, 2, Y, PRE, DR>(s, a, g, part, stream)
+                              : nr::backward<R, 4, Y, PRE, DR>(s, a, g, part, stream);
+        };
+        constexpr std::true_type with{};
+        constexpr std::false_type without{};
+        if (!a.gamma_pre) return form(with, without, with);  // dr_out is what it has instead of dn
+        if (!a.y) return g.dr_out ? form(without, with, with) : form(without, with, without);
+        return g.dr_out ? form(with, with, with) : form(with, with, without);
     };
     *launches = 1;
     const cudaError_t err = a.res_f32 ? go(float{}) : go(uint16_t{});
