@@ -43,9 +43,19 @@ constexpr int BWD_STAGES = 4;
 template <typename R>
 __host__ __device__ constexpr bool pipelined(int vpt, bool full) { return full && vpt == 2 && sizeof(R) == 2; }
 
+// How the rows of a backward share an SM: one at a time, two CTAs of a row each,
+// or a CTA whose teams of warps take a row each.  Teams leave one row of partial
+// sums per SM instead of one per row in flight (us, bf16: 65536 x 256 50.4 with a
+// CTA per row, 43.8 with teams; 16384 x 640 43.4 and 40.0; 2048 x 1024 19.2 and
+// 14.2; 8192 x 4096 72.0 and 70.5).  For two rows whose kernel does not read
+// ahead, CTAs of their own, which need not keep in step, are faster (8192 x 4096
+// fp32: 98.5, 112.6 with teams).
+enum Split { ALONE, PAIR, TEAM };
+
 // With what the launch adds to the caller's arguments.
 struct Args : NormResidualArgs {
-    int stages;  // rows in the ring
+    int stages;  // rows in a team's ring
+    int teams;   // of a backward's CTA
     bool wide;   // the fp32 rows that are written begin on 32-byte boundaries
 };
 
@@ -135,9 +145,8 @@ __device__ __forceinline__ void post_sums4(const float (&v)[4], float4 *red) {
     for (int o = 4; o; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
     if ((lane & 7) == 0) reinterpret_cast<float *>(red + (threadIdx.x >> 5))[lane >> 3] = s;
 }
-__device__ __forceinline__ float4 collect_sums4(const float4 *red) {
+__device__ __forceinline__ float4 collect_sums4(const float4 *red, int warps) {
     float2 a = both(0.0f), b = a;
-    const int warps = blockDim.x >> 5;
 #pragma unroll 4
     for (int w = 0; w < warps; ++w) {
         const float4 s = red[w];
@@ -145,6 +154,15 @@ __device__ __forceinline__ float4 collect_sums4(const float4 *red) {
         b = add2(b, make_float2(s.z, s.w));
     }
     return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// Between the warps of one of a CTA's teams (of at most 8, where they have two warps or more).  Not on
+// barrier 0: that is __syncthreads' own, where teams without further rows already wait for the others.
+__device__ __forceinline__ void team_sync(int team, int warps) {
+    if (warps == 1)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(32 * warps) : "memory");
 }
 
 // Weights of the eight columns from `col` (where the row has them): c of y
@@ -281,8 +299,8 @@ norm_residual_kernel(Args a, float inv_d, const R *r, R *r_out, uint16_t *__rest
 // after the sums, and the slot refilled after the second time.
 // PIPE: the first reading of row r + 1 stands between the sums of row r and
 // their use, so that no warp waits for the others' sums (8192 x 4096 bf16:
-// 77.2 us, 72.3 with it).  It needs a third row in the ring, which fp32 rows do
-// not leave room for.
+// 77.2 us, 72.3 with it, both with a CTA per row).  It needs a third row in the
+// ring, which fp32 rows do not leave room for.
 // One reduction gives both means of a row: with z = r' rq, m1 = rq mean(h z)
 // and c the weight of y without a token gate g,
 //   D = dr' + rq h - m1 z,   sum(c y D) = sum(c y dr') + rq sum(c y h) - m1 sum(c y z),
@@ -294,8 +312,8 @@ norm_residual_kernel(Args a, float inv_d, const R *r, R *r_out, uint16_t *__rest
 // loops, and a ring of the arrays that it reads only.  8192 x 4096 bf16 with one
 // kernel for all that lack one: 66.3 us without y, 57.3 without gamma_pre; with
 // their own 48.9 and 51.3.  A higher share of the SM's threads for these lighter
-// forms was slower: 768 of 80 registers 53.1 and 56.5, 1024 of 64 55.2 and 58.0.
-template <typename R, int VPT, bool Y, bool PRE, bool DR>
+// forms was slower (us): 768 of 80 registers 53.1 and 56.5, 1024 of 64 55.2 and 58.0.
+template <typename R, int VPT, bool Y, bool PRE, bool DR, Split SPLIT>
 __global__ void __launch_bounds__(MAX_THREADS)
 norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const R *dr_out,
                          const uint16_t *__restrict__ dn, const float *__restrict__ rstd_post,
@@ -304,12 +322,17 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float4 red[2][MAX_THREADS / 32];
     __shared__ uint64_t landed[MAX_THREADS / 32][BWD_STAGES];
-    __shared__ uint64_t posted;  // a phase per row, an arrival per warp
+    __shared__ uint64_t posted[MAX_THREADS / 32];  // of a team: a phase per row, an arrival per warp
     __shared__ int abort;
-    constexpr bool PIPE = pipelined<R>(VPT, Y && PRE);
+    constexpr bool PIPE = pipelined<R>(VPT, Y && PRE), TEAMS = SPLIT == TEAM;
+    // Whether the warps wait for the row's sums by an mbarrier, which lets the first ones through go on
+    // (4093 x 7168 fp32: 90.0 us, 95.3 with __syncthreads; 2048 x 16384, VPT 4: 214 and 186).
+    constexpr bool POSTS = PIPE || (SPLIT == ALONE && VPT == 2);
     const int stages = a.stages;
     constexpr bool HOLD = VPT <= 2;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int teams = TEAMS ? a.teams : 1;
+    const int lane = threadIdx.x & 31, all = blockDim.x >> 5, warps = all / teams;
+    const int team = TEAMS ? (threadIdx.x >> 5) / warps : 0, warp = TEAMS ? (threadIdx.x >> 5) % warps : threadIdx.x >> 5;
     constexpr bool has_y = Y, pre = PRE;
     const bool post = a.gamma_post != nullptr;
     const Owned<VPT> own(warp, lane, a.d / 8);
@@ -317,7 +340,7 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
     constexpr int B = VPT * piece_bytes<uint16_t>(), AT_DN = Y ? B : 0, AT_X = AT_DN + (PRE ? B : 0);
     constexpr int AT_DR = AT_X + (PRE ? VPT * piece_bytes<R>() : 0), PART = AT_DR + VPT * piece_bytes<R>();
     const int stage = warps * PART;
-    uint8_t *const mine = ring + warp * PART;
+    uint8_t *const mine = ring + team * stages * stage + warp * PART;
     float2 c[VPT][4], w[VPT][4], accq[VPT][4], accp[VPT][4];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -326,18 +349,19 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
         for (int i = 0; i < 4; ++i) accq[j][i] = accp[j][i] = both(0.0f);
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < warps; ++i)
+        for (int i = 0; i < all; ++i)
             for (int q = 0; q < BWD_STAGES; ++q) mbar_init(&landed[i][q], 1);
-        mbar_init(&posted, warps);
+        for (int i = 0; i < teams; ++i) mbar_init(&posted[i], warps);
         abort = 0;
         fence_mbar_init();
     }
     __syncthreads();
-    const Ring rows{landed[warp], &abort, a.status, a.wait_ns, own.cols > 0};
-    auto issue = [&](int64_t t, int slot) {
-        if (lane == 0 && t < a.T && own.cols > 0) {
+    const Ring rows{landed[threadIdx.x >> 5], &abort, a.status, a.wait_ns, own.cols > 0};
+    const uint32_t rows_end = a.T;  // a row number a few rows past it still fits
+    auto issue = [&](uint32_t t, int slot) {
+        if (lane == 0 && t < rows_end && own.cols > 0) {
             uint8_t *to = mine + slot * stage;
-            const int64_t from = t * a.d + own.first;
+            const int64_t from = static_cast<int64_t>(t) * a.d + own.first;
             const uint32_t nb = own.cols * 2, nr = own.cols * static_cast<int>(sizeof(R));
             uint64_t *full = rows.full;
             mbar_arrive_expect_tx(&full[slot], (has_y ? nb : 0) + (DR ? nr : 0) + (pre ? nb + nr : 0));
@@ -352,17 +376,17 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
     struct Row {  // the row's factors, loaded a row ahead
         float rp, rq, gt;
     };
-    auto factors = [&](int64_t t) {
+    auto factors = [&](uint32_t t) {
         Row f{1.0f, 0.0f, 1.0f};
-        if (t < a.T) {
+        if (t < rows_end) {
             if (post) f.rp = rstd_post[t];
             if (pre) f.rq = rstd_pre[t];
             if (a.gate && a.gate_per_token) f.gt = a.gate[t];
         }
         return f;
     };
-    const int64_t step = gridDim.x;
-    for (int s = 0; s < stages; ++s) issue(blockIdx.x + s * step, s);
+    const uint32_t begin = blockIdx.x + team * gridDim.x, step = gridDim.x * teams;
+    for (int s = 0; s < stages; ++s) issue(begin + s * step, s);
     // The first reading of the row in slot `slot`: the four sums (of h z,
     // c y dr', c y h, c y z) of the warp go to `sums`.
     auto first_pass = [&](int slot, float rq, float4 *sums) {
@@ -406,37 +430,37 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
         }
         const float s[4] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y, s3.x + s3.y};
         post_sums4(s, sums);
-        if (PIPE) {
+        if (POSTS) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(&posted);
+            if (lane == 0) mbar_arrive(&posted[team]);
         }
     };
-    // Until every warp has posted its sums of the row (the waits alternate in parity).
+    // Until every warp of the team has posted its sums of the row (the waits alternate in parity).
     int parity = 0;
     auto collect = [&](const float4 *sums) {
-        if (PIPE) {
-            mbar_wait(&posted, parity, &abort, a.status, a.wait_ns);
+        if (POSTS) {
+            mbar_wait(&posted[team], parity, &abort, a.status, a.wait_ns);
             parity ^= 1;
         } else {
-            __syncthreads();
+            TEAMS ? team_sync(team, warps) : __syncthreads();
         }
-        return collect_sums4(sums);
+        return collect_sums4(sums + team * warps, warps);
     };
-    Row f = factors(blockIdx.x), next = factors(blockIdx.x + step);
+    Row f = factors(begin), next = factors(begin + step);
     int slot = 0, turn = 0;
     int phase = 0;  // of the slot that first_pass reads next
-    if (PIPE) {
+    if (PIPE && begin < rows_end) {
         rows.wait(0, 0);
         first_pass(0, f.rq, red[0]);
     }
-    for (int64_t t = blockIdx.x; t < a.T; t += step) {
+    for (uint32_t t = begin; t < rows_end; t += step) {
         const Row after = factors(t + 2 * step);
         const int ahead = slot + 1 == stages ? 0 : slot + 1;
         float4 s;
         if (PIPE) {
             s = collect(red[turn]);
             if (ahead == 0) phase ^= 1;
-            if (t + step < a.T) {
+            if (t + step < rows_end) {
                 rows.wait(ahead, phase);
                 first_pass(ahead, next.rq, red[turn ^ 1]);
             }
@@ -451,10 +475,10 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
         const float m1 = f.rq * s.x * inv_d;
         const float cyD = s.y + f.rq * s.z - m1 * s.w;
         const float m2 = post ? f.gt * cyD * inv_d * f.rp * f.rp * f.rp : 0.0f;
-        if (a.gate && a.gate_per_token && threadIdx.x == 0) dgate[t] = f.rp * cyD;
+        if (a.gate && a.gate_per_token && warp == 0 && lane == 0) dgate[t] = f.rp * cyD;
         const float2 q = both(f.gt * f.rp), mz = both(-m1 * f.rq), my = both(-m2), rq = both(f.rq);
-        R *to_r = dr + t * a.d;
-        uint16_t *to_y = dy + t * a.d;
+        R *to_r = dr + static_cast<int64_t>(t) * a.d;
+        uint16_t *to_y = dy + static_cast<int64_t>(t) * a.d;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const uint32_t col = own.col + 256 * j;
@@ -496,18 +520,31 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
         f = next;
         next = after;
     }
-    float *sums = part + static_cast<size_t>(blockIdx.x) * 2 * a.d;
+    // the CTA's sums: the teams' ones in the rings, now empty, added in the teams' order
+    float *out = part + static_cast<size_t>(blockIdx.x) * 2 * a.d, *held = reinterpret_cast<float *>(ring);
+    float *sums = teams > 1 ? held + team * 2 * a.d : out;
+    if (teams > 1) __syncthreads();
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         if (!own.on[j]) break;
         store8(sums + own.col + 256 * j, 0, &accq[j][0].x);
         store8(sums + a.d + own.col + 256 * j, 0, &accp[j][0].x);
     }
+    if (teams == 1) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.d / 2; i += blockDim.x) {
+        float4 v = reinterpret_cast<const float4 *>(held)[i];
+        for (int k = 1; k < teams; ++k) {
+            const float4 u = reinterpret_cast<const float4 *>(held + k * 2 * a.d)[i];
+            v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+        }
+        reinterpret_cast<float4 *>(out)[i] = v;
+    }
 }
 
 // The CTAs' partial sums: 32 columns per block, each in 32 runs of CTAs in
-// their order, then the runs in theirs (runs of 5 to 10 for the usual 152 or
-// 304 CTAs: every load of a thread in flight at once).
+// their order, then the runs in theirs (runs of 5 or 10 for 152 or 304 CTAs:
+// every load of a thread in flight at once).
 constexpr int RUNS = 32;
 __global__ void __launch_bounds__(32 * RUNS)
 norm_residual_bwd_columns_kernel(NormResidualArgs a, const float *__restrict__ part, int ctas,
@@ -543,7 +580,8 @@ norm_residual_bwd_columns_kernel(NormResidualArgs a, const float *__restrict__ p
 
 // Threads of a CTA, its vectors per thread, the CTAs and the ring.
 struct Shape {
-    int vpt, threads, ctas, stages;
+    int vpt, threads, ctas, stages, teams = 1;
+    Split split = ALONE;
     size_t smem;
 };
 // `piece`: bytes of one piece of all the arrays that a row is read from.
@@ -565,9 +603,18 @@ template <typename R>
 Shape fwd_shape(int T, int d) {
     return shape(T, d, FWD_STAGES, piece_bytes<uint16_t>() + piece_bytes<R>());
 }
+// Teams are as many as rows spread over all SMs allow; the ring also holds their partial sums in the end.
 template <typename R>
 Shape bwd_shape(int T, int d, bool y, bool pre) {
-    return shape(T, d, BWD_STAGES, (y + pre) * piece_bytes<uint16_t>() + (1 + pre) * piece_bytes<R>());
+    Shape s = shape(T, d, BWD_STAGES, (y + pre) * piece_bytes<uint16_t>() + (1 + pre) * piece_bytes<R>());
+    const int per_sm = std::min(16, MAX_THREADS / s.threads);
+    s.split = per_sm == 1 ? ALONE : per_sm == 2 && !pipelined<R>(s.vpt, y && pre) ? PAIR : TEAM;
+    if (s.split != TEAM) return s;
+    s.teams = std::min(per_sm, (T + SMS - 1) / SMS);
+    s.ctas = std::min(T, SMS);
+    s.threads *= s.teams;
+    s.smem = std::max(s.smem * s.teams, static_cast<size_t>(s.teams > 1 ? s.teams * 2 * d * 4 : 0));
+    return s;
 }
 
 // Raises the kernel's limit of dynamic shared memory, once per device.
@@ -587,20 +634,20 @@ cudaError_t forward(const Shape &s, const NormResidualArgs &a, const void *r, vo
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_ring(norm_residual_kernel<R, VPT>, done);
     if (e != cudaSuccess) return e;
-    const Args args{a, s.stages, reinterpret_cast<uintptr_t>(r_out) % 32 == 0};
+    const Args args{a, s.stages, s.teams, reinterpret_cast<uintptr_t>(r_out) % 32 == 0};
     norm_residual_kernel<R, VPT><<<s.ctas, s.threads, s.smem, stream>>>(
         args, 1.0f / a.d, static_cast<const R *>(r), static_cast<R *>(r_out), n, rstd_post, rstd_pre);
     return cudaGetLastError();
 }
 
-template <typename R, int VPT, bool Y, bool PRE, bool DR>
+template <typename R, int VPT, bool Y, bool PRE, bool DR, Split SPLIT>
 cudaError_t backward(const Shape &s, const NormResidualArgs &a, const NormResidualGradArgs &g, float *part,
                      cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_ring(norm_residual_bwd_kernel<R, VPT, Y, PRE, DR>, done);
+    const cudaError_t e = allow_ring(norm_residual_bwd_kernel<R, VPT, Y, PRE, DR, SPLIT>, done);
     if (e != cudaSuccess) return e;
-    const Args args{a, s.stages, reinterpret_cast<uintptr_t>(g.dr) % 32 == 0};
-    norm_residual_bwd_kernel<R, VPT, Y, PRE, DR><<<s.ctas, s.threads, s.smem, stream>>>(
+    const Args args{a, s.stages, s.teams, reinterpret_cast<uintptr_t>(g.dr) % 32 == 0};
+    norm_residual_bwd_kernel<R, VPT, Y, PRE, DR, SPLIT><<<s.ctas, s.threads, s.smem, stream>>>(
         args, 1.0f / a.d, static_cast<const R *>(g.r_out), static_cast<const R *>(g.dr_out), g.dn, g.rstd_post,
         g.rstd_pre, static_cast<R *>(g.dr), g.dy, g.dgate, part);
     return cudaGetLastError();
@@ -621,7 +668,7 @@ cudaError_t launch_norm_residual(const NormResidualArgs &a, const void *r, void 
 }
 
 size_t norm_residual_bwd_part_bytes(int T, int d) {
-    return static_cast<size_t>(nr::bwd_shape<float>(T, d, true, true).ctas) * 2 * d * 4;
+    return static_cast<size_t>(nr::bwd_shape<float>(T, d, true, true).ctas) * 2 * d * 4;  // no form has more CTAs
 }
 
 cudaError_t launch_norm_residual_bwd(const NormResidualArgs &a, const NormResidualGradArgs &g, float *part,
@@ -633,9 +680,12 @@ cudaError_t launch_norm_residual_bwd(const NormResidualArgs &a, const NormResidu
         ctas = s.ctas;
         auto form = [&](auto y, auto pre, auto dr) {
             constexpr bool Y = decltype(y)::value, PRE = decltype(pre)::value, DR = decltype(dr)::value;
-            if (s.vpt == 1) return nr::backward<R, 1, Y, PRE, DR>(s, a, g, part, stream);
-            return s.vpt == 2 ? nr::backward<R, 2, Y, PRE, DR>(s, a, g, part, stream)
-                              : nr::backward<R, 4, Y, PRE, DR>(s, a, g, part, stream);
+            if (s.vpt == 1) return nr::backward<R, 1, Y, PRE, DR, nr::TEAM>(s, a, g, part, stream);
+            if (s.vpt == 4) return nr::backward<R, 4, Y, PRE, DR, nr::ALONE>(s, a, g, part, stream);
+            if (s.split == nr::TEAM) return nr::backward<R, 2, Y, PRE, DR, nr::TEAM>(s, a, g, part, stream);
+            if constexpr (!nr::pipelined<R>(2, Y && PRE))
+                if (s.split == nr::PAIR) return nr::backward<R, 2, Y, PRE, DR, nr::PAIR>(s, a, g, part, stream);
+            return nr::backward<R, 2, Y, PRE, DR, nr::ALONE>(s, a, g, part, stream);
         };
         constexpr std::true_type with{};
         constexpr std::false_type without{};

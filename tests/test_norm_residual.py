@@ -34,7 +34,10 @@ CASES = [(1, 7168, torch.float32, "both", "channel", 1.0), (1, 64, torch.bfloat1
          (20, 8256, torch.bfloat16, "both", "token", 1.0), (700, 320, torch.bfloat16, "both", "none", 1.0),
          (611, 7168, torch.float32, "both", "token", 1.0), (2, 12352, torch.float32, "pre", "none", 1.0),
          (1000, 2048, torch.bfloat16, "sum", "channel", 0.0), (45, 64, torch.float32, "post", "token", 1.0),
-         (1221, 512, torch.bfloat16, "both", "channel", 1.0), (3, 5120, torch.bfloat16, "add", "channel", 1.0)]
+         (1221, 512, torch.bfloat16, "both", "channel", 1.0), (3, 5120, torch.bfloat16, "add", "channel", 1.0),
+         (700, 2816, torch.float32, "both", "token", 1.0), (400, 4096, torch.float32, "pre", "none", 1.0),
+         (5000, 64, torch.bfloat16, "both", "channel", 1.0), (333, 1536, torch.float32, "both", "channel", 0.5),
+         (457, 5120, torch.bfloat16, "both", "token", 1.0), (2600, 256, torch.float32, "post", "token", 1.0)]
 
 
 def _case(c, seed=0):
