@@ -31,7 +31,9 @@ namespace nr {
 
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int SMS = 152;
-constexpr int MAX_THREADS = 512;       // of an SM, 128 registers each
+// Threads of an SM with 128 or 80 registers each.
+constexpr int MAX_THREADS = 512, MORE_THREADS = 768;
+constexpr int sm_threads(int regs) { return regs == 128 ? MAX_THREADS : MORE_THREADS; }
 constexpr int RING_BYTES = 208 * 1024; // the rings of an SM's CTAs
 // Rows in the ring.  More of them ahead made the forward slower (8192 x 4096
 // bf16, us: 46.5 with two rows, 50.4 with three, 52.5 with four); the backward,
@@ -186,15 +188,16 @@ __device__ __forceinline__ void weights(const NormResidualArgs &a, uint32_t col,
 // bulk copies of its own, so its rows come ahead of their use through a ring in
 // shared memory and wait for no other warp.  (With 16-byte copies by every lane
 // the backward of 8192 x 4096 took 78.3 us, 72.1 with bulk copies: the lanes'
-// requests, not the memory, were the limit.)  A row's slot is refilled as soon as the row is in registers, so
-// the ring's copies stay in flight through the row's sums and stores.
-template <typename R, int VPT>
-__global__ void __launch_bounds__(MAX_THREADS)
+// requests, not the memory, were the limit.)  A row's slot is refilled as soon as
+// the row is in registers, so the ring's copies stay in flight through the row's
+// sums and stores.
+template <typename R, int VPT, int REGS>
+__global__ void __launch_bounds__(sm_threads(REGS))
 norm_residual_kernel(Args a, float inv_d, const R *r, R *r_out, uint16_t *__restrict__ n,
                      float *__restrict__ rstd_post, float *__restrict__ rstd_pre) {
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float red[2][32];
-    __shared__ uint64_t landed[MAX_THREADS / 32][FWD_STAGES];
+    __shared__ uint64_t landed[MORE_THREADS / 32][FWD_STAGES];
     __shared__ int abort;
     const int stages = a.stages;
     constexpr bool HOLD = VPT <= 2;  // the weights stay in registers
@@ -312,16 +315,17 @@ norm_residual_kernel(Args a, float inv_d, const R *r, R *r_out, uint16_t *__rest
 // loops, and a ring of the arrays that it reads only.  8192 x 4096 bf16 with one
 // kernel for all that lack one: 66.3 us without y, 57.3 without gamma_pre; with
 // their own 48.9 and 51.3.  A higher share of the SM's threads for these lighter
-// forms was slower (us): 768 of 80 registers 53.1 and 56.5, 1024 of 64 55.2 and 58.0.
-template <typename R, int VPT, bool Y, bool PRE, bool DR, Split SPLIT>
-__global__ void __launch_bounds__(MAX_THREADS)
+// forms was slower up to 4096 columns (us): 768 of 80 registers 53.1 and 56.5, 1024
+// of 64 55.2 and 58.0.
+template <typename R, int VPT, bool Y, bool PRE, bool DR, Split SPLIT, int REGS>
+__global__ void __launch_bounds__(sm_threads(REGS))
 norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const R *dr_out,
                          const uint16_t *__restrict__ dn, const float *__restrict__ rstd_post,
                          const float *__restrict__ rstd_pre, R *dr, uint16_t *__restrict__ dy,
                          float *__restrict__ dgate, float *__restrict__ part) {
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float4 red[2][MAX_THREADS / 32];
-    __shared__ uint64_t landed[MAX_THREADS / 32][BWD_STAGES];
+    __shared__ float4 red[2][MORE_THREADS / 32];
+    __shared__ uint64_t landed[MORE_THREADS / 32][BWD_STAGES];
     __shared__ uint64_t posted[MAX_THREADS / 32];  // of a team: a phase per row, an arrival per warp
     __shared__ int abort;
     constexpr bool PIPE = pipelined<R>(VPT, Y && PRE), TEAMS = SPLIT == TEAM;
@@ -578,36 +582,49 @@ norm_residual_bwd_columns_kernel(NormResidualArgs a, const float *__restrict__ p
     if (channel) dgate[col] = a.gamma_post ? a.gamma_post[col] * v : v;
 }
 
-// Threads of a CTA, its vectors per thread, the CTAs and the ring.
+// Threads of a CTA, its vectors per thread and registers, the CTAs and the ring.
 struct Shape {
-    int vpt, threads, ctas, stages, teams = 1;
+    int vpt, regs, threads, ctas, stages, teams = 1;
     Split split = ALONE;
     size_t smem;
+    int per_sm() const { return sm_threads(regs) / threads; }
+    // `piece`: bytes of one piece of all the arrays that a row is read from.
+    Shape(int T, int d, int vpt_, int regs_, int most_stages, int piece) : vpt(vpt_), regs(regs_) {
+        threads = (d / 8 + 32 * vpt - 1) / (32 * vpt) * 32;
+        ctas = std::min(T, SMS * per_sm());
+        const int row = vpt * (threads / 32) * piece;
+        stages = std::max(1, std::min(most_stages, RING_BYTES / per_sm() / row));
+        smem = static_cast<size_t>(stages) * row;
+    }
 };
-// `piece`: bytes of one piece of all the arrays that a row is read from.
-Shape shape(int T, int d, int stages, int piece) {
-    Shape s;
-    // Two vectors per thread: the work of a warp per row is what bounds these
-    // kernels next to memory (one vector and twice the threads, us: forward of
-    // 8192 x 4096 bf16 56.5, 46.5 with two; backward 86.7 and 72.3).
-    s.vpt = d <= 256 ? 1 : d <= 16 * MAX_THREADS ? 2 : 4;
-    s.threads = (d / 8 + 32 * s.vpt - 1) / (32 * s.vpt) * 32;
-    const int per_sm = std::min(16, MAX_THREADS / s.threads);
-    s.ctas = std::min(T, SMS * per_sm);
-    const int row = s.vpt * (s.threads / 32) * piece;
-    s.stages = std::max(1, std::min(stages, RING_BYTES / per_sm / row));
-    s.smem = static_cast<size_t>(s.stages) * row;
-    return s;
-}
+// Rows that fit an SM with two vectors per thread.
+constexpr int sm_rows(int d, int regs) { return sm_threads(regs) / ((d / 8 + 63) / 64 * 32); }
+
+// Two vectors per thread: the work of a warp per row is what bounds these
+// kernels next to memory (one vector and twice the threads, us: forward of
+// 8192 x 4096 bf16 56.5, 46.5 with two; backward 86.7 and 72.3).  Fewer
+// registers where they give an SM another row of more than 4096 columns (us
+// bf16: 4096 x 5120 39.2 and 33.0, 2048 x 12288 61.0 and 39.3; narrower rows lose
+// by them, 8192 x 4096 46.2 and 48.4), or short rows more of them (16384 x 128
+// 12.5 and 10.6; fp32 rows of 1 KB and more lose, 65536 x 256 37.1 and 39.5).
 template <typename R>
 Shape fwd_shape(int T, int d) {
-    return shape(T, d, FWD_STAGES, piece_bytes<uint16_t>() + piece_bytes<R>());
+    const int piece = piece_bytes<uint16_t>() + piece_bytes<R>();
+    if (d <= 256) return Shape(T, d, 1, d * sizeof(R) <= 512 ? 80 : 128, FWD_STAGES, piece);
+    if (d > 4096 && sm_rows(d, 80) > sm_rows(d, 128)) return Shape(T, d, 2, 80, FWD_STAGES, piece);
+    return Shape(T, d, d <= 8192 ? 2 : 4, 128, FWD_STAGES, piece);
 }
-// Teams are as many as rows spread over all SMs allow; the ring also holds their partial sums in the end.
+// The same for a backward without y or gamma_pre (us, 2048 x 12288 without
+// gamma_pre: bf16 76.7 and 54.8, fp32 85.4 and 66.6; without y 4096 x 5120 bf16
+// 45.4 and 39.3, but fp32, whose ring gets too short, 51.8 and 53.9); one with
+// both needs its 128.  Teams are as many as rows spread over all SMs allow; the
+// ring also holds their partial sums in the end.
 template <typename R>
 Shape bwd_shape(int T, int d, bool y, bool pre) {
-    Shape s = shape(T, d, BWD_STAGES, (y + pre) * piece_bytes<uint16_t>() + (1 + pre) * piece_bytes<R>());
-    const int per_sm = std::min(16, MAX_THREADS / s.threads);
+    const int piece = (y + pre) * piece_bytes<uint16_t>() + (1 + pre) * piece_bytes<R>();
+    const bool fewer = !(y && pre) && d > (sizeof(R) == 2 ? 4096 : 8192) && sm_rows(d, 80) > sm_rows(d, 128);
+    Shape s(T, d, d <= 256 ? 1 : d <= 8192 || fewer ? 2 : 4, fewer ? 80 : 128, BWD_STAGES, piece);
+    const int per_sm = s.per_sm();
     s.split = per_sm == 1 ? ALONE : per_sm == 2 && !pipelined<R>(s.vpt, y && pre) ? PAIR : TEAM;
     if (s.split != TEAM) return s;
     s.teams = std::min(per_sm, (T + SMS - 1) / SMS);
@@ -628,26 +645,26 @@ cudaError_t allow_ring(Kernel kernel, std::atomic<uint64_t> &done) {
     return e;
 }
 
-template <typename R, int VPT>
+template <typename R, int VPT, int REGS>
 cudaError_t forward(const Shape &s, const NormResidualArgs &a, const void *r, void *r_out, uint16_t *n,
                     float *rstd_post, float *rstd_pre, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_ring(norm_residual_kernel<R, VPT>, done);
+    const cudaError_t e = allow_ring(norm_residual_kernel<R, VPT, REGS>, done);
     if (e != cudaSuccess) return e;
     const Args args{a, s.stages, s.teams, reinterpret_cast<uintptr_t>(r_out) % 32 == 0};
-    norm_residual_kernel<R, VPT><<<s.ctas, s.threads, s.smem, stream>>>(
+    norm_residual_kernel<R, VPT, REGS><<<s.ctas, s.threads, s.smem, stream>>>(
         args, 1.0f / a.d, static_cast<const R *>(r), static_cast<R *>(r_out), n, rstd_post, rstd_pre);
     return cudaGetLastError();
 }
 
-template <typename R, int VPT, bool Y, bool PRE, bool DR, Split SPLIT>
+template <typename R, int VPT, bool Y, bool PRE, bool DR, Split SPLIT, int REGS>
 cudaError_t backward(const Shape &s, const NormResidualArgs &a, const NormResidualGradArgs &g, float *part,
                      cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_ring(norm_residual_bwd_kernel<R, VPT, Y, PRE, DR, SPLIT>, done);
+    const cudaError_t e = allow_ring(norm_residual_bwd_kernel<R, VPT, Y, PRE, DR, SPLIT, REGS>, done);
     if (e != cudaSuccess) return e;
     const Args args{a, s.stages, s.teams, reinterpret_cast<uintptr_t>(g.dr) % 32 == 0};
-    norm_residual_bwd_kernel<R, VPT, Y, PRE, DR, SPLIT><<<s.ctas, s.threads, s.smem, stream>>>(
+    norm_residual_bwd_kernel<R, VPT, Y, PRE, DR, SPLIT, REGS><<<s.ctas, s.threads, s.smem, stream>>>(
         args, 1.0f / a.d, static_cast<const R *>(g.r_out), static_cast<const R *>(g.dr_out), g.dn, g.rstd_post,
         g.rstd_pre, static_cast<R *>(g.dr), g.dy, g.dgate, part);
     return cudaGetLastError();
@@ -660,15 +677,20 @@ cudaError_t launch_norm_residual(const NormResidualArgs &a, const void *r, void 
     auto go = [&](auto type) {
         using R = decltype(type);
         const nr::Shape s = nr::fwd_shape<R>(a.T, a.d);
-        if (s.vpt == 1) return nr::forward<R, 1>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
-        if (s.vpt == 2) return nr::forward<R, 2>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
-        return nr::forward<R, 4>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
+        if (s.vpt == 1) return nr::forward<R, 1, 80>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
+        if (s.regs == 80) return nr::forward<R, 2, 80>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
+        if (s.vpt == 2) return nr::forward<R, 2, 128>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
+        return nr::forward<R, 4, 128>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
     };
     return a.res_f32 ? go(float{}) : go(uint16_t{});
 }
 
 size_t norm_residual_bwd_part_bytes(int T, int d) {
-    return static_cast<size_t>(nr::bwd_shape<float>(T, d, true, true).ctas) * 2 * d * 4;  // no form has more CTAs
+    int ctas = 0;  // the most of any form
+    for (const bool y : {false, true})
+        for (const bool pre : {!y, true})
+            ctas = std::max({ctas, nr::bwd_shape<float>(T, d, y, pre).ctas, nr::bwd_shape<uint16_t>(T, d, y, pre).ctas});
+    return static_cast<size_t>(ctas) * 2 * d * 4;
 }
 
 cudaError_t launch_norm_residual_bwd(const NormResidualArgs &a, const NormResidualGradArgs &g, float *part,
@@ -680,12 +702,17 @@ cudaError_t launch_norm_residual_bwd(const NormResidualArgs &a, const NormResidu
         ctas = s.ctas;
         auto form = [&](auto y, auto pre, auto dr) {
             constexpr bool Y = decltype(y)::value, PRE = decltype(pre)::value, DR = decltype(dr)::value;
-            if (s.vpt == 1) return nr::backward<R, 1, Y, PRE, DR, nr::TEAM>(s, a, g, part, stream);
-            if (s.vpt == 4) return nr::backward<R, 4, Y, PRE, DR, nr::ALONE>(s, a, g, part, stream);
-            if (s.split == nr::TEAM) return nr::backward<R, 2, Y, PRE, DR, nr::TEAM>(s, a, g, part, stream);
+            if (s.vpt == 1) return nr::backward<R, 1, Y, PRE, DR, nr::TEAM, 128>(s, a, g, part, stream);
+            if (s.vpt == 4) return nr::backward<R, 4, Y, PRE, DR, nr::ALONE, 128>(s, a, g, part, stream);
+            if constexpr (!(Y && PRE)) {
+                if (s.regs == 80 && s.split == nr::PAIR)
+                    return nr::backward<R, 2, Y, PRE, DR, nr::PAIR, 80>(s, a, g, part, stream);
+                if (s.regs == 80) return nr::backward<R, 2, Y, PRE, DR, nr::ALONE, 80>(s, a, g, part, stream);
+            }
+            if (s.split == nr::TEAM) return nr::backward<R, 2, Y, PRE, DR, nr::TEAM, 128>(s, a, g, part, stream);
             if constexpr (!nr::pipelined<R>(2, Y && PRE))
-                if (s.split == nr::PAIR) return nr::backward<R, 2, Y, PRE, DR, nr::PAIR>(s, a, g, part, stream);
-            return nr::backward<R, 2, Y, PRE, DR, nr::ALONE>(s, a, g, part, stream);
+                if (s.split == nr::PAIR) return nr::backward<R, 2, Y, PRE, DR, nr::PAIR, 128>(s, a, g, part, stream);
+            return nr::backward<R, 2, Y, PRE, DR, nr::ALONE, 128>(s, a, g, part, stream);
         };
         constexpr std::true_type with{};
         constexpr std::false_type without{};
