@@ -45,14 +45,19 @@ constexpr int BWD_STAGES = 4;
 template <typename R>
 __host__ __device__ constexpr bool pipelined(int vpt, bool full) { return full && vpt == 2 && sizeof(R) == 2; }
 
-// How the rows of a backward share an SM: one at a time, two CTAs of a row each,
-// or a CTA whose teams of warps take a row each.  Teams leave one row of partial
-// sums per SM instead of one per row in flight (us, bf16: 65536 x 256 50.4 with a
-// CTA per row, 43.8 with teams; 16384 x 640 43.4 and 40.0; 2048 x 1024 19.2 and
-// 14.2; 8192 x 4096 72.0 and 70.5).  For two rows whose kernel does not read
-// ahead, CTAs of their own, which need not keep in step, are faster (8192 x 4096
-// fp32: 98.5, 112.6 with teams).
-enum Split { ALONE, PAIR, TEAM };
+// How the rows of a backward share the SMs.  TEAM: a CTA whose teams of warps
+// take a row each.  Teams leave one row of partial sums per SM instead of one per
+// row in flight (us, bf16: 65536 x 256 50.4 with a CTA per row, 43.8 with teams;
+// 16384 x 640 43.4 and 40.0; 2048 x 1024 19.2 and 14.2; 8192 x 4096 72.0 and 70.5).
+// PAIR: two CTAs of a row each.  For two rows whose kernel does not read ahead they
+// are faster than teams, as they need not keep in step (8192 x 4096 fp32: 98.5, 112.6
+// with teams).  ALONE: a row at a time.  HALVES: a row by a cluster of two CTAs,
+// which send each other their warps' sums; for rows that a CTA has too few registers
+// for (us: 2048 x 12288 bf16 121, four vectors per thread, and 70; 2048 x 16384 fp32
+// 179 and 104), and where three halves fit an SM instead of one row (4096 x 5120
+// bf16: 61.7 and 56.6; fp32, without reading ahead, 70.0 and 74.6; with two halves
+// 4096 x 8192 72.1 and 78.2).
+enum Split { ALONE, PAIR, TEAM, HALVES };
 
 // With what the launch adds to the caller's arguments.
 struct Args : NormResidualArgs {
@@ -91,11 +96,11 @@ struct Owned {
     uint32_t col;  // of the first vector (the j-th: + 256 j)
     bool on[VPT];  // whether the row has them
     int first, cols;  // the warp's columns
-    __device__ __forceinline__ Owned(int warp, int lane, int nvec) {
-        col = (warp * VPT * 32 + lane) * 8;
+    __device__ __forceinline__ Owned(int warp, int lane, int nvec, int from = 0) {
+        col = from + (warp * VPT * 32 + lane) * 8;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) on[j] = (warp * VPT + j) * 32 + lane < nvec;
-        first = warp * VPT * 256;
+        first = from + warp * VPT * 256;
         cols = max(0, min(VPT * 32, nvec - warp * VPT * 32)) * 8;
     }
 };
@@ -132,11 +137,12 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
     return warp_sum(lane < static_cast<int>(blockDim.x >> 5) ? red[lane] : 0.0f);
 }
 
-// The same for four values, in two steps around the caller's
-// barrier.  Each exchange of the first two halves the values that a lane
-// carries, so a warp takes 6 exchanges instead of 20; then every thread adds
-// the warps' sums.
-__device__ __forceinline__ void post_sums4(const float (&v)[4], float4 *red) {
+// The same for four values, in two steps around the caller's barrier.  Each
+// exchange of the first two halves the values that a lane carries, so a warp
+// takes 6 exchanges instead of 20; then every thread adds the warps' sums.
+// SEND: they also go to the peer of a cluster, each an arrival at its `bar`.
+template <bool SEND = false>
+__device__ __forceinline__ void post_sums4(const float (&v)[4], float4 *red, uint32_t peer = 0, uint64_t *bar = nullptr) {
     const int lane = threadIdx.x & 31;
     const bool up = lane & 16, odd = lane & 8;
     float a = up ? v[2] : v[0], b = up ? v[3] : v[1];
@@ -145,7 +151,11 @@ __device__ __forceinline__ void post_sums4(const float (&v)[4], float4 *red) {
     float s = (odd ? b : a) + __shfl_xor_sync(FULL, odd ? a : b, 8);
 #pragma unroll
     for (int o = 4; o; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
-    if ((lane & 7) == 0) reinterpret_cast<float *>(red + (threadIdx.x >> 5))[lane >> 3] = s;
+    if ((lane & 7) == 0) {
+        float *to = reinterpret_cast<float *>(red + (threadIdx.x >> 5)) + (lane >> 3);
+        *to = s;
+        if (SEND) send_to_peer(mapa_shared(smem_u32(to), peer), __float_as_int(s), mapa_shared(smem_u32(bar), peer));
+    }
 }
 __device__ __forceinline__ float4 collect_sums4(const float4 *red, int warps) {
     float2 a = both(0.0f), b = a;
@@ -324,22 +334,28 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
                          const float *__restrict__ rstd_pre, R *dr, uint16_t *__restrict__ dy,
                          float *__restrict__ dgate, float *__restrict__ part) {
     extern __shared__ __align__(16) uint8_t ring[];
-    __shared__ float4 red[2][MORE_THREADS / 32];
+    constexpr bool HALF = SPLIT == HALVES;
+    __shared__ float4 red[HALF ? 3 : 2][32];
     __shared__ uint64_t landed[MORE_THREADS / 32][BWD_STAGES];
-    __shared__ uint64_t posted[MAX_THREADS / 32];  // of a team: a phase per row, an arrival per warp
+    // Of a team: a phase per row, an arrival per warp.  Of halves: two that rows take in turn, five arrivals
+    // per warp (its own one, four sums from the peer's warp).  In turn, because a sum of the peer's next
+    // row may come before the last one of this row; no sum of the row after that can, as it
+    // waits for this CTA's own of the next row.  The same order of events frees the third set of `red`.
+    __shared__ uint64_t posted[MAX_THREADS / 32];
     __shared__ int abort;
     constexpr bool PIPE = pipelined<R>(VPT, Y && PRE), TEAMS = SPLIT == TEAM;
     // Whether the warps wait for the row's sums by an mbarrier, which lets the first ones through go on
-    // (4093 x 7168 fp32: 90.0 us, 95.3 with __syncthreads; 2048 x 16384, VPT 4: 214 and 186).
-    constexpr bool POSTS = PIPE || (SPLIT == ALONE && VPT == 2);
+    // (4093 x 7168 fp32: 90.0 us, 95.3 with __syncthreads).
+    constexpr bool POSTS = PIPE || SPLIT == ALONE || SPLIT == HALVES;
+    const uint32_t rank = HALF ? blockIdx.x & 1 : 0, group = HALF ? blockIdx.x >> 1 : blockIdx.x;
+    const uint32_t groups = HALF ? gridDim.x >> 1 : gridDim.x;
     const int stages = a.stages;
-    constexpr bool HOLD = VPT <= 2;
     const int teams = TEAMS ? a.teams : 1;
     const int lane = threadIdx.x & 31, all = blockDim.x >> 5, warps = all / teams;
     const int team = TEAMS ? (threadIdx.x >> 5) / warps : 0, warp = TEAMS ? (threadIdx.x >> 5) % warps : threadIdx.x >> 5;
     constexpr bool has_y = Y, pre = PRE;
     const bool post = a.gamma_post != nullptr;
-    const Owned<VPT> own(warp, lane, a.d / 8);
+    const Owned<VPT> own(warp, lane, HALF ? a.d / 16 : a.d / 8, rank * a.d / 2);
     // a warp's part of a row in the ring: its columns of y, dn, r' and dr'
     constexpr int B = VPT * piece_bytes<uint16_t>(), AT_DN = Y ? B : 0, AT_X = AT_DN + (PRE ? B : 0);
     constexpr int AT_DR = AT_X + (PRE ? VPT * piece_bytes<R>() : 0), PART = AT_DR + VPT * piece_bytes<R>();
@@ -348,18 +364,18 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
     float2 c[VPT][4], w[VPT][4], accq[VPT][4], accp[VPT][4];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        if (HOLD) weights(a, own.col + 256 * j, own.on[j], c[j], w[j]);
+        weights(a, own.col + 256 * j, own.on[j], c[j], w[j]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) accq[j][i] = accp[j][i] = both(0.0f);
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < all; ++i)
             for (int q = 0; q < BWD_STAGES; ++q) mbar_init(&landed[i][q], 1);
-        for (int i = 0; i < teams; ++i) mbar_init(&posted[i], warps);
+        for (int i = 0; i < (HALF ? 2 : teams); ++i) mbar_init(&posted[i], HALF ? 5 * warps : warps);
         abort = 0;
         fence_mbar_init();
     }
-    __syncthreads();
+    HALF ? cluster_sync() : __syncthreads();
     const Ring rows{landed[threadIdx.x >> 5], &abort, a.status, a.wait_ns, own.cols > 0};
     const uint32_t rows_end = a.T;  // a row number a few rows past it still fits
     auto issue = [&](uint32_t t, int slot) {
@@ -389,17 +405,16 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
         }
         return f;
     };
-    const uint32_t begin = blockIdx.x + team * gridDim.x, step = gridDim.x * teams;
+    const uint32_t begin = group + team * groups, step = groups * teams;
     for (int s = 0; s < stages; ++s) issue(begin + s * step, s);
     // The first reading of the row in slot `slot`: the four sums (of h z,
     // c y dr', c y h, c y z) of the warp go to `sums`.
-    auto first_pass = [&](int slot, float rq, float4 *sums) {
+    auto first_pass = [&](int slot, float rq, float4 *sums, uint32_t k) {
         const uint8_t *at16 = mine + slot * stage + lane * 16, *at_r = mine + slot * stage + lane * (8 * sizeof(R));
         float2 s0 = both(0.0f), s1 = s0, s2 = s0, s3 = s0;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             if (!own.on[j]) continue;
-            if (!HOLD) weights(a, own.col + 256 * j, true, c[j], w[j]);
             float2 cy[4];
             if (has_y) {
                 read8<uint16_t>(at16 + j * 512, cy);
@@ -433,53 +448,53 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
             }
         }
         const float s[4] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y, s3.x + s3.y};
-        post_sums4(s, sums);
+        post_sums4<HALF>(s, sums + rank * warps, rank ^ 1, &posted[k & 1]);
         if (POSTS) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(&posted[team]);
+            if (lane == 0) mbar_arrive(&posted[HALF ? k & 1 : team]);
         }
     };
-    // Until every warp of the team has posted its sums of the row (the waits alternate in parity).
-    int parity = 0;
-    auto collect = [&](const float4 *sums) {
+    // Until every warp of the team has posted its sums of the row (the k-th).
+    auto collect = [&](const float4 *sums, uint32_t k) {
         if (POSTS) {
-            mbar_wait(&posted[team], parity, &abort, a.status, a.wait_ns);
-            parity ^= 1;
+            mbar_wait<HALF>(&posted[HALF ? k & 1 : team], (HALF ? k >> 1 : k) & 1, &abort, a.status, a.wait_ns);
         } else {
             TEAMS ? team_sync(team, warps) : __syncthreads();
         }
-        return collect_sums4(sums + team * warps, warps);
+        return collect_sums4(sums + team * warps, HALF ? 2 * warps : warps);
     };
     Row f = factors(begin), next = factors(begin + step);
     int slot = 0, turn = 0;
     int phase = 0;  // of the slot that first_pass reads next
+    uint32_t k = 0;
     if (PIPE && begin < rows_end) {
         rows.wait(0, 0);
-        first_pass(0, f.rq, red[0]);
+        first_pass(0, f.rq, red[0], 0);
     }
     for (uint32_t t = begin; t < rows_end; t += step) {
         const Row after = factors(t + 2 * step);
-        const int ahead = slot + 1 == stages ? 0 : slot + 1;
+        const int ahead = slot + 1 == stages ? 0 : slot + 1, other = HALF ? (turn == 2 ? 0 : turn + 1) : turn ^ 1;
         float4 s;
         if (PIPE) {
-            s = collect(red[turn]);
+            s = collect(red[turn], k);
             if (ahead == 0) phase ^= 1;
             if (t + step < rows_end) {
                 rows.wait(ahead, phase);
-                first_pass(ahead, next.rq, red[turn ^ 1]);
+                first_pass(ahead, next.rq, red[other], k + 1);
             }
         } else {
             rows.wait(slot, phase);
-            first_pass(slot, f.rq, red[turn]);
-            s = collect(red[turn]);
+            first_pass(slot, f.rq, red[turn], k);
+            s = collect(red[turn], k);
             if (ahead == 0) phase ^= 1;
         }
-        turn ^= 1;
+        turn = other;
+        ++k;
         const uint8_t *at16 = mine + slot * stage + lane * 16, *at_r = mine + slot * stage + lane * (8 * sizeof(R));
         const float m1 = f.rq * s.x * inv_d;
         const float cyD = s.y + f.rq * s.z - m1 * s.w;
         const float m2 = post ? f.gt * cyD * inv_d * f.rp * f.rp * f.rp : 0.0f;
-        if (a.gate && a.gate_per_token && warp == 0 && lane == 0) dgate[t] = f.rp * cyD;
+        if (a.gate && a.gate_per_token && warp == 0 && lane == 0 && rank == 0) dgate[t] = f.rp * cyD;
         const float2 q = both(f.gt * f.rp), mz = both(-m1 * f.rq), my = both(-m2), rq = both(f.rq);
         R *to_r = dr + static_cast<int64_t>(t) * a.d;
         uint16_t *to_y = dy + static_cast<int64_t>(t) * a.d;
@@ -490,7 +505,6 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
 #pragma unroll
             for (int i = 0; i < 4; ++i) D[i] = both(0.0f);
             if (own.on[j]) {
-                if (!HOLD) weights(a, col, true, c[j], w[j]);
                 if (DR) read8<R>(at_r + j * piece_bytes<R>() + AT_DR, D);
                 if (pre) {
                     float2 x[4], g[4];
@@ -525,7 +539,7 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
         next = after;
     }
     // the CTA's sums: the teams' ones in the rings, now empty, added in the teams' order
-    float *out = part + static_cast<size_t>(blockIdx.x) * 2 * a.d, *held = reinterpret_cast<float *>(ring);
+    float *out = part + static_cast<size_t>(group) * 2 * a.d, *held = reinterpret_cast<float *>(ring);
     float *sums = teams > 1 ? held + team * 2 * a.d : out;
     if (teams > 1) __syncthreads();
 #pragma unroll
@@ -534,6 +548,7 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
         store8(sums + own.col + 256 * j, 0, &accq[j][0].x);
         store8(sums + a.d + own.col + 256 * j, 0, &accp[j][0].x);
     }
+    if (HALF) cluster_sync();  // a CTA stays while the other one may still post to it
     if (teams == 1) return;
     __syncthreads();
     for (int i = threadIdx.x; i < a.d / 2; i += blockDim.x) {
@@ -623,9 +638,16 @@ template <typename R>
 Shape bwd_shape(int T, int d, bool y, bool pre) {
     const int piece = (y + pre) * piece_bytes<uint16_t>() + (1 + pre) * piece_bytes<R>();
     const bool fewer = !(y && pre) && d > (sizeof(R) == 2 ? 4096 : 8192) && sm_rows(d, 80) > sm_rows(d, 128);
-    Shape s(T, d, d <= 256 ? 1 : d <= 8192 || fewer ? 2 : 4, fewer ? 80 : 128, BWD_STAGES, piece);
+    const bool ahead = pipelined<R>(2, y && pre);
+    if (!fewer && (d > 8192 || (d > 4096 && d <= 5120 && ahead))) {
+        Shape s(T, d / 2, 2, 128, BWD_STAGES, piece);
+        s.ctas = 2 * std::min(T, SMS / 2 * s.per_sm());
+        s.split = HALVES;
+        return s;
+    }
+    Shape s(T, d, d <= 256 ? 1 : 2, fewer ? 80 : 128, BWD_STAGES, piece);
     const int per_sm = s.per_sm();
-    s.split = per_sm == 1 ? ALONE : per_sm == 2 && !pipelined<R>(s.vpt, y && pre) ? PAIR : TEAM;
+    s.split = per_sm == 1 ? ALONE : per_sm == 2 && !ahead ? PAIR : TEAM;
     if (s.split != TEAM) return s;
     s.teams = std::min(per_sm, (T + SMS - 1) / SMS);
     s.ctas = std::min(T, SMS);
@@ -664,10 +686,16 @@ cudaError_t backward(const Shape &s, const NormResidualArgs &a, const NormResidu
     const cudaError_t e = allow_ring(norm_residual_bwd_kernel<R, VPT, Y, PRE, DR, SPLIT, REGS>, done);
     if (e != cudaSuccess) return e;
     const Args args{a, s.stages, s.teams, reinterpret_cast<uintptr_t>(g.dr) % 32 == 0};
-    norm_residual_bwd_kernel<R, VPT, Y, PRE, DR, SPLIT, REGS><<<s.ctas, s.threads, s.smem, stream>>>(
-        args, 1.0f / a.d, static_cast<const R *>(g.r_out), static_cast<const R *>(g.dr_out), g.dn, g.rstd_post,
-        g.rstd_pre, static_cast<R *>(g.dr), g.dy, g.dgate, part);
-    return cudaGetLastError();
+    cudaLaunchAttribute pairs;
+    pairs.id = cudaLaunchAttributeClusterDimension;
+    pairs.val.clusterDim.x = 2, pairs.val.clusterDim.y = pairs.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(s.ctas), cfg.blockDim = dim3(s.threads), cfg.dynamicSmemBytes = s.smem, cfg.stream = stream;
+    cfg.attrs = &pairs, cfg.numAttrs = SPLIT == HALVES;
+    return cudaLaunchKernelEx(&cfg, norm_residual_bwd_kernel<R, VPT, Y, PRE, DR, SPLIT, REGS>, args, 1.0f / a.d,
+                              static_cast<const R *>(g.r_out), static_cast<const R *>(g.dr_out),
+                              static_cast<const uint16_t *>(g.dn), static_cast<const float *>(g.rstd_post),
+                              static_cast<const float *>(g.rstd_pre), static_cast<R *>(g.dr), g.dy, g.dgate, part);
 }
 
 }  // namespace nr
@@ -695,15 +723,15 @@ size_t norm_residual_bwd_part_bytes(int T, int d) {
 
 cudaError_t launch_norm_residual_bwd(const NormResidualArgs &a, const NormResidualGradArgs &g, float *part,
                                      int *launches, cudaStream_t stream) {
-    int ctas = 0;
+    int parts = 0;
     auto go = [&](auto type) {
         using R = decltype(type);
         const nr::Shape s = nr::bwd_shape<R>(a.T, a.d, a.y, a.gamma_pre);
-        ctas = s.ctas;
+        parts = s.split == nr::HALVES ? s.ctas / 2 : s.ctas;
         auto form = [&](auto y, auto pre, auto dr) {
             constexpr bool Y = decltype(y)::value, PRE = decltype(pre)::value, DR = decltype(dr)::value;
             if (s.vpt == 1) return nr::backward<R, 1, Y, PRE, DR, nr::TEAM, 128>(s, a, g, part, stream);
-            if (s.vpt == 4) return nr::backward<R, 4, Y, PRE, DR, nr::ALONE, 128>(s, a, g, part, stream);
+            if (s.split == nr::HALVES) return nr::backward<R, 2, Y, PRE, DR, nr::HALVES, 128>(s, a, g, part, stream);
             if constexpr (!(Y && PRE)) {
                 if (s.regs == 80 && s.split == nr::PAIR)
                     return nr::backward<R, 2, Y, PRE, DR, nr::PAIR, 80>(s, a, g, part, stream);
@@ -725,7 +753,7 @@ cudaError_t launch_norm_residual_bwd(const NormResidualArgs &a, const NormResidu
     if (err != cudaSuccess || !(a.gamma_pre || a.gamma_post || (a.gate && !a.gate_per_token))) return err;
     *launches = 2;
     return launch_dependent(nr::norm_residual_bwd_columns_kernel, a.d / 32, 32 * nr::RUNS, stream,
-                            static_cast<const NormResidualArgs &>(a), static_cast<const float *>(part), ctas,
+                            static_cast<const NormResidualArgs &>(a), static_cast<const float *>(part), parts,
                             g.dgamma_pre, g.dgamma_post, g.dgate);
 }
 

@@ -39,7 +39,9 @@ CASES = [(1, 7168, torch.float32, "both", "channel", 1.0), (1, 64, torch.bfloat1
          (5000, 64, torch.bfloat16, "both", "channel", 1.0), (333, 1536, torch.float32, "both", "channel", 0.5),
          (457, 5120, torch.bfloat16, "both", "token", 1.0), (2600, 256, torch.float32, "post", "token", 1.0),
          (613, 5120, torch.bfloat16, "pre", "none", 1.0), (306, 6144, torch.bfloat16, "post", "channel", 1.0),
-         (155, 12288, torch.float32, "sum", "token", 1.0), (310, 5184, torch.float32, "post", "none", 1.0)]
+         (155, 12288, torch.float32, "sum", "token", 1.0), (310, 5184, torch.float32, "post", "none", 1.0),
+         (400, 8256, torch.bfloat16, "both", "channel", 0.5), (170, 16384, torch.float32, "both", "token", 1.0),
+         (161, 12352, torch.bfloat16, "post", "channel", 1.0), (239, 16384, torch.bfloat16, "both", "token", 1.0)]
 
 
 def _case(c, seed=0):
