@@ -629,15 +629,15 @@ Shape fwd_shape(int T, int d) {
     if (d > 4096 && sm_rows(d, 80) > sm_rows(d, 128)) return Shape(T, d, 2, 80, FWD_STAGES, piece);
     return Shape(T, d, d <= 8192 ? 2 : 4, 128, FWD_STAGES, piece);
 }
-// The same for a backward without y or gamma_pre (us, 2048 x 12288 without
-// gamma_pre: bf16 76.7 and 54.8, fp32 85.4 and 66.6; without y 4096 x 5120 bf16
-// 45.4 and 39.3, but fp32, whose ring gets too short, 51.8 and 53.9); one with
-// both needs its 128.  Teams are as many as rows spread over all SMs allow; the
-// ring also holds their partial sums in the end.
+// The same for a bf16 backward without y or gamma_pre (us: without y 4096 x 5120
+// 45.4 and 39.3, 2048 x 10240 in halves 49.4 and 44.5); an fp32 one's ring gets too
+// short (4096 x 5120 51.8 and 53.9, 2048 x 12288 in halves 62.7 and 80.8), and one
+// with both needs its 128.  Teams are as many as rows spread over all SMs allow;
+// the ring also holds their partial sums in the end.
 template <typename R>
 Shape bwd_shape(int T, int d, bool y, bool pre) {
     const int piece = (y + pre) * piece_bytes<uint16_t>() + (1 + pre) * piece_bytes<R>();
-    const bool fewer = !(y && pre) && d > (sizeof(R) == 2 ? 4096 : 8192) && sm_rows(d, 80) > sm_rows(d, 128);
+    const bool fewer = sizeof(R) == 2 && !(y && pre) && d > 4096 && sm_rows(d, 80) > sm_rows(d, 128);
     const bool ahead = pipelined<R>(2, y && pre);
     if (!fewer && (d > 8192 || (d > 4096 && d <= 5120 && ahead))) {
         Shape s(T, d / 2, 2, 128, BWD_STAGES, piece);
@@ -732,7 +732,7 @@ cudaError_t launch_norm_residual_bwd(const NormResidualArgs &a, const NormResidu
             constexpr bool Y = decltype(y)::value, PRE = decltype(pre)::value, DR = decltype(dr)::value;
             if (s.vpt == 1) return nr::backward<R, 1, Y, PRE, DR, nr::TEAM, 128>(s, a, g, part, stream);
             if (s.split == nr::HALVES) return nr::backward<R, 2, Y, PRE, DR, nr::HALVES, 128>(s, a, g, part, stream);
-            if constexpr (!(Y && PRE)) {
+            if constexpr (sizeof(R) == 2 && !(Y && PRE)) {
                 if (s.regs == 80 && s.split == nr::PAIR)
                     return nr::backward<R, 2, Y, PRE, DR, nr::PAIR, 80>(s, a, g, part, stream);
                 if (s.regs == 80) return nr::backward<R, 2, Y, PRE, DR, nr::ALONE, 80>(s, a, g, part, stream);
