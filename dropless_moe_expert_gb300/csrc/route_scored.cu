@@ -21,7 +21,7 @@
 //
 // Latency and the instructions of a token bound it, not memory.  Measured on
 // the device, all launches of a call: 1 token of 256 experts in 8 runs 5.1 us,
-// 4096 of them 11.8, 32768 of 64 experts 19.2 (its bytes: 1.7); the gradient of
+// 4096 of them 11.8, 32768 of 64 experts 14.2 (its bytes: 1.7); the gradient of
 // 16381 x 128 softmax scores 5.9 us (its bytes: 2.6).
 #include "kernels.h"
 #include "ptx.cuh"
@@ -303,6 +303,224 @@ route_scored_topk_kernel(const float *__restrict__ L, const float *__restrict__ 
         }
         row_of[static_cast<size_t>(t) * K + lane] = r;
     }
+}
+
+// The same for MANY tokens and more: 4 or 8 lanes per token, so that what is done
+// per token and choice is shared by the 4 or 8 tokens of a warp (instructions of a
+// token: 64 experts, softmax 173, half a warp 336; 256 in 8 runs 800 and 1250).
+// Lane l holds the octets (8 neighbouring experts) l, l + LANES, ..; their keys
+// also lie in shared memory, where the octet of a choice is read again for its next
+// largest.  The same sums in the same order, so the same bits as above.  Us, all
+// launches: 32768 tokens, 64 experts softmax 14.2, half a warp per token 19.2; 256
+// in 8 runs 43.8 and 56.0; with 8192 tokens 16.3 and 19.0; but, fewer warps taking
+// longer each, with 4096 tokens 12.7 and 11.8, and for 8192 x 32 8.2 and 6.7.
+// E and a run's experts are multiples of four, with at most RUNS runs.
+constexpr int MANY = 8192;
+constexpr int RUNS = 16;
+constexpr int OCTET_THREADS = 128;
+template <int LANES, int OCTETS>
+__global__ void __launch_bounds__(OCTET_THREADS, 5)
+route_scored_topk_octets_kernel(const float *__restrict__ L, const float *__restrict__ bias, int T, int E, int K,
+                                RouteRule rule, int32_t *__restrict__ topk_idx, float *__restrict__ topk_w,
+                                int32_t *__restrict__ row_of, uint8_t *__restrict__ chunk_counts) {
+    constexpr int TOKENS = OCTET_THREADS / LANES, CHUNKS = TOKENS / CH, MOST = 8 * LANES * OCTETS;
+    constexpr int PITCH = MOST + 8;
+    static_assert(TOKENS % CH == 0, "whole chunks");
+    __shared__ __align__(16) uint32_t s_keys[TOKENS * PITCH];
+    __shared__ __align__(16) float s_chosen[TOKENS][16];  // the choices' scores
+    __shared__ uint32_t s_runs[TOKENS][RUNS];             // the runs' scores
+    __shared__ uint8_t s_e[TOKENS][16];                   // the choices
+    __shared__ uint32_t chose[CHUNKS][MOST];              // bit i: token i of the chunk chose the expert
+    const int tok = threadIdx.x / LANES, l = threadIdx.x % LANES;
+    const int t = blockIdx.x * TOKENS + tok;
+    const float *row = L + static_cast<size_t>(min(t, T - 1)) * E;  // a token beyond the last is routed as the last
+    uint32_t *const keys = s_keys + tok * PITCH;
+    for (int i = threadIdx.x; i < CHUNKS * MOST; i += OCTET_THREADS) (&chose[0][0])[i] = 0u;
+
+    float v[OCTETS][8];
+    auto load = [&](const float *from, float absent) {
+#pragma unroll
+        for (int j = 0; j < OCTETS; ++j)
+#pragma unroll
+            for (int h = 0; h < 8; h += 4) {
+                const int e = 8 * (l + LANES * j) + h;
+                const float4 x = e < E ? *reinterpret_cast<const float4 *>(from + e)
+                                       : make_float4(absent, absent, absent, absent);
+                v[j][h] = x.x, v[j][h + 1] = x.y, v[j][h + 2] = x.z, v[j][h + 3] = x.w;
+            }
+    };
+    load(row, -INFINITY);
+    float m = -INFINITY, sum = 1.0f;
+    if (rule.softmax) {
+#pragma unroll
+        for (int j = 0; j < OCTETS; ++j)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) m = fmaxf(m, v[j][q]);
+#pragma unroll
+        for (int o = LANES / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+        float f[OCTETS][8];
+#pragma unroll
+        for (int j = 0; j < OCTETS; ++j)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) f[j][q] = v[j][q] = expf(v[j][q] - m);
+        // element i + h to element i: over a lane's octets, the lanes, an octet's experts
+#pragma unroll
+        for (int h = OCTETS / 2; h; h >>= 1)
+#pragma unroll
+            for (int j = 0; j < h; ++j)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) f[j][q] += f[j + h][q];
+#pragma unroll
+        for (int o = LANES / 2; o; o >>= 1)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) f[0][q] += __shfl_xor_sync(FULL, f[0][q], o);
+#pragma unroll
+        for (int h = 4; h; h >>= 1)
+#pragma unroll
+            for (int q = 0; q < h; ++q) f[0][q] += f[0][q + h];
+        sum = f[0][0];
+    }
+    auto score = [&](float x) { return rule.softmax ? x / sum : sigmoid(x); };  // of a logit, or its exponential
+    uint32_t key[OCTETS][8];
+#pragma unroll
+    for (int j = 0; j < OCTETS; ++j)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[j][q] = score(v[j][q]);
+#pragma unroll
+    for (int j = 0; j < OCTETS; ++j)
+#pragma unroll
+        for (int h = 0; h < 8; h += 4) {
+            const int e = 8 * (l + LANES * j) + h;
+            float4 b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (bias && e < E) b = *reinterpret_cast<const float4 *>(bias + e);
+            const float add[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                key[j][h + q] = e < E ? order_key(bias ? v[j][h + q] + add[q] : v[j][h + q]) : 0u;
+            *reinterpret_cast<uint4 *>(keys + e) =
+                make_uint4(key[j][h], key[j][h + 1], key[j][h + 2], key[j][h + 3]);
+        }
+    __syncwarp();
+    if (rule.topk_group < rule.n_group) {
+        const int G = rule.n_group, per = E / G;
+        for (int g = l; g < G; g += LANES) {
+            uint32_t a = 0, b = 0;  // its two largest
+            for (int i = 0; i < per; i += 4) {
+                const uint4 k = *reinterpret_cast<const uint4 *>(keys + g * per + i);
+                b = max(b, min(a, k.x)), a = max(a, k.x);
+                b = max(b, min(a, k.y)), a = max(a, k.y);
+                b = max(b, min(a, k.z)), a = max(a, k.z);
+                b = max(b, min(a, k.w)), a = max(a, k.w);
+            }
+            s_runs[tok][g] = rule.group_top == 2 && b ? order_key(key_value(a) + key_value(b)) : a;
+        }
+        __syncwarp();
+        uint32_t open = 0;
+        for (int g = l; g < G; g += LANES) {
+            const uint32_t mine = s_runs[tok][g];
+            int above = 0;  // runs that come before this one
+            for (int o = 0; o < G; ++o) above += s_runs[tok][o] > mine || (s_runs[tok][o] == mine && o < g);
+            open |= static_cast<uint32_t>(above < rule.topk_group) << g;
+        }
+#pragma unroll
+        for (int o = LANES / 2; o; o >>= 1) open |= __shfl_xor_sync(FULL, open, o);
+#pragma unroll
+        for (int j = 0; j < OCTETS; ++j)
+#pragma unroll
+            for (int h = 0; h < 8; h += 4) {
+                const int e = 8 * (l + LANES * j) + h;
+                if (open >> (e * rule.run_of >> 20) & 1u) continue;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) key[j][h + q] = 0u;
+                *reinterpret_cast<uint4 *>(keys + e) = make_uint4(0u, 0u, 0u, 0u);
+            }
+    }
+    uint32_t best[OCTETS];
+#pragma unroll
+    for (int j = 0; j < OCTETS; ++j) {
+        best[j] = key[j][0];
+#pragma unroll
+        for (int q = 1; q < 8; ++q) best[j] = max(best[j], key[j][q]);
+    }
+    for (int k = 0; k < K; ++k) {
+        uint32_t top = best[0];
+#pragma unroll
+        for (int j = 1; j < OCTETS; ++j) top = max(top, best[j]);
+#pragma unroll
+        for (int o = LANES / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(FULL, top, o));
+        int octet = MOST;  // the lowest that holds it
+#pragma unroll
+        for (int j = OCTETS - 1; j >= 0; --j) octet = best[j] == top ? l + LANES * j : octet;
+#pragma unroll
+        for (int o = LANES / 2; o; o >>= 1) octet = min(octet, __shfl_xor_sync(FULL, octet, o));
+        if (octet % LANES == l) {  // taken: the octet is searched again
+            const uint4 a = *reinterpret_cast<const uint4 *>(keys + 8 * octet);
+            const uint4 b = *reinterpret_cast<const uint4 *>(keys + 8 * octet + 4);
+            const uint32_t held[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            int q = 7;
+#pragma unroll
+            for (int i = 6; i >= 0; --i) q = held[i] == top ? i : q;
+            uint32_t next = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) next = max(next, i == q ? 0u : held[i]);
+            keys[8 * octet + q] = 0u;
+            s_e[tok][k] = static_cast<uint8_t>(8 * octet + q);
+#pragma unroll
+            for (int j = 0; j < OCTETS; ++j) best[j] = octet / LANES == j ? next : best[j];
+        }
+        __syncwarp();
+    }
+    constexpr int MINE = 16 / LANES;  // choices l, l + LANES, .. are this lane's
+    int my_e[MINE];
+    float my_s[MINE];
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+        my_e[i] = l + LANES * i < K ? s_e[tok][l + LANES * i] : -1;
+        my_s[i] = my_e[i] >= 0 ? row[my_e[i]] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+        if (my_e[i] >= 0) my_s[i] = score(rule.softmax ? expf(my_s[i] - m) : my_s[i]);
+        s_chosen[tok][l + LANES * i] = my_s[i];
+    }
+    __syncthreads();  // and `chose` is zero
+    float total = 1.0f;
+    if (rule.renorm) {
+        float f[16];  // added as a warp does: element i + h to element i
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(&s_chosen[tok][i]);
+            f[i] = x.x, f[i + 1] = x.y, f[i + 2] = x.z, f[i + 3] = x.w;
+        }
+#pragma unroll
+        for (int h = 8; h; h >>= 1)
+#pragma unroll
+            for (int i = 0; i < h; ++i) f[i] += f[i + h];
+        total = f[0] + kRouteEps;
+    }
+    if (t >= T) {
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) my_e[i] = -1;
+    }
+    const size_t p = static_cast<size_t>(t) * K + l;
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+        if (my_e[i] < 0) continue;
+        topk_idx[p + LANES * i] = my_e[i];
+        topk_w[p + LANES * i] = rule.scale * (rule.renorm ? my_s[i] / total : my_s[i]);
+        atomicOr(&chose[tok / CH][my_e[i]], 1u << tok % CH);  // the final mask does not depend on the order
+    }
+    __syncthreads();
+    const int pitch = count_pitch(E), first = blockIdx.x * CHUNKS, chunks = (T + CH - 1) / CH;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+        if (first + c < chunks)
+            for (int e = threadIdx.x; e < pitch; e += OCTET_THREADS)
+                chunk_counts[static_cast<size_t>(first + c) * pitch + e] =
+                    static_cast<uint8_t>(e < E ? __popc(chose[c][e]) : 0);
+#pragma unroll
+    for (int i = 0; i < MINE; ++i)
+        if (my_e[i] >= 0) row_of[p + LANES * i] = __popc(chose[tok / CH][my_e[i]] & ((1u << tok % CH) - 1u));
 }
 
 // Sums of the rows [from, to) of byte counts: thread (word, slice) of the
@@ -587,10 +805,24 @@ cudaError_t launch_route_scored(const float *logits, const float *sel_bias, int 
         return few ? topk(rs::route_scored_topk_kernel<LANES, EPL, true>, LANES)
                    : topk(rs::route_scored_topk_kernel<LANES, EPL, false>, LANES);
     };
+    auto octets = [&](auto kernel, int lanes) {
+        const int tokens = rs::OCTET_THREADS / lanes;
+        kernel<<<(T + tokens - 1) / tokens, rs::OCTET_THREADS, 0, stream>>>(logits, sel_bias, T, E, K, rule, topk_idx,
+                                                                            topk_w, row_of, workspace);
+        return cudaGetLastError();
+    };
+    const bool grouped = rule.topk_group < rule.n_group;
+    const bool fours = E % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0 &&
+                       reinterpret_cast<uintptr_t>(sel_bias) % 16 == 0 &&
+                       (!grouped || (rule.n_group <= rs::RUNS && E / rule.n_group % 4 == 0));
     using std::integral_constant;
     const integral_constant<int, 16> half;
     const integral_constant<int, 32> whole;
-    cudaError_t err = E <= 16    ? by_experts(half, integral_constant<int, 1>{})
+    cudaError_t err = fours && E > 32 && T >= rs::MANY
+                          ? E <= 64    ? octets(rs::route_scored_topk_octets_kernel<4, 2>, 4)
+                            : E <= 128 ? octets(rs::route_scored_topk_octets_kernel<4, 4>, 4)
+                                       : octets(rs::route_scored_topk_octets_kernel<8, 4>, 8)
+                      : E <= 16  ? by_experts(half, integral_constant<int, 1>{})
                       : E <= 32  ? by_experts(half, integral_constant<int, 2>{})
                       : E <= 64  ? by_experts(half, integral_constant<int, 4>{})
                       : E <= 128 ? by_experts(whole, integral_constant<int, 4>{})

@@ -50,6 +50,12 @@ CASES = [
     (127, 33, 16, "sigmoid", 1, 1, 1, True, -0.5, True),
     (63, 96, 3, "sigmoid", 2, 1, 1, True, 1.0, False),
     (129, 192, 10, "softmax", 12, 5, 2, True, 1.0, True),
+    (8192, 64, 6, "softmax", 1, 1, 1, False, 1.0, True),     # the fewest tokens of the kernel for many
+    (8203, 256, 8, "sigmoid", 8, 4, 2, True, 2.5, True),
+    (8239, 100, 12, "sigmoid", 1, 1, 1, True, 1.0, False),
+    (8201, 160, 16, "softmax", 8, 3, 1, True, 1.0, True),
+    (8255, 20, 3, "softmax", 5, 2, 2, True, -0.5, True),
+    (8192, 63, 5, "sigmoid", 3, 2, 2, True, 1.0, True),      # not in fours
 ]
 
 
@@ -250,3 +256,42 @@ def test_offsets_past_32_bits():
     d = moe.route_scored_backward(L, r.topk_idx, torch.ones((T, K), device="cuda"), rule)
     ref, mag = op.route_scored_backward(tail, idx, np.ones((64, K)), renorm=False)
     assert np.all(np.abs(to_np(d[-64:]) - ref) <= 64 * ULP * mag)
+
+
+@pytest.mark.parametrize("c", [
+    (8192, 64, 6, "softmax", 1, 1, 1, True, 1.0, True), (8205, 256, 8, "sigmoid", 8, 4, 2, True, 2.5, True),
+    (9000, 128, 16, "softmax", 16, 4, 2, True, 1.0, False), (8230, 36, 9, "sigmoid", 3, 2, 1, False, 1.0, True),
+    (8193, 240, 7, "softmax", 1, 1, 1, False, 1.0, True), (8200, 64, 16, "sigmoid", 16, 4, 2, True, 1.0, True),
+    (8192, 20, 20 - 4, "softmax", 1, 1, 1, True, 1.0, False)], ids=str)
+def test_the_same_bits_among_many_tokens_as_among_few(c):
+    T, E, K = c[:3]
+    L, b, rule = _case(c)
+    L[::7] = np.round(L[::7])                    # ties
+    L[3::97] = 0.0
+    L[5::101, 1::3] = -np.inf
+    L[6::103, 2] = np.inf
+    L[8::107, E // 2] = np.nan
+    L[9::109] = -np.inf
+    L[10::113, ::2] = -0.0
+    L[11::127] *= 1e30
+    many = moe.route_scored(_dev(L), K, rule, _dev(b))
+    _check_dispatch(many, T, E, K)
+    for i in range(0, T, 1024):
+        few = moe.route_scored(_dev(L[i:i + 1024]), K, rule, _dev(b))
+        assert torch.equal(many.topk_idx[i:i + 1024], few.topk_idx)
+        assert torch.equal(many.topk_w[i:i + 1024].view(torch.int32), few.topk_w.view(torch.int32))
+
+
+def test_addresses_that_are_not_on_sixteen_bytes():
+    """Among many tokens too: the logits and the bias at any fp32 address."""
+    T, E, K = 8192, 64, 6
+    L, b, rule = _case((T, E, K, "sigmoid", 4, 2, 2, True, 1.0, True))
+    ref = moe.route_scored(_dev(L), K, rule, _dev(b))
+    held = torch.empty(T * E + 1, device="cuda")
+    bias = torch.empty(E + 1, device="cuda")
+    held[1:] = _dev(L).flatten()
+    bias[1:] = _dev(b)
+    for logits, add in ((held[1:].view(T, E), _dev(b)), (_dev(L), bias[1:])):
+        r = moe.route_scored(logits, K, rule, add)
+        assert torch.equal(r.topk_idx, ref.topk_idx)
+        assert torch.equal(r.topk_w.view(torch.int32), ref.topk_w.view(torch.int32))
