@@ -307,12 +307,12 @@ route_scored_topk_kernel(const float *__restrict__ L, const float *__restrict__ 
 
 // The same for MANY tokens and more: 4 or 8 lanes per token, so that what is done
 // per token and choice is shared by the 4 or 8 tokens of a warp (instructions of a
-// token: 64 experts, softmax 173, half a warp 336; 256 in 8 runs 800 and 1250).
+// token: 64 experts, softmax 164, half a warp 336; 256 in 8 runs 570 and 1250).
 // Lane l holds the octets (8 neighbouring experts) l, l + LANES, ..; their keys
 // also lie in shared memory, where the octet of a choice is read again for its next
 // largest.  The same sums in the same order, so the same bits as above.  Us, all
 // launches: 32768 tokens, 64 experts softmax 14.2, half a warp per token 19.2; 256
-// in 8 runs 43.8 and 56.0; with 8192 tokens 16.3 and 19.0; but, fewer warps taking
+// in 8 runs 39.9 and 56.0; with 8192 tokens 15.0 and 19.0; but, fewer warps taking
 // longer each, with 4096 tokens 12.7 and 11.8, and for 8192 x 32 8.2 and 6.7.
 // E and a run's experts are multiples of four, with at most RUNS runs.
 constexpr int MANY = 8192;
@@ -405,8 +405,8 @@ route_scored_topk_octets_kernel(const float *__restrict__ L, const float *__rest
         const int G = rule.n_group, per = E / G;
         for (int g = l; g < G; g += LANES) {
             uint32_t a = 0, b = 0;  // its two largest
-            for (int i = 0; i < per; i += 4) {
-                const uint4 k = *reinterpret_cast<const uint4 *>(keys + g * per + i);
+            for (int i = 0, at = 4 * l % per; i < per; i += 4, at = at + 4 == per ? 0 : at + 4) {  // lanes off each other's banks
+                const uint4 k = *reinterpret_cast<const uint4 *>(keys + g * per + at);
                 b = max(b, min(a, k.x)), a = max(a, k.x);
                 b = max(b, min(a, k.y)), a = max(a, k.y);
                 b = max(b, min(a, k.z)), a = max(a, k.z);
