@@ -305,7 +305,7 @@ route_scored_topk_kernel(const float *__restrict__ L, const float *__restrict__ 
     }
 }
 
-// The same for MANY tokens and more: 4 or 8 lanes per token, so that what is done
+// The same for many tokens: 4 or 8 lanes per token, so that what is done
 // per token and choice is shared by the 4 or 8 tokens of a warp (instructions of a
 // token: 64 experts, softmax 164, half a warp 336; 256 in 8 runs 570 and 1250).
 // Lane l holds the octets (8 neighbouring experts) l, l + LANES, ..; their keys
@@ -313,9 +313,10 @@ route_scored_topk_kernel(const float *__restrict__ L, const float *__restrict__ 
 // largest.  The same sums in the same order, so the same bits as above.  Us, all
 // launches: 32768 tokens, 64 experts softmax 14.2, half a warp per token 19.2; 256
 // in 8 runs 39.9 and 56.0; with 8192 tokens 15.0 and 19.0; but, fewer warps taking
-// longer each, with 4096 tokens 12.7 and 11.8, and for 8192 x 32 8.2 and 6.7.
+// longer each, with 4096 tokens (no runs) 10.7 and 9.8, and for 8192 x 32 8.2 and 6.7;
+// 6144 x 256 13.0 and 15.3, without runs 12.0 and 12.2, 6144 x 128 10.0 and 9.7.
 // E and a run's experts are multiples of four, with at most RUNS runs.
-constexpr int MANY = 8192;
+constexpr int many(int E) { return E > 128 ? 5120 : 8192; }
 constexpr int RUNS = 16;
 constexpr int OCTET_THREADS = 128;
 template <int LANES, int OCTETS>
@@ -818,7 +819,7 @@ cudaError_t launch_route_scored(const float *logits, const float *sel_bias, int 
     using std::integral_constant;
     const integral_constant<int, 16> half;
     const integral_constant<int, 32> whole;
-    cudaError_t err = fours && E > 32 && T >= rs::MANY
+    cudaError_t err = fours && E > 32 && T >= rs::many(E)
                           ? E <= 64    ? octets(rs::route_scored_topk_octets_kernel<4, 2>, 4)
                             : E <= 128 ? octets(rs::route_scored_topk_octets_kernel<4, 4>, 4)
                                        : octets(rs::route_scored_topk_octets_kernel<8, 4>, 8)
