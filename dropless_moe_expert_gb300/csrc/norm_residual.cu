@@ -14,10 +14,10 @@
 // The sums over t run in a fixed order: each CTA over its own rows, then the
 // CTAs' partial sums in their order.
 //
-// Memory bounds both.  Measured: forward of 8192 x 4096 bf16 46.0 us, 5.8 TB/s,
-// the time of a plain copy of as many bytes (46.8); backward 71.7 us, 5.6 TB/s,
-// 91% of it the main kernel, which takes as long with its arithmetic left out;
-// backward of 4093 x 7168 with the stream in fp32 93.8 us, 5.6 TB/s.
+// Memory bounds both.  Measured: forward of 8192 x 4096 bf16 46.2 us, 5.8 TB/s,
+// the time of a plain copy of as many bytes (46.8); backward 70.1 us, 5.7 TB/s,
+// 93% of it the main kernel, which takes as long with its arithmetic left out;
+// backward of 4093 x 7168 with the stream in fp32 88.9 us, 5.9 TB/s.
 #include "kernels.h"
 #include "ptx.cuh"
 #include "vec8.cuh"

@@ -37,13 +37,13 @@ constexpr int CH = 16;             // tokens of a chunk, which a CTA of the top-
 constexpr int OPEN = MAX_E / 16;   // words of a token's open runs
 constexpr int SPANS = 152;         // CTAs of the dispatch kernel, each a run of chunks
 // Of counts that every dispatch CTA adds up itself, not another launch before
-// it (32768 x 64, 128 KB: 19.2 us, 24.2 with the launch; 131072 x 64, 512 KB:
-// 68.0 and 61.5).
+// it (32768 x 64, 128 KB: 14.1 us, 18.7 with the launch; 131072 x 64, 512 KB:
+// 46.2 and 42.6).
 constexpr size_t SELF_SUM_BYTES = 256 * 1024;
 constexpr unsigned FULL = 0xffffffffu;
 
 // Of a dispatch CTA: 512 while it adds the counts up itself (4096 x 256: 11.8 us,
-// 12.3 with 1024), 1024 where its span is long (131072 x 64: 61.5 us, 65.5 with 512).
+// 12.3 with 1024), 1024 where its span is long (131072 x 64: 42.6 us, 44.3 with 512).
 __host__ __device__ constexpr int dispatch_threads(bool spanned) { return spanned ? 1024 : 512; }
 
 // Bytes of a chunk's row of counts (one byte per expert, whole 16-byte words).
@@ -166,8 +166,8 @@ __device__ __forceinline__ uint32_t open_runs(const uint32_t *keys, uint32_t *sc
 // and the CTA writes the dispatch order too; else it writes its chunk's counts
 // and each pair's rank inside the chunk (in row_of) for the dispatch kernel.
 // The instructions of a token bound it: half a warp per token up to 64 experts
-// (32768 tokens, 64 experts: 19.5 us for the whole routing, 20.9 with a warp;
-// 128 experts the other way round, 17.7 and 18.8 for 16384 tokens).
+// (32768 tokens, 64 experts, all routed by this kernel: 19.5 us for the whole
+// routing, 20.9 with a warp; 128 experts the other way round, 17.7 and 18.8 for 16384).
 template <int LANES, int EPL, bool FINAL>
 __global__ void __launch_bounds__(CH *LANES, !FINAL && LANES == 32 ? 3 : 1)
 route_scored_topk_kernel(const float *__restrict__ L, const float *__restrict__ bias, int T, int E, int K,
