@@ -171,10 +171,8 @@ __device__ __forceinline__ float4 collect_sums4(const float4 *red, int warps) {
 // Between the warps of one of a CTA's teams (of at most 8, where they have two warps or more).  Not on
 // barrier 0: that is __syncthreads' own, where teams without further rows already wait for the others.
 __device__ __forceinline__ void team_sync(int team, int warps) {
-    if (warps == 1)
-        __syncwarp();
-    else
-        asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(32 * warps) : "memory");
+    __syncwarp();  // the barrier, and that of a cluster below, is for whole warps at once
+    if (warps > 1) asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(32 * warps) : "memory");
 }
 
 // Weights of the eight columns from `col` (where the row has them): c of y
@@ -375,6 +373,7 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
         abort = 0;
         fence_mbar_init();
     }
+    __syncwarp();
     HALF ? cluster_sync() : __syncthreads();
     const Ring rows{landed[threadIdx.x >> 5], &abort, a.status, a.wait_ns, own.cols > 0};
     const uint32_t rows_end = a.T;  // a row number a few rows past it still fits
@@ -548,6 +547,7 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
         store8(sums + own.col + 256 * j, 0, &accq[j][0].x);
         store8(sums + a.d + own.col + 256 * j, 0, &accp[j][0].x);
     }
+    __syncwarp();
     if (HALF) cluster_sync();  // a CTA stays while the other one may still post to it
     if (teams == 1) return;
     __syncthreads();
