@@ -261,7 +261,11 @@ class RouteRule:
             raise ValueError(f"score must be 'sigmoid' or 'softmax', got {self.score!r}")
         object.__setattr__(self, "_struct", _RouteRule(int(self.score == "softmax"), self.n_group, self.topk_group,
                                                        self.group_top, int(self.renorm), self.scale))
-        object.__setattr__(self, "_c", ctypes.addressof(self._struct))
+
+    @property
+    def _c(self) -> int:
+        """The struct's address, asked for at each call: a copy of the rule has a struct of its own."""
+        return ctypes.addressof(self._struct)
 
 
 class RouteBuffers:
