@@ -183,6 +183,21 @@ def _in(t, dtype, shape, name) -> int:
     return _need(t, dtype, shape, name).data_ptr()
 
 
+class _Buffers:
+    """Output buffers that are checked once.  ``_checked`` is what the last
+    check went by, the tensors' addresses among it; tensors that stand at other
+    addresses (replaced, resized, copied) are checked again.  ``_held`` keeps
+    that memory, so that another tensor cannot come to lie at an old address."""
+    _checked, _held = None, ()
+
+    def _hold(self, checked, *tensors):
+        self._held = tuple(t.untyped_storage() for t in tensors if t is not None)
+        self._checked = checked
+
+    def __getstate__(self):  # copies are checked by themselves
+        return {k: v for k, v in self.__dict__.items() if k not in ("_checked", "_held")}
+
+
 def _empty(shape, dtype, like):
     return torch.empty(shape, dtype=dtype, device=like.device)
 
@@ -268,9 +283,10 @@ class RouteRule:
         return ctypes.addressof(self._struct)
 
 
-class RouteBuffers:
+class RouteBuffers(_Buffers):
     """The outputs and the workspace of route_scored for one size, to be used
-    again from call to call."""
+    again from call to call: a call overwrites what the last one returned, so
+    calls on two streams need buffers of their own."""
 
     def __init__(self, T: int, E: int, K: int, device="cuda"):
         i32, n = torch.int32, int(lib.moe_route_scored_workspace_size(T, E, K))
@@ -284,9 +300,23 @@ class RouteBuffers:
         self.routing = Routing(make(i32, T, K), make(torch.float32, T, K), make(i32, E), make(i32, E + 1),
                                make(i32, T, K), make(i32, T * K))
         self.workspace = make(torch.uint8, n)
-        r = self.routing
-        self._args = (_ptr(r.topk_idx), _ptr(r.topk_w), _ptr(r.counts), _ptr(r.offsets), _ptr(r.row_of),
-                      _ptr(r.src_tok), _ptr(self.workspace), n)
+
+    def _pointers(self):
+        """Addresses of the outputs and of the workspace, and its bytes."""
+        r, ws = self.routing, self.workspace
+        at = (r.topk_idx.data_ptr(), r.topk_w.data_ptr(), r.counts.data_ptr(), r.offsets.data_ptr(),
+              r.row_of.data_ptr(), r.src_tok.data_ptr(), ws.data_ptr(), ws.numel())
+        if (self.size, at) != self._checked:
+            (T, E, K), i32 = self.size, torch.int32
+            _need(r.topk_idx, i32, (T, K), "buffers.routing.topk_idx")
+            _need(r.topk_w, torch.float32, (T, K), "buffers.routing.topk_w")
+            _need(r.counts, i32, (E,), "buffers.routing.counts")
+            _need(r.offsets, i32, (E + 1,), "buffers.routing.offsets")
+            _need(r.row_of, i32, (T, K), "buffers.routing.row_of")
+            _need(r.src_tok, i32, (T * K,), "buffers.routing.src_tok")
+            _need(ws, torch.uint8, (ws.numel(),), "buffers.workspace")
+            self._hold((self.size, at), r.topk_idx, r.topk_w, r.counts, r.offsets, r.row_of, r.src_tok, ws)
+        return at
 
 
 def route_scored(logits, K: int, rule: RouteRule, sel_bias=None, buffers: RouteBuffers | None = None,
@@ -301,7 +331,7 @@ def route_scored(logits, K: int, rule: RouteRule, sel_bias=None, buffers: RouteB
         buffers = RouteBuffers(T, E, K, logits.device)
     elif buffers.size != (T, E, K):
         raise ValueError(f"buffers are for (T, E, K) = {buffers.size}, not {(T, E, K)}")
-    _check(lib.moe_route_scored(lp, bp, T, E, K, rule._c, *buffers._args, _stream_of(logits, stream)),
+    _check(lib.moe_route_scored(lp, bp, T, E, K, rule._c, *buffers._pointers(), _stream_of(logits, stream)),
            "moe_route_scored")
     return buffers.routing
 

@@ -31,3 +31,66 @@ def test_copies_of_a_rule_pass_their_own_values(how):
     assert rule._c == ctypes.addressof(rule._struct)
     assert _fields(moe._RouteRule.from_address(rule._c)) == (1, 8, 4, 2, 1, 2.5)
     assert len(others) == 64
+
+
+# ------------------------------------------------------------------ RouteBuffers
+ROUTING = ("topk_idx", "topk_w", "counts", "offsets", "row_of", "src_tok")
+
+
+@pytest.fixture
+def called(monkeypatch):
+    """The arguments of the library's calls, which are recorded instead of made; tensors may lie on the CPU."""
+    calls = []
+
+    class Recorder:
+        def __getattr__(self, name):
+            if name.endswith("_size"):
+                return getattr(real, name)
+            return lambda *a: calls.append((name, a)) or 0
+
+    real = moe.lib
+    monkeypatch.setattr(moe, "lib", Recorder())
+    monkeypatch.setattr(moe, "_need", lambda t, dtype, shape, name: t)
+    monkeypatch.setattr(moe, "_in", lambda t, dtype, shape, name: t.data_ptr())
+    monkeypatch.setattr(moe, "_stream_of", lambda t, stream=None: 0)
+    return calls
+
+
+def test_buffers_pass_the_addresses_of_their_own_tensors(called):
+    """Copies of the buffers, and buffers one of whose tensors was replaced or given other memory."""
+    logits, rule = torch.zeros(40, 16), moe.RouteRule()
+    first = moe.RouteBuffers(40, 16, 2, "cpu")
+    moe.route_scored(logits, 2, rule, buffers=first)
+    replaced = moe.RouteBuffers(40, 16, 2, "cpu")
+    moe.route_scored(logits, 2, rule, buffers=replaced)
+    replaced.routing.topk_w = torch.empty(40, 2)
+    replaced.routing.row_of.data = torch.empty(40, 2, dtype=torch.int32)
+    replaced.workspace = torch.empty(replaced.workspace.numel() + 16, dtype=torch.uint8)
+    for b in (copy.deepcopy(first), pickle.loads(pickle.dumps(first)), replaced, first):
+        called.clear()
+        r = moe.route_scored(logits, 2, rule, buffers=b)
+        (_, args), = called
+        assert r is b.routing
+        assert args[6:14] == (*[getattr(r, k).data_ptr() for k in ROUTING], b.workspace.data_ptr(), b.workspace.numel())
+
+
+@pytest.mark.gpu
+def test_buffers_that_are_copied_or_replaced():
+    logits, rule = torch.randn(700, 64, device="cuda"), moe.RouteRule("sigmoid", 8, 4, 2)
+    first = moe.RouteBuffers(700, 64, 6)
+    kept = {k: getattr(moe.route_scored(logits, 6, rule, buffers=first), k).clone() for k in ROUTING}
+    other = copy.deepcopy(first)
+    flipped = {k: getattr(moe.route_scored(-logits, 6, rule), k) for k in ROUTING}
+    moe.route_scored(-logits, 6, rule, buffers=other)
+    for k in ROUTING:
+        assert torch.equal(getattr(first.routing, k), kept[k]) and torch.equal(getattr(other.routing, k), flipped[k])
+    first.routing.topk_idx = torch.empty_like(kept["topk_idx"])
+    assert torch.equal(moe.route_scored(-logits, 6, rule, buffers=first).topk_idx, flipped["topk_idx"])
+    first.routing.topk_w.data = torch.empty(10, 6, device="cuda")
+    with pytest.raises(ValueError, match="topk_w"):
+        moe.route_scored(logits, 6, rule, buffers=first)
+    other.workspace = torch.empty(16, dtype=torch.uint8, device="cuda")
+    with pytest.raises(moe.MoEError, match="WORKSPACE"):
+        moe.route_scored(logits, 6, rule, buffers=other)
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.route_scored(logits, 6, rule, buffers=moe.RouteBuffers(700, 64, 6, "cpu"))
