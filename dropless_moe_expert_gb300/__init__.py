@@ -458,17 +458,15 @@ def norm_residual(r, y=None, *, gamma_post=None, gate=None, gamma_pre=None, res_
     gate * norm(y) * gamma_post and n = norm(r') * gamma_pre (RMS norms; parts
     without their tensor are left out).  r [T, d] bf16 or fp32, y [T, d] bf16,
     gammas [d] fp32, gate fp32 [d] (per channel) or [T, 1] (per token).
-    Without y: n = norm(r) * gamma_pre, and the result's r is r itself.
-    ``out.r`` may be r (updated in place)."""
+    Without y: n = norm(r) * gamma_pre, and the result's r is r itself (``out``
+    keeps its own).  ``out.r`` may be r (updated in place)."""
     T, d, kind, rp, yp, postp, gatep, prep = _norm_args(r, y, gamma_post, gate, gamma_pre)
     key = (T, d, r.dtype, yp is not None, postp is not None, prep is not None)
     if out is None:
         out = NormResidual.empty(*key, r.device)
     _check(lib.moe_norm_residual(rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep, eps, T, d,
                                  *out._pointers(key), _stream_of(r, stream)), "moe_norm_residual")
-    if y is None:
-        out.r = r
-    return out
+    return out if y is not None else NormResidual(r, out.n, None, out.rstd_pre)
 
 
 def norm_residual_backward(r, dr, dn=None, y=None, *, gamma_post=None, gate=None, gamma_pre=None,

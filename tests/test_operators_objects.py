@@ -94,3 +94,29 @@ def test_buffers_that_are_copied_or_replaced():
         moe.route_scored(logits, 6, rule, buffers=other)
     with pytest.raises(ValueError, match="CUDA"):
         moe.route_scored(logits, 6, rule, buffers=moe.RouteBuffers(700, 64, 6, "cpu"))
+
+
+# ------------------------------------------------------------------ NormResidual
+def test_buffers_keep_their_stream_in_a_call_without_y(called):
+    """The form without y leaves ``out`` as it was; a later call with y does not write the earlier one's input."""
+    T, d = 5, 64
+    r, y, g = torch.zeros(T, d), torch.zeros(T, d, dtype=torch.bfloat16), torch.ones(d)
+    out = moe.NormResidual.empty(T, d, torch.float32, post=False, device="cpu")
+    own = out.r
+    o = moe.norm_residual(r, gamma_pre=g, out=out)
+    assert o.r is r and o.n is out.n and o.rstd_pre is out.rstd_pre and out.r is own
+    o = moe.norm_residual(r, y, gamma_pre=g, out=out)
+    assert o is out and called[-1][1][11] == own.data_ptr()
+
+
+@pytest.mark.gpu
+def test_one_buffer_for_two_forms():
+    T, d = 33, 320
+    r, g = torch.randn(T, d, device="cuda"), torch.rand(d, device="cuda")
+    y = torch.randn(T, d, device="cuda").to(torch.bfloat16)
+    raw, out = r.clone(), moe.NormResidual.empty(T, d, torch.float32, post=False)
+    n = moe.norm_residual(r, gamma_pre=g, out=out).n.clone()
+    with_y = moe.norm_residual(r, y, gamma_pre=g, out=out)
+    ref = moe.norm_residual(raw, y, gamma_pre=g)
+    assert torch.equal(r, raw) and torch.equal(with_y.r, ref.r) and torch.equal(with_y.n, ref.n)
+    assert torch.equal(moe.norm_residual(r, gamma_pre=g, out=out).n, n) and torch.equal(with_y.r, ref.r)
