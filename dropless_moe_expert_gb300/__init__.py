@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from dataclasses import dataclass, field
+from dataclasses import dataclass
 
 import torch
 
@@ -351,12 +351,11 @@ def route_scored_backward(logits, topk_idx, dw, rule: RouteRule, out=None, strea
 
 # ------------------------------------------------------------------ norms, gate and residual
 @dataclass
-class NormResidual:
+class NormResidual(_Buffers):
     r: torch.Tensor                      # [T, d], the residual stream
     n: torch.Tensor | None = None        # [T, d] bf16, what the next layer reads
     rstd_post: torch.Tensor | None = None   # [T] fp32
     rstd_pre: torch.Tensor | None = None    # [T] fp32
-    _made: tuple | None = field(default=None, repr=False, compare=False)  # by empty(): its arguments and tensors
 
     @classmethod
     def empty(cls, T: int, d: int, dtype=torch.bfloat16, y=True, post=True, pre=True, device="cuda"):
@@ -365,16 +364,19 @@ class NormResidual:
         def make(on, dt, *shape):
             return torch.empty(shape, dtype=dt, device=device) if on else None
 
-        out = cls(make(y, dtype, T, d), make(pre, torch.bfloat16, T, d), make(post, torch.float32, T),
-                  make(pre, torch.float32, T))
-        out._made = ((T, d, dtype, y, post, pre), out.r, out.n, out.rstd_post, out.rstd_pre)
-        return out
+        return cls(make(y, dtype, T, d), make(pre, torch.bfloat16, T, d), make(post, torch.float32, T),
+                   make(pre, torch.float32, T))
+
+    def _addresses(self, key):
+        """Of the buffers that the call (T, d, dtype, y, post, pre) writes."""
+        _, _, _, y, post, pre = key
+        return (_ptr(self.r) if y else None, _ptr(self.n) if pre else None, _ptr(self.rstd_post) if post else None,
+                _ptr(self.rstd_pre) if pre else None)
 
     def _pointers(self, key):
-        """Addresses of the buffers; those that empty() made for the same arguments need no check."""
-        m = self._made
-        if m is None or m[0] != key or m[1] is not self.r or m[2] is not self.n or m[3] is not self.rstd_post \
-                or m[4] is not self.rstd_pre:
+        """The addresses, checked."""
+        at = self._addresses(key)
+        if (key, at) != self._checked:
             T, d, dtype, y, post, pre = key
             if y:
                 _need(self.r, dtype, (T, d), "out.r")
@@ -383,18 +385,18 @@ class NormResidual:
                 _need(self.rstd_pre, torch.float32, (T,), "out.rstd_pre")
             if post:
                 _need(self.rstd_post, torch.float32, (T,), "out.rstd_post")
-        return (_ptr(self.r) if key[3] else None, _ptr(self.n), _ptr(self.rstd_post), _ptr(self.rstd_pre))
+            self._hold((key, at), self.r, self.n, self.rstd_post, self.rstd_pre)
+        return at
 
 
 @dataclass
-class NormResidualGrads:
+class NormResidualGrads(_Buffers):
     dr: torch.Tensor                        # [T, d], the residual's type
     dy: torch.Tensor | None = None          # [T, d] bf16
     dgamma_pre: torch.Tensor | None = None  # [d] fp32
     dgamma_post: torch.Tensor | None = None
     dgate: torch.Tensor | None = None       # shaped like the gate
     workspace: torch.Tensor | None = None
-    _made: tuple | None = field(default=None, repr=False, compare=False)  # by empty(): its arguments and tensors
 
     @classmethod
     def empty(cls, T: int, d: int, dtype=torch.bfloat16, y=True, post=True, pre=True, gate="none", device="cuda"):
@@ -405,17 +407,26 @@ class NormResidualGrads:
         f32, n = torch.float32, int(lib.moe_norm_residual_backward_workspace_size(T, d))
         if n == 0:
             raise MoEError(2, "moe_norm_residual_backward_workspace_size")
-        out = cls(make(True, dtype, T, d), make(y, torch.bfloat16, T, d), make(pre, f32, d), make(post, f32, d),
-                  make(gate != "none", f32, *((d,) if gate == "channel" else (T, 1))), make(True, torch.uint8, n))
-        out._made = ((T, d, dtype, y, post, pre, gate), out.dr, out.dy, out.dgamma_pre, out.dgamma_post, out.dgate,
-                     out.workspace)
-        return out
+        return cls(make(True, dtype, T, d), make(y, torch.bfloat16, T, d), make(pre, f32, d), make(post, f32, d),
+                   make(gate != "none", f32, *((d,) if gate == "channel" else (T, 1))), make(True, torch.uint8, n))
+
+    def _addresses(self, key):
+        """Of the buffers that the call (T, d, dtype, y, post, pre, gate) writes, and the workspace's bytes."""
+        _, _, _, y, post, pre, gate = key
+        ws = self.workspace
+        return (_ptr(self.dr), _ptr(self.dy) if y else None, _ptr(self.dgamma_pre) if pre else None,
+                _ptr(self.dgamma_post) if post else None, _ptr(self.dgate) if gate != "none" else None, ws.data_ptr(),
+                ws.numel())
 
     def _pointers(self, key):
-        m = self._made
-        if m is None or m[0] != key or m[1] is not self.dr or m[2] is not self.dy or m[3] is not self.dgamma_pre \
-                or m[4] is not self.dgamma_post or m[5] is not self.dgate or m[6] is not self.workspace:
+        """The addresses, checked."""
+        if self.workspace is None:
+            n = int(lib.moe_norm_residual_backward_workspace_size(*key[:2]))
+            self.workspace = _empty((n,), torch.uint8, _need(self.dr, key[2], key[:2], "out.dr"))
+        at = self._addresses(key)
+        if (key, at) != self._checked:
             T, d, dtype, y, post, pre, gate = key
+            ws = self.workspace
             _need(self.dr, dtype, (T, d), "out.dr")
             if y:
                 _need(self.dy, torch.bfloat16, (T, d), "out.dy")
@@ -425,12 +436,9 @@ class NormResidualGrads:
                 _need(self.dgamma_post, torch.float32, (d,), "out.dgamma_post")
             if gate != "none":
                 _need(self.dgate, torch.float32, (d,) if gate == "channel" else (T, 1), "out.dgate")
-            if self.workspace is None:
-                n = int(lib.moe_norm_residual_backward_workspace_size(T, d))
-                self.workspace = _empty((n,), torch.uint8, self.dr)
-        ws = self.workspace
-        return (_ptr(self.dr), _ptr(self.dy), _ptr(self.dgamma_pre), _ptr(self.dgamma_post), _ptr(self.dgate),
-                ws.data_ptr(), ws.numel())
+            _need(ws, torch.uint8, (ws.numel(),), "out.workspace")
+            self._hold((key, at), self.dr, self.dy, self.dgamma_pre, self.dgamma_post, self.dgate, ws)
+        return at
 
 
 _GATES = ("none", "channel", "token")
@@ -464,8 +472,11 @@ def norm_residual(r, y=None, *, gamma_post=None, gate=None, gamma_pre=None, res_
     key = (T, d, r.dtype, yp is not None, postp is not None, prep is not None)
     if out is None:
         out = NormResidual.empty(*key, r.device)
+        at = out._addresses(key)
+    else:
+        at = out._pointers(key)
     _check(lib.moe_norm_residual(rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep, eps, T, d,
-                                 *out._pointers(key), _stream_of(r, stream)), "moe_norm_residual")
+                                 *at, _stream_of(r, stream)), "moe_norm_residual")
     return out if y is not None else NormResidual(r, out.n, None, out.rstd_pre)
 
 
@@ -483,9 +494,12 @@ def norm_residual_backward(r, dr, dn=None, y=None, *, gamma_post=None, gate=None
     key = (T, d, r.dtype, yp is not None, postp is not None, prep is not None, _GATES[kind])
     if out is None:
         out = NormResidualGrads.empty(*key, r.device)
+        at = out._addresses(key)
+    else:
+        at = out._pointers(key)
     _check(lib.moe_norm_residual_backward(
         rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep, rpp, rqp, drp, dnp, T, d,
-        *out._pointers(key), _stream_of(r, stream)), "moe_norm_residual_backward")
+        *at, _stream_of(r, stream)), "moe_norm_residual_backward")
     return out
 
 

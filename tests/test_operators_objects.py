@@ -120,3 +120,87 @@ def test_one_buffer_for_two_forms():
     ref = moe.norm_residual(raw, y, gamma_pre=g)
     assert torch.equal(r, raw) and torch.equal(with_y.r, ref.r) and torch.equal(with_y.n, ref.n)
     assert torch.equal(moe.norm_residual(r, gamma_pre=g, out=out).n, n) and torch.equal(with_y.r, ref.r)
+
+
+@pytest.mark.gpu
+def test_norm_buffers_with_other_memory():
+    """Buffers that were accepted once and then given other memory: written there where it fits, else refused."""
+    T, d, bf = 40, 256, torch.bfloat16
+    r, g = torch.randn(T, d, device="cuda"), torch.rand(d, device="cuda")
+    y = torch.randn(T, d, device="cuda").to(bf)
+    ref = moe.norm_residual(r, y, gamma_pre=g)
+    out = moe.NormResidual.empty(T, d, torch.float32, post=False)
+    moe.norm_residual(r, y, gamma_pre=g, out=out)
+    out.n.data = torch.zeros(T, d, dtype=bf, device="cuda")
+    out.r.set_(torch.zeros(2 * T, d, device="cuda")[T:])
+    moe.norm_residual(r, y, gamma_pre=g, out=out)
+    assert torch.equal(out.n, ref.n) and torch.equal(out.r, ref.r)
+    twin = copy.deepcopy(out)
+    moe.norm_residual(2 * r, y, gamma_pre=g, out=twin)
+    assert torch.equal(out.r, ref.r) and not torch.equal(twin.r, ref.r)
+    dr = torch.randn(T, d, device="cuda")
+    grads = moe.NormResidualGrads.empty(T, d, torch.float32, post=False)
+
+    def backward(o):
+        return moe.norm_residual_backward(ref.r, dr, y, y, gamma_pre=g, rstd_pre=ref.rstd_pre, out=o)
+
+    gref = moe.norm_residual_backward(ref.r, dr, y, y, gamma_pre=g, rstd_pre=ref.rstd_pre)
+    backward(grads)
+    grads.dgamma_pre.data = torch.zeros(d, device="cuda")
+    grads.workspace = None
+    backward(grads)
+    assert torch.equal(grads.dgamma_pre, gref.dgamma_pre) and torch.equal(grads.dy, gref.dy)
+
+
+@pytest.mark.gpu
+def test_norm_buffers_are_refused_once_they_do_not_fit():
+    """The same objects, now shorter, of another type or on the host: no call reads or writes them."""
+    T, d, bf = 40, 256, torch.bfloat16
+    r, g = torch.randn(T, d, device="cuda"), torch.rand(d, device="cuda")
+    y = torch.randn(T, d, device="cuda").to(bf)
+    ref = moe.norm_residual(r, y, gamma_pre=g)
+    before = moe.launch_count()
+    for name, other, what in (("n", torch.zeros(3, d, dtype=bf, device="cuda"), ValueError),
+                              ("r", torch.zeros(T, d, dtype=bf, device="cuda"), TypeError),
+                              ("rstd_pre", torch.zeros(T - 1, device="cuda"), ValueError)):
+        out = moe.NormResidual.empty(T, d, torch.float32, post=False)
+        out._pointers((T, d, torch.float32, True, False, True))      # as a call does
+        getattr(out, name).data = other
+        with pytest.raises(what, match="out." + name):
+            moe.norm_residual(r, y, gamma_pre=g, out=out)
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.norm_residual(r, y, gamma_pre=g, out=moe.NormResidual.empty(T, d, torch.float32, device="cpu"))
+    for name, other in (("dy", torch.zeros(T, 2 * d, dtype=bf, device="cuda")[:, :d]), ("dr", torch.zeros(1, device="cuda")),
+                        ("workspace", torch.zeros(1 << 20, dtype=torch.uint8)),
+                        ("workspace", torch.zeros(1 << 20, device="cuda")),
+                        ("workspace", torch.zeros(4096, dtype=torch.uint8, device="cuda"))):
+        grads = moe.NormResidualGrads.empty(T, d, torch.float32, post=False)
+        setattr(grads, name, other)
+        with pytest.raises((ValueError, TypeError, moe.MoEError)):
+            moe.norm_residual_backward(ref.r, r, y, y, gamma_pre=g, rstd_pre=ref.rstd_pre, out=grads)
+    assert moe.launch_count() == before
+
+
+def test_norm_buffers_are_checked_again(called, monkeypatch):
+    """The check runs once for buffers that stay as they are, and again for those that were given other memory."""
+    checked = []
+    monkeypatch.setattr(moe, "_need", lambda t, dtype, shape, name: checked.append(name) or t)
+    T, d, f32 = 4, 64, torch.float32
+    r, y, g = torch.zeros(T, d), torch.zeros(T, d, dtype=torch.bfloat16), torch.ones(d)
+    out = moe.NormResidual.empty(T, d, f32, post=False, device="cpu")
+    grads = moe.NormResidualGrads.empty(T, d, f32, post=False, device="cpu")
+
+    def call():
+        checked.clear()
+        moe.norm_residual(r, y, gamma_pre=g, out=out)
+        moe.norm_residual_backward(r, r, y, y, gamma_pre=g, rstd_pre=g[:T], out=grads)
+        return set(checked)
+
+    assert {"out.r", "out.n", "out.rstd_pre", "out.dr", "out.dy", "out.dgamma_pre", "out.workspace"} <= call()
+    assert not call()
+    out.n.data = torch.zeros(T - 1, d, dtype=torch.bfloat16)
+    assert "out.n" in call() and not call()
+    grads.dy.resize_(8 * T, d)
+    assert "out.dy" in call() and not call()
+    grads.workspace = torch.zeros(16, dtype=torch.uint8)
+    assert "out.workspace" in call()
