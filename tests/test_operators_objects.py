@@ -204,3 +204,69 @@ def test_norm_buffers_are_checked_again(called, monkeypatch):
     assert "out.dy" in call() and not call()
     grads.workspace = torch.zeros(16, dtype=torch.uint8)
     assert "out.workspace" in call()
+
+
+# ------------------------------------------------------------------ GradClipper
+def test_clipper_passes_where_the_tensors_lie(called):
+    """Gradients and outputs that were given other memory, and copies of a clipper."""
+    grads = [torch.ones(n) for n in (5, 40, 0, 7)]
+    outs = [torch.ones(n) for n in (5, 40, 0, 7)]
+
+    def check(clipper, gs, os):
+        called.clear()
+        clipper(1.0)
+        clipper()
+        (_, clip), (_, norm) = called
+        for args in (clip, norm):
+            assert [p or 0 for p in args[0]] == [g.data_ptr() for g in gs]
+        assert (clip[1] is None) == (os is None)
+        assert os is None or [p or 0 for p in clip[1]] == [o.data_ptr() for o in os]
+        assert clip[6] == norm[4] == clipper.norm.data_ptr()
+
+    beside, in_place = moe.GradClipper(grads, outs), moe.GradClipper(grads)
+    check(beside, grads, outs)
+    check(in_place, grads, None)
+    grads[1].data = torch.ones(40)
+    grads[3].set_(torch.ones(20)[3:10])
+    outs[0].data = torch.ones(5)
+    check(beside, grads, outs)
+    check(in_place, grads, None)
+    for twin in (copy.copy(beside), copy.deepcopy(beside), pickle.loads(pickle.dumps(beside))):
+        check(twin, twin.grads, twin.outs)
+    assert [tuple(g.shape) for g in copy.deepcopy(in_place).grads] == [(5,), (40,), (0,), (7,)]
+
+
+def test_clipper_holds_the_memory_whose_address_it_keeps(called):
+    """Memory that a call went by is not given to another tensor while its address is kept."""
+    grads = [torch.ones(1 << 20)]
+    clipper = moe.GradClipper(grads)
+    old = grads[0].data_ptr()
+    grads[0].data = torch.ones(1 << 20)
+    later = [torch.empty(1 << 20) for _ in range(4)]
+    assert all(t.data_ptr() != old for t in later)
+
+
+@pytest.mark.gpu
+def test_clipper_follows_its_tensors():
+    g = torch.Generator(device="cuda").manual_seed(3)
+    grads = [torch.randn(n, generator=g, device="cuda").to(k) for n, k in ((5000, torch.float32), (333, torch.bfloat16))]
+    clipper = moe.GradClipper(grads)
+    clipper(0.5)
+    old = grads[0].detach()
+    kept = old.clone()
+    fresh = torch.randn(5000, generator=g, device="cuda")
+    grads[0].data = fresh.clone()
+    want = [fresh.clone(), grads[1].clone()]
+    ref = moe.GradClipper(want)(0.5)
+    assert torch.equal(clipper(0.5), ref) and all(torch.equal(a, b) for a, b in zip(grads, want))
+    assert torch.equal(old, kept)                       # the memory that the gradient had left
+    twin = copy.deepcopy(clipper)
+    norm = clipper().clone()
+    assert torch.equal(twin(), norm) and twin.grads[0].data_ptr() != grads[0].data_ptr()
+    for other, what in ((torch.zeros(5, device="cuda"), ValueError), (torch.zeros(5000, 2, device="cuda")[:, 0], ValueError),
+                        (torch.zeros(5000, dtype=torch.bfloat16, device="cuda"), TypeError)):
+        grads[0].data = other
+        with pytest.raises(what, match=r"grads\[0\]"):
+            clipper(0.5)
+    with pytest.raises(AttributeError):
+        clipper.norm = torch.zeros(1, device="cuda")
