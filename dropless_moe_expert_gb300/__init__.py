@@ -545,8 +545,25 @@ class GradClipper:
             if self.outs is not None:
                 _need(self.outs[i], dtype, shape, f"outs[{i}]")
 
+    def _check_overlap(self, at):
+        """No element is written that is read or written elsewhere too: it would be scaled twice, or when it is late."""
+        n = len(self.grads)
+        nbytes = [m * (2 if k else 4) for m, k in zip(self._sizes, self._kinds)]
+        spans = [(a, a + m, True) for a, m in zip(at if self.outs is None else at[n:2 * n], nbytes) if m]
+        if self.outs is not None:
+            spans += [(a, a + m, False) for a, o, m in zip(at, at[n:], nbytes) if m and a != o]
+        spans.sort()
+        written = used = 0  # the ends of what lies before
+        for first, end, write in spans:
+            if first < (used if write else written):
+                raise ValueError("the tensors to be written overlap each other or another gradient")
+            used = max(used, end)
+            if write:
+                written = max(written, end)
+
     def _take_addresses(self):
         n, at = len(self.grads), [t.data_ptr() for t in self._tensors]
+        self._check_overlap(at)
         # held, so that no other tensor comes to lie at one of these addresses
         self._held = [t.untyped_storage() for t in self._tensors]
         self._ptrs = (ctypes.c_void_p * n)(*at[:n])

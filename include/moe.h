@@ -233,7 +233,8 @@ moe_status_t moe_norm_residual_backward(const void *r_out, int residual_fp32, co
  * grads[i] (and outs[i], of the same type) are device pointers to sizes[i]
  * (>= 0) contiguous elements, fp32 or bf16 by kinds[i], aligned to their type
  * only; the four arrays themselves are HOST memory, read before the call
- * returns.  outs NULL clips in place.  Squares are summed in fp32 per CTA, the
+ * returns.  outs NULL clips in place.  What is written must not overlap any
+ * other tensor that is read or written (outs[i] may be grads[i] itself).  Squares are summed in fp32 per CTA, the
  * CTAs' sums in fp64, in a fixed order: deterministic (entries beyond 1.8e19
  * give an infinite norm).  An infinite norm
  * scales by 0 and a NaN by NaN, as the formula does.  max_norm > 0 (INFINITY

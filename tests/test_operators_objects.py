@@ -270,3 +270,22 @@ def test_clipper_follows_its_tensors():
             clipper(0.5)
     with pytest.raises(AttributeError):
         clipper.norm = torch.zeros(1, device="cuda")
+
+
+def test_clipper_refuses_tensors_that_are_written_over(called):
+    """What a call writes overlaps nothing else that it reads or writes, but an output may be its own gradient."""
+    flat, other = torch.ones(100), torch.ones(100)
+    a, b, c = flat[:40], flat[40:90], flat[90:]
+    moe.GradClipper([a, b, c])
+    moe.GradClipper([a, a, flat], [other[:40], other[40:80], torch.ones(100)])   # gradients are only read
+    moe.GradClipper([a, b], [a, b])                                              # in place, said twice
+    moe.GradClipper([a, b, flat[:0]], [other[10:50], other[50:], flat[20:20]])   # nothing lies in no elements
+    for grads, outs in (([a, a], None), ([flat, c], None), ([a, flat[39:60]], None), ([a], [flat[1:41]]),
+                        ([a, b], [other[:40], other[39:89]]), ([a, b], [flat[50:90], other[:50]]),
+                        ([a, a], [a, other[:40]]), ([a, flat], [other[:40], flat])):
+        with pytest.raises(ValueError, match="overlap"):
+            moe.GradClipper(grads, outs)
+    clipper = moe.GradClipper([a, b])
+    b.set_(flat[30:80])
+    with pytest.raises(ValueError, match="overlap"):
+        clipper(1.0)
