@@ -4,9 +4,12 @@ Thin ctypes binding over the C ABI in ``include/moe.h`` (library
 ``libmoe_gb300.so`` built in-tree by ``build.py``).  Functions carry the C
 names without the ``moe_`` prefix, take torch tensors (device memory only,
 any stream), check dtypes/shapes/contiguity, and pass raw pointers plus the
-current CUDA stream.  Every step of the layer runs in the library's kernels;
-there is no fallback: if the library is missing, importing this package
-raises.
+current CUDA stream, or the one given as ``stream``.  What a call allocates is
+safe on both: it belongs to the stream of the call, and its memory is not used
+again before the current one has passed the tensor's end.  (Either waits for
+the other, where it reads the other's results, by the caller's doing.)  Every
+step of the layer runs in the library's kernels; there is no fallback: if the
+library is missing, importing this package raises.
 """
 from __future__ import annotations
 
@@ -198,8 +201,31 @@ class _Buffers:
         return {k: v for k, v in self.__dict__.items() if k not in ("_checked", "_held")}
 
 
-def _empty(shape, dtype, like):
-    return torch.empty(shape, dtype=dtype, device=like.device)
+def _on(stream, make):
+    """make()'s tensors for a call on ``stream`` (None: the current one): they
+    belong to that stream, so that their memory is not given to work of another
+    one while the call still uses it, nor back to that stream before the
+    current one, which may read the results, has passed their end."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        made = make()
+    reader = torch.cuda.current_stream()
+    for t in [made] if isinstance(made, torch.Tensor) else _tensors_of(made):
+        t.record_stream(reader)
+    return made
+
+
+def _tensors_of(buffers):
+    for v in vars(buffers).values():
+        if isinstance(v, torch.Tensor):
+            yield v
+        elif isinstance(v, Routing):
+            yield from _tensors_of(v)
+
+
+def _empty(shape, dtype, like, stream=None):
+    return _on(stream, lambda: torch.empty(shape, dtype=dtype, device=like.device))
 
 
 # ------------------------------------------------------------------ a0
@@ -216,12 +242,12 @@ def router_logits(x, Wr, bias=None, out=None, workspace=None, stream=None):
     _need(Wr, torch.float32, (d, E), "Wr")
     if bias is not None:
         _need(bias, torch.float32, (E,), "bias")
-    out = _empty((T, E), torch.float32, x) if out is None else _need(out, torch.float32, (T, E), "logits")
+    out = _empty((T, E), torch.float32, x, stream) if out is None else _need(out, torch.float32, (T, E), "logits")
     nbytes = router_workspace_size(d, E)
     if nbytes == 0:
         raise MoEError(2, "moe_router_workspace_size")
     if workspace is None:
-        workspace = _empty((nbytes,), torch.uint8, x)
+        workspace = _empty((nbytes,), torch.uint8, x, stream)
     _check(lib.moe_router_logits(_ptr(x), _ptr(Wr), _ptr(bias), T, d, E, _ptr(out), _ptr(workspace),
                                  workspace.numel(), _stream(stream)), "moe_router_logits")
     return out
@@ -246,11 +272,12 @@ def route(logits, K: int, workspace=None, stream=None) -> Routing:
     T, E = logits.shape
     _need(logits, torch.float32, (T, E), "logits")
     i32 = torch.int32
-    r = Routing(_empty((T, K), i32, logits), _empty((T, K), torch.float32, logits), _empty((E,), i32, logits),
-                _empty((E + 1,), i32, logits), _empty((T, K), i32, logits), _empty((T * K,), i32, logits))
+    r = Routing(_empty((T, K), i32, logits, stream), _empty((T, K), torch.float32, logits, stream),
+                _empty((E,), i32, logits, stream), _empty((E + 1,), i32, logits, stream),
+                _empty((T, K), i32, logits, stream), _empty((T * K,), i32, logits, stream))
     nbytes = route_workspace_size(T, E, K)
     if workspace is None:
-        workspace = _empty((max(nbytes, 4),), torch.uint8, logits)
+        workspace = _empty((max(nbytes, 4),), torch.uint8, logits, stream)
     _check(lib.moe_route(_ptr(logits), T, E, K, _ptr(r.topk_idx), _ptr(r.topk_w), _ptr(r.counts),
                          _ptr(r.offsets), _ptr(r.row_of), _ptr(r.src_tok), _ptr(workspace),
                          workspace.numel() * workspace.element_size(), _stream(stream)), "moe_route")
@@ -328,7 +355,7 @@ def route_scored(logits, K: int, rule: RouteRule, sel_bias=None, buffers: RouteB
     lp = _in(logits, torch.float32, (T, E), "logits")
     bp = None if sel_bias is None else _in(sel_bias, torch.float32, (E,), "sel_bias")
     if buffers is None:
-        buffers = RouteBuffers(T, E, K, logits.device)
+        buffers = _on(stream, lambda: RouteBuffers(T, E, K, logits.device))
     elif buffers.size != (T, E, K):
         raise ValueError(f"buffers are for (T, E, K) = {buffers.size}, not {(T, E, K)}")
     _check(lib.moe_route_scored(lp, bp, T, E, K, rule._c, *buffers._pointers(), _stream_of(logits, stream)),
@@ -343,7 +370,7 @@ def route_scored_backward(logits, topk_idx, dw, rule: RouteRule, out=None, strea
     args = (_in(logits, torch.float32, (T, E), "logits"), _in(topk_idx, torch.int32, (T, K), "topk_idx"),
             _in(dw, torch.float32, (T, K), "dw"))
     if out is None:
-        out = _empty((T, E), torch.float32, logits)
+        out = _empty((T, E), torch.float32, logits, stream)
     _check(lib.moe_route_scored_backward(*args, T, E, K, rule._c, _in(out, torch.float32, (T, E), "dlogits"),
                                          _stream_of(logits, stream)), "moe_route_scored_backward")
     return out
@@ -418,11 +445,11 @@ class NormResidualGrads(_Buffers):
                 _ptr(self.dgamma_post) if post else None, _ptr(self.dgate) if gate != "none" else None, ws.data_ptr(),
                 ws.numel())
 
-    def _pointers(self, key):
+    def _pointers(self, key, stream=None):
         """The addresses, checked."""
         if self.workspace is None:
             n = int(lib.moe_norm_residual_backward_workspace_size(*key[:2]))
-            self.workspace = _empty((n,), torch.uint8, _need(self.dr, key[2], key[:2], "out.dr"))
+            self.workspace = _empty((n,), torch.uint8, _need(self.dr, key[2], key[:2], "out.dr"), stream)
         at = self._addresses(key)
         if (key, at) != self._checked:
             T, d, dtype, y, post, pre, gate = key
@@ -471,7 +498,7 @@ def norm_residual(r, y=None, *, gamma_post=None, gate=None, gamma_pre=None, res_
     T, d, kind, rp, yp, postp, gatep, prep = _norm_args(r, y, gamma_post, gate, gamma_pre)
     key = (T, d, r.dtype, yp is not None, postp is not None, prep is not None)
     if out is None:
-        out = NormResidual.empty(*key, r.device)
+        out = _on(stream, lambda: NormResidual.empty(*key, r.device))
         at = out._addresses(key)
     else:
         at = out._pointers(key)
@@ -493,10 +520,10 @@ def norm_residual_backward(r, dr, dn=None, y=None, *, gamma_post=None, gate=None
     rpp = _in(rstd_post, torch.float32, (T,), "rstd_post") if postp is not None else None
     key = (T, d, r.dtype, yp is not None, postp is not None, prep is not None, _GATES[kind])
     if out is None:
-        out = NormResidualGrads.empty(*key, r.device)
+        out = _on(stream, lambda: NormResidualGrads.empty(*key, r.device))
         at = out._addresses(key)
     else:
-        at = out._pointers(key)
+        at = out._pointers(key, stream)
     _check(lib.moe_norm_residual_backward(
         rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep, rpp, rqp, drp, dnp, T, d,
         *at, _stream_of(r, stream)), "moe_norm_residual_backward")
@@ -595,7 +622,8 @@ def permute(x, row_of, out=None, stream=None):
     K = row_of.shape[1]
     _need(x, torch.bfloat16, (T, d), "x")
     _need(row_of, torch.int32, (T, K), "row_of")
-    out = _empty((T * K, d), torch.bfloat16, x) if out is None else _need(out, torch.bfloat16, (T * K, d), "x_perm")
+    out = _empty((T * K, d), torch.bfloat16, x, stream) if out is None else \
+        _need(out, torch.bfloat16, (T * K, d), "x_perm")
     _check(lib.moe_permute(_ptr(x), _ptr(row_of), T, K, d, _ptr(out), _stream(stream)), "moe_permute")
     return out
 
@@ -614,7 +642,7 @@ def grouped_gemm1_swiglu(x_perm, offsets, W1, h=None, preact=None, stream=None):
     _need(x_perm, torch.bfloat16, (TK, d), "x_perm")
     _need(offsets, torch.int32, (E + 1,), "offsets")
     _need(W1, torch.bfloat16, (E, 2 * f, d), "W1")
-    h = _empty((TK, f), torch.bfloat16, x_perm) if h is None else _need(h, torch.bfloat16, (TK, f), "h")
+    h = _empty((TK, f), torch.bfloat16, x_perm, stream) if h is None else _need(h, torch.bfloat16, (TK, f), "h")
     if preact is None:
         _check(lib.moe_grouped_gemm1_swiglu(_ptr(x_perm), _ptr(offsets), E, TK, d, f, _ptr(W1), _ptr(h),
                                             _stream(stream)), "moe_grouped_gemm1_swiglu")
@@ -637,7 +665,7 @@ def grouped_gemm1_swiglu_gather(x, src_tok, offsets, W1, h=None, stream=None):
     _need(src_tok, torch.int32, (TK,), "src_tok")
     _need(offsets, torch.int32, (E + 1,), "offsets")
     _need(W1, torch.bfloat16, (E, 2 * f, d), "W1")
-    h = _empty((TK, f), torch.bfloat16, x) if h is None else _need(h, torch.bfloat16, (TK, f), "h")
+    h = _empty((TK, f), torch.bfloat16, x, stream) if h is None else _need(h, torch.bfloat16, (TK, f), "h")
     _check(lib.moe_grouped_gemm1_swiglu_gather(_ptr(x), _ptr(src_tok), _ptr(offsets), T, E, TK, d, f, _ptr(W1),
                                                _ptr(h), _stream(stream)), "moe_grouped_gemm1_swiglu_gather")
     return h
@@ -650,7 +678,8 @@ def grouped_gemm2(h, offsets, W2, y_perm=None, stream=None):
     _need(h, torch.bfloat16, (TK, f), "h")
     _need(offsets, torch.int32, (E + 1,), "offsets")
     _need(W2, torch.bfloat16, (E, d, f), "W2")
-    y_perm = _empty((TK, d), torch.bfloat16, h) if y_perm is None else _need(y_perm, torch.bfloat16, (TK, d), "y_perm")
+    y_perm = _empty((TK, d), torch.bfloat16, h, stream) if y_perm is None else \
+        _need(y_perm, torch.bfloat16, (TK, d), "y_perm")
     _check(lib.moe_grouped_gemm2(_ptr(h), _ptr(offsets), E, TK, d, f, _ptr(W2), _ptr(y_perm), _stream(stream)),
            "moe_grouped_gemm2")
     return y_perm
@@ -662,8 +691,9 @@ def grouped_mlp(x_perm, offsets, W1, W2, h=None, y_perm=None, stream=None):
     _need(offsets, torch.int32, (E + 1,), "offsets")
     _need(W1, torch.bfloat16, (E, 2 * f, d), "W1")
     _need(W2, torch.bfloat16, (E, d, f), "W2")
-    h = _empty((TK, f), torch.bfloat16, x_perm) if h is None else _need(h, torch.bfloat16, (TK, f), "h")
-    y_perm = _empty((TK, d), torch.bfloat16, x_perm) if y_perm is None else _need(y_perm, torch.bfloat16, (TK, d), "y_perm")
+    h = _empty((TK, f), torch.bfloat16, x_perm, stream) if h is None else _need(h, torch.bfloat16, (TK, f), "h")
+    y_perm = _empty((TK, d), torch.bfloat16, x_perm, stream) if y_perm is None else \
+        _need(y_perm, torch.bfloat16, (TK, d), "y_perm")
     _check(lib.moe_grouped_mlp(_ptr(x_perm), _ptr(offsets), E, TK, d, f, _ptr(W1), _ptr(W2), _ptr(h), _ptr(y_perm),
                                _stream(stream)), "moe_grouped_mlp")
     return h, y_perm
@@ -677,7 +707,7 @@ def unpermute(y_perm, row_of, topk_w, out=None, stream=None):
     _need(y_perm, torch.bfloat16, (T * K, d), "y_perm")
     _need(row_of, torch.int32, (T, K), "row_of")
     _need(topk_w, torch.float32, (T, K), "topk_w")
-    out = _empty((T, d), torch.bfloat16, y_perm) if out is None else _need(out, torch.bfloat16, (T, d), "y")
+    out = _empty((T, d), torch.bfloat16, y_perm, stream) if out is None else _need(out, torch.bfloat16, (T, d), "y")
     _check(lib.moe_unpermute(_ptr(y_perm), _ptr(row_of), _ptr(topk_w), T, K, d, _ptr(out), _stream(stream)),
            "moe_unpermute")
     return out
@@ -693,10 +723,10 @@ def grouped_gemm2_combine(h, r: "Routing", W2, out=None, y_perm=None, counters=N
     _need(h, torch.bfloat16, (TK, f), "h")
     _need(W2, torch.bfloat16, (E, d, f), "W2")
     if y_perm is None:
-        y_perm = _empty((TK, d), torch.bfloat16, h)
+        y_perm = _empty((TK, d), torch.bfloat16, h, stream)
     if counters is None:
-        counters = _empty((max(1, int(lib.moe_combine_counters_size(T, d)) // 4),), torch.int32, h)
-    out = _empty((T, d), torch.bfloat16, h) if out is None else _need(out, torch.bfloat16, (T, d), "y")
+        counters = _empty((max(1, int(lib.moe_combine_counters_size(T, d)) // 4),), torch.int32, h, stream)
+    out = _empty((T, d), torch.bfloat16, h, stream) if out is None else _need(out, torch.bfloat16, (T, d), "y")
     _check(lib.moe_grouped_gemm2_combine(_ptr(h), _ptr(r.offsets), E, TK, d, f, _ptr(W2), _ptr(r.src_tok),
                                          _ptr(r.row_of), _ptr(r.topk_w), T, K, _ptr(y_perm), _ptr(counters),
                                          counters.numel() * 4, _ptr(out), _stream(stream)),
@@ -739,8 +769,8 @@ def forward(x, Wr, bias, W1, W2, K: int, out=None, workspace=None, stream=None, 
     if nbytes == 0:
         raise MoEError(2, "moe_forward_workspace_size")
     if workspace is None:
-        workspace = _empty((nbytes,), torch.uint8, x)
-    out = _empty((T, d), torch.bfloat16, x) if out is None else _need(out, torch.bfloat16, (T, d), "y")
+        workspace = _empty((nbytes,), torch.uint8, x, stream)
+    out = _empty((T, d), torch.bfloat16, x, stream) if out is None else _need(out, torch.bfloat16, (T, d), "y")
     if preact is not None:
         _need(preact, torch.bfloat16, (T * K, 2 * f), "preact")
     if rule is not None:
@@ -771,7 +801,7 @@ def forward_host(x_host, Wr, bias, W1, W2, K: int, y_host=None, workspace=None, 
     _, _, E, f = _weights_check(x_host, Wr, bias, W1, W2, K)
     nbytes = forward_workspace_size(T, d, E, K, f)
     if workspace is None:
-        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=W1.device)
+        workspace = _empty((nbytes,), torch.uint8, W1, stream)
     if y_host is None:
         y_host = torch.empty((T, d), dtype=torch.bfloat16, pin_memory=x_host.is_pinned())
     _check(lib.moe_forward_host(_ptr(x_host), _ptr(Wr), _ptr(bias), _ptr(W1), _ptr(W2), T, d, E, K, f,
@@ -804,7 +834,7 @@ def forward_host_pipelined(x_hosts, y_hosts, Wr, bias, W1, W2, K: int, workspace
     if nbytes == 0:
         raise MoEError(2, "moe_forward_host_pipelined_workspace_size")
     if workspace is None:
-        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=W1.device)
+        workspace = _empty((nbytes,), torch.uint8, W1, stream)
     _check(lib.moe_forward_host_pipelined(xp, yp, len(x_hosts), _ptr(Wr), _ptr(bias), _ptr(W1), _ptr(W2), T, d, E,
                                           K, f, _ptr(workspace), workspace.numel(), _stream(stream)),
            "moe_forward_host_pipelined")
@@ -822,7 +852,7 @@ def forward_mxfp8_host_pipelined(x_hosts, y_hosts, Wr, bias, W1q, W1s, W2q, W2s,
     if nbytes == 0:
         raise MoEError(2, "moe_forward_mxfp8_host_pipelined_workspace_size")
     if workspace is None:
-        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=W1q.device)
+        workspace = _empty((nbytes,), torch.uint8, W1q, stream)
     _check(lib.moe_forward_mxfp8_host_pipelined(xp, yp, len(x_hosts), _ptr(Wr), _ptr(bias), _ptr(W1q), _ptr(W1s),
                                                 _ptr(W2q), _ptr(W2s), T, d, E, K, f, _ptr(workspace),
                                                 workspace.numel(), _stream(stream)),
@@ -841,7 +871,7 @@ def last_device_status(out: torch.Tensor | None = None, stream=None) -> torch.Te
     ``out`` (one int32 on the device, allocated when None), without
     synchronizing: capture-safe.  Read ``out`` after the stream has run."""
     if out is None:
-        out = torch.empty((1,), dtype=torch.int32, device="cuda")
+        out = _on(stream, lambda: torch.empty((1,), dtype=torch.int32, device="cuda"))
     if out.dtype != torch.int32 or not out.is_cuda or out.numel() < 1:
         raise ValueError("out must be an int32 CUDA tensor with at least one element")
     _check(lib.moe_last_device_status(out.data_ptr(), _stream(stream)), "moe_last_device_status")
@@ -897,8 +927,7 @@ class MoELayer:
         if save_preact:
             n = x.shape[0] * self.K * 2 * self.f
             if self._preact_buf is None or self._preact_buf.numel() < n:
-                self._preact_buf = torch.empty((self.T_max * self.K * 2 * self.f,), dtype=torch.bfloat16,
-                                               device=x.device)
+                self._preact_buf = _empty((self.T_max * self.K * 2 * self.f,), torch.bfloat16, x, stream)
             pre = self._preact_buf[:n].view(x.shape[0] * self.K, 2 * self.f)
         self.preact = pre
         # moe_forward may fuse the permute into GEMM1 and leave x_perm
@@ -919,7 +948,7 @@ class MoELayer:
         if n == 0:
             raise MoEError(2, "moe_backward_workspace_size")
         if workspace is None:
-            workspace = torch.empty((n,), dtype=torch.uint8, device=x.device)
+            workspace = _empty((n,), torch.uint8, x, stream)
         if not getattr(self, "_x_perm_written", True):
             # the last forward fused the permute: write the grouped rows the
             # backward reads (one permute kernel)
@@ -927,10 +956,10 @@ class MoELayer:
             permute(x, v["row_of"], out=v["x_perm"], stream=stream)
             self._x_perm_written = True
         if grads is None:
-            f32 = dict(dtype=torch.float32, device=x.device)
-            grads = dict(dx=torch.empty((T, d), dtype=torch.bfloat16, device=x.device),
-                         dWr=torch.empty(self.Wr.shape, **f32), dbias=torch.empty((self.E,), **f32),
-                         dW1=torch.empty(self.W1.shape, **f32), dW2=torch.empty(self.W2.shape, **f32))
+            f32 = torch.float32
+            grads = dict(dx=_empty((T, d), torch.bfloat16, x, stream), dWr=_empty(self.Wr.shape, f32, x, stream),
+                         dbias=_empty((self.E,), f32, x, stream), dW1=_empty(self.W1.shape, f32, x, stream),
+                         dW2=_empty(self.W2.shape, f32, x, stream))
         fn, name, route = (lib.moe_backward, "moe_backward", _ptr(self.bias)) if self.rule is None else \
             (lib.moe_backward_scored, "moe_backward_scored", self.rule._c)
         _check(fn(_ptr(x), _ptr(self.Wr), route, _ptr(self.W1), _ptr(self.W2), T, d, self.E,
@@ -1053,8 +1082,8 @@ def mxfp8_quantize(src, stream=None):
     n = mxfp8_scales_size(rows, K)
     if n == 0:
         raise MoEError(2, "moe_mxfp8_scales_size")
-    codes = torch.empty(src.shape, dtype=torch.uint8, device=src.device)
-    scales = torch.empty((n,), dtype=torch.uint8, device=src.device)
+    codes = _empty(src.shape, torch.uint8, src, stream)
+    scales = _empty((n,), torch.uint8, src, stream)
     _check(lib.moe_mxfp8_quantize(_ptr(src), rows, K, _ptr(codes), _ptr(scales), _stream(stream)),
            "moe_mxfp8_quantize")
     return codes, scales
@@ -1069,8 +1098,8 @@ def permute_mxfp8(x, r: "Routing", stream=None):
     n = mxfp8_act_scales_size(T * K, E, d)
     if n == 0:
         raise MoEError(2, "moe_mxfp8_act_scales_size")
-    xq = torch.empty((T * K, d), dtype=torch.uint8, device=x.device)
-    sfa = torch.empty((n,), dtype=torch.uint8, device=x.device)
+    xq = _empty((T * K, d), torch.uint8, x, stream)
+    sfa = _empty((n,), torch.uint8, x, stream)
     _check(lib.moe_permute_mxfp8(_ptr(x), _ptr(r.topk_idx), _ptr(r.row_of), _ptr(r.offsets), T, K, d, E, _ptr(xq),
                                  _ptr(sfa), sfa.numel(), _stream(stream)), "moe_permute_mxfp8")
     return xq, sfa
@@ -1082,8 +1111,8 @@ def grouped_gemm1_swiglu_mxfp8(xq, sfa, offsets, W1q, W1s, stream=None):
     E, two_f, _ = W1q.shape
     f = two_f // 2
     n = mxfp8_act_scales_size(TK, E, f)
-    hq = torch.empty((TK, f), dtype=torch.uint8, device=xq.device)
-    sfh = torch.empty((n,), dtype=torch.uint8, device=xq.device)
+    hq = _empty((TK, f), torch.uint8, xq, stream)
+    sfh = _empty((n,), torch.uint8, xq, stream)
     _check(lib.moe_grouped_gemm1_swiglu_mxfp8(_ptr(xq), _ptr(sfa), sfa.numel(), _ptr(offsets), E, TK, d, f,
                                               _ptr(W1q), _ptr(W1s), _ptr(hq), _ptr(sfh), sfh.numel(),
                                               _stream(stream)), "moe_grouped_gemm1_swiglu_mxfp8")
@@ -1094,7 +1123,7 @@ def grouped_gemm2_mxfp8(hq, sfh, offsets, W2q, W2s, out=None, stream=None):
     """y_perm bf16 [TK, d]."""
     TK, f = hq.shape
     E, d, _ = W2q.shape
-    out = _empty((TK, d), torch.bfloat16, hq) if out is None else _need(out, torch.bfloat16, (TK, d), "y_perm")
+    out = _empty((TK, d), torch.bfloat16, hq, stream) if out is None else _need(out, torch.bfloat16, (TK, d), "y_perm")
     _check(lib.moe_grouped_gemm2_mxfp8(_ptr(hq), _ptr(sfh), sfh.numel(), _ptr(offsets), E, TK, d, f, _ptr(W2q),
                                        _ptr(W2s), _ptr(out), _stream(stream)), "moe_grouped_gemm2_mxfp8")
     return out
@@ -1121,8 +1150,8 @@ def forward_mxfp8(x, Wr, bias, W1q, W1s, W2q, W2s, K: int, out=None, workspace=N
     if nbytes == 0:
         raise MoEError(2, "moe_forward_mxfp8_workspace_size")
     if workspace is None:
-        workspace = _empty((nbytes,), torch.uint8, x)
-    out = _empty((T, d), torch.bfloat16, x) if out is None else _need(out, torch.bfloat16, (T, d), "y")
+        workspace = _empty((nbytes,), torch.uint8, x, stream)
+    out = _empty((T, d), torch.bfloat16, x, stream) if out is None else _need(out, torch.bfloat16, (T, d), "y")
     _check(lib.moe_forward_mxfp8(_ptr(x), _ptr(Wr), _ptr(bias), _ptr(W1q), _ptr(W1s), _ptr(W2q), _ptr(W2s), T, d,
                                  E, K, f, _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream)),
            "moe_forward_mxfp8")

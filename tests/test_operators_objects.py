@@ -289,3 +289,94 @@ def test_clipper_refuses_tensors_that_are_written_over(called):
     b.set_(flat[30:80])
     with pytest.raises(ValueError, match="overlap"):
         clipper(1.0)
+
+
+# ------------------------------------------------------------------ streams
+class _Side:
+    cuda_stream = 7
+
+
+def _small_block(device, T=24, E=8, K=2, d=128, f=64):
+    g = torch.Generator(device="cpu").manual_seed(1)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g)
+
+    Wr, W1, W2 = normal(d, E), 0.1 * normal(E, 2 * f, d), 0.1 * normal(E, d, f)
+    layer = moe.MoELayer(Wr.to(device), torch.zeros(E, device=device), W1.to(torch.bfloat16).to(device),
+                         W2.to(torch.bfloat16).to(device), K, T, rule=moe.RouteRule("sigmoid", 4, 2, 2))
+    block = moe.MoEBlock(layer, torch.ones(d, device=device), torch.ones(d, device=device))
+    return block, normal(T, d).to(device), normal(T, d).to(device)
+
+
+def test_a_call_on_a_stream_allocates_there(called, monkeypatch):
+    """What a call with ``stream`` allocates belongs to that stream, and is not reused before the current one has passed."""
+    inside, made, recorded = [], [], set()
+    empty = torch.empty
+
+    class Inside:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            inside.append(self.stream)
+
+        def __exit__(self, *a):
+            inside.pop()
+
+    def record(*shape, **kw):
+        t = empty(*shape, **kw)
+        made.append((bool(inside), t))
+        return t
+
+    monkeypatch.setattr(torch.cuda, "stream", Inside)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: _Side())
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.add(id(t)))
+    block, r, dr = _small_block("cpu")
+    bf = torch.bfloat16
+    logits, rule, side = torch.zeros(24, 8), moe.RouteRule(), _Side()
+    calls = [lambda s: moe.route_scored(logits, 2, rule, stream=s),
+             lambda s: moe.route_scored_backward(logits, torch.zeros(24, 2, dtype=torch.int32), logits[:, :2], rule, stream=s),
+             lambda s: moe.norm_residual(r, r.to(bf), gamma_pre=r[0], stream=s),
+             lambda s: moe.norm_residual_backward(r, r, r.to(bf), r.to(bf), gamma_pre=r[0], rstd_pre=r[:, 0], stream=s),
+             lambda s: moe.norm_residual_backward(r, r, None, r.to(bf), stream=s, out=moe.NormResidualGrads(r, r.to(bf))),
+             lambda s: moe.route(logits, 2, stream=s), lambda s: block(r, save=True, stream=s),
+             lambda s: block.backward(dr, stream=s)]
+    monkeypatch.setattr(torch, "empty", record)
+    for call in calls:
+        made.clear()
+        recorded.clear()
+        call(side)
+        assert made and all(on for on, _ in made) and {id(t) for _, t in made} <= recorded
+        made.clear()
+        call(None)
+        assert not any(on for on, _ in made)
+
+
+@pytest.mark.gpu
+def test_a_block_on_a_stream_keeps_its_memory():
+    """Work of the current stream that allocates while a side stream is late gets none of the memory that is in use there."""
+    block, r, dr = _small_block("cuda", T=700, d=256)
+    want = block(r, save=True)
+    wantg = block.backward(dr)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    sizes = sorted({t.numel() * t.element_size() for t in [want.r, want.rstd_post, r.to(torch.bfloat16), *wantg.values()]
+                    if t is not None} | {int(moe.lib.moe_norm_residual_backward_workspace_size(700, 256)), 1 << 20})
+    rule, logits = moe.RouteRule(), torch.randn(5000, 64, device="cuda")
+    routed = moe.route_scored(logits, 6, rule)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)          # about ten milliseconds
+    out = block(r, save=True, stream=side)
+    grads = block.backward(dr, stream=side)
+    again = moe.route_scored(logits, 6, rule, stream=side)
+    filled = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(12)]
+    filled += [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in range(512, 8192, 512)]
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out.r, want.r)
+    for k, v in wantg.items():
+        assert (v is None and grads[k] is None) or torch.equal(grads[k], v), k
+    for k in ROUTING:
+        assert torch.equal(getattr(again, k), getattr(routed, k)), k
+    assert all(bool((t == 255).all()) for t in filled)
