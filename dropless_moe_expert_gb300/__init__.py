@@ -916,6 +916,7 @@ class MoELayer:
         self.workspace = torch.empty((n,), dtype=torch.uint8, device=W1.device)
         self._preact_buf = None
         self.preact = None
+        self.calls = 0   # whose intermediates the workspace holds
 
     def __call__(self, x, out=None, stream=None, save_preact=False):
         """y = layer(x).  ``save_preact``: also keep GEMM1's pre-activations
@@ -923,6 +924,7 @@ class MoELayer:
         then skips recomputing them."""
         if x.shape[0] > self.T_max:
             raise ValueError("more tokens than the workspace was sized for")
+        self.calls += 1
         pre = None
         if save_preact:
             n = x.shape[0] * self.K * 2 * self.f
@@ -1020,7 +1022,9 @@ class MoEBlock:
 
     ``layer``: a MoELayer; ``gamma_post`` and ``gate`` may be None.  Blocks
     that follow one another share a kernel: ``block(r, n)`` takes the n that
-    the block before it returned for ``next_gamma=block.gamma_pre``."""
+    the block before it returned for ``next_gamma=block.gamma_pre``.  The layer
+    keeps the routing and activations of its last call only, so blocks that share
+    one run forward and backward one after the other."""
 
     def __init__(self, layer: MoELayer, gamma_pre, gamma_post=None, gate=None, res_scale: float = 1.0,
                  eps: float = 1e-6):
@@ -1039,7 +1043,7 @@ class MoEBlock:
         y = self.layer(pre.n, stream=stream, save_preact=save)
         out = norm_residual(r, y, gamma_post=self.gamma_post, gate=self.gate, gamma_pre=next_gamma,
                             res_scale=self.res_scale, eps=self.eps, stream=stream)
-        self._saved = (pre, y, out, next_gamma, own_pre) if save else None
+        self._saved = (pre, y, out, next_gamma, own_pre, self.layer.calls) if save else None
         return out
 
     def backward(self, dr, dn=None, stream=None) -> dict:
@@ -1049,7 +1053,9 @@ class MoEBlock:
         dr), the layer's gradients, dgamma_pre, dgamma_post, dgate, dnext_gamma."""
         if self._saved is None:
             raise RuntimeError("backward() needs a forward with save=True")
-        pre, y, out, next_gamma, own_pre = self._saved
+        pre, y, out, next_gamma, own_pre, call = self._saved
+        if self.layer.calls != call:
+            raise RuntimeError("the layer has run since this block's forward: what backward() needs is no longer there")
         g = norm_residual_backward(out.r, dr, dn, y, gamma_post=self.gamma_post, gate=self.gate,
                                    gamma_pre=next_gamma, res_scale=self.res_scale, rstd_post=out.rstd_post,
                                    rstd_pre=out.rstd_pre, stream=stream)

@@ -380,3 +380,37 @@ def test_a_block_on_a_stream_keeps_its_memory():
     for k in ROUTING:
         assert torch.equal(getattr(again, k), getattr(routed, k)), k
     assert all(bool((t == 255).all()) for t in filled)
+
+
+# ------------------------------------------------------------------ blocks that share a layer
+def test_backward_refuses_a_layer_that_has_run_since(called, monkeypatch):
+    """The layer keeps one call's routing and activations: a later call of it, by another block or by itself, is noticed."""
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: _Side())
+    block, r, dr = _small_block("cpu")
+    other = moe.MoEBlock(block.layer, block.gamma_pre)
+    for run in (lambda: other(r), lambda: block.layer(r.to(torch.bfloat16)), lambda: block.layer(r.to(torch.bfloat16), save_preact=True)):
+        block(r, save=True)
+        run()
+        called.clear()
+        with pytest.raises(RuntimeError, match="layer"):
+            block.backward(dr)
+        assert not called
+    block(r, save=True)
+    block.backward(dr)
+    block.backward(dr)      # the saved call may be differentiated again
+
+
+@pytest.mark.gpu
+def test_blocks_that_share_a_layer():
+    block, r, dr = _small_block("cuda")
+    other = moe.MoEBlock(block.layer, 2 * block.gamma_pre)
+    a = block(r, save=True)
+    want = block.backward(dr)
+    block(r, save=True)
+    b = other(a.r, save=True)
+    with pytest.raises(RuntimeError, match="layer"):
+        block.backward(dr)
+    other.backward(dr)
+    assert torch.equal(block(r, save=True).r, a.r) and not torch.equal(a.r, b.r)
+    for k, v in block.backward(dr).items():
+        assert (v is None and want[k] is None) or torch.equal(v, want[k]), k
