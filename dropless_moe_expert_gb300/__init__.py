@@ -383,6 +383,7 @@ class NormResidual(_Buffers):
     n: torch.Tensor | None = None        # [T, d] bf16, what the next layer reads
     rstd_post: torch.Tensor | None = None   # [T] fp32
     rstd_pre: torch.Tensor | None = None    # [T] fp32
+    _eps = None                             # that a call used
 
     @classmethod
     def empty(cls, T: int, d: int, dtype=torch.bfloat16, y=True, post=True, pre=True, device="cuda"):
@@ -504,7 +505,10 @@ def norm_residual(r, y=None, *, gamma_post=None, gate=None, gamma_pre=None, res_
         at = out._pointers(key)
     _check(lib.moe_norm_residual(rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep, eps, T, d,
                                  *at, _stream_of(r, stream)), "moe_norm_residual")
-    return out if y is not None else NormResidual(r, out.n, None, out.rstd_pre)
+    if y is None:
+        out = NormResidual(r, out.n, None, out.rstd_pre)
+    out._eps = eps
+    return out
 
 
 def norm_residual_backward(r, dr, dn=None, y=None, *, gamma_post=None, gate=None, gamma_pre=None,
@@ -1022,7 +1026,9 @@ class MoEBlock:
 
     ``layer``: a MoELayer; ``gamma_post`` and ``gate`` may be None.  Blocks
     that follow one another share a kernel: ``block(r, n)`` takes the n that
-    the block before it returned for ``next_gamma=block.gamma_pre``.  The layer
+    the block before it returned for ``next_gamma=block.gamma_pre``
+    (that norm is taken with the eps of the block before, so theirs must agree).
+    The layer
     keeps the routing and activations of its last call only, so blocks that share
     one run forward and backward one after the other."""
 
@@ -1040,6 +1046,8 @@ class MoEBlock:
         own_pre = pre is None
         if own_pre:
             pre = norm_residual(r, gamma_pre=self.gamma_pre, eps=self.eps, stream=stream)
+        elif pre._eps not in (None, self.eps):
+            raise ValueError(f"pre was taken with eps {pre._eps}, this block's is {self.eps}")
         y = self.layer(pre.n, stream=stream, save_preact=save)
         out = norm_residual(r, y, gamma_post=self.gamma_post, gate=self.gate, gamma_pre=next_gamma,
                             res_scale=self.res_scale, eps=self.eps, stream=stream)

@@ -414,3 +414,20 @@ def test_blocks_that_share_a_layer():
     assert torch.equal(block(r, save=True).r, a.r) and not torch.equal(a.r, b.r)
     for k, v in block.backward(dr).items():
         assert (v is None and want[k] is None) or torch.equal(v, want[k]), k
+
+
+def test_a_norm_of_another_eps_is_refused(called, monkeypatch):
+    """A block takes the norm that the block before it left only where that used this block's eps."""
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: _Side())
+    first, r, _ = _small_block("cpu")
+    same, other = (moe.MoEBlock(first.layer, first.gamma_pre, eps=e) for e in (1e-6, 1e-5))
+    n = first(r, next_gamma=same.gamma_pre)
+    same(n.r, pre=n)
+    with pytest.raises(ValueError, match="eps"):
+        other(n.r, pre=n)
+    own = moe.norm_residual(r, gamma_pre=other.gamma_pre, eps=1e-5, out=moe.NormResidual.empty(24, 128, y=False, post=False,
+                                                                                            device="cpu"))
+    other(r, pre=own)
+    with pytest.raises(ValueError, match="eps"):
+        same(r, pre=copy.copy(own))
+    same(r, pre=moe.NormResidual(r, own.n))     # the caller's own
