@@ -903,7 +903,8 @@ class MoELayer:
     runs the forward with one C call.  Intermediates can be read back with
     ``views()`` after a call (they live in the workspace).  With ``rule`` (and
     ``sel_bias`` [E] fp32, which may be changed between calls) it routes by
-    route_scored."""
+    route_scored; backward() then takes every rule but softmax without renorm
+    (route_scored_backward has that one's gradient)."""
 
     def __init__(self, Wr, bias, W1, W2, K: int, T_max: int, rule: RouteRule | None = None, sel_bias=None):
         if sel_bias is not None and rule is None:
@@ -1025,12 +1026,11 @@ class MoEBlock:
         r' = res_scale * r + gate * norm(y) * gamma_post
 
     ``layer``: a MoELayer; ``gamma_post`` and ``gate`` may be None.  Blocks
-    that follow one another share a kernel: ``block(r, n)`` takes the n that
-    the block before it returned for ``next_gamma=block.gamma_pre``
-    (that norm is taken with the eps of the block before, so theirs must agree).
-    The layer
-    keeps the routing and activations of its last call only, so blocks that share
-    one run forward and backward one after the other."""
+    that follow one another share a kernel: ``block(r, pre)`` takes what the
+    block before it returned for ``next_gamma=block.gamma_pre`` (that norm is
+    taken with the eps of the block before, so theirs must agree).  The layer
+    keeps the routing and activations of its last call only, so blocks that
+    share one run forward and backward one after the other."""
 
     def __init__(self, layer: MoELayer, gamma_pre, gamma_post=None, gate=None, res_scale: float = 1.0,
                  eps: float = 1e-6):
@@ -1043,6 +1043,9 @@ class MoEBlock:
         """The stream after the block, and with ``next_gamma`` its norm for the
         next block.  ``pre``: what the block before returned for this block's
         gamma_pre (else the norm is taken here).  ``save`` keeps what backward() needs."""
+        rule = self.layer.rule
+        if save and rule is not None and rule.score == "softmax" and not rule.renorm:
+            raise ValueError("raw softmax scores have no backward in the layer: save=True needs a rule with renorm")
         own_pre = pre is None
         if own_pre:
             pre = norm_residual(r, gamma_pre=self.gamma_pre, eps=self.eps, stream=stream)

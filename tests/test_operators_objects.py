@@ -431,3 +431,17 @@ def test_a_norm_of_another_eps_is_refused(called, monkeypatch):
     with pytest.raises(ValueError, match="eps"):
         same(r, pre=copy.copy(own))
     same(r, pre=moe.NormResidual(r, own.n))     # the caller's own
+
+
+def test_a_block_that_has_no_backward_refuses_to_save_for_it(called, monkeypatch):
+    """Raw softmax scores: the layer's backward does not take them, so a training forward of a block stops before it runs."""
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: _Side())
+    block, r, _ = _small_block("cpu")
+    block.layer.rule = moe.RouteRule("softmax", renorm=False)
+    with pytest.raises(ValueError, match="softmax"):
+        block(r, save=True)
+    assert not called
+    block(r)
+    for rule in (moe.RouteRule("softmax"), moe.RouteRule("sigmoid", renorm=False), None):
+        block.layer.rule = rule
+        block(r, save=True)
