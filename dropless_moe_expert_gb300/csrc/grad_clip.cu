@@ -191,7 +191,7 @@ __device__ __forceinline__ float total_norm(const float *part, int parts) {
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
-    return sqrtf(static_cast<float>(s));
+    return static_cast<float>(sqrt(s));  // the root first: s may pass what fp32 holds where the norm does not
 }
 
 __global__ void __launch_bounds__(32)

@@ -234,9 +234,11 @@ moe_status_t moe_norm_residual_backward(const void *r_out, int residual_fp32, co
  * (>= 0) contiguous elements, fp32 or bf16 by kinds[i], aligned to their type
  * only; the four arrays themselves are HOST memory, read before the call
  * returns.  outs NULL clips in place.  What is written must not overlap any
- * other tensor that is read or written (outs[i] may be grads[i] itself).  Squares are summed in fp32 per CTA, the
- * CTAs' sums in fp64, in a fixed order: deterministic (entries beyond 1.8e19
- * give an infinite norm).  An infinite norm
+ * other tensor that is read or written (outs[i] may be grads[i] itself).
+ * Squares are summed in fp32 per CTA, the CTAs' sums in fp64, in a fixed order:
+ * deterministic.  A CTA's sum that passes 3.4e38 (one entry of 1.8e19 does)
+ * gives an infinite norm; squares of entries below 1e-19 are subnormal and lose
+ * digits, those of entries below 2.6e-23 are zero.  An infinite norm
  * scales by 0 and a NaN by NaN, as the formula does.  max_norm > 0 (INFINITY
  * allowed).  `workspace` (4-byte aligned) holds
  * moe_grad_norm_workspace_size(n_tensors) bytes.  Two launches for every 512
