@@ -235,11 +235,12 @@ moe_status_t moe_norm_residual_backward(const void *r_out, int residual_fp32, co
  * only; the four arrays themselves are HOST memory, read before the call
  * returns.  outs NULL clips in place.  What is written must not overlap any
  * other tensor that is read or written (outs[i] may be grads[i] itself).
- * Squares are summed in fp32 per CTA, the CTAs' sums in fp64, in a fixed order:
- * deterministic.  A CTA's sum that passes 3.4e38 (one entry of 1.8e19 does)
- * gives an infinite norm; squares of entries below 1e-19 are subnormal and lose
- * digits, those of entries below 2.6e-23 are zero.  An infinite norm
- * scales by 0 and a NaN by NaN, as the formula does.  max_norm > 0 (INFINITY
+ * Squares are summed in fp32, 64 at most one after the other, and those sums in
+ * fp64, in a fixed order: deterministic, and as exact for many elements as for
+ * few.  A CTA's sum, held in fp32, gives an infinite norm where it passes
+ * 3.4e38 (one entry of 1.8e19 does); squares of entries below 1e-19 are
+ * subnormal and lose digits, those of entries below 2.6e-23 are zero.  An
+ * infinite norm scales by 0 and a NaN by NaN, as the formula does.  max_norm > 0 (INFINITY
  * allowed).  `workspace` (4-byte aligned) holds
  * moe_grad_norm_workspace_size(n_tensors) bytes.  Two launches for every 512
  * tensors (moe_grad_norm: one, and one more).  */

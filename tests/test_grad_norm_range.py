@@ -24,3 +24,19 @@ def test_sums_of_squares_near_the_ends_of_the_range(value):
     want = float(grads[0]) * min(1.0, limit / (ref + 1e-6))
     for o in clipper.outs:
         assert abs(float(o) - want) <= 8 * ULP * want
+
+
+@pytest.mark.parametrize("value", [1.4247491, 1.9464883, 1.2040133, 1.0], ids=str)
+def test_the_error_does_not_grow_with_the_number_of_elements(value):
+    """8.6e9 equal entries (512 times one tensor, which is only read): equal terms round the same way every time,
+    so a sum that takes them one after the other drifts.  Bound: a thread's sum of a chunk rounds 18 times, to fp32
+    once, the warp's and the block's 21 times, the total 4; half of that after the root, and its rounding."""
+    n, times = 1 << 24, 512
+    g = torch.full((n,), value, device="cuda")
+    norm = torch.zeros(1, device="cuda")
+    ws = torch.empty(moe.lib.moe_grad_norm_workspace_size(times), dtype=torch.uint8, device="cuda")
+    assert moe.lib.moe_grad_norm((ctypes.c_void_p * times)(*[g.data_ptr()] * times), (ctypes.c_int64 * times)(*[n] * times),
+                                 (ctypes.c_int32 * times)(), times, norm.data_ptr(), ws.data_ptr(), ws.numel(),
+                                 torch.cuda.current_stream().cuda_stream) == 0
+    ref = math.sqrt(n * times) * float(g[0])
+    assert abs(float(norm) - ref) <= 24 * ULP * ref
