@@ -195,7 +195,8 @@ __device__ __forceinline__ float total_norm(const float *part, int parts) {
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
-    return static_cast<float>(sqrt(s));  // the root first: s may pass what fp32 holds where the norm does not
+    // s may pass what fp32 holds where its root does not; an fp64 root every time took 0.3 us of a call
+    return s < 1e38 ? sqrtf(static_cast<float>(s)) : static_cast<float>(sqrt(s));
 }
 
 __global__ void __launch_bounds__(32)
