@@ -312,7 +312,7 @@ route_scored_topk_kernel(const float *__restrict__ L, const float *__restrict__ 
 // also lie in shared memory, where the octet of a choice is read again for its next
 // largest.  The same sums in the same order, so the same bits as above.  Us, all
 // launches: 32768 tokens, 64 experts softmax 14.2, half a warp per token 19.2; 256
-// in 8 runs 39.9 and 56.0; with 8192 tokens 15.0 and 19.0; but, fewer warps taking
+// in 8 runs 41.6 and 56.0; with 8192 tokens 15.0 and 19.0; but, fewer warps taking
 // longer each, with 4096 tokens (no runs) 10.7 and 9.8, and for 8192 x 32 8.2 and 6.7;
 // 6144 x 256 13.0 and 15.3, without runs 12.0 and 12.2, 6144 x 128 10.0 and 9.7.
 // E and a run's experts are multiples of four, with at most RUNS runs.

@@ -240,8 +240,8 @@ moe_status_t moe_norm_residual_backward(const void *r_out, int residual_fp32, co
  * few.  A CTA's sum, held in fp32, gives an infinite norm where it passes
  * 3.4e38 (one entry of 1.8e19 does); squares of entries below 1e-19 are
  * subnormal and lose digits, those of entries below 2.6e-23 are zero.  An
- * infinite norm scales by 0 and a NaN by NaN, as the formula does.  max_norm > 0 (INFINITY
- * allowed).  `workspace` (4-byte aligned) holds
+ * infinite norm scales by 0 and a NaN by NaN, as the formula does.
+ * max_norm > 0 (INFINITY allowed).  `workspace` (4-byte aligned) holds
  * moe_grad_norm_workspace_size(n_tensors) bytes.  Two launches for every 512
  * tensors (moe_grad_norm: one, and one more).  */
 enum { MOE_GRAD_FP32 = 0, MOE_GRAD_BF16 = 1 };
