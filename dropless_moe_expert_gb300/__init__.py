@@ -569,6 +569,7 @@ class GradClipper:
     grads = property(lambda self: self._grads)
     outs = property(lambda self: self._clipped)
     norm = property(lambda self: self._norm)
+    workspace = property(lambda self: self._workspace)
 
     def _check_tensors(self):
         for i, (dtype, shape) in enumerate(self._kept):
