@@ -30,7 +30,8 @@ __all__ = [
     "grouped_gemm1_swiglu_mxfp8", "grouped_gemm2_mxfp8", "forward_mxfp8", "forward_mxfp8_views", "MoELayerMXFP8",
     "grouped_gemm2_combine", "grouped_gemm1_swiglu_gather", "last_device_status", "forward_fuses_permute",
     "RouteRule", "RouteBuffers", "route_scored", "route_scored_backward", "NormResidual", "NormResidualGrads",
-    "norm_residual", "norm_residual_backward", "GradClipper", "MoEBlock",
+    "norm_residual", "norm_residual_backward", "GradClipper", "MoEBlock", "gated_ffn", "gated_ffn_backward",
+    "GatedFFN", "GatedFFNGrads",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -75,6 +76,7 @@ def _load():
             "(python -c 'import __graft_entry__ as g; g.build()')")
     L = ctypes.CDLL(path)
     P, I, S, U64, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64, ctypes.c_float
+    D = ctypes.c_double
     RULE = P  # moe_route_rule_t *
     sig = {
         "moe_status_string": (ctypes.c_char_p, [I]),
@@ -123,6 +125,13 @@ def _load():
         "moe_norm_residual": (I, [P, I, P, P, P, I, F, P, F, I, I, P, P, P, P, P]),
         "moe_norm_residual_backward_workspace_size": (S, [I, I]),
         "moe_norm_residual_backward": (I, [P, I, P, P, P, I, F, P, P, P, P, P, I, I, P, P, P, P, P, P, S, P]),
+        "moe_norm_residual_dropout": (I, [P, I, P, P, P, I, F, P, F, D, P, I, I, P, P, P, P, P, P]),
+        "moe_norm_residual_dropout_backward": (I, [P, I, P, P, P, I, F, P, D, P, P, P, P, P, I, I, P, P, P, P, P, P, S,
+                                                   P]),
+        "moe_gated_ffn_workspace_size": (S, [I, I, I]),
+        "moe_gated_ffn": (I, [P, P, P, P, I, I, I, I, P, P, P, S, P]),
+        "moe_gated_ffn_backward_workspace_size": (S, [I, I, I]),
+        "moe_gated_ffn_backward": (I, [P, P, P, P, P, P, I, I, I, I, P, P, P, I, P, S, P]),
         "moe_grad_norm_workspace_size": (S, [I]),
         "moe_grad_norm": (I, [P, P, P, I, P, P, S, P]),
         "moe_grad_norm_clip": (I, [P, P, P, P, I, F, P, P, S, P]),
@@ -383,23 +392,31 @@ class NormResidual(_Buffers):
     n: torch.Tensor | None = None        # [T, d] bf16, what the next layer reads
     rstd_post: torch.Tensor | None = None   # [T] fp32
     rstd_pre: torch.Tensor | None = None    # [T] fp32
+    rng: torch.Tensor | None = None         # [2] int64, what a call with dropout drew from
     _eps = None                             # that a call used
 
     @classmethod
-    def empty(cls, T: int, d: int, dtype=torch.bfloat16, y=True, post=True, pre=True, device="cuda"):
+    def empty(cls, T: int, d: int, dtype=torch.bfloat16, y=True, post=True, pre=True, device="cuda", rng=False):
         """Output buffers of norm_residual: ``dtype`` of the residual stream;
-        with an output ``y`` to add, its norm (``post``) and the next norm (``pre``)."""
+        with an output ``y`` to add, its norm (``post``), the next norm (``pre``)
+        and dropout (``rng``)."""
         def make(on, dt, *shape):
             return torch.empty(shape, dtype=dt, device=device) if on else None
 
         return cls(make(y, dtype, T, d), make(pre, torch.bfloat16, T, d), make(post, torch.float32, T),
-                   make(pre, torch.float32, T))
+                   make(pre, torch.float32, T), make(rng, torch.int64, 2))
 
     def _addresses(self, key):
         """Of the buffers that the call (T, d, dtype, y, post, pre) writes."""
         _, _, _, y, post, pre = key
         return (_ptr(self.r) if y else None, _ptr(self.n) if pre else None, _ptr(self.rstd_post) if post else None,
                 _ptr(self.rstd_pre) if pre else None)
+
+    def _rng_pointer(self, like, stream):
+        """Where a call with dropout leaves its state."""
+        if self.rng is None:
+            self.rng = _empty((2,), torch.int64, like, stream)
+        return _in(self.rng, torch.int64, (2,), "out.rng")
 
     def _pointers(self, key):
         """The addresses, checked."""
@@ -488,14 +505,28 @@ def _norm_args(r, y, gamma_post, gate, gamma_pre):
             None if gamma_pre is None else _in(gamma_pre, f32, cols, "gamma_pre"))
 
 
+def _rng_in(rng) -> int:
+    """The address of a dropout's state."""
+    if rng is None:
+        raise ValueError("dropout needs rng, its seed and call number: an int64 CUDA tensor [2]")
+    return _in(rng, torch.int64, (2,), "rng")
+
+
 def norm_residual(r, y=None, *, gamma_post=None, gate=None, gamma_pre=None, res_scale: float = 1.0,
-                  eps: float = 1e-6, out: NormResidual | None = None, stream=None) -> NormResidual:
+                  eps: float = 1e-6, dropout: float = 0.0, rng=None, out: NormResidual | None = None,
+                  stream=None) -> NormResidual:
     """What stands between two layers, in one kernel: r' = res_scale * r +
     gate * norm(y) * gamma_post and n = norm(r') * gamma_pre (RMS norms; parts
     without their tensor are left out).  r [T, d] bf16 or fp32, y [T, d] bf16,
     gammas [d] fp32, gate fp32 [d] (per channel) or [T, 1] (per token).
     Without y: n = norm(r) * gamma_pre, and the result's r is r itself (``out``
-    keeps its own).  ``out.r`` may be r (updated in place)."""
+    keeps its own).  ``out.r`` may be r (updated in place).
+
+    ``dropout`` > 0 drops that share of what is added to res_scale * r (and
+    scales the rest by 1 / (1 - dropout)), by draws from ``rng``, a seed and a
+    call number [2] int64 on the device: another number in each call draws anew.
+    The result's ``rng`` is a copy of them for the backward; no mask is kept.
+    0 drops nothing, and rng is not read."""
     T, d, kind, rp, yp, postp, gatep, prep = _norm_args(r, y, gamma_post, gate, gamma_pre)
     key = (T, d, r.dtype, yp is not None, postp is not None, prep is not None)
     if out is None:
@@ -503,8 +534,13 @@ def norm_residual(r, y=None, *, gamma_post=None, gate=None, gamma_pre=None, res_
         at = out._addresses(key)
     else:
         at = out._pointers(key)
-    _check(lib.moe_norm_residual(rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep, eps, T, d,
-                                 *at, _stream_of(r, stream)), "moe_norm_residual")
+    if dropout:
+        _check(lib.moe_norm_residual_dropout(rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep,
+                                             eps, dropout, _rng_in(rng), T, d, *at, out._rng_pointer(r, stream),
+                                             _stream_of(r, stream)), "moe_norm_residual_dropout")
+    else:
+        _check(lib.moe_norm_residual(rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep, eps,
+                                     T, d, *at, _stream_of(r, stream)), "moe_norm_residual")
     if y is None:
         out = NormResidual(r, out.n, None, out.rstd_pre)
     out._eps = eps
@@ -512,11 +548,12 @@ def norm_residual(r, y=None, *, gamma_post=None, gate=None, gamma_pre=None, res_
 
 
 def norm_residual_backward(r, dr, dn=None, y=None, *, gamma_post=None, gate=None, gamma_pre=None,
-                           res_scale: float = 1.0, rstd_post=None, rstd_pre=None,
+                           res_scale: float = 1.0, rstd_post=None, rstd_pre=None, dropout: float = 0.0, rng=None,
                            out: NormResidualGrads | None = None, stream=None) -> NormResidualGrads:
     """Gradients of norm_residual for ``dr`` (of its output stream, the
     residual's type; None: zero, with gamma_pre) and ``dn`` (with gamma_pre),
-    from its output stream ``r`` as stored, y and the factors it returned."""
+    from its output stream ``r`` as stored, y and the factors it returned; with
+    ``dropout`` its share and the ``rng`` it returned."""
     T, d, kind, rp, yp, postp, gatep, prep = _norm_args(r, y, gamma_post, gate, gamma_pre)
     drp = None if dr is None else _in(dr, r.dtype, (T, d), "dr")
     dnp = _in(dn, torch.bfloat16, (T, d), "dn") if prep is not None else None
@@ -528,9 +565,115 @@ def norm_residual_backward(r, dr, dn=None, y=None, *, gamma_post=None, gate=None
         at = out._addresses(key)
     else:
         at = out._pointers(key, stream)
-    _check(lib.moe_norm_residual_backward(
-        rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep, rpp, rqp, drp, dnp, T, d,
-        *at, _stream_of(r, stream)), "moe_norm_residual_backward")
+    if dropout:
+        _check(lib.moe_norm_residual_dropout_backward(
+            rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep, dropout, _rng_in(rng), rpp, rqp,
+            drp, dnp, T, d, *at, _stream_of(r, stream)), "moe_norm_residual_dropout_backward")
+    else:
+        _check(lib.moe_norm_residual_backward(
+            rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep, rpp, rqp, drp, dnp, T, d,
+            *at, _stream_of(r, stream)), "moe_norm_residual_backward")
+    return out
+
+
+# ------------------------------------------------------------------ gated feed-forward of all tokens
+_ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+
+
+def _act(name) -> int:
+    if name not in _ACTS:
+        raise ValueError(f"act must be one of {', '.join(_ACTS)}, got {name!r}")
+    return _ACTS[name]
+
+
+def _ffn_sizes(W1, W2):
+    """d, f of a feed-forward's weights, and their addresses; checked."""
+    d, f = W2.shape
+    bf16 = torch.bfloat16
+    return d, f, _in(W1, bf16, (2 * f, d), "W1"), _in(W2, bf16, (d, f), "W2")
+
+
+def gated_ffn(x, W1, W2, act: str = "silu", *, add=None, out=None, preact=None, workspace=None, stream=None):
+    """y = (act(x W1g^T) * (x W1u^T)) W2^T + add: x, add and y [T, d], W1 [2f, d]
+    (gate rows, then up rows) and W2 [d, f], all bf16; ``act`` "silu", "gelu",
+    "gelu_tanh" or "relu".  ``out`` may be ``add`` (y += ...).  ``preact``
+    [T, 2f] bf16 receives what the activation and the product take, for
+    gated_ffn_backward.  d and f are multiples of 8."""
+    T = x.shape[0]
+    d, f, w1, w2 = _ffn_sizes(W1, W2)
+    bf16, shape = torch.bfloat16, (T, d)
+    xp, ap = _in(x, bf16, shape, "x"), None if add is None else _in(add, bf16, shape, "add")
+    pp = None if preact is None else _in(preact, bf16, (T, 2 * f), "preact")
+    if out is None:
+        out = _empty(shape, bf16, x, stream)
+    yp = _in(out, bf16, shape, "y")
+    if workspace is None:
+        workspace = _empty((int(lib.moe_gated_ffn_workspace_size(T, d, f)),), torch.uint8, x, stream)
+    _check(lib.moe_gated_ffn(xp, w1, w2, ap, _act(act), T, d, f, yp, pp, workspace.data_ptr(), workspace.numel(),
+                             _stream_of(x, stream)), "moe_gated_ffn")
+    return out
+
+
+@dataclass
+class GatedFFNGrads(_Buffers):
+    dx: torch.Tensor | None = None    # [T, d] bf16
+    dW1: torch.Tensor | None = None   # shaped like the weights, bf16 or fp32
+    dW2: torch.Tensor | None = None
+    workspace: torch.Tensor | None = None
+
+    @classmethod
+    def empty(cls, T: int, d: int, f: int, dtype=torch.bfloat16, dx=True, weights=True, device="cuda"):
+        """Output buffers of gated_ffn_backward; ``dtype`` of the weights' gradients."""
+        n = int(lib.moe_gated_ffn_backward_workspace_size(T, d, f))
+        if n == 0:
+            raise MoEError(2, "moe_gated_ffn_backward_workspace_size")
+
+        def make(on, dt, *shape):
+            return torch.empty(shape, dtype=dt, device=device) if on else None
+
+        return cls(make(dx, torch.bfloat16, T, d), make(weights, dtype, 2 * f, d), make(weights, dtype, d, f),
+                   make(True, torch.uint8, n))
+
+    def _pointers(self, T, d, f, stream):
+        """Addresses of dx, dW1, dW2, whether the weights' are fp32, the workspace and its bytes; checked."""
+        if self.workspace is None:
+            n = int(lib.moe_gated_ffn_backward_workspace_size(T, d, f))
+            like = next((t for t in (self.dx, self.dW1, self.dW2) if t is not None), None)
+            if like is None:
+                raise ValueError("out has none of dx, dW1 and dW2")
+            self.workspace = _empty((n,), torch.uint8, like, stream)
+        ws = self.workspace
+        at = (_ptr(self.dx), _ptr(self.dW1), _ptr(self.dW2), ws.data_ptr(), ws.numel())
+        kinds = tuple(None if t is None else t.dtype for t in (self.dW1, self.dW2))
+        key = (T, d, f, at, kinds)
+        if key != self._checked:
+            wide = torch.float32 if torch.float32 in kinds else torch.bfloat16
+            if self.dx is not None:
+                _need(self.dx, torch.bfloat16, (T, d), "out.dx")
+            if self.dW1 is not None:
+                _need(self.dW1, wide, (2 * f, d), "out.dW1")
+            if self.dW2 is not None:
+                _need(self.dW2, wide, (d, f), "out.dW2")
+            _need(ws, torch.uint8, (ws.numel(),), "out.workspace")
+            self._hold(key, self.dx, self.dW1, self.dW2, ws)
+        return (*at[:3], int(torch.float32 in kinds), *at[3:])
+
+
+def gated_ffn_backward(x, preact, dy, W1, W2, act: str = "silu", *, add=None, out: GatedFFNGrads | None = None,
+                       stream=None) -> GatedFFNGrads:
+    """Gradients of gated_ffn for ``dy``, from x and the ``preact`` it kept.
+    ``add`` [T, d] bf16 is added to dx (``out.dx`` may be ``add``).  What ``out``
+    has no tensor for is not computed; without ``out`` all are, the weights' in bf16."""
+    T = x.shape[0]
+    d, f, w1, w2 = _ffn_sizes(W1, W2)
+    bf16, shape = torch.bfloat16, (T, d)
+    xp, dyp, ap = _in(x, bf16, shape, "x"), _in(dy, bf16, shape, "dy"), None if add is None else _in(add, bf16, shape,
+                                                                                                    "add")
+    pp = _in(preact, bf16, (T, 2 * f), "preact")
+    if out is None:
+        out = _on(stream, lambda: GatedFFNGrads.empty(T, d, f, device=x.device))
+    _check(lib.moe_gated_ffn_backward(xp, pp, dyp, w1, w2, ap, _act(act), T, d, f, *out._pointers(T, d, f, stream),
+                                      _stream_of(x, stream)), "moe_gated_ffn_backward")
     return out
 
 
@@ -1019,31 +1162,85 @@ class MoELayer:
         )
 
 
+class GatedFFN:
+    """A gated feed-forward's weights (see gated_ffn) and a persistent workspace
+    for up to T_max tokens: a dense layer, or the ``shared`` expert of a MoEBlock.
+    ``__call__(x)`` runs the forward; with ``save_preact`` it keeps what
+    backward() needs of it (its last call's), as MoELayer does."""
+    rule = None
+
+    def __init__(self, W1, W2, act: str = "silu", T_max: int = 1):
+        self.W1, self.W2, self.act, self.T_max = W1, W2, act, T_max
+        self.d, self.f, _, _ = _ffn_sizes(W1, W2)
+        _act(act)
+        n = int(lib.moe_gated_ffn_workspace_size(T_max, self.d, self.f))
+        if n == 0:
+            raise MoEError(2, "moe_gated_ffn_workspace_size")
+        self.workspace = torch.empty((n,), dtype=torch.uint8, device=W1.device)
+        self._preact_buf = None
+        self.preact = None
+        self.calls = 0   # whose pre-activations are kept
+
+    def __call__(self, x, out=None, stream=None, save_preact=False, add=None):
+        T = x.shape[0]
+        if T > self.T_max:
+            raise ValueError("more tokens than the workspace was sized for")
+        pre = None
+        if save_preact:
+            if self._preact_buf is None:
+                self._preact_buf = _empty((self.T_max, 2 * self.f), torch.bfloat16, x, stream)
+            pre = self._preact_buf[:T]
+        self.preact = pre
+        self.calls += 1
+        return gated_ffn(x, self.W1, self.W2, self.act, add=add, out=out, preact=pre, workspace=self.workspace,
+                         stream=stream)
+
+    def backward(self, x, dy, grads=None, workspace=None, stream=None, add=None):
+        """Gradients of sum(dy * y) for the last call (same x, with
+        save_preact): dict of dx [T, d] bf16 (plus ``add``) and dW1, dW2 (fp32
+        like MoELayer's, or of the type of those in ``grads``)."""
+        if self.preact is None or self.preact.shape[0] != x.shape[0]:
+            raise RuntimeError("backward() needs the last call to be of these tokens, with save_preact=True")
+        if grads is None:
+            f32 = torch.float32
+            grads = dict(dx=_empty(x.shape, torch.bfloat16, x, stream), dW1=_empty(self.W1.shape, f32, x, stream),
+                         dW2=_empty(self.W2.shape, f32, x, stream))
+        gated_ffn_backward(x, self.preact, dy, self.W1, self.W2, self.act, add=add, stream=stream,
+                           out=GatedFFNGrads(grads.get("dx"), grads.get("dW1"), grads.get("dW2"), workspace))
+        return grads
+
+
 class MoEBlock:
     """A layer inside a residual stream, as a model trains it:
 
         n  = norm(r) * gamma_pre
-        y  = layer(n)
-        r' = res_scale * r + gate * norm(y) * gamma_post
+        y  = layer(n) + shared(n)
+        r' = res_scale * r + drop(gate * norm(y) * gamma_post)
 
-    ``layer``: a MoELayer; ``gamma_post`` and ``gate`` may be None.  Blocks
+    ``layer``: a MoELayer, or a GatedFFN (a dense block); ``shared``: a GatedFFN
+    that every token passes beside the routed experts, or None; ``gamma_post``
+    and ``gate`` may be None; ``dropout``: the share that drop() drops.  Blocks
     that follow one another share a kernel: ``block(r, pre)`` takes what the
     block before it returned for ``next_gamma=block.gamma_pre`` (that norm is
     taken with the eps of the block before, so theirs must agree).  The layer
     keeps the routing and activations of its last call only, so blocks that
     share one run forward and backward one after the other."""
 
-    def __init__(self, layer: MoELayer, gamma_pre, gamma_post=None, gate=None, res_scale: float = 1.0,
-                 eps: float = 1e-6):
+    def __init__(self, layer: MoELayer | GatedFFN, gamma_pre, gamma_post=None, gate=None, res_scale: float = 1.0,
+                 eps: float = 1e-6, shared: GatedFFN | None = None, dropout: float = 0.0):
+        if shared is not None and shared is layer:
+            raise ValueError("shared must be another feed-forward than the layer")
         self.layer, self.gamma_pre, self.gamma_post, self.gate = layer, gamma_pre, gamma_post, gate
-        self.res_scale, self.eps = res_scale, eps
+        self.res_scale, self.eps, self.shared, self.dropout = res_scale, eps, shared, dropout
         self._saved = None
 
     def __call__(self, r, pre: NormResidual | None = None, next_gamma=None, save: bool = False,
-                 stream=None) -> NormResidual:
+                 stream=None, rng=None) -> NormResidual:
         """The stream after the block, and with ``next_gamma`` its norm for the
         next block.  ``pre``: what the block before returned for this block's
-        gamma_pre (else the norm is taken here).  ``save`` keeps what backward() needs."""
+        gamma_pre (else the norm is taken here).  ``save`` keeps what backward()
+        needs.  ``rng`` (see norm_residual) turns the dropout on: without it
+        nothing is dropped, as when a model answers."""
         rule = self.layer.rule
         if save and rule is not None and rule.score == "softmax" and not rule.renorm:
             raise ValueError("raw softmax scores have no backward in the layer: save=True needs a rule with renorm")
@@ -1053,25 +1250,38 @@ class MoEBlock:
         elif pre._eps not in (None, self.eps):
             raise ValueError(f"pre was taken with eps {pre._eps}, this block's is {self.eps}")
         y = self.layer(pre.n, stream=stream, save_preact=save)
+        if self.shared is not None:
+            y = self.shared(pre.n, out=y, add=y, stream=stream, save_preact=save)
+        drop = self.dropout if rng is not None else 0.0
         out = norm_residual(r, y, gamma_post=self.gamma_post, gate=self.gate, gamma_pre=next_gamma,
-                            res_scale=self.res_scale, eps=self.eps, stream=stream)
-        self._saved = (pre, y, out, next_gamma, own_pre, self.layer.calls) if save else None
+                            res_scale=self.res_scale, eps=self.eps, dropout=drop, rng=rng, stream=stream)
+        self._saved = (pre, y, out, next_gamma, own_pre, self._calls(), drop) if save else None
         return out
+
+    def _calls(self):
+        return self.layer.calls, None if self.shared is None else self.shared.calls
 
     def backward(self, dr, dn=None, stream=None) -> dict:
         """Gradients for ``dr`` of the stream after the block and ``dn`` of its
         norm (with next_gamma): dr [T, d] of the stream before it, dn of its
         own norm's output (None when the norm was taken here: then it is in
-        dr), the layer's gradients, dgamma_pre, dgamma_post, dgate, dnext_gamma."""
+        dr), the layer's gradients, those of the shared expert (shared_dW1,
+        shared_dW2), dgamma_pre, dgamma_post, dgate, dnext_gamma."""
         if self._saved is None:
             raise RuntimeError("backward() needs a forward with save=True")
-        pre, y, out, next_gamma, own_pre, call = self._saved
-        if self.layer.calls != call:
+        pre, y, out, next_gamma, own_pre, calls, drop = self._saved
+        if self._calls() != calls:
             raise RuntimeError("the layer has run since this block's forward: what backward() needs is no longer there")
         g = norm_residual_backward(out.r, dr, dn, y, gamma_post=self.gamma_post, gate=self.gate,
                                    gamma_pre=next_gamma, res_scale=self.res_scale, rstd_post=out.rstd_post,
-                                   rstd_pre=out.rstd_pre, stream=stream)
+                                   rstd_pre=out.rstd_pre, dropout=drop, rng=out.rng, stream=stream)
         grads = self.layer.backward(pre.n, g.dy, stream=stream)
+        if self.shared is not None:
+            f32 = torch.float32
+            both = dict(dx=grads["dx"], dW1=_empty(self.shared.W1.shape, f32, pre.n, stream),
+                        dW2=_empty(self.shared.W2.shape, f32, pre.n, stream))
+            self.shared.backward(pre.n, g.dy, both, stream=stream, add=both["dx"])
+            grads.update(shared_dW1=both["dW1"], shared_dW2=both["dW2"])
         grads.update(dgamma_post=g.dgamma_post, dgate=g.dgate, dnext_gamma=g.dgamma_pre, dr=g.dr, dn=grads.pop("dx"))
         if own_pre:
             # the stream before the block feeds the sum and the norm

@@ -106,6 +106,12 @@ struct NormResidualArgs {
     bool res_f32;
     int *status;  // of the bounded waits
     uint64_t wait_ns;
+    // Dropout of what is added (rng null: none): the generator's seed and call,
+    // on the device; of 2^16 draws `drop` drop an element, the others scale it.
+    const uint64_t *rng = nullptr;
+    uint64_t *rng_out = nullptr;  // forward: what was used
+    uint32_t drop = 0;
+    float keep_scale = 1.0f;
 };
 cudaError_t launch_norm_residual(const NormResidualArgs &a, const void *r, void *r_out, uint16_t *n, float *rstd_post,
                                  float *rstd_pre, cudaStream_t stream);
@@ -186,6 +192,7 @@ struct GemmLaunch {
     int pairs_plain = 0;
     int wgrad_pairs = 0;  // resident CTA pairs of the weight-gradient pair kernel
     int mx_pairs = 0;  // ... of the MXFP8 GEMM2 pair kernel
+    int ffn_pairs = 0;  // ... of the gated feed-forward's kernel, whatever its form
     int device = -1;
     int *sched_base = nullptr;  // device address of the dynamic tile order's counter table
 };
@@ -222,6 +229,32 @@ cudaError_t launch_grouped_gemm(bool swiglu, const void *A, int TK, int Kdim, co
                                 const int32_t *offsets, void *out, const GemmLaunch &cfg, int *status,
                                 uint64_t timeout_ns, cudaStream_t stream, const CombineArgs *comb = nullptr,
                                 bool b_trans = false, void *preact = nullptr, const GatherArgs *gather = nullptr);
+
+// The gated feed-forward of all tokens (gated_ffn.cu): y [T, d] from x [T, d],
+// W1 [2f, d], W2 [d, f]; h [T, f] is scratch; preact [T, 2f] and add [T, d]
+// (which may be y) are nullable.  d and f multiples of 8.  Two launches.
+struct FfnArgs {
+    const uint16_t *x, *W1, *W2, *add;
+    int act, T, d, f;
+    uint16_t *y, *h, *preact;
+    int *status;
+    uint64_t timeout_ns;
+};
+// Its gradients, dx, dW1 and dW2 nullable (not computed); add (which may be
+// dx) is nullable; da [T, 2f] and h [T, f] are scratch.  Launches counted.
+struct FfnGradArgs {
+    const uint16_t *x, *preact, *dy, *W1, *W2, *add;
+    int act, T, d, f;
+    uint16_t *dx;
+    void *dW1, *dW2;
+    bool weights_f32;  // dW1 and dW2 are fp32, else bf16
+    uint16_t *da, *h;
+    int *status;
+    uint64_t timeout_ns;
+};
+cudaError_t ffn_setup(GemmLaunch *cfg);
+cudaError_t launch_ffn(const FfnArgs &a, const GemmLaunch &lc, cudaStream_t stream);
+cudaError_t launch_ffn_bwd(const FfnGradArgs &a, const GemmLaunch &lc, int *launches, cudaStream_t stream);
 
 // A kernel whose only wait never completes: it times out after limit_ns and
 // records MOE_ERR_DEVICE_TIMEOUT in *status.

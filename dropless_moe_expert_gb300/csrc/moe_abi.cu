@@ -57,6 +57,7 @@ moe_status_t device_state(DeviceState **out) {
         if (moe::router_setup() != cudaSuccess) return MOE_ERR_CUDA;
         if (moe::grouped_gemm_mx_setup(&s.gemm) != cudaSuccess) return MOE_ERR_CUDA;
         if (moe::wgrad_setup(&s.gemm) != cudaSuccess) return MOE_ERR_CUDA;
+        if (moe::ffn_setup(&s.gemm) != cudaSuccess) return MOE_ERR_CUDA;
         if (cudaGetSymbolAddress(reinterpret_cast<void **>(&s.status), g_device_status) != cudaSuccess)
             return MOE_ERR_CUDA;
         s.ready = true;
@@ -169,6 +170,32 @@ moe_status_t check_norm(int residual_fp32, const uint16_t *y, const float *gamma
                                  residual_fp32 == 1, nullptr, kWaitLimitNs};
     return MOE_OK;
 }
+
+// The dropout of the norm entry points, into their common arguments.
+moe_status_t check_dropout(double p, const uint64_t *rng, moe::NormResidualArgs *a) {
+    if (!(p >= 0.0) || !rng || !aligned(rng, 8) || !a->y) return MOE_ERR_INVALID_ARG;  // it acts on y
+    const double drop = std::nearbyint(p * 65536.0);
+    if (!(drop < 65536.0)) return MOE_ERR_INVALID_ARG;
+    a->rng = rng;
+    a->drop = static_cast<uint32_t>(drop);
+    a->keep_scale = static_cast<float>(65536.0 / (65536.0 - drop));
+    return MOE_OK;
+}
+
+moe_status_t check_ffn(int act, int T, int d, int f) {
+    if (T < 1 || d < 1 || f < 1 || act < MOE_ACT_SILU || act > MOE_ACT_RELU) return MOE_ERR_INVALID_ARG;
+    if (d % 8 != 0 || f % 8 != 0 || f >= (1 << 30)) return MOE_ERR_UNSUPPORTED;
+    // tiles of 256 x 128 are counted in 32 bits
+    const int64_t T_ = T / 256 + 1, f_ = f / 128 + 1, d_ = d / 128 + 1;
+    if (std::max({T_ * f_, T_ * d_, 2 * f_ * d_}) >= (int64_t(1) << 30)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+// A matrix that may be written over, by the same elements: `out` and `add` are the same or apart.
+bool same_or_apart(const void *out, const void *add, size_t bytes) {
+    const uintptr_t o = reinterpret_cast<uintptr_t>(out), a = reinterpret_cast<uintptr_t>(add);
+    return !add || o == a || o + bytes <= a || a + bytes <= o;
+}
+size_t ffn_bytes(int T, int f) { return (static_cast<size_t>(T) * f * 2 + 255) / 256 * 256; }  // of [T, f] bf16
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
@@ -415,14 +442,24 @@ moe_status_t moe_route_scored_backward(const float *logits, const int32_t *topk_
     return cuda_status(moe::launch_route_scored_bwd(logits, topk_idx, dw, T, E, K, r, dlogits, stream));
 }
 
-moe_status_t moe_norm_residual(const void *r, int residual_fp32, const uint16_t *y, const float *gamma_post,
-                               const float *gate, int gate_kind, float res_scale, const float *gamma_pre, float eps,
-                               int T, int d, void *r_out, uint16_t *n, float *rstd_post, float *rstd_pre,
-                               cudaStream_t stream) {
-    MOE_RANGE();
+}  // extern "C"
+
+namespace {
+
+// moe_norm_residual, and with dropout where there is a `rng`.
+moe_status_t norm_residual_impl(const void *r, int residual_fp32, const uint16_t *y, const float *gamma_post,
+                                const float *gate, int gate_kind, float res_scale, const float *gamma_pre, float eps,
+                                int T, int d, void *r_out, uint16_t *n, float *rstd_post, float *rstd_pre,
+                                cudaStream_t stream, bool dropout = false, double p = 0.0,
+                                const uint64_t *rng = nullptr, uint64_t *rng_out = nullptr) {
     moe::NormResidualArgs a;
     moe_status_t st = check_norm(residual_fp32, y, gamma_post, gate, gate_kind, res_scale, gamma_pre, eps, T, d, &a);
     if (st != MOE_OK) return st;
+    if (dropout) {
+        if ((st = check_dropout(p, rng, &a)) != MOE_OK) return st;
+        if (!rng_out || !aligned(rng_out, 8)) return MOE_ERR_INVALID_ARG;
+        a.rng_out = rng_out;
+    }
     if (!r || !aligned(r, 16)) return MOE_ERR_INVALID_ARG;
     if (y && (!r_out || !aligned(r_out, 16))) return MOE_ERR_INVALID_ARG;
     if (gamma_pre && (!n || !rstd_pre || !aligned(n, 16) || !aligned(rstd_pre, 4))) return MOE_ERR_INVALID_ARG;
@@ -434,21 +471,48 @@ moe_status_t moe_norm_residual(const void *r, int residual_fp32, const uint16_t 
     return cuda_status(moe::launch_norm_residual(a, r, r_out, n, rstd_post, rstd_pre, stream));
 }
 
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_norm_residual(const void *r, int residual_fp32, const uint16_t *y, const float *gamma_post,
+                               const float *gate, int gate_kind, float res_scale, const float *gamma_pre, float eps,
+                               int T, int d, void *r_out, uint16_t *n, float *rstd_post, float *rstd_pre,
+                               cudaStream_t stream) {
+    MOE_RANGE();
+    return norm_residual_impl(r, residual_fp32, y, gamma_post, gate, gate_kind, res_scale, gamma_pre, eps, T, d, r_out,
+                              n, rstd_post, rstd_pre, stream);
+}
+
+moe_status_t moe_norm_residual_dropout(const void *r, int residual_fp32, const uint16_t *y, const float *gamma_post,
+                                       const float *gate, int gate_kind, float res_scale, const float *gamma_pre,
+                                       float eps, double p, const uint64_t *rng, int T, int d, void *r_out, uint16_t *n,
+                                       float *rstd_post, float *rstd_pre, uint64_t *rng_out, cudaStream_t stream) {
+    MOE_RANGE();
+    return norm_residual_impl(r, residual_fp32, y, gamma_post, gate, gate_kind, res_scale, gamma_pre, eps, T, d, r_out,
+                              n, rstd_post, rstd_pre, stream, true, p, rng, rng_out);
+}
+
 size_t moe_norm_residual_backward_workspace_size(int T, int d) {
     if (T < 1 || d < 64 || d % 64 != 0 || d > moe::kNormMaxD) return 0;
     return moe::norm_residual_bwd_part_bytes(T, d);
 }
 
-moe_status_t moe_norm_residual_backward(const void *r_out, int residual_fp32, const uint16_t *y,
-                                        const float *gamma_post, const float *gate, int gate_kind, float res_scale,
-                                        const float *gamma_pre, const float *rstd_post, const float *rstd_pre,
-                                        const void *dr_out, const uint16_t *dn, int T, int d, void *dr, uint16_t *dy,
-                                        float *dgamma_pre, float *dgamma_post, float *dgate, void *workspace,
-                                        size_t workspace_bytes, cudaStream_t stream) {
-    MOE_RANGE();
+}  // extern "C"
+
+namespace {
+
+moe_status_t norm_residual_backward_impl(const void *r_out, int residual_fp32, const uint16_t *y,
+                                         const float *gamma_post, const float *gate, int gate_kind, float res_scale,
+                                         const float *gamma_pre, const float *rstd_post, const float *rstd_pre,
+                                         const void *dr_out, const uint16_t *dn, int T, int d, void *dr, uint16_t *dy,
+                                         float *dgamma_pre, float *dgamma_post, float *dgate, void *workspace,
+                                         size_t workspace_bytes, cudaStream_t stream, bool dropout = false,
+                                         double p = 0.0, const uint64_t *rng = nullptr) {
     moe::NormResidualArgs a;
     moe_status_t st = check_norm(residual_fp32, y, gamma_post, gate, gate_kind, res_scale, gamma_pre, 1.0f, T, d, &a);
     if (st != MOE_OK) return st;
+    if (dropout && (st = check_dropout(p, rng, &a)) != MOE_OK) return st;
     if (!dr || !aligned(dr, 16) || !workspace || !aligned(workspace, 16)) return MOE_ERR_INVALID_ARG;
     if (dr_out ? !aligned(dr_out, 16) : !gamma_pre) return MOE_ERR_INVALID_ARG;
     if (gamma_pre && (!r_out || !dn || !rstd_pre || !dgamma_pre || !aligned(r_out, 16) || !aligned(dn, 16) ||
@@ -465,6 +529,90 @@ moe_status_t moe_norm_residual_backward(const void *r_out, int residual_fp32, co
     const moe::NormResidualGradArgs g{r_out, dr_out, dn, rstd_post, rstd_pre, dr, dy, dgamma_pre, dgamma_post, dgate};
     int launches = 0;
     const cudaError_t e = moe::launch_norm_residual_bwd(a, g, static_cast<float *>(workspace), &launches, stream);
+    g_launches.fetch_add(launches, std::memory_order_relaxed);
+    return cuda_status(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_norm_residual_backward(const void *r_out, int residual_fp32, const uint16_t *y,
+                                        const float *gamma_post, const float *gate, int gate_kind, float res_scale,
+                                        const float *gamma_pre, const float *rstd_post, const float *rstd_pre,
+                                        const void *dr_out, const uint16_t *dn, int T, int d, void *dr, uint16_t *dy,
+                                        float *dgamma_pre, float *dgamma_post, float *dgate, void *workspace,
+                                        size_t workspace_bytes, cudaStream_t stream) {
+    MOE_RANGE();
+    return norm_residual_backward_impl(r_out, residual_fp32, y, gamma_post, gate, gate_kind, res_scale, gamma_pre,
+                                       rstd_post, rstd_pre, dr_out, dn, T, d, dr, dy, dgamma_pre, dgamma_post, dgate,
+                                       workspace, workspace_bytes, stream);
+}
+
+moe_status_t moe_norm_residual_dropout_backward(const void *r_out, int residual_fp32, const uint16_t *y,
+                                                const float *gamma_post, const float *gate, int gate_kind,
+                                                float res_scale, const float *gamma_pre, double p, const uint64_t *rng,
+                                                const float *rstd_post, const float *rstd_pre, const void *dr_out,
+                                                const uint16_t *dn, int T, int d, void *dr, uint16_t *dy,
+                                                float *dgamma_pre, float *dgamma_post, float *dgate, void *workspace,
+                                                size_t workspace_bytes, cudaStream_t stream) {
+    MOE_RANGE();
+    return norm_residual_backward_impl(r_out, residual_fp32, y, gamma_post, gate, gate_kind, res_scale, gamma_pre,
+                                       rstd_post, rstd_pre, dr_out, dn, T, d, dr, dy, dgamma_pre, dgamma_post, dgate,
+                                       workspace, workspace_bytes, stream, true, p, rng);
+}
+
+size_t moe_gated_ffn_workspace_size(int T, int d, int f) {
+    return check_ffn(MOE_ACT_SILU, T, d, f) == MOE_OK ? ffn_bytes(T, f) : 0;
+}
+
+moe_status_t moe_gated_ffn(const uint16_t *x, const uint16_t *W1, const uint16_t *W2, const uint16_t *add, int act,
+                           int T, int d, int f, uint16_t *y, uint16_t *preact, void *workspace, size_t workspace_bytes,
+                           cudaStream_t stream) {
+    MOE_RANGE();
+    if (!x || !W1 || !W2 || !y || !workspace) return MOE_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(W1, 16) || !aligned(W2, 16) || !aligned(add, 16) || !aligned(y, 16) ||
+        !aligned(preact, 16) || !aligned(workspace, 16))
+        return MOE_ERR_INVALID_ARG;
+    moe_status_t st = check_ffn(act, T, d, f);
+    if (st != MOE_OK) return st;
+    if (!same_or_apart(y, add, static_cast<size_t>(T) * d * 2)) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < ffn_bytes(T, f)) return MOE_ERR_WORKSPACE;
+    DeviceState *ds = nullptr;
+    if ((st = device_state(&ds)) != MOE_OK) return st;
+    const moe::FfnArgs a{x, W1, W2, add, act, T, d, f, y, static_cast<uint16_t *>(workspace), preact, ds->status,
+                         kWaitLimitNs};
+    g_launches.fetch_add(2, std::memory_order_relaxed);
+    return cuda_status(moe::launch_ffn(a, ds->gemm, stream));
+}
+
+size_t moe_gated_ffn_backward_workspace_size(int T, int d, int f) {
+    return check_ffn(MOE_ACT_SILU, T, d, f) == MOE_OK ? 3 * ffn_bytes(T, f) : 0;  // da [T, 2f], h [T, f]
+}
+
+moe_status_t moe_gated_ffn_backward(const uint16_t *x, const uint16_t *preact, const uint16_t *dy, const uint16_t *W1,
+                                    const uint16_t *W2, const uint16_t *add, int act, int T, int d, int f, uint16_t *dx,
+                                    void *dW1, void *dW2, int weights_fp32, void *workspace, size_t workspace_bytes,
+                                    cudaStream_t stream) {
+    MOE_RANGE();
+    if (!preact || !dy || !W2 || !workspace || (!dx && !dW1 && !dW2)) return MOE_ERR_INVALID_ARG;
+    if ((dx && !W1) || (dW1 && !x) || (add && !dx)) return MOE_ERR_INVALID_ARG;
+    if (weights_fp32 != 0 && weights_fp32 != 1) return MOE_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(preact, 16) || !aligned(dy, 16) || !aligned(W1, 16) || !aligned(W2, 16) ||
+        !aligned(add, 16) || !aligned(dx, 16) || !aligned(dW1, 16) || !aligned(dW2, 16) || !aligned(workspace, 16))
+        return MOE_ERR_INVALID_ARG;
+    moe_status_t st = check_ffn(act, T, d, f);
+    if (st != MOE_OK) return st;
+    if (!same_or_apart(dx, add, static_cast<size_t>(T) * d * 2)) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < 3 * ffn_bytes(T, f)) return MOE_ERR_WORKSPACE;
+    DeviceState *ds = nullptr;
+    if ((st = device_state(&ds)) != MOE_OK) return st;
+    uint16_t *da = static_cast<uint16_t *>(workspace);
+    const moe::FfnGradArgs a{x,  preact, dy,  W1,  W2,  add,
+                             act, T, d, f, dx, dW1, dW2, weights_fp32 == 1,
+                             da, da + ffn_bytes(T, f), ds->status, kWaitLimitNs};
+    int launches = 0;
+    const cudaError_t e = moe::launch_ffn_bwd(a, ds->gemm, &launches, stream);
     g_launches.fetch_add(launches, std::memory_order_relaxed);
     return cuda_status(e);
 }

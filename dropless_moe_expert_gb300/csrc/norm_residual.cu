@@ -11,6 +11,10 @@
 //   dr  = a D,   dgq = sum_t dn r' rq
 //   k   = g D gp,  dy = rp (k - y rp^2 mean(k y))      (dy = g D without gamma_post)
 //   dgp = sum_t g D y rp,   dg = u D summed over the axis that g is shared along
+// With dropout (DROP) what is added is g u / (1 - p) where an element is kept and 0 where it is not:
+//   r' = a r + m g u,   and D in all of the y side's gradients is m D,   m = 0 or 1 / (1 - p)
+// drawn again in the backward from the same state.  It adds no bytes, and about 10
+// integer instructions per element.
 // The sums over t run in a fixed order: each CTA over its own rows, then the
 // CTAs' partial sums in their order.
 //
@@ -19,6 +23,7 @@
 // 4 of it the column sums; the main kernel takes as long with its arithmetic left out;
 // backward of 4093 x 7168 with the stream in fp32 88.9 us, 5.9 TB/s.
 #include "kernels.h"
+#include "philox.cuh"
 #include "ptx.cuh"
 #include "vec8.cuh"
 
@@ -191,6 +196,19 @@ __device__ __forceinline__ void weights(const NormResidualArgs &a, uint32_t col,
     if (a.gamma_pre) load8(a.gamma_pre + col, 0, &w[0].x);
 }
 
+// The draws of an operator with dropout, by the element that begins a vector.
+template <bool DROP>
+struct Draws {
+    __device__ __forceinline__ explicit Draws(const NormResidualArgs &) {}
+};
+template <>
+struct Draws<true> : Dropout {
+    __device__ __forceinline__ explicit Draws(const NormResidualArgs &a) : Dropout(a.rng, a.drop) {}
+    __device__ __forceinline__ uint32_t kept(int64_t element) const {
+        return Dropout::kept(static_cast<uint64_t>(element) >> 3);
+    }
+};
+
 // Row r of CTA blockIdx.x is blockIdx.x + r gridDim.x.  A thread owns VPT
 // vectors of eight columns; each warp fetches the columns that it reads with
 // bulk copies of its own, so its rows come ahead of their use through a ring in
@@ -199,7 +217,7 @@ __device__ __forceinline__ void weights(const NormResidualArgs &a, uint32_t col,
 // requests, not the memory, were the limit.)  A row's slot is refilled as soon as
 // the row is in registers, so the ring's copies stay in flight through the row's
 // sums and stores.
-template <typename R, int VPT, int REGS>
+template <typename R, int VPT, int REGS, bool DROP>
 __global__ void __launch_bounds__(sm_threads(REGS))
 norm_residual_kernel(Args a, float inv_d, const R *r, R *r_out, uint16_t *__restrict__ n,
                      float *__restrict__ rstd_post, float *__restrict__ rstd_pre) {
@@ -242,6 +260,8 @@ norm_residual_kernel(Args a, float inv_d, const R *r, R *r_out, uint16_t *__rest
     for (int s = 0; s < stages; ++s) issue(blockIdx.x + s * step, s);
     const bool token_gate = a.gate && a.gate_per_token;
     float gt = token_gate ? a.gate[blockIdx.x] : 1.0f;
+    const Draws<DROP> draws(a);
+    if (DROP && blockIdx.x == 0 && threadIdx.x < 2) a.rng_out[threadIdx.x] = a.rng[threadIdx.x];
     int slot = 0, turn = 0, phase = 0;
     for (int64_t t = blockIdx.x; t < a.T; t += step) {
         const float gt_next = token_gate && t + step < a.T ? a.gate[t + step] : 1.0f;
@@ -273,13 +293,22 @@ norm_residual_kernel(Args a, float inv_d, const R *r, R *r_out, uint16_t *__rest
                 if (threadIdx.x == 0) rstd_post[t] = rp;
                 f *= rp;
             }
+            if (DROP) f *= a.keep_scale;
             R *out = r_out + t * a.d;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 if (!HOLD) weights(a, own.col + 256 * j, own.on[j], c[j], w[j]);
+                if constexpr (DROP) {
+                    const uint32_t kept = draws.kept(t * a.d + own.col + 256 * j);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[j][i] = fma2(mul2(both(f), c[j][i]), y[j][i], mul2(both(a.res_scale), x[j][i]));
+                    for (int i = 0; i < 4; ++i)
+                        x[j][i] = fma2(both(a.res_scale), x[j][i],
+                                       only(kept, i, mul2(mul2(both(f), c[j][i]), y[j][i])));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[j][i] = fma2(mul2(both(f), c[j][i]), y[j][i], mul2(both(a.res_scale), x[j][i]));
+                }
                 if (own.on[j]) store(out, own.col + 256 * j, x[j], a.wide);
             }
         }
@@ -325,7 +354,7 @@ norm_residual_kernel(Args a, float inv_d, const R *r, R *r_out, uint16_t *__rest
 // their own 48.9 and 51.3.  A higher share of the SM's threads for these lighter
 // forms was slower up to 4096 columns (us): 768 of 80 registers 53.1 and 56.5, 1024
 // of 64 55.2 and 58.0.
-template <typename R, int VPT, bool Y, bool PRE, bool DR, Split SPLIT, int REGS>
+template <typename R, int VPT, bool Y, bool PRE, bool DR, Split SPLIT, int REGS, bool DROP>
 __global__ void __launch_bounds__(sm_threads(REGS))
 norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const R *dr_out,
                          const uint16_t *__restrict__ dn, const float *__restrict__ rstd_post,
@@ -408,7 +437,10 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
     for (int s = 0; s < stages; ++s) issue(begin + s * step, s);
     // The first reading of the row in slot `slot`: the four sums (of h z,
     // c y dr', c y h, c y z) of the warp go to `sums`.
-    auto first_pass = [&](int slot, float rq, float4 *sums, uint32_t k) {
+    // With dropout `kept` takes the row's draws, a byte per vector, for the second reading.
+    const Draws<DROP> draws(a);
+    auto first_pass = [&](int slot, float rq, float4 *sums, uint32_t k, uint32_t t, uint32_t &kept) {
+        kept = 0;
         const uint8_t *at16 = mine + slot * stage + lane * 16, *at_r = mine + slot * stage + lane * (8 * sizeof(R));
         float2 s0 = both(0.0f), s1 = s0, s2 = s0, s3 = s0;
 #pragma unroll
@@ -419,6 +451,12 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
                 read8<uint16_t>(at16 + j * 512, cy);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) cy[i] = mul2(cy[i], c[j][i]);
+                if constexpr (DROP) {
+                    const uint32_t m = draws.kept(static_cast<int64_t>(t) * a.d + own.col + 256 * j);
+                    kept |= m << (8 * j);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) cy[i] = only(m, i, mul2(cy[i], both(a.keep_scale)));
+                }
                 if (DR) {
                     float2 g[4];
                     read8<R>(at_r + j * piece_bytes<R>() + AT_DR, g);
@@ -465,10 +503,10 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
     Row f = factors(begin), next = factors(begin + step);
     int slot = 0, turn = 0;
     int phase = 0;  // of the slot that first_pass reads next
-    uint32_t k = 0;
+    uint32_t k = 0, kept = 0, kept_next = 0;
     if (PIPE && begin < rows_end) {
         rows.wait(0, 0);
-        first_pass(0, f.rq, red[0], 0);
+        first_pass(0, f.rq, red[0], 0, begin, kept);
     }
     for (uint32_t t = begin; t < rows_end; t += step) {
         const Row after = factors(t + 2 * step);
@@ -479,11 +517,11 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
             if (ahead == 0) phase ^= 1;
             if (t + step < rows_end) {
                 rows.wait(ahead, phase);
-                first_pass(ahead, next.rq, red[other], k + 1);
+                first_pass(ahead, next.rq, red[other], k + 1, t + step, kept_next);
             }
         } else {
             rows.wait(slot, phase);
-            first_pass(slot, f.rq, red[turn], k);
+            first_pass(slot, f.rq, red[turn], k, t, kept);
             s = collect(red[turn], k);
             if (ahead == 0) phase ^= 1;
         }
@@ -494,7 +532,7 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
         const float cyD = s.y + f.rq * s.z - m1 * s.w;
         const float m2 = post ? f.gt * cyD * inv_d * f.rp * f.rp * f.rp : 0.0f;
         if (a.gate && a.gate_per_token && warp == 0 && lane == 0 && rank == 0) dgate[t] = f.rp * cyD;
-        const float2 q = both(f.gt * f.rp), mz = both(-m1 * f.rq), my = both(-m2), rq = both(f.rq);
+        const float2 q = both(DROP ? f.gt * f.rp * a.keep_scale : f.gt * f.rp), mz = both(-m1 * f.rq), my = both(-m2), rq = both(f.rq);
         R *to_r = dr + static_cast<int64_t>(t) * a.d;
         uint16_t *to_y = dy + static_cast<int64_t>(t) * a.d;
 #pragma unroll
@@ -527,8 +565,16 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     D[i] = mul2(D[i], q);
-                    accp[j][i] = fma2(y[i], D[i], accp[j][i]);
-                    o[i] = fma2(my, y[i], mul2(D[i], c[j][i]));
+                    if constexpr (DROP) {
+                        const uint32_t m = kept >> (8 * j);
+                        D[i] = only(m, i, D[i]);
+                        accp[j][i] = fma2(only(m, i, y[i]), D[i], accp[j][i]);
+                        o[i] = mul2(D[i], c[j][i]);
+                        if (post) o[i] = fma2(my, y[i], o[i]);
+                    } else {
+                        accp[j][i] = fma2(y[i], D[i], accp[j][i]);
+                        o[i] = fma2(my, y[i], mul2(D[i], c[j][i]));
+                    }
                 }
                 store(to_y, col, o, true);
             }
@@ -536,6 +582,7 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
         slot = ahead;
         f = next;
         next = after;
+        if (PIPE) kept = kept_next;
     }
     // the CTA's sums: the teams' ones in the rings, now empty, added in the teams' order
     float *out = part + static_cast<size_t>(group) * 2 * a.d, *held = reinterpret_cast<float *>(ring);
@@ -667,23 +714,23 @@ cudaError_t allow_ring(Kernel kernel, std::atomic<uint64_t> &done) {
     return e;
 }
 
-template <typename R, int VPT, int REGS>
+template <typename R, int VPT, int REGS, bool DROP>
 cudaError_t forward(const Shape &s, const NormResidualArgs &a, const void *r, void *r_out, uint16_t *n,
                     float *rstd_post, float *rstd_pre, cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_ring(norm_residual_kernel<R, VPT, REGS>, done);
+    const cudaError_t e = allow_ring(norm_residual_kernel<R, VPT, REGS, DROP>, done);
     if (e != cudaSuccess) return e;
     const Args args{a, s.stages, s.teams, reinterpret_cast<uintptr_t>(r_out) % 32 == 0};
-    norm_residual_kernel<R, VPT, REGS><<<s.ctas, s.threads, s.smem, stream>>>(
+    norm_residual_kernel<R, VPT, REGS, DROP><<<s.ctas, s.threads, s.smem, stream>>>(
         args, 1.0f / a.d, static_cast<const R *>(r), static_cast<R *>(r_out), n, rstd_post, rstd_pre);
     return cudaGetLastError();
 }
 
-template <typename R, int VPT, bool Y, bool PRE, bool DR, Split SPLIT, int REGS>
+template <typename R, int VPT, bool Y, bool PRE, bool DR, Split SPLIT, int REGS, bool DROP>
 cudaError_t backward(const Shape &s, const NormResidualArgs &a, const NormResidualGradArgs &g, float *part,
                      cudaStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_ring(norm_residual_bwd_kernel<R, VPT, Y, PRE, DR, SPLIT, REGS>, done);
+    const cudaError_t e = allow_ring(norm_residual_bwd_kernel<R, VPT, Y, PRE, DR, SPLIT, REGS, DROP>, done);
     if (e != cudaSuccess) return e;
     const Args args{a, s.stages, s.teams, reinterpret_cast<uintptr_t>(g.dr) % 32 == 0};
     cudaLaunchAttribute pairs;
@@ -692,7 +739,7 @@ cudaError_t backward(const Shape &s, const NormResidualArgs &a, const NormResidu
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(s.ctas), cfg.blockDim = dim3(s.threads), cfg.dynamicSmemBytes = s.smem, cfg.stream = stream;
     cfg.attrs = &pairs, cfg.numAttrs = SPLIT == HALVES;
-    return cudaLaunchKernelEx(&cfg, norm_residual_bwd_kernel<R, VPT, Y, PRE, DR, SPLIT, REGS>, args, 1.0f / a.d,
+    return cudaLaunchKernelEx(&cfg, norm_residual_bwd_kernel<R, VPT, Y, PRE, DR, SPLIT, REGS, DROP>, args, 1.0f / a.d,
                               static_cast<const R *>(g.r_out), static_cast<const R *>(g.dr_out),
                               static_cast<const uint16_t *>(g.dn), static_cast<const float *>(g.rstd_post),
                               static_cast<const float *>(g.rstd_pre), static_cast<R *>(g.dr), g.dy, g.dgate, part);
@@ -702,15 +749,17 @@ cudaError_t backward(const Shape &s, const NormResidualArgs &a, const NormResidu
 
 cudaError_t launch_norm_residual(const NormResidualArgs &a, const void *r, void *r_out, uint16_t *n, float *rstd_post,
                                  float *rstd_pre, cudaStream_t stream) {
-    auto go = [&](auto type) {
+    auto go = [&](auto type, auto dropout) {
         using R = decltype(type);
+        constexpr bool DROP = decltype(dropout)::value;
         const nr::Shape s = nr::fwd_shape<R>(a.T, a.d);
-        if (s.vpt == 1) return nr::forward<R, 1, 80>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
-        if (s.regs == 80) return nr::forward<R, 2, 80>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
-        if (s.vpt == 2) return nr::forward<R, 2, 128>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
-        return nr::forward<R, 4, 128>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
+        if (s.vpt == 1) return nr::forward<R, 1, 80, DROP>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
+        if (s.regs == 80) return nr::forward<R, 2, 80, DROP>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
+        if (s.vpt == 2) return nr::forward<R, 2, 128, DROP>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
+        return nr::forward<R, 4, 128, DROP>(s, a, r, r_out, n, rstd_post, rstd_pre, stream);
     };
-    return a.res_f32 ? go(float{}) : go(uint16_t{});
+    if (a.rng) return a.res_f32 ? go(float{}, std::true_type{}) : go(uint16_t{}, std::true_type{});
+    return a.res_f32 ? go(float{}, std::false_type{}) : go(uint16_t{}, std::false_type{});
 }
 
 size_t norm_residual_bwd_part_bytes(int T, int d) {
@@ -724,23 +773,24 @@ size_t norm_residual_bwd_part_bytes(int T, int d) {
 cudaError_t launch_norm_residual_bwd(const NormResidualArgs &a, const NormResidualGradArgs &g, float *part,
                                      int *launches, cudaStream_t stream) {
     int parts = 0;
-    auto go = [&](auto type) {
+    auto go = [&](auto type, auto dropout) {
         using R = decltype(type);
         const nr::Shape s = nr::bwd_shape<R>(a.T, a.d, a.y, a.gamma_pre);
         parts = s.split == nr::HALVES ? s.ctas / 2 : s.ctas;
         auto form = [&](auto y, auto pre, auto dr) {
             constexpr bool Y = decltype(y)::value, PRE = decltype(pre)::value, DR = decltype(dr)::value;
-            if (s.vpt == 1) return nr::backward<R, 1, Y, PRE, DR, nr::TEAM, 128>(s, a, g, part, stream);
-            if (s.split == nr::HALVES) return nr::backward<R, 2, Y, PRE, DR, nr::HALVES, 128>(s, a, g, part, stream);
+            constexpr bool DROP = Y && decltype(dropout)::value;
+            if (s.vpt == 1) return nr::backward<R, 1, Y, PRE, DR, nr::TEAM, 128, DROP>(s, a, g, part, stream);
+            if (s.split == nr::HALVES) return nr::backward<R, 2, Y, PRE, DR, nr::HALVES, 128, DROP>(s, a, g, part, stream);
             if constexpr (sizeof(R) == 2 && !(Y && PRE)) {
                 if (s.regs == 80 && s.split == nr::PAIR)
-                    return nr::backward<R, 2, Y, PRE, DR, nr::PAIR, 80>(s, a, g, part, stream);
-                if (s.regs == 80) return nr::backward<R, 2, Y, PRE, DR, nr::ALONE, 80>(s, a, g, part, stream);
+                    return nr::backward<R, 2, Y, PRE, DR, nr::PAIR, 80, DROP>(s, a, g, part, stream);
+                if (s.regs == 80) return nr::backward<R, 2, Y, PRE, DR, nr::ALONE, 80, DROP>(s, a, g, part, stream);
             }
-            if (s.split == nr::TEAM) return nr::backward<R, 2, Y, PRE, DR, nr::TEAM, 128>(s, a, g, part, stream);
+            if (s.split == nr::TEAM) return nr::backward<R, 2, Y, PRE, DR, nr::TEAM, 128, DROP>(s, a, g, part, stream);
             if constexpr (!nr::pipelined<R>(2, Y && PRE))
-                if (s.split == nr::PAIR) return nr::backward<R, 2, Y, PRE, DR, nr::PAIR, 128>(s, a, g, part, stream);
-            return nr::backward<R, 2, Y, PRE, DR, nr::ALONE, 128>(s, a, g, part, stream);
+                if (s.split == nr::PAIR) return nr::backward<R, 2, Y, PRE, DR, nr::PAIR, 128, DROP>(s, a, g, part, stream);
+            return nr::backward<R, 2, Y, PRE, DR, nr::ALONE, 128, DROP>(s, a, g, part, stream);
         };
         constexpr std::true_type with{};
         constexpr std::false_type without{};
@@ -749,7 +799,8 @@ cudaError_t launch_norm_residual_bwd(const NormResidualArgs &a, const NormResidu
         return g.dr_out ? form(with, with, with) : form(with, with, without);
     };
     *launches = 1;
-    const cudaError_t err = a.res_f32 ? go(float{}) : go(uint16_t{});
+    const cudaError_t err = a.rng ? (a.res_f32 ? go(float{}, std::true_type{}) : go(uint16_t{}, std::true_type{}))
+                                  : (a.res_f32 ? go(float{}, std::false_type{}) : go(uint16_t{}, std::false_type{}));
     if (err != cudaSuccess || !(a.gamma_pre || a.gamma_post || (a.gate && !a.gate_per_token))) return err;
     *launches = 2;
     return launch_dependent(nr::norm_residual_bwd_columns_kernel, a.d / 32, 32 * nr::RUNS, stream,

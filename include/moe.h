@@ -2,7 +2,8 @@
  * moe.h -- C ABI of a dropless Mixture-of-Experts SwiGLU FFN layer on one
  * NVIDIA GB300 (sm_103a): the forward (bf16, and MXFP8 expert matmuls) and the
  * backward of a training step; and of the operators around it in a model:
- * routing by scores, the norms, gate and residual between two layers, and the
+ * routing by scores, the norms, gate, dropout and residual between two layers,
+ * a gated feed-forward of all tokens (a shared expert, a dense layer), and the
  * clipping of a step's gradients.
  *
  * The operation follows "Accelerating dropless MoE training in JAX with NVIDIA
@@ -225,6 +226,63 @@ moe_status_t moe_norm_residual_backward(const void *r_out, int residual_fp32, co
                                         const void *dr_out, const uint16_t *dn, int T, int d, void *dr, uint16_t *dy,
                                         float *dgamma_pre, float *dgamma_post, float *dgate, void *workspace,
                                         size_t workspace_bytes, cudaStream_t stream);
+
+/* The same with dropout of what is added to the stream:
+ *   r_out = res_scale * r + m * gate * u,  m = 1 / (1 - p) where an element is kept, 0 where it is not
+ * (a dropped element adds nothing, whatever its value), and n of that r_out;
+ * in the backward the gradients of y, gamma_post and gate take m times the
+ * stream's.  `rng` holds two words on the device, a seed and a call number,
+ * read when the kernel runs: a captured graph draws anew on each replay where
+ * they were changed meanwhile.  Element i = t d + c has the draw of 16 bits
+ * that is piece i % 8 (low halves of the words first) of Philox4x32-10 with the
+ * key seed and the counter (i / 8, call), and is kept where that is at least
+ * round(65536 p).  p counts in those steps of 2^-16, in the scale too; 0 <= p
+ * and round(65536 p) < 65536.  y is required.  The mask is not stored:
+ * rng_out [2] (which may be rng) receives the two words, and the backward draws
+ * the same again from them.  As many launches and the same workspace as without. */
+moe_status_t moe_norm_residual_dropout(const void *r, int residual_fp32, const uint16_t *y, const float *gamma_post,
+                                       const float *gate, int gate_kind, float res_scale, const float *gamma_pre,
+                                       float eps, double p, const uint64_t *rng, int T, int d, void *r_out, uint16_t *n,
+                                       float *rstd_post, float *rstd_pre, uint64_t *rng_out, cudaStream_t stream);
+moe_status_t moe_norm_residual_dropout_backward(const void *r_out, int residual_fp32, const uint16_t *y,
+                                                const float *gamma_post, const float *gate, int gate_kind,
+                                                float res_scale, const float *gamma_pre, double p, const uint64_t *rng,
+                                                const float *rstd_post, const float *rstd_pre, const void *dr_out,
+                                                const uint16_t *dn, int T, int d, void *dr, uint16_t *dy,
+                                                float *dgamma_pre, float *dgamma_post, float *dgate, void *workspace,
+                                                size_t workspace_bytes, cudaStream_t stream);
+
+/* A gated feed-forward that every token passes: the shared expert beside the
+ * routed ones, or a dense layer.
+ *   [g | u] = x W1^T,  h = act(g) * u,  y = h W2^T + add
+ * x, y, add [T, d], W1 [2f, d] (gate rows, then up rows), W2 [d, f], all bf16
+ * and 16-byte aligned; add is nullable and may be y itself (y += ...), else
+ * they are apart.  act: silu g s(g) with s the logistic function, gelu
+ * g Phi(g), gelu with its tanh, or relu.  Sums are fp32; h is rounded to bf16
+ * once, as the second product's operand, y once after add.  preact [T, 2f] bf16
+ * (nullable) receives [g | u], which the backward needs.  `workspace` (16-byte
+ * aligned, moe_gated_ffn_workspace_size(T, d, f) bytes) holds h.  d and f
+ * multiples of 8.  Sums have a fixed order: deterministic.  2 kernel launches. */
+enum { MOE_ACT_SILU = 0, MOE_ACT_GELU = 1, MOE_ACT_GELU_TANH = 2, MOE_ACT_RELU = 3 };
+size_t moe_gated_ffn_workspace_size(int T, int d, int f);
+moe_status_t moe_gated_ffn(const uint16_t *x, const uint16_t *W1, const uint16_t *W2, const uint16_t *add, int act,
+                           int T, int d, int f, uint16_t *y, uint16_t *preact, void *workspace, size_t workspace_bytes,
+                           cudaStream_t stream);
+/* Its gradients for dy [T, d], from x and the forward's preact as stored:
+ *   dh = dy W2,  da = [dh * u * act'(g) | dh * act(g)]     (act'(0) = 0 for relu)
+ *   dx = da W1 + add,  dW1 = da^T x,  dW2 = dy^T h
+ * dx [T, d] bf16; dW1 and dW2, shaped like the weights, bf16 (weights_fp32 0)
+ * or fp32 (1).  Each of the three is NULL where it is not wanted (then W1, or
+ * x, may be NULL too).  add [T, d] bf16 (nullable, with dx) may be dx itself,
+ * else they are apart.  dh is not rounded, da and h to bf16 once each, as
+ * operands.  `workspace` (16-byte aligned) holds
+ * moe_gated_ffn_backward_workspace_size(T, d, f) bytes.  Deterministic.  Up to
+ * 4 kernel launches. */
+size_t moe_gated_ffn_backward_workspace_size(int T, int d, int f);
+moe_status_t moe_gated_ffn_backward(const uint16_t *x, const uint16_t *preact, const uint16_t *dy, const uint16_t *W1,
+                                    const uint16_t *W2, const uint16_t *add, int act, int T, int d, int f, uint16_t *dx,
+                                    void *dW1, void *dW2, int weights_fp32, void *workspace, size_t workspace_bytes,
+                                    cudaStream_t stream);
 
 /* The global norm of a step's gradients and clipping by it, over many
  * tensors, nothing read back to the host:

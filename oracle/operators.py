@@ -1,13 +1,16 @@
 """Operators around the layer, in fp64 -- TEST INFRASTRUCTURE ONLY.
 
-Routing by scores, the norms with gate and residual between two layers, and
-the global gradient norm, each straight from its definition (include/moe.h)
-and with the gradients' formulas; it shares no code with the CUDA library.
+Routing by scores, the norms with gate, dropout and residual between two
+layers, the gated feed-forward of all tokens, and the global gradient norm,
+each straight from its definition (include/moe.h) and with the gradients'
+formulas; it shares no code with the CUDA library.
 Pins (central differences, closed forms): tests/test_oracle_operators.py.
 Next to a value the gradients return its magnitude: the sum of its terms'
 magnitudes, for error bounds that scale with the terms.
 """
 from __future__ import annotations
+
+import math
 
 import numpy as np
 
@@ -107,8 +110,32 @@ def route_scored_backward(L, idx, dw, score="sigmoid", renorm=True, scale=1.0):
             s * (fmag + np.sum(s * fmag, axis=1, keepdims=True)))
 
 
-def norm_residual(r, y=None, gamma_post=None, gate=None, gamma_pre=None, res_scale=1.0, eps=1e-6):
-    """r', n, rstd_post, rstd_pre, and |res_scale r| + |gate u|."""
+def philox4x32_10(seed, call, blocks):
+    """[len(blocks), 4] words of Philox4x32-10 for the 64-bit key `seed` and the counters (block, call)."""
+    low = (1 << 32) - 1
+    key, out = (seed & low, seed >> 32 & low), []
+    for b in blocks:
+        c, (k0, k1) = [b & low, b >> 32 & low, call & low, call >> 32 & low], key
+        for _ in range(10):
+            p, q = 0xD2511F53 * c[0], 0xCD9E8D57 * c[2]
+            c = [q >> 32 ^ c[1] ^ k0, q & low, p >> 32 ^ c[3] ^ k1, p & low]
+            k0, k1 = k0 + 0x9E3779B9 & low, k1 + 0xBB67AE85 & low
+        out.append(c)
+    return out
+
+
+def dropout_mask(T, d, p, seed, call, rows=None):
+    """[T, d] of 0 and 1 / (1 - p), p in steps of 2^-16 (`rows`: of these rows only)."""
+    rows = np.arange(T) if rows is None else np.asarray(rows)
+    blocks = ((rows[:, None].astype(object) * d + np.arange(0, d, 8)) // 8).reshape(-1)
+    words = np.array(philox4x32_10(seed, call, [int(b) for b in blocks]), np.uint64)
+    draws = np.stack([words & np.uint64(0xFFFF), words >> np.uint64(16)], axis=2).reshape(len(rows), d)
+    drop = round(p * 65536)
+    return np.where(draws >= drop, 65536.0 / (65536 - drop), 0.0)
+
+
+def norm_residual(r, y=None, gamma_post=None, gate=None, gamma_pre=None, res_scale=1.0, eps=1e-6, mask=None):
+    """r', n, rstd_post, rstd_pre, and |res_scale r| + |gate u|; `mask`: dropout_mask."""
     x = np.asarray(r, np.float64)
     mag = np.abs(x)
     rp = rq = n = None
@@ -119,6 +146,8 @@ def norm_residual(r, y=None, gamma_post=None, gate=None, gamma_pre=None, res_sca
             u = u * rp[:, None] * np.asarray(gamma_post, np.float64)
         if gate is not None:
             u = u * np.asarray(gate, np.float64)
+        if mask is not None:
+            u = np.where(mask > 0, u * mask, 0.0)
         mag = np.abs(res_scale * x) + np.abs(u)
         x = res_scale * x + u
     if gamma_pre is not None:
@@ -128,7 +157,7 @@ def norm_residual(r, y=None, gamma_post=None, gate=None, gamma_pre=None, res_sca
 
 
 def norm_residual_backward(r_out, dr_out, dn=None, y=None, gamma_post=None, gate=None, gamma_pre=None, res_scale=1.0,
-                           rstd_post=None, rstd_pre=None):
+                           rstd_post=None, rstd_pre=None, mask=None):
     """Gradients for dr_out and dn with the rows' factors given; a dict of
     (value, magnitude) for dr, dy, dgamma_pre, dgamma_post, dgate."""
     x = np.asarray(r_out, np.float64)
@@ -146,6 +175,8 @@ def norm_residual_backward(r_out, dr_out, dn=None, y=None, gamma_post=None, gate
     out["dr"] = (a * D, abs(a) * Dm)
     if y is None:
         return out
+    if mask is not None:
+        D, Dm = D * mask, Dm * mask
     y = np.asarray(y, np.float64)
     v = y if gamma_post is None else y * np.asarray(rstd_post, np.float64)[:, None]
     w = 1.0 if gamma_post is None else np.asarray(gamma_post, np.float64)
@@ -163,6 +194,49 @@ def norm_residual_backward(r_out, dr_out, dn=None, y=None, gamma_post=None, gate
         k = f * (k - y * f * f * np.mean(k * y, axis=1, keepdims=True))
     out["dy"] = (k, km)
     return out
+
+
+_erfc = np.vectorize(math.erfc, otypes=[np.float64])
+
+
+def activation(name, g):
+    """act(g), act'(g)."""
+    g = np.asarray(g, np.float64)
+    if name == "relu":
+        return np.maximum(g, 0.0), (g > 0).astype(np.float64)
+    if name == "gelu":
+        cdf = 0.5 * _erfc(-g / math.sqrt(2.0))
+        return g * cdf, cdf + g * np.exp(-0.5 * g * g) / math.sqrt(2 * math.pi)
+    if name == "silu":
+        s = 0.5 * (1 + np.tanh(0.5 * g))
+        s = np.where(g < -30, np.exp(np.minimum(g, 0.0)), s)
+        return g * s, s * (1 + g * (1 - s))
+    c = math.sqrt(2 / math.pi)
+    t = np.tanh(c * (g + 0.044715 * g ** 3))
+    low = np.exp(np.clip(2 * c * (g + 0.044715 * g ** 3), -700, 0))      # (1 + t) / 2 where t is near -1
+    s = np.where(t < -0.9999, low / (1 + low), 0.5 * (1 + t))
+    return g * s, s + g * s * (1 - s) * 2 * c * (1 + 3 * 0.044715 * g * g)
+
+
+def gated_ffn(x, W1, W2, act="silu", add=None):
+    """y, h and the pre-activations [g | u]."""
+    x, W1, W2 = (np.asarray(t, np.float64) for t in (x, W1, W2))
+    f = W2.shape[1]
+    a = x @ W1.T
+    h = activation(act, a[:, :f])[0] * a[:, f:]
+    y = h @ W2.T
+    return y if add is None else y + np.asarray(add, np.float64), h, a
+
+
+def gated_ffn_backward(x, a, dy, W1, W2, act="silu", add=None):
+    """dx, dW1, dW2 for the pre-activations a = [g | u]."""
+    x, a, dy, W1, W2 = (np.asarray(t, np.float64) for t in (x, a, dy, W1, W2))
+    f = W2.shape[1]
+    v, slope = activation(act, a[:, :f])
+    dh = dy @ W2
+    da = np.concatenate([dh * a[:, f:] * slope, dh * v], axis=1)
+    dx = da @ W1
+    return dx if add is None else dx + np.asarray(add, np.float64), da.T @ x, dy.T @ (v * a[:, f:])
 
 
 def grad_norm(grads):
