@@ -196,16 +196,31 @@ __device__ __forceinline__ void weights(const NormResidualArgs &a, uint32_t col,
     if (a.gamma_pre) load8(a.gamma_pre + col, 0, &w[0].x);
 }
 
-// The draws of an operator with dropout, by the element that begins a vector.
-template <bool DROP>
+// The draws of a thread's vectors of row t, and as a mask, a byte per vector (of four
+// at most); without dropout, nothing.
+template <bool DROP, int VPT>
 struct Draws {
+    uint4 w[VPT];
+    static constexpr uint32_t bar = 0;
     __device__ __forceinline__ explicit Draws(const NormResidualArgs &) {}
+    __device__ __forceinline__ void row(int64_t, int, uint32_t) {}
+    __device__ __forceinline__ uint32_t mask(int64_t, int, uint32_t) { return 0; }
 };
-template <>
-struct Draws<true> : Dropout {
+template <int VPT>
+struct Draws<true, VPT> : Dropout {
+    uint4 w[VPT];
     __device__ __forceinline__ explicit Draws(const NormResidualArgs &a) : Dropout(a.rng, a.drop) {}
-    __device__ __forceinline__ uint32_t kept(int64_t element) const {
-        return Dropout::kept(static_cast<uint64_t>(element) >> 3);
+    __device__ __forceinline__ void row(int64_t t, int d, uint32_t col) {
+        words(static_cast<uint64_t>(t * d + col) >> 3, 32, w);
+    }
+    __device__ __forceinline__ uint32_t mask(int64_t t, int d, uint32_t col) {
+        row(t, d, col);
+        uint32_t m[4] = {};  // four at once: each bit waits for the one before
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mark_kept(m[i >> 1], 1u << (8 * j + i), draw(w[j], i), bar);
+        return m[0] | m[1] | m[2] | m[3];
     }
 };
 
@@ -260,11 +275,12 @@ norm_residual_kernel(Args a, float inv_d, const R *r, R *r_out, uint16_t *__rest
     for (int s = 0; s < stages; ++s) issue(blockIdx.x + s * step, s);
     const bool token_gate = a.gate && a.gate_per_token;
     float gt = token_gate ? a.gate[blockIdx.x] : 1.0f;
-    const Draws<DROP> draws(a);
+    Draws<DROP, VPT> draws(a);
     if (DROP && blockIdx.x == 0 && threadIdx.x < 2) a.rng_out[threadIdx.x] = a.rng[threadIdx.x];
     int slot = 0, turn = 0, phase = 0;
     for (int64_t t = blockIdx.x; t < a.T; t += step) {
         const float gt_next = token_gate && t + step < a.T ? a.gate[t + step] : 1.0f;
+        draws.row(t, a.d, own.col);  // while the row is on its way
         rows.wait(slot, phase);
         const uint8_t *at = mine + slot * stage;
         float2 x[VPT][4], y[VPT][4];
@@ -299,11 +315,13 @@ norm_residual_kernel(Args a, float inv_d, const R *r, R *r_out, uint16_t *__rest
             for (int j = 0; j < VPT; ++j) {
                 if (!HOLD) weights(a, own.col + 256 * j, own.on[j], c[j], w[j]);
                 if constexpr (DROP) {
-                    const uint32_t kept = draws.kept(t * a.d + own.col + 256 * j);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[j][i] = fma2(both(a.res_scale), x[j][i],
-                                       only(kept, i, mul2(mul2(both(f), c[j][i]), y[j][i])));
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 fc = mul2(both(f), c[j][i]);
+                        x[j][i] = mul2(both(a.res_scale), x[j][i]);
+                        fma_kept(x[j][i].x, fc.x, y[j][i].x, draw(draws.w[j], 2 * i), draws.bar);
+                        fma_kept(x[j][i].y, fc.y, y[j][i].y, draw(draws.w[j], 2 * i + 1), draws.bar);
+                    }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -437,10 +455,10 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
     for (int s = 0; s < stages; ++s) issue(begin + s * step, s);
     // The first reading of the row in slot `slot`: the four sums (of h z,
     // c y dr', c y h, c y z) of the warp go to `sums`.
-    // With dropout `kept` takes the row's draws, a byte per vector, for the second reading.
-    const Draws<DROP> draws(a);
-    auto first_pass = [&](int slot, float rq, float4 *sums, uint32_t k, uint32_t t, uint32_t &kept) {
-        kept = 0;
+    // With dropout (`kept`: the row's mask) only the kept elements' products with
+    // y enter, and s1 and s2 as the one sum that is needed of them, s1 + rq s2.
+    Draws<DROP, VPT> draws(a);
+    auto first_pass = [&](int slot, float rq, float4 *sums, uint32_t k, uint32_t kept) {
         const uint8_t *at16 = mine + slot * stage + lane * 16, *at_r = mine + slot * stage + lane * (8 * sizeof(R));
         float2 s0 = both(0.0f), s1 = s0, s2 = s0, s3 = s0;
 #pragma unroll
@@ -451,18 +469,18 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
                 read8<uint16_t>(at16 + j * 512, cy);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) cy[i] = mul2(cy[i], c[j][i]);
-                if constexpr (DROP) {
-                    const uint32_t m = draws.kept(static_cast<int64_t>(t) * a.d + own.col + 256 * j);
-                    kept |= m << (8 * j);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) cy[i] = only(m, i, mul2(cy[i], both(a.keep_scale)));
-                }
-                if (DR) {
+                if (DR && !DROP) {
                     float2 g[4];
                     read8<R>(at_r + j * piece_bytes<R>() + AT_DR, g);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) s1 = fma2(cy[i], g[i], s1);
                 }
+            }
+            float2 e[4];
+            if constexpr (DROP) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) e[i] = both(0.0f);
+                if (DR) read8<R>(at_r + j * piece_bytes<R>() + AT_DR, e);
             }
             if (pre) {
                 float2 z[4], g[4];
@@ -474,13 +492,25 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
                     accq[j][i] = fma2(g[i], z[i], accq[j][i]);
                     g[i] = mul2(g[i], w[j][i]);  // h
                     s0 = fma2(g[i], z[i], s0);
+                    if constexpr (DROP) {
+                        e[i] = fma2(both(rq), g[i], e[i]);
+                        fma_masked(s1.x, cy[i].x, e[i].x, s3.x, cy[i].x, z[i].x, kept, 1u << (8 * j + 2 * i));
+                        fma_masked(s1.y, cy[i].y, e[i].y, s3.y, cy[i].y, z[i].y, kept, 2u << (8 * j + 2 * i));
+                    }
                 }
-                if (has_y) {
+                if (has_y && !DROP) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         s2 = fma2(cy[i], g[i], s2);
                         s3 = fma2(cy[i], z[i], s3);
                     }
+                }
+            } else if constexpr (DROP) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float none = 0.0f;
+                    fma_masked(s1.x, cy[i].x, e[i].x, none, 0.0f, 0.0f, kept, 1u << (8 * j + 2 * i));
+                    fma_masked(s1.y, cy[i].y, e[i].y, none, 0.0f, 0.0f, kept, 2u << (8 * j + 2 * i));
                 }
             }
         }
@@ -505,8 +535,9 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
     int phase = 0;  // of the slot that first_pass reads next
     uint32_t k = 0, kept = 0, kept_next = 0;
     if (PIPE && begin < rows_end) {
+        kept = draws.mask(begin, a.d, own.col);
         rows.wait(0, 0);
-        first_pass(0, f.rq, red[0], 0, begin, kept);
+        first_pass(0, f.rq, red[0], 0, kept);
     }
     for (uint32_t t = begin; t < rows_end; t += step) {
         const Row after = factors(t + 2 * step);
@@ -516,12 +547,14 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
             s = collect(red[turn], k);
             if (ahead == 0) phase ^= 1;
             if (t + step < rows_end) {
+                kept_next = draws.mask(t + step, a.d, own.col);  // while the row is on its way
                 rows.wait(ahead, phase);
-                first_pass(ahead, next.rq, red[other], k + 1, t + step, kept_next);
+                first_pass(ahead, next.rq, red[other], k + 1, kept_next);
             }
         } else {
+            kept = draws.mask(t, a.d, own.col);
             rows.wait(slot, phase);
-            first_pass(slot, f.rq, red[turn], k, t, kept);
+            first_pass(slot, f.rq, red[turn], k, kept);
             s = collect(red[turn], k);
             if (ahead == 0) phase ^= 1;
         }
@@ -529,7 +562,8 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
         ++k;
         const uint8_t *at16 = mine + slot * stage + lane * 16, *at_r = mine + slot * stage + lane * (8 * sizeof(R));
         const float m1 = f.rq * s.x * inv_d;
-        const float cyD = s.y + f.rq * s.z - m1 * s.w;
+        float cyD = s.y + f.rq * s.z - m1 * s.w;
+        if (DROP) cyD *= a.keep_scale;
         const float m2 = post ? f.gt * cyD * inv_d * f.rp * f.rp * f.rp : 0.0f;
         if (a.gate && a.gate_per_token && warp == 0 && lane == 0 && rank == 0) dgate[t] = f.rp * cyD;
         const float2 q = both(DROP ? f.gt * f.rp * a.keep_scale : f.gt * f.rp), mz = both(-m1 * f.rq), my = both(-m2), rq = both(f.rq);
@@ -566,11 +600,9 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
                 for (int i = 0; i < 4; ++i) {
                     D[i] = mul2(D[i], q);
                     if constexpr (DROP) {
-                        const uint32_t m = kept >> (8 * j);
-                        D[i] = only(m, i, D[i]);
-                        accp[j][i] = fma2(only(m, i, y[i]), D[i], accp[j][i]);
-                        o[i] = mul2(D[i], c[j][i]);
-                        if (post) o[i] = fma2(my, y[i], o[i]);
+                        o[i] = post ? mul2(my, y[i]) : both(0.0f);
+                        fma_masked(accp[j][i].x, y[i].x, D[i].x, o[i].x, c[j][i].x, D[i].x, kept, 1u << (8 * j + 2 * i));
+                        fma_masked(accp[j][i].y, y[i].y, D[i].y, o[i].y, c[j][i].y, D[i].y, kept, 2u << (8 * j + 2 * i));
                     } else {
                         accp[j][i] = fma2(y[i], D[i], accp[j][i]);
                         o[i] = fma2(my, y[i], mul2(D[i], c[j][i]));
