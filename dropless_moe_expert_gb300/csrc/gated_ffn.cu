@@ -18,6 +18,7 @@
 //            DACT    da and h from the tile of dh and the tiles of g and u
 // Warps: 0 TMA loads, 1 MMAs and TMEM, 2 to 5 epilogue.  Every wait is bounded.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "gated_ffn.cuh"
@@ -31,7 +32,7 @@ namespace ff {
 
 using gg::pack_bf16x2;
 
-enum Epi { GATED, PLAIN, ADD, DACT };
+enum Epi { GATED, PLAIN, ADD, DACT, GRADS };
 
 constexpr int BK = 64;          // a slice of K: 128 bytes, one swizzle line
 constexpr int UMMA_K = 16;
@@ -43,52 +44,88 @@ constexpr int STAGE = 4 * BOX;    // of a CTA: 128 rows of A, 128 columns of B
 constexpr int CHUNK = 32;         // the epilogue takes 32 rows x 32 columns per warp at a time
 constexpr int BUF = CHUNK * CHUNK * 2;
 
-// An epilogue warp's buffers in shared memory: `sets` of `boxes` 32 x 32 boxes,
-// of which the first `in` are filled by TMA before a chunk is computed.
+// An epilogue warp's buffers in shared memory.  A chunk without inputs takes
+// one of two boxes in turn.  One with inputs takes one of `sets` of `boxes`
+// boxes, of which TMA fills the first `in` before it is computed.
 struct Buffers {
     int sets, boxes, in, bytes;
 };
 template <Epi EPI, typename Out>
 __host__ __device__ constexpr Buffers buffers() {
-    return EPI == DACT ? Buffers{2, 3, 2, BUF} : EPI == ADD ? Buffers{3, 1, 1, BUF}
-                                               : Buffers{2, 1, 0, CHUNK * CHUNK * static_cast<int>(sizeof(Out))};
+    constexpr int plain = 2 * CHUNK * CHUNK * static_cast<int>(sizeof(Out));
+    return EPI == DACT                  ? Buffers{2, 3, 2, 2 * 3 * BUF}
+           : EPI == ADD || EPI == GRADS ? Buffers{3, 1, 1, 3 * BUF > plain ? 3 * BUF : plain}
+                                        : Buffers{2, 1, 0, plain};
 }
 
 template <Epi EPI, typename Out>
 struct Layout {
     static constexpr Buffers B = buffers<EPI, Out>();
-    static constexpr int WARP_BYTES = B.sets * B.boxes * B.bytes;
     static constexpr int STAGES = EPI == DACT ? 5 : 6;
+    static constexpr int QUEUE = EPI == GRADS ? gg::queue_slots(STAGES) : 0;
     static constexpr int OFF_EPI = STAGES * STAGE;
-    static constexpr int OFF_BARS = OFF_EPI + 4 * WARP_BYTES;
-    static constexpr int NUM_BARS = 2 * STAGES + 5 + 4 * B.sets;  // full, empty, tfull[2], tempty[2], drain, landed[4][sets]
-    static constexpr int OFF_TMEM = OFF_BARS + NUM_BARS * 8;
+    static constexpr int OFF_BARS = OFF_EPI + 4 * B.bytes;
+    // full, empty, tfull[2], tempty[2], drain, landed[4][sets], queued[QUEUE]
+    static constexpr int NUM_BARS = 2 * STAGES + 5 + 4 * B.sets + QUEUE;
+    static constexpr int OFF_QUEUE = OFF_BARS + NUM_BARS * 8;
+    static constexpr int OFF_TMEM = OFF_QUEUE + QUEUE * 4;
     static constexpr int OFF_ABORT = OFF_TMEM + 4;
     static constexpr int BYTES = OFF_ABORT + 4 + 1024;  // slack for 1024-byte alignment
     static_assert(BYTES <= 227 * 1024, "shared memory budget");
 };
 
+// One product: a result of M x N (GATED: N = f) and a sum of length K, in MT x NT
+// tiles, band by band; those from `halves` on are cut into two of half the width,
+// which come in the list in their place.
+struct Product {
+    int M, N, K, MT, NT;
+    int halves, first, tiles;   // `first`: of this product in the list of tiles
+};
+constexpr int PRODUCTS = 3;     // GRADS: dx, dW1, dW2, in the order that the host gives
 struct Params {
-    int M, N, K;   // of the result and the sum; GATED: N = f
-    int MT, NT;    // tiles
+    Product product[PRODUCTS];
+    int products, tiles;
+    int kind[PRODUCTS];         // GRADS: which of KIND_*
+    bool add;                   // GRADS: dx has a matrix to be added
     int act;
-    bool keep;     // GATED: store a
+    bool keep;                  // GATED: store a
+    bool behind;                // launched before the kernel that writes the operands has ended
+    int *tickets;               // GRADS, nullable: of the order of tiles (gg::Params::sched)
     int *status;
     uint64_t timeout_ns;
 };
-// a, b: operands.  GATED: out h, more g and u of `a`.  ADD: in.  DACT: in, in2 g and u, out h, more dg and du.
+constexpr int KIND_DX = 0, KIND_WEIGHTS = 1;
+// a, b: operands (half_b: b with boxes for half a tile, where b is K-major).
+// GATED: out h, more g and u of `a`.  ADD: in.  DACT: in, in2 g and u, out h, more dg and du.
 struct Maps {
-    CUtensorMap a, b, out, more[2], in, in2;
+    CUtensorMap a, b, half_b, out, more[2], in, in2;
+};
+struct GradMaps {
+    CUtensorMap a[PRODUCTS], b[PRODUCTS], out[PRODUCTS], in;
 };
 
 struct Tile {
-    int m0, n0;
+    int product, m0, n0, width;  // width: accumulator columns
 };
 template <Epi EPI>
 __device__ __forceinline__ Tile decode(const Params &p, int tile) {
-    const int band = tile / (BAND * p.NT), within = tile - band * BAND * p.NT;
-    const int height = min(BAND, p.MT - band * BAND), n = within / height;
-    return Tile{(band * BAND + within - n * height) * TILE_M, n * (EPI == GATED ? TILE_N / 2 : TILE_N)};
+    Tile t;
+    t.product = 0;
+    if (EPI == GRADS)
+        while (t.product + 1 < p.products && tile >= p.product[t.product + 1].first) ++t.product;
+    const Product &q = p.product[t.product];
+    int at = tile - q.first, sub = 0;
+    t.width = TILE_N;
+    if (at >= q.halves) {
+        sub = (at - q.halves) & 1;
+        at = q.halves + ((at - q.halves) >> 1);
+        t.width = TILE_N / 2;
+    }
+    const int band = at / (BAND * q.NT), within = at - band * BAND * q.NT;
+    const int height = min(BAND, q.MT - band * BAND), n = within / height;
+    t.m0 = (band * BAND + within - n * height) * TILE_M;
+    t.n0 = (2 * n + sub) * (EPI == GATED ? TILE_N / 4 : TILE_N / 2);
+    return t;
 }
 
 // One lane's 32 values into its row of a 32 x 32 bf16 box (64-byte swizzle), and back.
@@ -114,27 +151,27 @@ __device__ __forceinline__ void write_row(uint8_t *box, int lane, const uint32_t
 }
 __device__ __forceinline__ float low(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float high(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+__device__ __forceinline__ void pack(const uint32_t (&v)[32], uint32_t (&packed)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) packed[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+}
 
 // An epilogue warp: its 32 rows of a CTA's 128, and its buffers.
 template <Epi EPI, typename Out>
 struct Warp {
     using L = Layout<EPI, Out>;
     const Params &p;
-    const Maps &maps;
     uint8_t *bufs;
     uint64_t *landed;
     volatile int *abort;
     int lane, row_of_tile;   // the first of its rows within a tile
-    int pair, npairs;
-    uint32_t turn = 0;       // chunks stored (without inputs: boxes stored)
-    // the next chunk whose inputs are to be loaded
-    int next_tile, next_c = 0;
-    uint32_t asked = 0;
+    uint32_t boxes = 0;      // stored by put()
+    uint32_t asked = 0, taken = 0;  // chunks whose inputs were asked for, and used
 
-    // Without inputs: a box of packed values out through the next buffer.
+    // A box of values out through the next buffer.
     template <typename Values>
     __device__ __forceinline__ void put(const CUtensorMap *tm, const Values &v, int col, int row) {
-        uint8_t *box = bufs + (turn & 1) * L::B.bytes;
+        uint8_t *box = bufs + (boxes & 1) * sizeof(v) * 32;
         if (lane == 0) bulk_wait_read<1>();  // the store from two boxes ago has read it
         __syncwarp();
         write_row(box, lane, v);
@@ -144,153 +181,144 @@ struct Warp {
             tma_store_2d_evict_first(tm, box, col, row, l2_policy_evict_first());
             bulk_commit();
         }
-        ++turn;
+        ++boxes;
     }
 
-    // With inputs: asks for those of the next chunk (every lane follows the order, lane 0 loads).
-    __device__ __forceinline__ void ask() {
-        const int total = p.MT * p.NT;
-        for (; next_tile < total; next_tile += npairs, next_c = 0) {
-            const Tile t = decode<EPI>(p, next_tile);
-            const int row = t.m0 + row_of_tile, col = t.n0 + next_c;
-            if (row >= p.M || next_c >= TILE_N || col >= p.N) continue;
-            if (lane == 0) {
-                const int set = asked % L::B.sets;
-                uint8_t *box = bufs + set * L::B.boxes * L::B.bytes;
-                bulk_wait_read<L::B.sets - 2>();  // the stores of the chunk that used the set have read it
-                mbar_arrive_expect_tx(&landed[set], L::B.in * L::B.bytes);
-                tma_load_2d(box, &maps.in, &landed[set], col, row);
-                if (EPI == DACT) tma_load_2d(box + L::B.bytes, &maps.in2, &landed[set], col, row);
-            }
-            ++asked;
-            next_c += CHUNK;
-            return;
+    // Asks for the inputs of the next chunk.  FIRST: of a tile, whose buffers may be in other use.
+    template <bool FIRST>
+    __device__ __forceinline__ void ask(const CUtensorMap *in, const CUtensorMap *in2, int col, int row) {
+        if (lane == 0) {
+            const int set = asked % L::B.sets;
+            uint8_t *box = bufs + set * L::B.boxes * BUF;
+            bulk_wait_read<FIRST ? 0 : L::B.sets - 2>();  // the stores of the chunk that used the set have read it
+            mbar_arrive_expect_tx(&landed[set], L::B.in * BUF);
+            tma_load_2d(box, in, &landed[set], col, row);
+            if (EPI == DACT) tma_load_2d(box + BUF, in2, &landed[set], col, row);
         }
-    }
-    __device__ __forceinline__ bool inputs(uint32_t chunk) {
-        return mbar_wait(&landed[chunk % L::B.sets], (chunk / L::B.sets) & 1, abort, p.status, p.timeout_ns);
+        ++asked;
     }
     // Before the warp leaves: its own copies have landed.
     __device__ __forceinline__ void finish() {
         volatile int no_abort = 0;
-        for (uint32_t c = turn; L::B.in && c < asked; ++c)
+        for (uint32_t c = taken; L::B.in && c != asked; ++c)
             mbar_wait(&landed[c % L::B.sets], (c / L::B.sets) & 1, &no_abort, p.status, p.timeout_ns);
         if (lane == 0) bulk_wait_all();
     }
 
-    // The warp's part of a tile, its accumulator (lane quarter) at tbase.
-    __device__ __forceinline__ bool tile(const Tile &t, uint32_t tbase) {
-        const int row = t.m0 + row_of_tile;
-        if (row >= p.M) return true;  // the same for the warp
-        if constexpr (EPI == GATED) {
+    // 64 columns at a time of a product that is stored as it is
+    __device__ __forceinline__ void plain(const CUtensorMap *out, const Product &q, const Tile &t, uint32_t tbase, int row) {
+        // the boxes may hold inputs' chunks that are still being stored
+        if (EPI == GRADS && lane == 0) bulk_wait_read<0>();
+        __syncwarp();
 #pragma unroll 1
-            for (int c = 0; c < TILE_N / 2 && t.n0 + c < p.N; c += CHUNK) {
-                uint32_t g[32], u[32], packed[16];
-                tmem_ld_32x32b_x32(tbase + c, g);
-                tmem_ld_32x32b_x32(tbase + TILE_N / 2 + c, u);
-                tmem_ld_wait();
+        for (int c = 0; c < t.width && t.n0 + c < q.N; c += 2 * CHUNK) {
+            uint32_t v[2][32];
+            tmem_ld_32x32b_x32(tbase + c, v[0]);
+            tmem_ld_32x32b_x32(tbase + c + CHUNK, v[1]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int col = t.n0 + c + k * CHUNK;
+                if (col >= q.N) break;
+                if constexpr (sizeof(Out) == 4) {
+                    put(out, v[k], col, row);
+                } else {
+                    uint32_t packed[16];
+                    pack(v[k], packed);
+                    put(out, packed, col, row);
+                }
+            }
+        }
+    }
+
+    // h of a tile whose accumulator holds gate columns and then as many up columns
+    __device__ __forceinline__ void gated(const Maps &maps, const Product &q, const Tile &t, uint32_t tbase, int row) {
+#pragma unroll 1
+        for (int c = 0; c < t.width / 2 && t.n0 + c < q.N; c += CHUNK) {
+            uint32_t g[32], u[32], packed[16];
+            tmem_ld_32x32b_x32(tbase + c, g);
+            tmem_ld_32x32b_x32(tbase + t.width / 2 + c, u);
+            tmem_ld_wait();
+            with_activation(p.act, [&](auto act) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    packed[i] =
+                        pack_bf16x2(activate<act.value>(__uint_as_float(g[2 * i])) * __uint_as_float(u[2 * i]),
+                                    activate<act.value>(__uint_as_float(g[2 * i + 1])) * __uint_as_float(u[2 * i + 1]));
+            });
+            put(&maps.out, packed, t.n0 + c, row);
+            if (p.keep) {
+                pack(g, packed);
+                put(&maps.more[0], packed, t.n0 + c, row);
+                pack(u, packed);
+                put(&maps.more[1], packed, t.n0 + c, row);
+            }
+        }
+    }
+
+    // A chunk's inputs are on their way while the one before it is computed; the outputs take their place.
+    __device__ __forceinline__ bool with_inputs(const CUtensorMap *in, const CUtensorMap *in2, const CUtensorMap *out,
+                                                const CUtensorMap *out2, const CUtensorMap *out3, const Product &q,
+                                                const Tile &t, uint32_t tbase, int row) {
+#pragma unroll 1
+        for (int c = 0; c < t.width && t.n0 + c < q.N; c += CHUNK) {
+            const int col = t.n0 + c;
+            if (c + CHUNK < t.width && col + CHUNK < q.N) ask<false>(in, in2, col + CHUNK, row);
+            uint32_t v[32], e[16];
+            tmem_ld_32x32b_x32(tbase + c, v);
+            tmem_ld_wait();
+            const uint32_t set = taken % L::B.sets;
+            if (!mbar_wait(&landed[set], (taken / L::B.sets) & 1, abort, p.status, p.timeout_ns)) return false;
+            ++taken;
+            uint8_t *box = bufs + set * L::B.boxes * BUF;
+            read_row(box, lane, e);
+            if constexpr (EPI != DACT) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    e[i] = pack_bf16x2(__uint_as_float(v[2 * i]) + low(e[i]), __uint_as_float(v[2 * i + 1]) + high(e[i]));
+                write_row(box, lane, e);
+            } else {
+                uint32_t u[16], h[16];
+                read_row(box + BUF, lane, u);
                 with_activation(p.act, [&](auto act) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        packed[i] = pack_bf16x2(
-                            activate<act.value>(__uint_as_float(g[2 * i])) * __uint_as_float(u[2 * i]),
-                            activate<act.value>(__uint_as_float(g[2 * i + 1])) * __uint_as_float(u[2 * i + 1]));
-                });
-                put(&maps.out, packed, t.n0 + c, row);
-                if (p.keep) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        packed[i] = pack_bf16x2(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
-                    put(&maps.more[0], packed, t.n0 + c, row);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        packed[i] = pack_bf16x2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-                    put(&maps.more[1], packed, t.n0 + c, row);
-                }
-            }
-        } else if constexpr (EPI == PLAIN && sizeof(Out) == 4) {
-#pragma unroll 1
-            for (int c = 0; c < TILE_N && t.n0 + c < p.N; c += CHUNK) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(tbase + c, v);
-                tmem_ld_wait();
-                put(&maps.out, v, t.n0 + c, row);
-            }
-        } else if constexpr (EPI == PLAIN) {
-#pragma unroll 1
-            for (int c = 0; c < TILE_N && t.n0 + c < p.N; c += 2 * CHUNK) {
-                uint32_t v[2][32], packed[16];
-                tmem_ld_32x32b_x32(tbase + c, v[0]);
-                tmem_ld_32x32b_x32(tbase + c + CHUNK, v[1]);
-                tmem_ld_wait();
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if (t.n0 + c + k * CHUNK >= p.N) break;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        packed[i] = pack_bf16x2(__uint_as_float(v[k][2 * i]), __uint_as_float(v[k][2 * i + 1]));
-                    put(&maps.out, packed, t.n0 + c + k * CHUNK, row);
-                }
-            }
-        } else {
-#pragma unroll 1
-            for (int c = 0; c < TILE_N && t.n0 + c < p.N; c += CHUNK) {
-                ask();  // for the chunk after this one
-                uint32_t v[32], e[16];
-                tmem_ld_32x32b_x32(tbase + c, v);
-                tmem_ld_wait();
-                if (!inputs(turn)) return false;
-                uint8_t *box = bufs + (turn % L::B.sets) * L::B.boxes * L::B.bytes;
-                read_row(box, lane, e);
-                if constexpr (EPI == ADD) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        e[i] = pack_bf16x2(__uint_as_float(v[2 * i]) + low(e[i]),
-                                           __uint_as_float(v[2 * i + 1]) + high(e[i]));
-                    write_row(box, lane, e);
-                } else {
-                    uint32_t u[16], h[16];
-                    read_row(box + L::B.bytes, lane, u);
-                    with_activation(p.act, [&](auto act) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float slope[2];
-                            const float a0 = activate<act.value>(low(e[i]), slope[0]);
-                            const float a1 = activate<act.value>(high(e[i]), slope[1]);
-                            const float d0 = __uint_as_float(v[2 * i]), d1 = __uint_as_float(v[2 * i + 1]);
-                            const float u0 = low(u[i]), u1 = high(u[i]);
-                            h[i] = pack_bf16x2(a0 * u0, a1 * u1);
-                            e[i] = pack_bf16x2(d0 * u0 * slope[0], d1 * u1 * slope[1]);
-                            u[i] = pack_bf16x2(d0 * a0, d1 * a1);
-                        }
-                    });
-                    write_row(box, lane, e);
-                    write_row(box + L::B.bytes, lane, u);
-                    write_row(box + 2 * L::B.bytes, lane, h);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    const int col = t.n0 + c;
-                    tma_store_2d_evict_first(EPI == ADD ? &maps.out : &maps.more[0], box, col, row,
-                                             l2_policy_evict_first());
-                    if (EPI == DACT) {
-                        tma_store_2d_evict_first(&maps.more[1], box + L::B.bytes, col, row, l2_policy_evict_first());
-                        tma_store_2d_evict_first(&maps.out, box + 2 * L::B.bytes, col, row, l2_policy_evict_first());
+                    for (int i = 0; i < 16; ++i) {
+                        float slope[2];
+                        const float a0 = activate<act.value>(low(e[i]), slope[0]);
+                        const float a1 = activate<act.value>(high(e[i]), slope[1]);
+                        const float d0 = __uint_as_float(v[2 * i]), d1 = __uint_as_float(v[2 * i + 1]);
+                        const float u0 = low(u[i]), u1 = high(u[i]);
+                        h[i] = pack_bf16x2(a0 * u0, a1 * u1);
+                        e[i] = pack_bf16x2(d0 * u0 * slope[0], d1 * u1 * slope[1]);
+                        u[i] = pack_bf16x2(d0 * a0, d1 * a1);
                     }
-                    bulk_commit();
+                });
+                write_row(box, lane, e);
+                write_row(box + BUF, lane, u);
+                write_row(box + 2 * BUF, lane, h);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d_evict_first(out, box, col, row, l2_policy_evict_first());
+                if (EPI == DACT) {
+                    tma_store_2d_evict_first(out2, box + BUF, col, row, l2_policy_evict_first());
+                    tma_store_2d_evict_first(out3, box + 2 * BUF, col, row, l2_policy_evict_first());
                 }
-                ++turn;
+                bulk_commit();
             }
         }
         return true;
     }
 };
 
-template <Epi EPI, bool A_MN, bool B_MN, typename Out>
-__global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_constant__ Maps maps, const Params p) {
+// M: Maps, or GradMaps for GRADS, whose products have operands of their own:
+// dx an A that is K-major, the weights' gradients one that is MN-major; B is MN-major in all.
+template <Epi EPI, bool A_MN, bool B_MN, typename Out, typename M>
+__global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_constant__ M maps, const Params p) {
     using L = Layout<EPI, Out>;
-    constexpr int STAGES = L::STAGES;
+    constexpr int STAGES = L::STAGES, QUEUE = L::QUEUE;
+    constexpr bool MANY = EPI == GRADS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::OFF_BARS);  // used in CTA 0 only
@@ -299,12 +327,15 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
     uint64_t *tempty = tfull + 2;                                       // CTA 0: 4 warps x 2 CTAs arrive
     uint64_t *drain = tempty + 2;
     uint64_t *landed = drain + 1;
+    uint64_t *queued = landed + 4 * L::B.sets;                          // both CTAs
+    volatile int *queue = reinterpret_cast<volatile int *>(smem + L::OFF_QUEUE);
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + L::OFF_TMEM);
     volatile int *s_abort = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();  // 0 issues the MMAs
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
     const int half = 128 * static_cast<int>(rank);
+    const bool drawn = MANY && p.tickets != nullptr;  // the order of tiles: by tickets, else in turn
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
@@ -317,10 +348,9 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
         }
         mbar_init(drain, 1);
         for (int i = 0; i < 4 * L::B.sets; ++i) mbar_init(&landed[i], 1);
+        for (int i = 0; i < QUEUE; ++i) mbar_init(&queued[i], 1);
         *s_abort = 0;
         fence_mbar_init();
-        tma_prefetch_desc(&maps.a);
-        tma_prefetch_desc(&maps.b);
     }
     __syncthreads();
     // both CTAs' barriers exist before anything crosses the pair, and before
@@ -334,22 +364,75 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *s_tmem;
-    const int total = p.MT * p.NT, KB = (p.K + BK - 1) / BK;
+    // the kernel behind this one may take the SMs that fall free, up to where it reads what this one writes
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // The k-th tile of the pair (a negative one ends the list) for the roles that do not decide it.
+    auto tile_of = [&](int k, int *tile) {
+        if (!drawn) {
+            *tile = pair + k * npairs < p.tiles ? pair + k * npairs : -1;
+            return true;
+        }
+        if (!mbar_wait<true>(&queued[k % max(QUEUE, 1)], (k / max(QUEUE, 1)) & 1, s_abort, p.status, p.timeout_ns))
+            return false;
+        *tile = queue[k % max(QUEUE, 1)];
+        return true;
+    };
+    auto slices = [&](const Tile &t) { return (p.product[t.product].K + BK - 1) / BK; };
 
     if (warp == 0) {
         if (lane == 0) {
+            if (p.behind) grid_dependency_wait();
             const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);  // both CTAs' copies signal CTA 0's barriers
+            const uint32_t queue1 = mapa_shared(smem_u32(const_cast<int *>(queue)), 1);
+            const uint32_t queued1 = mapa_shared(smem_u32(queued), 1);
+            // CTA 0 draws the pair's tiles and tells both CTAs: tile k + 1 when the loads of tile k begin
+            auto publish = [&](int k, int tile) {
+                queue[k % max(QUEUE, 1)] = tile;
+                mbar_arrive(&queued[k % max(QUEUE, 1)]);
+                send_to_peer(queue1 + 4u * (k % max(QUEUE, 1)), tile, queued1 + 8u * (k % max(QUEUE, 1)));
+            };
+            int current = -1, next = -1;
+            if (drawn && rank == 0) {
+                current = atomicAdd(p.tickets, 1);
+                if (current >= p.tiles) current = -1;
+                next = current >= 0 ? atomicAdd(p.tickets, 1) : p.tiles;
+                publish(0, current);
+            }
             int armed[STAGES];
 #pragma unroll
             for (int i = 0; i < STAGES; ++i) armed[i] = -1;
             uint32_t stage = 0, phase = 0;
             bool ok = true;
-            for (int tile = pair; ok && tile < total; tile += npairs) {
+            for (int k = 0; ok; ++k) {
+                int tile;
+                if (drawn && rank == 0) {
+                    tile = current;
+                    if (tile >= 0) {
+                        current = next < p.tiles ? next : -1;
+                        publish(k + 1, current);
+                        if (current >= 0) next = atomicAdd(p.tickets, 1);
+                    }
+                } else if (!tile_of(k, &tile)) {
+                    ok = false;
+                    break;
+                }
+                if (tile < 0) break;
                 const Tile t = decode<EPI>(p, tile);
-                const int a0 = t.m0 + half;
+                const bool whole = t.width == TILE_N;
+                const CUtensorMap *ma, *mb;
+                bool a_mn = A_MN;
+                if constexpr (MANY) {
+                    ma = &maps.a[t.product], mb = &maps.b[t.product];
+                    a_mn = p.kind[t.product] == KIND_WEIGHTS;
+                } else {
+                    ma = &maps.a, mb = whole || B_MN ? &maps.b : &maps.half_b;
+                }
+                const int a0 = t.m0 + half, KB = slices(t);
                 // GATED: CTA 0 loads the gate rows, CTA 1 the up rows (those of a last
                 // block past their half of W1 give columns that are not stored)
-                const int b0 = EPI == GATED ? t.n0 + static_cast<int>(rank) * p.N : t.n0 + half;
+                const int b0 = EPI == GATED ? t.n0 + static_cast<int>(rank) * p.product[0].N
+                                            : t.n0 + static_cast<int>(rank) * (t.width / 2);
                 for (int kb = 0; kb < KB; ++kb) {
                     if (!mbar_wait<true>(&empty[stage], phase ^ 1u, s_abort, p.status, p.timeout_ns)) {
                         ok = false;
@@ -357,18 +440,18 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
                     }
                     uint8_t *sa = smem + stage * STAGE, *sb = sa + 2 * BOX;
                     const uint32_t bar = full0 + 8u * stage;
-                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * STAGE);
-                    if (A_MN) {
-                        tma_load_2d_pair(sa, &maps.a, bar, a0, kb * BK);
-                        tma_load_2d_pair(sa + BOX, &maps.a, bar, a0 + 64, kb * BK);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], whole ? 2 * STAGE : 2 * (STAGE - BOX));
+                    if (a_mn) {
+                        tma_load_2d_pair(sa, ma, bar, a0, kb * BK);
+                        tma_load_2d_pair(sa + BOX, ma, bar, a0 + 64, kb * BK);
                     } else {
-                        tma_load_2d_pair(sa, &maps.a, bar, kb * BK, a0);
+                        tma_load_2d_pair(sa, ma, bar, kb * BK, a0);
                     }
                     if (B_MN) {
-                        tma_load_2d_pair(sb, &maps.b, bar, b0, kb * BK);
-                        tma_load_2d_pair(sb + BOX, &maps.b, bar, b0 + 64, kb * BK);
+                        tma_load_2d_pair(sb, mb, bar, b0, kb * BK);
+                        if (whole) tma_load_2d_pair(sb + BOX, mb, bar, b0 + 64, kb * BK);
                     } else {
-                        tma_load_2d_pair(sb, &maps.b, bar, kb * BK, b0);
+                        tma_load_2d_pair(sb, mb, bar, kb * BK, b0);
                     }
                     armed[stage] = static_cast<int>(phase);
                     if (++stage == STAGES) stage = 0, phase ^= 1u;
@@ -390,10 +473,20 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
-            constexpr uint32_t idesc = idesc_bf16_f32(TILE_M, TILE_N, A_MN, B_MN);
             uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
             bool ok = true, issued = false;
-            for (int tile = pair; ok && tile < total; tile += npairs) {
+            for (int k = 0; ok; ++k) {
+                int tile;
+                if (!tile_of(k, &tile)) {
+                    ok = false;
+                    break;
+                }
+                if (tile < 0) break;
+                const Tile t = decode<EPI>(p, tile);
+                const bool a_mn = MANY ? p.kind[t.product] == KIND_WEIGHTS : A_MN;
+                const uint32_t idesc = idesc_bf16_f32(TILE_M, TILE_N, false, B_MN) - ((TILE_N - t.width) >> 3 << 17) +
+                                       (a_mn ? 1u << 15 : 0u);
+                const int KB = slices(t);
                 if (!mbar_wait<true>(&tempty[acc], acc_phase ^ 1u, s_abort, p.status, p.timeout_ns)) {
                     ok = false;
                     break;
@@ -407,13 +500,13 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
                     }
                     tc_fence_after();
                     const uint32_t sa = smem_u32(smem + stage * STAGE);
-                    const uint64_t adesc = A_MN ? smem_desc_mnmajor_sw128(sa, BOX) : smem_desc_kmajor_sw128(sa);
+                    const uint64_t adesc = a_mn ? smem_desc_mnmajor_sw128(sa, BOX) : smem_desc_kmajor_sw128(sa);
                     const uint64_t bdesc =
                         B_MN ? smem_desc_mnmajor_sw128(sa + 2 * BOX, BOX) : smem_desc_kmajor_sw128(sa + 2 * BOX);
+                    const uint32_t step = a_mn ? 128 : 2;
 #pragma unroll
                     for (int j = 0; j < BK / UMMA_K; ++j)
-                        umma_bf16_pair(d_tmem, adesc + (A_MN ? 128 : 2) * j, bdesc + (B_MN ? 128 : 2) * j, idesc,
-                                       (kb | j) != 0);
+                        umma_bf16_pair(d_tmem, adesc + step * j, bdesc + (B_MN ? 128 : 2) * j, idesc, (kb | j) != 0);
                     issued = true;
                     umma_commit_pair_multicast(&empty[stage], 0x3);
                     if (++stage == STAGES) stage = 0, phase ^= 1u;
@@ -431,15 +524,50 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
         }
     } else {
         const int q = warp & 3;  // the lane quarter that a warp may read
-        Warp<EPI, Out> w{p, maps, smem + L::OFF_EPI + (warp - 2) * L::WARP_BYTES, landed + (warp - 2) * L::B.sets, s_abort,
-                         lane, half + 32 * q, pair, npairs, 0, pair};
-        if (L::B.in) w.ask();
+        Warp<EPI, Out> w{p, smem + L::OFF_EPI + (warp - 2) * L::B.bytes, landed + (warp - 2) * L::B.sets, s_abort, lane,
+                         half + 32 * q};
         const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
         uint32_t acc = 0, acc_phase = 0;
-        for (int tile = pair; tile < total; tile += npairs) {
+        for (int k = 0;; ++k) {
+            int tile;
+            if (!tile_of(k, &tile) || tile < 0) break;
+            const Tile t = decode<EPI>(p, tile);
+            const Product &pr = p.product[t.product];
+            const int row = t.m0 + w.row_of_tile;
+            const bool any = row < pr.M && t.n0 < pr.N;  // the same for the warp
+            const bool inputs = EPI == DACT || EPI == ADD || (MANY && p.add && p.kind[t.product] == KIND_DX);
+            if constexpr (L::B.in > 0)
+                if (any && inputs) {
+                    if constexpr (EPI == DACT)
+                        w.template ask<true>(&maps.in, &maps.in2, t.n0, row);
+                    else
+                        w.template ask<true>(&maps.in, nullptr, t.n0, row);
+                }
             if (!mbar_wait<true>(&tfull[acc], acc_phase, s_abort, p.status, p.timeout_ns)) break;
             tc_fence_after();
-            if (!w.tile(decode<EPI>(p, tile), tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * TILE_N)) break;
+            const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * TILE_N;
+            bool ok = true;
+            if (any) {
+                if constexpr (EPI == GATED) {
+                    w.gated(maps, pr, t, tbase, row);
+                } else if constexpr (EPI == DACT) {
+                    ok = w.with_inputs(&maps.in, &maps.in2, &maps.more[0], &maps.more[1], &maps.out, pr, t, tbase, row);
+                } else if constexpr (EPI == ADD) {
+                    ok = w.with_inputs(&maps.in, nullptr, &maps.out, nullptr, nullptr, pr, t, tbase, row);
+                } else if constexpr (EPI == PLAIN) {
+                    w.plain(&maps.out, pr, t, tbase, row);
+                } else if (p.kind[t.product] == KIND_WEIGHTS) {
+                    w.plain(&maps.out[t.product], pr, t, tbase, row);
+                } else if (inputs) {
+                    ok = w.with_inputs(&maps.in, nullptr, &maps.out[t.product], nullptr, nullptr, pr, t, tbase, row);
+                } else {
+                    Warp<PLAIN, uint16_t> dx{p, w.bufs, nullptr, s_abort, lane, w.row_of_tile};
+                    if (lane == 0) bulk_wait_read<0>();  // the boxes may still be being stored
+                    __syncwarp();
+                    dx.plain(&maps.out[t.product], pr, t, tbase, row);
+                }
+            }
+            if (!ok) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster_cta(tempty0 + 8u * acc);
@@ -457,6 +585,15 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, 2 * TILE_N);
+    }
+    if (drawn && threadIdx.x == 0) {
+        // the last CTA of the launch leaves the tickets as it found them
+        __threadfence();
+        if (atomicAdd(p.tickets + 1, 1) == static_cast<int>(gridDim.x) - 1) {
+            atomicExch(p.tickets, 0);
+            atomicExch(p.tickets + 1, 0);
+            __threadfence();
+        }
     }
 }
 
@@ -632,41 +769,63 @@ __global__ void __launch_bounds__(FEW_THREADS) ffn_few_kernel(const __grid_const
             for (int i = 0; i < 16; ++i) store(t0 + c + i, __uint_as_float(a[i]), GATE ? __uint_as_float(u[i]) : 0.0f);
         }
     } else {
-        // [source CTA][token of this CTA's share][gate, up][row], over the ring
+        // The partial sums that this CTA gets, over its ring: of each CTA and part (gate,
+        // up) a row of its share of the tokens, in groups of V that the lanes of
+        // a warp write and read side by side.
         constexpr int PARTS = GATE ? 2 : 1;
         const int share = p.tokens / p.split;
-        float *sums = reinterpret_cast<float *>(smem);
-        cluster_sync();  // no CTA's ring is in use any more
-        for (int c = 0; c < p.tokens; c += 16) {
-            if (t0 + c >= p.T) break;
-            uint32_t v[PARTS][16];
-            tmem_ld_32x32b_x16(tbase + c, v[0]);
-            if (GATE) tmem_ld_32x32b_x16(tbase + p.tokens + c, v[PARTS - 1]);
-            tmem_ld_wait();
+        auto exchange = [&](auto vector) {
+            using Vec = decltype(vector);
+            constexpr int V = sizeof(Vec) / 4;
+            const int groups = share / V;
+            Vec *sums = reinterpret_cast<Vec *>(smem);
+            cluster_sync();  // no CTA's ring is in use any more
+            for (int c = 0; c < p.tokens; c += 16) {
+                if (t0 + c >= p.T) break;
+                uint32_t v[PARTS][16];
+                tmem_ld_32x32b_x16(tbase + c, v[0]);
+                if (GATE) tmem_ld_32x32b_x16(tbase + p.tokens + c, v[PARTS - 1]);
+                tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int owner = (c + i) / share, mine = (c + i) % share;
+                for (int i = 0; i < 16; i += V) {
+                    if (t0 + c + i >= p.T) break;
+                    const int owner = (c + i) / share, group = ((c + i) % share) / V;
 #pragma unroll
-                for (int k = 0; k < PARTS; ++k) {
-                    const int at = ((rank * share + mine) * PARTS + k) * FEW_ROWS + static_cast<int>(threadIdx.x);
-                    const uint32_t to = mapa_shared(smem_u32(sums + at), owner);
-                    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(v[k][i]) : "memory");
+                    for (int k = 0; k < PARTS; ++k) {
+                        const uint32_t to =
+                            mapa_shared(smem_u32(sums + ((rank * PARTS + k) * groups + group) * FEW_ROWS + threadIdx.x), owner);
+                        if constexpr (V == 4)
+                            asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v[k][i]),
+                                         "r"(v[k][i + 1]), "r"(v[k][i + 2]), "r"(v[k][i + 3])
+                                         : "memory");
+                        else
+                            asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(v[k][i]), "r"(v[k][i + 1])
+                                         : "memory");
+                    }
                 }
             }
-        }
-        cluster_sync();  // every CTA's sums are there
-        __syncwarp();
-        if (!GATE && p.behind) grid_dependency_wait();
-        for (int mine = 0; mine < share; ++mine) {
-            const int t = t0 + rank * share + mine;
-            if (t >= p.T) break;
-            float v[PARTS] = {};
-            for (int s = 0; s < p.split; ++s)
+            __syncwarp();
+            cluster_sync();  // every CTA's sums are there
+            if (!GATE && p.behind) grid_dependency_wait();
+            for (int g = 0; g < groups; ++g) {
+                const int t = t0 + rank * share + g * V;
+                if (t >= p.T) break;
+                float v[PARTS][V] = {};
+                for (int s = 0; s < p.split; ++s)
 #pragma unroll
-                for (int k = 0; k < PARTS; ++k)
-                    v[k] += sums[((s * share + mine) * PARTS + k) * FEW_ROWS + threadIdx.x];
-            store(t, v[0], v[PARTS - 1]);
-        }
+                    for (int k = 0; k < PARTS; ++k) {
+                        const Vec u = sums[((s * PARTS + k) * groups + g) * FEW_ROWS + threadIdx.x];
+#pragma unroll
+                        for (int i = 0; i < V; ++i) v[k][i] += reinterpret_cast<const float *>(&u)[i];
+                    }
+#pragma unroll
+                for (int i = 0; i < V; ++i) store(t + i, v[0][i], v[PARTS - 1][i]);
+            }
+        };
+        if (share % 4 == 0)
+            exchange(float4{});
+        else
+            exchange(float2{});
     }
     tc_fence_before();
     __syncthreads();
@@ -696,28 +855,35 @@ bool map2d(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t
 bool operand(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, bool mn) {
     return map2d(m, base, rows, cols, cols, mn ? 64 : 128, BK, CU_TENSOR_MAP_SWIZZLE_128B);
 }
+// A K-major B operand of tiles of half the width: 64 rows per CTA.
+bool half_operand(CUtensorMap *m, const void *base, int64_t rows, int64_t cols) {
+    return map2d(m, base, rows, cols, cols, 64, BK, CU_TENSOR_MAP_SWIZZLE_128B);
+}
 // A matrix that the epilogue reads or writes in 32 x 32 boxes.
 bool boxes(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld) {
     return map2d(m, base, rows, cols, ld, CHUNK, CHUNK, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-cudaLaunchConfig_t pair_config(int grid, int smem, cudaStream_t stream, cudaLaunchAttribute *attr) {
+// attr[0]: pairs; attr[1]: may start before the kernel in front of it ends.
+cudaLaunchConfig_t pair_config(int grid, int smem, cudaStream_t stream, cudaLaunchAttribute *attr, bool behind) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid), cfg.blockDim = dim3(THREADS), cfg.dynamicSmemBytes = smem, cfg.stream = stream;
-    attr->id = cudaLaunchAttributeClusterDimension;
-    attr->val.clusterDim.x = 2, attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
-    cfg.attrs = attr, cfg.numAttrs = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr, cfg.numAttrs = behind ? 2 : 1;
     return cfg;
 }
 
-template <Epi EPI, bool A_MN, bool B_MN, typename Out>
+template <Epi EPI, bool A_MN, bool B_MN, typename Out, typename M = Maps>
 cudaError_t set_up(int *pairs) {
-    auto kernel = ffn_gemm_kernel<EPI, A_MN, B_MN, Out>;
+    auto kernel = ffn_gemm_kernel<EPI, A_MN, B_MN, Out, M>;
     constexpr int smem = Layout<EPI, Out>::BYTES;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr;
-    cudaLaunchConfig_t cfg = pair_config(2, smem, nullptr, &attr);
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = pair_config(2, smem, nullptr, attr, false);
     int n = 0;
     const cudaError_t q = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
     if (q != cudaSuccess) return q;
@@ -725,36 +891,75 @@ cudaError_t set_up(int *pairs) {
     return cudaSuccess;
 }
 
-template <Epi EPI, bool A_MN, bool B_MN, typename Out = uint16_t>
-cudaError_t gemm(const Maps &maps, Params p, const GemmLaunch &lc, cudaStream_t stream) {
-    constexpr int n = EPI == GATED ? TILE_N / 2 : TILE_N;
-    p.MT = (p.M + TILE_M - 1) / TILE_M, p.NT = (p.N + n - 1) / n;
-    cudaLaunchAttribute attr;
-    const int64_t tiles = static_cast<int64_t>(p.MT) * p.NT;
-    const int grid = 2 * static_cast<int>(std::min<int64_t>(tiles, lc.ffn_pairs));
-    cudaLaunchConfig_t cfg = pair_config(grid, Layout<EPI, Out>::BYTES, stream, &attr);
-    return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<EPI, A_MN, B_MN, Out>, maps, p);
+// The tiles of a product that the list goes on with; those from the `whole`-th on are cut in two.
+Product product(int M, int N, int K, bool gate, int first) {
+    const int n = gate ? TILE_N / 2 : TILE_N;
+    Product q{M, N, K, (M + TILE_M - 1) / TILE_M, (N + n - 1) / n, 0, first, 0};
+    q.halves = q.tiles = q.MT * q.NT;
+    return q;
+}
+void cut(Product *q, int whole) {
+    q->tiles = 2 * q->tiles - whole;
+    q->halves = whole;
+}
+
+template <Epi EPI, bool A_MN, bool B_MN>
+cudaError_t gemm(const Maps &maps, Params p, int M, int N, int K, const GemmLaunch &lc, cudaStream_t stream) {
+    Product q = product(M, N, K, EPI == GATED, 0);
+    // a last round that leaves half of the pairs without a tile takes tiles of half the width
+    const int rest = q.tiles % lc.ffn_pairs;
+    if (2 * rest <= lc.ffn_pairs) cut(&q, q.tiles - rest);
+    p.product[0] = q, p.products = 1, p.tiles = q.tiles;
+    cudaLaunchAttribute attr[2];
+    const int grid = 2 * std::min(q.tiles, lc.ffn_pairs);
+    cudaLaunchConfig_t cfg = pair_config(grid, Layout<EPI, uint16_t>::BYTES, stream, attr, p.behind);
+    return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<EPI, A_MN, B_MN, uint16_t, Maps>, maps, p);
+}
+
+template <typename Out>
+cudaError_t gradients(const GradMaps &maps, const Params &p, const GemmLaunch &lc, cudaStream_t stream) {
+    cudaLaunchAttribute attr[2];
+    const int grid = 2 * std::min(p.tiles, lc.ffn_pairs);
+    cudaLaunchConfig_t cfg = pair_config(grid, Layout<GRADS, Out>::BYTES, stream, attr, p.behind);
+    return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<GRADS, true, true, Out, GradMaps>, maps, p);
 }
 
 constexpr int FEW_SMEM = 224 * 1024;
 
-// How a product of few tokens is cut.
+// How a product of few tokens is cut: the block of tokens and the split of K of
+// the least time by a model of a CTA's steps, fitted to the times of 12 cuts of 14
+// products (d, f from 512 to 14336) at 9 token counts each (the model's choice is
+// 0.14 us behind the best of them on the mean, 2.6 at most).  In ns: 2700 until
+// the first sums and after the last, the stages' bytes at 109 per SM and ns or
+// 14000 together, 9 per token for the result, 55 where it is exchanged.
 struct FewShape {
     int tokens, blocks, rows, split, stages, smem;
-    FewShape(int T, int N, int K, bool gate, int sms) {
-        blocks = (T + FEW_MAX_TOKENS - 1) / FEW_MAX_TOKENS;
-        tokens = ((T + blocks - 1) / blocks + 15) / 16 * 16;
+    double ns = 1e30;
+    FewShape(int T, int N, int K, bool gate, const GemmLaunch &lc) {
         rows = (N + FEW_ROWS - 1) / FEW_ROWS;
         const int slices = gate ? 1 : 2, KB = (K + slices * BK - 1) / (slices * BK);
-        const int stage = FEW_A + slices * tokens * BK * 2;
-        const int per_sm = tokens <= 16 ? 2 : 1;
-        const int room = (FEW_SMEM / per_sm - 2048) / stage;
-        split = 1;
-        while (split < 8 && 2 * split * rows * blocks <= per_sm * sms && KB >= 4 * split) split *= 2;
-        stages = std::min({room, FEW_MAX_STAGES, (KB + split - 1) / split});
-        // the ring also holds the partial sums
-        const int sums = split > 1 ? tokens * FEW_ROWS * 4 * (gate ? 2 : 1) : 0;
-        smem = std::max(stages * stage, sums) + 1024;
+        for (int most = 16; most <= FEW_MAX_TOKENS; most *= 2) {
+            const int nb = (T + most - 1) / most, nt = ((T + nb - 1) / nb + 15) / 16 * 16;
+            const int stage = FEW_A + slices * nt * BK * 2;
+            for (int i = 0, s = 1; i < 4 && s <= KB; ++i, s *= 2) {
+                if (lc.few_clusters[i] < 1) break;
+                const int per_sm = nt <= 16 ? 2 : 1;
+                const double at_once = static_cast<double>(lc.few_clusters[i]) * per_sm;
+                const double rounds = std::ceil(static_cast<double>(rows) * nb / at_once);
+                const double bytes = static_cast<double>((KB + s - 1) / s) * stage;
+                const double t = rounds * (2700 + bytes * std::max(1 / 109.0, at_once * s / 14000) +
+                                           (s == 1 ? 9.0 : 55.0) * nt);
+                if (t < ns) {
+                    ns = t, tokens = nt, blocks = nb, split = s;
+                    const int room = (FEW_SMEM / per_sm - 2048) / stage;
+                    stages = std::min({room, FEW_MAX_STAGES, (KB + s - 1) / s});
+                    // the ring also holds the partial sums
+                    const int sums = s > 1 ? nt * FEW_ROWS * 4 * (gate ? 2 : 1) : 0;
+                    smem = std::max(stages * stage, sums) + 1024;
+                }
+            }
+            if (most >= T) break;
+        }
     }
 };
 
@@ -762,7 +967,7 @@ struct FewShape {
 template <bool GATE>
 cudaError_t few(const uint16_t *w, const uint16_t *x, int T, int N, int K, FewParams p, bool behind,
                 const GemmLaunch &lc, cudaStream_t stream) {
-    const FewShape s(T, N, K, GATE, lc.num_sms);
+    const FewShape s(T, N, K, GATE, lc);
     FewMaps maps;
     if (!operand(&maps.w, w, GATE ? 2 * static_cast<int64_t>(N) : N, K, false) ||
         !map2d(&maps.x, x, T, K, K, s.tokens, BK, CU_TENSOR_MAP_SWIZZLE_128B))
@@ -800,22 +1005,33 @@ cudaError_t ffn_setup(GemmLaunch *cfg) {
         (e = set_up<PLAIN, false, false, uint16_t>(&pairs)) != cudaSuccess ||
         (e = set_up<ADD, false, false, uint16_t>(&pairs)) != cudaSuccess ||
         (e = set_up<DACT, false, true, uint16_t>(&pairs)) != cudaSuccess ||
-        (e = set_up<PLAIN, false, true, uint16_t>(&pairs)) != cudaSuccess ||
-        (e = set_up<ADD, false, true, uint16_t>(&pairs)) != cudaSuccess ||
-        (e = set_up<PLAIN, true, true, uint16_t>(&pairs)) != cudaSuccess ||
-        (e = set_up<PLAIN, true, true, float>(&pairs)) != cudaSuccess)
+        (e = set_up<GRADS, true, true, uint16_t, GradMaps>(&pairs)) != cudaSuccess ||
+        (e = set_up<GRADS, true, true, float, GradMaps>(&pairs)) != cudaSuccess)
         return e;
-    for (const void *k : {reinterpret_cast<const void *>(ffn_few_kernel<true>),
-                          reinterpret_cast<const void *>(ffn_few_kernel<false>)})
-        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM)) != cudaSuccess) return e;
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     cfg->ffn_pairs = pairs;
-    return cudaSuccess;
+    for (const void *k : {reinterpret_cast<const void *>(ffn_few_kernel<true>),
+                          reinterpret_cast<const void *>(ffn_few_kernel<false>)})
+        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess)
+            return e;
+    // clusters of 1, 2, 4 and 8 CTAs that are resident at once, one CTA per SM
+    for (int i = 0; i < 4; ++i) {
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 1 << i, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t c = {};
+        c.gridDim = dim3(1 << i), c.blockDim = dim3(FEW_THREADS), c.dynamicSmemBytes = FEW_SMEM;
+        c.attrs = &attr, c.numAttrs = 1;
+        if ((e = cudaOccupancyMaxActiveClusters(&cfg->few_clusters[i], ffn_few_kernel<true>, &c)) != cudaSuccess) return e;
+    }
+    return cfg->few_clusters[0] < 1 ? cudaErrorInvalidConfiguration : cudaSuccess;
 }
 
 cudaError_t launch_ffn(const FfnArgs &a, const GemmLaunch &lc, cudaStream_t stream) {
     using namespace ff;
     const bool few_up = use_few(a.T, a.f, true, lc.ffn_pairs), few_down = use_few(a.T, a.d, false, lc.ffn_pairs);
+    const int64_t f = a.f;
     FewParams fp = {};
     fp.act = a.act, fp.status = a.status, fp.timeout_ns = a.timeout_ns;
     Params p = {};
@@ -826,26 +1042,26 @@ cudaError_t launch_ffn(const FfnArgs &a, const GemmLaunch &lc, cudaStream_t stre
         e = few<true>(a.W1, a.x, a.T, a.f, a.d, fp, false, lc, stream);
     } else {
         Maps m = {};
-        p.M = a.T, p.N = a.f, p.K = a.d, p.keep = a.preact != nullptr;
-        if (!operand(&m.a, a.x, a.T, a.d, false) || !operand(&m.b, a.W1, 2 * static_cast<int64_t>(a.f), a.d, false) ||
-            !boxes(&m.out, a.h, a.T, a.f, a.f) ||
-            (a.preact && (!boxes(&m.more[0], a.preact, a.T, a.f, 2 * static_cast<int64_t>(a.f)) ||
-                          !boxes(&m.more[1], a.preact + a.f, a.T, a.f, 2 * static_cast<int64_t>(a.f)))))
+        p.keep = a.preact != nullptr;
+        if (!operand(&m.a, a.x, a.T, a.d, false) || !operand(&m.b, a.W1, 2 * f, a.d, false) ||
+            !half_operand(&m.half_b, a.W1, 2 * f, a.d) || !boxes(&m.out, a.h, a.T, f, f) ||
+            (a.preact && (!boxes(&m.more[0], a.preact, a.T, f, 2 * f) || !boxes(&m.more[1], a.preact + f, a.T, f, 2 * f))))
             return cudaErrorInvalidValue;
-        e = gemm<GATED, false, false>(m, p, lc, stream);
+        e = gemm<GATED, false, false>(m, p, a.T, a.f, a.d, lc, stream);
     }
     if (e != cudaSuccess) return e;
     if (few_down) {
         fp.out = reinterpret_cast<__nv_bfloat16 *>(a.y), fp.preact = nullptr;
         fp.add = reinterpret_cast<const __nv_bfloat16 *>(a.add);
-        return few<false>(a.W2, a.h, a.T, a.d, a.f, fp, few_up, lc, stream);
+        return few<false>(a.W2, a.h, a.T, a.d, a.f, fp, true, lc, stream);
     }
     Maps m = {};
-    p.M = a.T, p.N = a.d, p.K = a.f;
-    if (!operand(&m.a, a.h, a.T, a.f, false) || !operand(&m.b, a.W2, a.d, a.f, false) ||
+    p.behind = true;
+    if (!operand(&m.a, a.h, a.T, f, false) || !operand(&m.b, a.W2, a.d, f, false) || !half_operand(&m.half_b, a.W2, a.d, f) ||
         !boxes(&m.out, a.y, a.T, a.d, a.d) || (a.add && !boxes(&m.in, a.add, a.T, a.d, a.d)))
         return cudaErrorInvalidValue;
-    return a.add ? gemm<ADD, false, false>(m, p, lc, stream) : gemm<PLAIN, false, false>(m, p, lc, stream);
+    return a.add ? gemm<ADD, false, false>(m, p, a.T, a.d, a.f, lc, stream)
+                 : gemm<PLAIN, false, false>(m, p, a.T, a.d, a.f, lc, stream);
 }
 
 cudaError_t launch_ffn_bwd(const FfnGradArgs &a, const GemmLaunch &lc, int *launches, cudaStream_t stream) {
@@ -857,45 +1073,58 @@ cudaError_t launch_ffn_bwd(const FfnGradArgs &a, const GemmLaunch &lc, int *laun
     // da and h, from dh = dy W2 (W2 read as stored)
     {
         Maps m = {};
-        p.M = a.T, p.N = a.f, p.K = a.d;
         if (!operand(&m.a, a.dy, a.T, a.d, false) || !operand(&m.b, a.W2, a.d, f, true) ||
             !boxes(&m.in, a.preact, a.T, f, 2 * f) || !boxes(&m.in2, a.preact + f, a.T, f, 2 * f) ||
             !boxes(&m.more[0], a.da, a.T, f, 2 * f) || !boxes(&m.more[1], a.da + f, a.T, f, 2 * f) ||
             !boxes(&m.out, a.h, a.T, f, f))
             return cudaErrorInvalidValue;
-        const cudaError_t e = gemm<DACT, false, true>(m, p, lc, stream);
+        const cudaError_t e = gemm<DACT, false, true>(m, p, a.T, a.f, a.d, lc, stream);
         if (e != cudaSuccess) return e;
         ++*launches;
     }
-    // dW [rows, cols] = left [T, rows]^T right [T, cols]
-    auto wgrad = [&](const uint16_t *left, int64_t rows, const uint16_t *right, int64_t cols, void *out) {
-        Maps m = {};
-        p.M = static_cast<int>(rows), p.N = static_cast<int>(cols), p.K = a.T;
-        if (!operand(&m.a, left, a.T, rows, true) || !operand(&m.b, right, a.T, cols, true)) return cudaErrorInvalidValue;
-        ++*launches;
-        if (a.weights_f32)
-            return make_tmap_2d(&m.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, out, rows, cols, CHUNK, CHUNK,
-                                CU_TENSOR_MAP_SWIZZLE_128B)
-                       ? gemm<PLAIN, true, true, float>(m, p, lc, stream)
-                       : cudaErrorInvalidValue;
-        return boxes(&m.out, out, rows, cols, cols) ? gemm<PLAIN, true, true>(m, p, lc, stream) : cudaErrorInvalidValue;
+    // The three products of these: one list of tiles, the longest ones first, handed
+    // out as pairs fall free, so that one tail is left instead of three.
+    GradMaps m = {};
+    struct {
+        int kind, M, N, K;
+        const uint16_t *left, *right;
+        void *out;
+    } list[PRODUCTS];
+    int n = 0;
+    auto weights = [&] {
+        if (a.dW1) list[n++] = {KIND_WEIGHTS, 2 * a.f, a.d, a.T, a.da, a.x, a.dW1};
+        if (a.dW2) list[n++] = {KIND_WEIGHTS, a.d, a.f, a.T, a.dy, a.h, a.dW2};
     };
-    if (a.dW2) {
-        const cudaError_t e = wgrad(a.dy, a.d, a.h, f, a.dW2);
-        if (e != cudaSuccess) return e;
+    if (a.T > 2 * a.f) weights();
+    if (a.dx) list[n++] = {KIND_DX, a.T, a.d, 2 * a.f, a.da, a.W1, a.dx};
+    if (a.T <= 2 * a.f) weights();
+    int64_t work = 0;  // slices of all tiles
+    for (int i = 0; i < n; ++i) {
+        const Product q = product(list[i].M, list[i].N, list[i].K, false, 0);
+        work += static_cast<int64_t>(q.tiles) * ((q.K + BK - 1) / BK);
     }
-    if (a.dW1) {
-        const cudaError_t e = wgrad(a.da, 2 * f, a.x, a.d, a.dW1);
-        if (e != cudaSuccess) return e;
+    p.add = a.add != nullptr, p.behind = true, p.products = n;
+    for (int i = 0; i < n; ++i) {
+        const auto &l = list[i];
+        const bool dx = l.kind == KIND_DX;
+        Product q = product(l.M, l.N, l.K, false, p.tiles);
+        // tiles that take longer than a pair's share of all work are halved
+        if (static_cast<int64_t>((q.K + BK - 1) / BK) * lc.ffn_pairs > work) cut(&q, 0);
+        p.product[i] = q, p.kind[i] = l.kind, p.tiles += q.tiles;
+        // the weights' gradients sum over the tokens, the rows of both operands; dx over W1's rows
+        const int64_t K = l.K;
+        if (!(dx ? operand(&m.a[i], l.left, l.M, K, false) : operand(&m.a[i], l.left, K, l.M, true)) ||
+            !operand(&m.b[i], l.right, K, l.N, true))
+            return cudaErrorInvalidValue;
+        if (!dx && a.weights_f32 ? !make_tmap_2d(&m.out[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, l.out, l.M, l.N, CHUNK,
+                                                 CHUNK, CU_TENSOR_MAP_SWIZZLE_128B)
+                                 : !boxes(&m.out[i], l.out, l.M, l.N, l.N))
+            return cudaErrorInvalidValue;
     }
-    if (!a.dx) return cudaSuccess;
-    Maps m = {};
-    p.M = a.T, p.N = a.d, p.K = 2 * a.f;
-    if (!operand(&m.a, a.da, a.T, 2 * f, false) || !operand(&m.b, a.W1, 2 * f, a.d, true) ||
-        !boxes(&m.out, a.dx, a.T, a.d, a.d) || (a.add && !boxes(&m.in, a.add, a.T, a.d, a.d)))
-        return cudaErrorInvalidValue;
+    if (a.add && !boxes(&m.in, a.add, a.T, a.d, a.d)) return cudaErrorInvalidValue;
+    p.tickets = p.tiles > lc.ffn_pairs ? gemm_tickets(lc, stream) : nullptr;
     ++*launches;
-    return a.add ? gemm<ADD, false, true>(m, p, lc, stream) : gemm<PLAIN, false, true>(m, p, lc, stream);
+    return a.weights_f32 ? gradients<float>(m, p, lc, stream) : gradients<uint16_t>(m, p, lc, stream);
 }
 
 }  // namespace moe

@@ -7,7 +7,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
-#include <math_constants.h>
+#include <type_traits>
 
 namespace moe {
 namespace ff {
@@ -15,6 +15,26 @@ namespace ff {
 enum Act { SILU = 0, GELU = 1, GELU_TANH = 2, RELU = 3 };
 
 __device__ __forceinline__ float logistic(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+
+// Phi(g) of the normal distribution, and e = exp(-g^2 / 2).  The smaller tail is
+// e t Q(t) with t = 1 / (1 + 0.3 |g| / sqrt 2): Q, a polynomial of degree 8, was fitted
+// to exp(x^2) erfc(x) / (2 t) at x = |g| / sqrt 2, from 0 to 10, least relative error
+// at most 2e-8 (in fp32 about 5e-7 near 0; the rounding of g^2 / 2 counts beyond).
+__device__ __forceinline__ float normal_cdf(float g, float &e) {
+    const float t = __fdividef(1.0f, __fmaf_rn(0.21213203435596426f, fabsf(g), 1.0f));
+    e = __expf(-0.5f * g * g);
+    float q = -0.06476146727800369f;
+    q = __fmaf_rn(q, t, 0.24278171360492706f);
+    q = __fmaf_rn(q, t, -0.2561393082141876f);
+    q = __fmaf_rn(q, t, 0.2738603949546814f);
+    q = __fmaf_rn(q, t, -0.047325700521469116f);
+    q = __fmaf_rn(q, t, 0.10746320337057114f);
+    q = __fmaf_rn(q, t, 0.07416953146457672f);
+    q = __fmaf_rn(q, t, 0.08535762131214142f);
+    q = __fmaf_rn(q, t, 0.0845940038561821f);
+    const float tail = e * (q * t);
+    return g > 0.0f ? 1.0f - tail : tail;
+}
 
 constexpr float kTanhScale = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kTanhCubic = 0.044715f;
@@ -26,7 +46,8 @@ __device__ __forceinline__ float activate(float g) {
     } else if constexpr (ACT == GELU_TANH) {
         return g * logistic(g * __fmaf_rn(kTanhScale * kTanhCubic, g * g, kTanhScale));
     } else if constexpr (ACT == GELU) {
-        return g * normcdff(g);
+        float e;
+        return g * normal_cdf(g, e);
     } else {
         return g < 0.0f ? 0.0f : g;  // a NaN stays one
     }
@@ -44,7 +65,8 @@ __device__ __forceinline__ float activate(float g, float &slope) {
         slope = v == 0.0f ? s : __fmaf_rn(g * v, dz, s);
         return g * s;
     } else if constexpr (ACT == GELU) {
-        const float cdf = normcdff(g), e = __expf(-0.5f * g * g);
+        float e;
+        const float cdf = normal_cdf(g, e);
         slope = e == 0.0f ? cdf : __fmaf_rn(g * e, 0.3989422804014327f, cdf);  // 1 / sqrt(2 pi)
         return g * cdf;
     } else {

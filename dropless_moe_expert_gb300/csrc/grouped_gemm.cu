@@ -817,6 +817,8 @@ int max_pairs() {
 
 }  // namespace
 
+int *gemm_tickets(const GemmLaunch &cfg, cudaStream_t stream) { return sched_slot(cfg, stream); }
+
 bool grouped_gemm_use_pair(int TK, int E) {
     // a 256-row pair tile pays off once the average group holds a few of them
     return static_cast<int64_t>(TK) >= static_cast<int64_t>(E) * 384;

@@ -193,11 +193,16 @@ struct GemmLaunch {
     int wgrad_pairs = 0;  // resident CTA pairs of the weight-gradient pair kernel
     int mx_pairs = 0;  // ... of the MXFP8 GEMM2 pair kernel
     int ffn_pairs = 0;  // ... of the gated feed-forward's kernel, whatever its form
+    int few_clusters[4] = {};  // resident clusters of 1, 2, 4 and 8 CTAs of its kernel for few tokens
     int device = -1;
     int *sched_base = nullptr;  // device address of the dynamic tile order's counter table
 };
 // Kernel attributes and occupancy queries; once per device, before any capture.
 cudaError_t grouped_gemm_setup(int num_sms, GemmLaunch *cfg);
+// Two ints, zero when a launch on the stream begins and left so by it: the next
+// ticket of an order of tiles that its CTAs draw, and the CTAs that are done (a
+// slot of the table at sched_base).  Null where there is none: a static order.
+int *gemm_tickets(const GemmLaunch &cfg, cudaStream_t stream);
 // True when the CTA-pair kernel is used for this shape (decided on host
 // sizes only, so the choice is the same for every routing).
 bool grouped_gemm_use_pair(int TK, int E);
@@ -241,7 +246,7 @@ struct FfnArgs {
     uint64_t timeout_ns;
 };
 // Its gradients, dx, dW1 and dW2 nullable (not computed); add (which may be
-// dx) is nullable; da [T, 2f] and h [T, f] are scratch.  Launches counted.
+// dx) is nullable; da [T, 2f] and h [T, f] are scratch.  Two launches, counted.
 struct FfnGradArgs {
     const uint16_t *x, *preact, *dy, *W1, *W2, *add;
     int act, T, d, f;

@@ -195,6 +195,10 @@ bool same_or_apart(const void *out, const void *add, size_t bytes) {
     const uintptr_t o = reinterpret_cast<uintptr_t>(out), a = reinterpret_cast<uintptr_t>(add);
     return !add || o == a || o + bytes <= a || a + bytes <= o;
 }
+bool apart(const void *a, size_t an, const void *b, size_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return !a || !b || x + an <= y || y + bn <= x;
+}
 size_t ffn_bytes(int T, int f) { return (static_cast<size_t>(T) * f * 2 + 255) / 256 * 256; }  // of [T, f] bf16
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -603,8 +607,11 @@ moe_status_t moe_gated_ffn_backward(const uint16_t *x, const uint16_t *preact, c
         return MOE_ERR_INVALID_ARG;
     moe_status_t st = check_ffn(act, T, d, f);
     if (st != MOE_OK) return st;
-    if (!same_or_apart(dx, add, static_cast<size_t>(T) * d * 2)) return MOE_ERR_INVALID_ARG;
+    const size_t rows = static_cast<size_t>(T) * d * 2;
+    if (!same_or_apart(dx, add, rows)) return MOE_ERR_INVALID_ARG;
     if (workspace_bytes < 3 * ffn_bytes(T, f)) return MOE_ERR_WORKSPACE;
+    // dx is written beside the weights' gradients, which read these
+    if (!apart(dx, rows, dW1 ? x : nullptr, rows) || !apart(dx, rows, dW2 ? dy : nullptr, rows)) return MOE_ERR_INVALID_ARG;
     DeviceState *ds = nullptr;
     if ((st = device_state(&ds)) != MOE_OK) return st;
     uint16_t *da = static_cast<uint16_t *>(workspace);

@@ -47,6 +47,9 @@ def test_feed_forward_refusals(moe):
     n, m = moe.lib.moe_gated_ffn_workspace_size(4, 64, 72), moe.lib.moe_gated_ffn_backward_workspace_size(4, 64, 72)
     assert n >= 4 * 72 * 2 and m >= 3 * n
     assert _ffn(moe, n=n - 1) == 3 and _bwd(moe, n=m - 1) == 3
+    # dx over what the weights' gradients read beside it
+    far = FAKE + (1 << 16)
+    assert _bwd(moe) == 1 and _bwd(moe, x=far) == 1 and _bwd(moe, dy=far) == 1 and _bwd(moe, x=far, dy=FAKE + 496) == 1
     for size in ((0, 64, 64), (4, 60, 64), (4, 64, 4), (4, 0, 8), (1 << 30, 64, 1 << 20)):
         assert moe.lib.moe_gated_ffn_workspace_size(*size) == 0
         assert moe.lib.moe_gated_ffn_backward_workspace_size(*size) == 0
