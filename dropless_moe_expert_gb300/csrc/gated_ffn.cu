@@ -835,6 +835,149 @@ __global__ void __launch_bounds__(FEW_THREADS) ffn_few_kernel(const __grid_const
     }
 }
 
+// ======================================================================
+// Up to 64 tokens where that is faster: nothing but the weights' bytes counts, so they go straight
+// to registers, each once.  A CTA has 16 weight rows (GATED: 8 gate rows and their 8 up
+// rows), its warps every 8th 64 columns of them.  A quad of lanes reads 64 bytes of
+// a row, 16 per lane, and multiplies them by mma.m16n8k16: which lane's elements stand for
+// which k does not matter as long as the tokens' do for the same, so a lane's
+// 8 consecutive elements of a weight row and of a token are two steps' operands as
+// they are loaded.  A lane ends with the sums of a row (gate and up) for two
+// tokens; the warps' are added in their order.
+// ======================================================================
+constexpr int TINY_WARPS = 8, TINY_SPLIT = 8;
+// 64-column steps whose loads a warp has in flight, of 64 bytes of weights per lane each
+__host__ __device__ constexpr int tiny_deep(int eights) { return eights == 1 ? 4 : eights <= 4 ? 2 : 1; }
+
+struct TinyParams {
+    const uint16_t *w, *x;  // [N or 2N, K], [T, K]
+    int T, N, K;
+    int act;
+    __nv_bfloat16 *out, *preact;
+    const __nv_bfloat16 *add;
+    bool behind;
+    int split;  // CTAs of a cluster that share K
+};
+
+__device__ __forceinline__ uint4 load_once(const uint16_t *at, bool on) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    // volatile: these stay in front of the wait for the kernel before
+    if (on)
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(at));
+    return v;
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// EIGHTS: of tokens.
+template <bool GATE, int EIGHTS>
+__global__ void __launch_bounds__(32 * TINY_WARPS, 2) ffn_tiny_kernel(const TinyParams p) {
+    constexpr int DEEP = tiny_deep(EIGHTS);
+    __shared__ float4 sums[TINY_WARPS][EIGHTS][32], parts[TINY_SPLIT][EIGHTS][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    // the lane's two rows: of the gate and of the up weights, or 8 apart
+    const int rank = static_cast<int>(blockIdx.x) % p.split, unit = static_cast<int>(blockIdx.x) / p.split;
+    const int row = unit * (GATE ? 8 : 16) + g, row2 = GATE ? p.N + row : row + 8;
+    const bool on = row < p.N, on2 = GATE ? on : row2 < p.N;
+    const int64_t K = p.K;
+    const uint16_t *w = p.w + row * K, *w2 = p.w + row2 * K, *x = p.x + g * K;
+    if (GATE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (p.split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA runs
+    float c[EIGHTS][4] = {};
+    const int first_k = 64 * (rank * TINY_WARPS + warp), step = 64 * TINY_WARPS * p.split;
+    for (int k0 = first_k; k0 < p.K; k0 += step * DEEP) {
+        uint4 a[DEEP][2], b[DEEP][2];
+#pragma unroll
+        for (int i = 0; i < DEEP; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = k0 + step * i + 32 * h + 8 * q;
+                a[i][h] = load_once(w + k, on && k < p.K);
+                b[i][h] = load_once(w2 + k, on2 && k < p.K);
+            }
+        if (p.behind && k0 == first_k) grid_dependency_wait();  // the weights' first loads did not wait for it
+        uint4 t[DEEP][2][EIGHTS];
+#pragma unroll
+        for (int i = 0; i < DEEP; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = k0 + step * i + 32 * h + 8 * q;
+#pragma unroll
+                for (int n = 0; n < EIGHTS; ++n) {
+                    t[i][h][n] = make_uint4(0, 0, 0, 0);
+                    if (8 * n + g < p.T && k < p.K) t[i][h][n] = *reinterpret_cast<const uint4 *>(x + 8 * n * K + k);
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < DEEP; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 &u = a[i][h], &v = b[i][h];
+#pragma unroll
+                for (int n = 0; n < EIGHTS; ++n) {
+                    mma_bf16(c[n], u.x, v.x, u.y, v.y, t[i][h][n].x, t[i][h][n].y);
+                    mma_bf16(c[n], u.z, v.z, u.w, v.w, t[i][h][n].z, t[i][h][n].w);
+                }
+            }
+    }
+#pragma unroll
+    for (int n = 0; n < EIGHTS; ++n) sums[warp][n][lane] = make_float4(c[n][0], c[n][1], c[n][2], c[n][3]);
+    __syncthreads();
+    if (p.behind) grid_dependency_wait();  // (a warp without columns has not waited yet)
+    // warp n: the n-th eight tokens
+    auto add = [&](float4 &s, const float4 &v) { s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w; };
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (warp < EIGHTS) {
+        s = sums[0][warp][lane];
+#pragma unroll
+        for (int i = 1; i < TINY_WARPS; ++i) add(s, sums[i][warp][lane]);
+    }
+    if (p.split > 1) {  // the CTAs' sums, by the first one in their order
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        if (warp < EIGHTS) {
+            const uint32_t to = mapa_shared(smem_u32(&parts[rank][warp][lane]), 0);
+            asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(s.x), "f"(s.y), "f"(s.z), "f"(s.w)
+                         : "memory");
+        }
+        __syncwarp();
+        cluster_sync();
+        if (rank != 0) return;
+        if (warp < EIGHTS) {
+            s = parts[0][warp][lane];
+            for (int i = 1; i < p.split; ++i) add(s, parts[i][warp][lane]);
+        }
+    }
+    if (warp >= EIGHTS) return;
+    // s.x, s.y: of the first row for tokens 2q and 2q + 1; s.z, s.w: of the second
+    const float first[2] = {s.x, s.y}, second[2] = {s.z, s.w};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int64_t t = 8 * warp + 2 * q + i;
+        if (t >= p.T) break;
+        if constexpr (GATE) {
+            if (!on) break;
+            float act = 0.0f;
+            with_activation(p.act, [&](auto k) { act = activate<k.value>(first[i]); });
+            p.out[t * p.N + row] = __float2bfloat16_rn(act * second[i]);
+            if (p.preact) {
+                p.preact[2 * t * p.N + row] = __float2bfloat16_rn(first[i]);
+                p.preact[(2 * t + 1) * p.N + row] = __float2bfloat16_rn(second[i]);
+            }
+        } else {
+            const float add1 = p.add && on ? __bfloat162float(p.add[t * p.N + row]) : 0.0f;
+            const float add2 = p.add && on2 ? __bfloat162float(p.add[t * p.N + row2]) : 0.0f;
+            if (on) p.out[t * p.N + row] = __float2bfloat16_rn(first[i] + add1);
+            if (on2) p.out[t * p.N + row2] = __float2bfloat16_rn(second[i] + add2);
+        }
+    }
+}
+
 // ------------------------------------------------------------------ host side
 namespace {
 
@@ -987,12 +1130,81 @@ cudaError_t few(const uint16_t *w, const uint16_t *x, int T, int N, int K, FewPa
     return cudaLaunchKernelEx(&cfg, ffn_few_kernel<GATE>, maps, p);
 }
 
-// Where the tiles of CTA pairs are too few to keep the SMs busy.
-bool use_few(int T, int N, bool gate, int pairs) {
+// How a product of at most 64 tokens is cut without tiles.  K is shared by a cluster
+// of CTAs where a CTA's bytes, at the 53 per ns of half an SM, would take longer than their
+// share and the 1000 ns of adding up (us at one token: 1024 x 4096 11.4 behind by one
+// CTA, 0 by four; 2048 x 768 5.4 by one, 6.4 by two).
+struct TinyShape {
+    int units, split = 1;
+    TinyShape(int T, int N, int K, bool gate, int sms) {
+        units = (N + (gate ? 7 : 15)) / (gate ? 8 : 16);
+        const double ns = (32.0 + 2 * T) * K / 53;
+        double best = ns;
+        for (int s = 2; s <= TINY_SPLIT && units * s <= 2 * sms; s *= 2)
+            if (ns / s + 1000 < best) best = ns / s + 1000, split = s;
+    }
+};
+template <bool GATE>
+cudaError_t tiny(TinyParams p, bool behind, const GemmLaunch &lc, cudaStream_t stream) {
+    const TinyShape s(p.T, p.N, p.K, GATE, lc.num_sms);
+    cudaLaunchAttribute attr[2];
+    int attrs = 0;
+    if (s.split > 1) {
+        attr[attrs].id = cudaLaunchAttributeClusterDimension;
+        attr[attrs].val.clusterDim.x = s.split, attr[attrs].val.clusterDim.y = attr[attrs].val.clusterDim.z = 1;
+        ++attrs;
+    }
+    if (behind) {
+        attr[attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[attrs].val.programmaticStreamSerializationAllowed = 1;
+        ++attrs;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(s.units * s.split), cfg.blockDim = dim3(32 * TINY_WARPS), cfg.stream = stream;
+    cfg.attrs = attr, cfg.numAttrs = attrs;
+    p.behind = behind, p.split = s.split;
+    return p.T <= 8    ? cudaLaunchKernelEx(&cfg, ffn_tiny_kernel<GATE, 1>, p)
+           : p.T <= 16 ? cudaLaunchKernelEx(&cfg, ffn_tiny_kernel<GATE, 2>, p)
+           : p.T <= 32 ? cudaLaunchKernelEx(&cfg, ffn_tiny_kernel<GATE, 4>, p)
+                       : cudaLaunchKernelEx(&cfg, ffn_tiny_kernel<GATE, 8>, p);
+}
+
+// Whether CTA pairs take longer than the kernel for few tokens, by their model beside
+// FewShape's, in ns: 3200, and of each round 370 and 346 per slice of K (274 where
+// the tiles are halved).  Fitted to 8 sizes at 37 to 1003 tokens, where it is 0.1 us
+// behind the better choice on the mean (8 at most: 384 tokens, d = 4096, f = 14336).
+bool prefer_few(int T, int N, int K, bool gate, double few_ns, int pairs) {
     const int n = gate ? TILE_N / 2 : TILE_N;
     const int64_t tiles = static_cast<int64_t>((T + TILE_M - 1) / TILE_M) * ((N + n - 1) / n);
-    return T <= FEW_MAX_TOKENS || 2 * tiles <= pairs;
+    const int64_t rest = tiles % pairs;
+    const double KB = (K + BK - 1) / BK, rounds = static_cast<double>(tiles / pairs);
+    const double last = rest == 0 ? 0 : 2 * rest <= pairs ? 185 + 274 * KB : 370 + 346 * KB;
+    return few_ns + 600 < 3200 + rounds * (370 + 346 * KB) + last;
 }
+struct Ways {
+    bool tiny = false, few_up = false, few_down = false;
+    Ways(int T, int d, int f, const GemmLaunch &lc) {
+        if (T <= 16) {
+            tiny = true;
+            return;
+        }
+        // a product of so many tokens keeps the pairs busy whatever its other sizes
+        if (T > 4096) return;
+        const FewShape up(T, f, d, true, lc), down(T, d, f, false, lc);
+        // Without tiles every row block reads all tokens again: the bytes of both products from L2
+        // (6 df of weights, 3/8 df per token) at 12900 per ns, 11400 with over 32 tokens, and
+        // 7900 ns, against the other's.  us with and without tiles: 2048 x 768, 37 tokens 13.7 and 9.7;
+        // 7168 x 2048, 24 tokens 30.6 and 27.6, 48 tokens 30.6 and 38.9; 4096 x 14336, 17 tokens 65 and 86.
+        // (One way for both products: behind one with tiles, one without took up to 50 us longer.)
+        const double bytes = static_cast<double>(d) * f * (6 + 0.375 * T);
+        if (T <= 64 && 7900 + bytes / (T <= 32 ? 12900 : 11400) < up.ns + down.ns + 1950) {
+            tiny = true;
+            return;
+        }
+        few_up = prefer_few(T, f, d, true, up.ns, lc.ffn_pairs);
+        few_down = prefer_few(T, d, f, false, down.ns, lc.ffn_pairs);
+    }
+};
 
 }  // namespace
 }  // namespace ff
@@ -1030,15 +1242,18 @@ cudaError_t ffn_setup(GemmLaunch *cfg) {
 
 cudaError_t launch_ffn(const FfnArgs &a, const GemmLaunch &lc, cudaStream_t stream) {
     using namespace ff;
-    const bool few_up = use_few(a.T, a.f, true, lc.ffn_pairs), few_down = use_few(a.T, a.d, false, lc.ffn_pairs);
+    const Ways way(a.T, a.d, a.f, lc);
     const int64_t f = a.f;
+    const auto bf16 = [](auto *t) { return reinterpret_cast<__nv_bfloat16 *>(const_cast<uint16_t *>(t)); };
     FewParams fp = {};
     fp.act = a.act, fp.status = a.status, fp.timeout_ns = a.timeout_ns;
     Params p = {};
     p.act = a.act, p.status = a.status, p.timeout_ns = a.timeout_ns;
     cudaError_t e;
-    if (few_up) {
-        fp.out = reinterpret_cast<__nv_bfloat16 *>(a.h), fp.preact = reinterpret_cast<__nv_bfloat16 *>(a.preact);
+    if (way.tiny) {
+        e = tiny<true>({a.W1, a.x, a.T, a.f, a.d, a.act, bf16(a.h), bf16(a.preact), nullptr}, false, lc, stream);
+    } else if (way.few_up) {
+        fp.out = bf16(a.h), fp.preact = bf16(a.preact);
         e = few<true>(a.W1, a.x, a.T, a.f, a.d, fp, false, lc, stream);
     } else {
         Maps m = {};
@@ -1050,9 +1265,10 @@ cudaError_t launch_ffn(const FfnArgs &a, const GemmLaunch &lc, cudaStream_t stre
         e = gemm<GATED, false, false>(m, p, a.T, a.f, a.d, lc, stream);
     }
     if (e != cudaSuccess) return e;
-    if (few_down) {
-        fp.out = reinterpret_cast<__nv_bfloat16 *>(a.y), fp.preact = nullptr;
-        fp.add = reinterpret_cast<const __nv_bfloat16 *>(a.add);
+    if (way.tiny)
+        return tiny<false>({a.W2, a.h, a.T, a.d, a.f, a.act, bf16(a.y), nullptr, bf16(a.add)}, true, lc, stream);
+    if (way.few_down) {
+        fp.out = bf16(a.y), fp.preact = nullptr, fp.add = bf16(a.add);
         return few<false>(a.W2, a.h, a.T, a.d, a.f, fp, true, lc, stream);
     }
     Maps m = {};
