@@ -16,7 +16,7 @@
 //   epilogue GATED   h (and a) from a tile whose B rows are 128 gate and 128 up rows
 //            PLAIN   the product, plus a matrix (ADD); fp32 for weight gradients on request
 //            DACT    da and h from the tile of dh and the tiles of g and u
-// Warps: 0 TMA loads, 1 MMAs and TMEM, 2 to 5 epilogue.  Every wait is bounded.
+// Warps: 0 TMA loads, 1 MMAs and TMEM, the others epilogue.  Every wait is bounded.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -38,7 +38,12 @@ constexpr int BK = 64;          // a slice of K: 128 bytes, one swizzle line
 constexpr int UMMA_K = 16;
 constexpr int TILE_M = 256, TILE_N = 256;
 constexpr int BAND = 8;         // row blocks that sweep the column blocks together
-constexpr int THREADS = 192;
+// Epilogue warps: of GATED eight, two per lane quarter with half of a tile's columns
+// each, as the last tile's epilogue is waited for (1003 x 2056 x 1368: 30.9 us with
+// four, 30.0); DACT's buffers would leave eight a shorter ring (its backward 64
+// and 66.5 us, 4096 x 7168 x 2048 400 and 411).
+__host__ __device__ constexpr int epi_warps(Epi epi) { return epi == GATED ? 8 : 4; }
+__host__ __device__ constexpr int threads_of(Epi epi) { return 64 + 32 * epi_warps(epi); }
 constexpr int BOX = 64 * 64 * 2;  // an MN-major box: 64 rows of K x 64 columns
 constexpr int STAGE = 4 * BOX;    // of a CTA: 128 rows of A, 128 columns of B
 constexpr int CHUNK = 32;         // the epilogue takes 32 rows x 32 columns per warp at a time
@@ -61,12 +66,13 @@ __host__ __device__ constexpr Buffers buffers() {
 template <Epi EPI, typename Out>
 struct Layout {
     static constexpr Buffers B = buffers<EPI, Out>();
+    static constexpr int WARPS = epi_warps(EPI);
     static constexpr int STAGES = EPI == DACT ? 5 : 6;
     static constexpr int QUEUE = EPI == GRADS ? gg::queue_slots(STAGES) : 0;
     static constexpr int OFF_EPI = STAGES * STAGE;
-    static constexpr int OFF_BARS = OFF_EPI + 4 * B.bytes;
-    // full, empty, tfull[2], tempty[2], drain, landed[4][sets], queued[QUEUE]
-    static constexpr int NUM_BARS = 2 * STAGES + 5 + 4 * B.sets + QUEUE;
+    static constexpr int OFF_BARS = OFF_EPI + WARPS * B.bytes;
+    // full, empty, tfull[2], tempty[2], drain, landed[WARPS][sets], queued[QUEUE]
+    static constexpr int NUM_BARS = 2 * STAGES + 5 + WARPS * B.sets + QUEUE;
     static constexpr int OFF_QUEUE = OFF_BARS + NUM_BARS * 8;
     static constexpr int OFF_TMEM = OFF_QUEUE + QUEUE * 4;
     static constexpr int OFF_ABORT = OFF_TMEM + 4;
@@ -149,8 +155,14 @@ __device__ __forceinline__ void write_row(uint8_t *box, int lane, const uint32_t
         *reinterpret_cast<uint4 *>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) =
             make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
 }
-__device__ __forceinline__ float low(uint32_t p) { return __uint_as_float(p << 16); }
-__device__ __forceinline__ float high(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+// The i-th pair of a row's fp32 values; a pair of bf16, and back.
+__device__ __forceinline__ float2 pair_of(const uint32_t (&v)[32], int i) {
+    return make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+}
+__device__ __forceinline__ float2 unpack(uint32_t p) {
+    return make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack(float2 v) { return pack_bf16x2(v.x, v.y); }
 __device__ __forceinline__ void pack(const uint32_t (&v)[32], uint32_t (&packed)[16]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) packed[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
@@ -165,6 +177,7 @@ struct Warp {
     uint64_t *landed;
     volatile int *abort;
     int lane, row_of_tile;   // the first of its rows within a tile
+    int part;                // of the columns: the first or the second half, where two warps share a lane quarter
     uint32_t boxes = 0;      // stored by put()
     uint32_t asked = 0, taken = 0;  // chunks whose inputs were asked for, and used
 
@@ -231,20 +244,21 @@ struct Warp {
         }
     }
 
+    // The first of the warp's columns of a tile that has `columns`, and the end of them.
+    __device__ __forceinline__ int begin(int columns) const { return L::WARPS == 8 ? part * columns / 2 : 0; }
+    __device__ __forceinline__ int end(int columns) const { return L::WARPS == 8 ? (part + 1) * columns / 2 : columns; }
+
     // h of a tile whose accumulator holds gate columns and then as many up columns
     __device__ __forceinline__ void gated(const Maps &maps, const Product &q, const Tile &t, uint32_t tbase, int row) {
 #pragma unroll 1
-        for (int c = 0; c < t.width / 2 && t.n0 + c < q.N; c += CHUNK) {
+        for (int c = begin(t.width / 2); c < end(t.width / 2) && t.n0 + c < q.N; c += CHUNK) {
             uint32_t g[32], u[32], packed[16];
             tmem_ld_32x32b_x32(tbase + c, g);
             tmem_ld_32x32b_x32(tbase + t.width / 2 + c, u);
             tmem_ld_wait();
             with_activation(p.act, [&](auto act) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    packed[i] =
-                        pack_bf16x2(activate<act.value>(__uint_as_float(g[2 * i])) * __uint_as_float(u[2 * i]),
-                                    activate<act.value>(__uint_as_float(g[2 * i + 1])) * __uint_as_float(u[2 * i + 1]));
+                for (int i = 0; i < 16; ++i) packed[i] = pack(mul2(activate<act.value>(pair_of(g, i)), pair_of(u, i)));
             });
             put(&maps.out, packed, t.n0 + c, row);
             if (p.keep) {
@@ -261,9 +275,9 @@ struct Warp {
                                                 const CUtensorMap *out2, const CUtensorMap *out3, const Product &q,
                                                 const Tile &t, uint32_t tbase, int row) {
 #pragma unroll 1
-        for (int c = 0; c < t.width && t.n0 + c < q.N; c += CHUNK) {
+        for (int c = begin(t.width); c < end(t.width) && t.n0 + c < q.N; c += CHUNK) {
             const int col = t.n0 + c;
-            if (c + CHUNK < t.width && col + CHUNK < q.N) ask<false>(in, in2, col + CHUNK, row);
+            if (c + CHUNK < end(t.width) && col + CHUNK < q.N) ask<false>(in, in2, col + CHUNK, row);
             uint32_t v[32], e[16];
             tmem_ld_32x32b_x32(tbase + c, v);
             tmem_ld_wait();
@@ -274,8 +288,7 @@ struct Warp {
             read_row(box, lane, e);
             if constexpr (EPI != DACT) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    e[i] = pack_bf16x2(__uint_as_float(v[2 * i]) + low(e[i]), __uint_as_float(v[2 * i + 1]) + high(e[i]));
+                for (int i = 0; i < 16; ++i) e[i] = pack(add2(pair_of(v, i), unpack(e[i])));
                 write_row(box, lane, e);
             } else {
                 uint32_t u[16], h[16];
@@ -283,14 +296,11 @@ struct Warp {
                 with_activation(p.act, [&](auto act) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float slope[2];
-                        const float a0 = activate<act.value>(low(e[i]), slope[0]);
-                        const float a1 = activate<act.value>(high(e[i]), slope[1]);
-                        const float d0 = __uint_as_float(v[2 * i]), d1 = __uint_as_float(v[2 * i + 1]);
-                        const float u0 = low(u[i]), u1 = high(u[i]);
-                        h[i] = pack_bf16x2(a0 * u0, a1 * u1);
-                        e[i] = pack_bf16x2(d0 * u0 * slope[0], d1 * u1 * slope[1]);
-                        u[i] = pack_bf16x2(d0 * a0, d1 * a1);
+                        float2 slope;
+                        const float2 a = activate<act.value>(unpack(e[i]), slope), up = unpack(u[i]), d = pair_of(v, i);
+                        h[i] = pack(mul2(a, up));
+                        e[i] = pack(mul2(mul2(d, up), slope));
+                        u[i] = pack(mul2(d, a));
                     }
                 });
                 write_row(box, lane, e);
@@ -315,7 +325,7 @@ struct Warp {
 // M: Maps, or GradMaps for GRADS, whose products have operands of their own:
 // dx an A that is K-major, the weights' gradients one that is MN-major; B is MN-major in all.
 template <Epi EPI, bool A_MN, bool B_MN, typename Out, typename M>
-__global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_constant__ M maps, const Params p) {
+__global__ void __launch_bounds__(threads_of(EPI), 1) ffn_gemm_kernel(const __grid_constant__ M maps, const Params p) {
     using L = Layout<EPI, Out>;
     constexpr int STAGES = L::STAGES, QUEUE = L::QUEUE;
     constexpr bool MANY = EPI == GRADS;
@@ -324,10 +334,10 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::OFF_BARS);  // used in CTA 0 only
     uint64_t *empty = full + STAGES;                                    // both CTAs
     uint64_t *tfull = empty + STAGES;                                   // both CTAs
-    uint64_t *tempty = tfull + 2;                                       // CTA 0: 4 warps x 2 CTAs arrive
+    uint64_t *tempty = tfull + 2;                                       // CTA 0: the warps of both CTAs arrive
     uint64_t *drain = tempty + 2;
     uint64_t *landed = drain + 1;
-    uint64_t *queued = landed + 4 * L::B.sets;                          // both CTAs
+    uint64_t *queued = landed + L::WARPS * L::B.sets;                          // both CTAs
     volatile int *queue = reinterpret_cast<volatile int *>(smem + L::OFF_QUEUE);
     uint32_t *s_tmem = reinterpret_cast<uint32_t *>(smem + L::OFF_TMEM);
     volatile int *s_abort = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
@@ -344,10 +354,10 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], 8);
+            mbar_init(&tempty[i], 2 * L::WARPS);
         }
         mbar_init(drain, 1);
-        for (int i = 0; i < 4 * L::B.sets; ++i) mbar_init(&landed[i], 1);
+        for (int i = 0; i < L::WARPS * L::B.sets; ++i) mbar_init(&landed[i], 1);
         for (int i = 0; i < QUEUE; ++i) mbar_init(&queued[i], 1);
         *s_abort = 0;
         fence_mbar_init();
@@ -525,7 +535,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
     } else {
         const int q = warp & 3;  // the lane quarter that a warp may read
         Warp<EPI, Out> w{p, smem + L::OFF_EPI + (warp - 2) * L::B.bytes, landed + (warp - 2) * L::B.sets, s_abort, lane,
-                         half + 32 * q};
+                         half + 32 * q, (warp - 2) >> 2};
         const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
         uint32_t acc = 0, acc_phase = 0;
         for (int k = 0;; ++k) {
@@ -534,14 +544,15 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
             const Tile t = decode<EPI>(p, tile);
             const Product &pr = p.product[t.product];
             const int row = t.m0 + w.row_of_tile;
-            const bool any = row < pr.M && t.n0 < pr.N;  // the same for the warp
+            const int columns = EPI == GATED ? t.width / 2 : t.width, col = t.n0 + w.begin(columns);
+            const bool any = row < pr.M && col < pr.N;  // the same for the warp
             const bool inputs = EPI == DACT || EPI == ADD || (MANY && p.add && p.kind[t.product] == KIND_DX);
             if constexpr (L::B.in > 0)
                 if (any && inputs) {
                     if constexpr (EPI == DACT)
-                        w.template ask<true>(&maps.in, &maps.in2, t.n0, row);
+                        w.template ask<true>(&maps.in, &maps.in2, col, row);
                     else
-                        w.template ask<true>(&maps.in, nullptr, t.n0, row);
+                        w.template ask<true>(&maps.in, nullptr, col, row);
                 }
             if (!mbar_wait<true>(&tfull[acc], acc_phase, s_abort, p.status, p.timeout_ns)) break;
             tc_fence_after();
@@ -561,7 +572,7 @@ __global__ void __launch_bounds__(THREADS, 1) ffn_gemm_kernel(const __grid_const
                 } else if (inputs) {
                     ok = w.with_inputs(&maps.in, nullptr, &maps.out[t.product], nullptr, nullptr, pr, t, tbase, row);
                 } else {
-                    Warp<PLAIN, uint16_t> dx{p, w.bufs, nullptr, s_abort, lane, w.row_of_tile};
+                    Warp<PLAIN, uint16_t> dx{p, w.bufs, nullptr, s_abort, lane, w.row_of_tile, 0};
                     if (lane == 0) bulk_wait_read<0>();  // the boxes may still be being stored
                     __syncwarp();
                     dx.plain(&maps.out[t.product], pr, t, tbase, row);
@@ -1008,9 +1019,9 @@ bool boxes(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t
 }
 
 // attr[0]: pairs; attr[1]: may start before the kernel in front of it ends.
-cudaLaunchConfig_t pair_config(int grid, int smem, cudaStream_t stream, cudaLaunchAttribute *attr, bool behind) {
+cudaLaunchConfig_t pair_config(int grid, int threads, int smem, cudaStream_t stream, cudaLaunchAttribute *attr, bool behind) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid), cfg.blockDim = dim3(THREADS), cfg.dynamicSmemBytes = smem, cfg.stream = stream;
+    cfg.gridDim = dim3(grid), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1026,7 +1037,7 @@ cudaError_t set_up(int *pairs) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = pair_config(2, smem, nullptr, attr, false);
+    cudaLaunchConfig_t cfg = pair_config(2, threads_of(EPI), smem, nullptr, attr, false);
     int n = 0;
     const cudaError_t q = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
     if (q != cudaSuccess) return q;
@@ -1055,7 +1066,7 @@ cudaError_t gemm(const Maps &maps, Params p, int M, int N, int K, const GemmLaun
     p.product[0] = q, p.products = 1, p.tiles = q.tiles;
     cudaLaunchAttribute attr[2];
     const int grid = 2 * std::min(q.tiles, lc.ffn_pairs);
-    cudaLaunchConfig_t cfg = pair_config(grid, Layout<EPI, uint16_t>::BYTES, stream, attr, p.behind);
+    cudaLaunchConfig_t cfg = pair_config(grid, threads_of(EPI), Layout<EPI, uint16_t>::BYTES, stream, attr, p.behind);
     return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<EPI, A_MN, B_MN, uint16_t, Maps>, maps, p);
 }
 
@@ -1063,7 +1074,7 @@ template <typename Out>
 cudaError_t gradients(const GradMaps &maps, const Params &p, const GemmLaunch &lc, cudaStream_t stream) {
     cudaLaunchAttribute attr[2];
     const int grid = 2 * std::min(p.tiles, lc.ffn_pairs);
-    cudaLaunchConfig_t cfg = pair_config(grid, Layout<GRADS, Out>::BYTES, stream, attr, p.behind);
+    cudaLaunchConfig_t cfg = pair_config(grid, threads_of(GRADS), Layout<GRADS, Out>::BYTES, stream, attr, p.behind);
     return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<GRADS, true, true, Out, GradMaps>, maps, p);
 }
 
