@@ -396,7 +396,11 @@ __global__ void __launch_bounds__(threads_of(EPI), 1) ffn_gemm_kernel(const __gr
             const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);  // both CTAs' copies signal CTA 0's barriers
             const uint32_t queue1 = mapa_shared(smem_u32(const_cast<int *>(queue)), 1);
             const uint32_t queued1 = mapa_shared(smem_u32(queued), 1);
-            // CTA 0 draws the pair's tiles and tells both CTAs: tile k + 1 when the loads of tile k begin
+            // CTA 0 draws the pair's tiles and tells both CTAs: the ticket of tile k + 1 at most
+            // 24 slices before the loads of tile k end, so that a pair with a long tile keeps no
+            // others from those that are free (777 x 1032 x 2056: 64 us with two tiles drawn
+            // ahead, 48).  Not by a test in the loop over the slices: this thread's latency per
+            // slice counts (4096 x 7168 x 2048: 428 us with it, 394).
             auto publish = [&](int k, int tile) {
                 queue[k % max(QUEUE, 1)] = tile;
                 mbar_arrive(&queued[k % max(QUEUE, 1)]);
@@ -406,7 +410,6 @@ __global__ void __launch_bounds__(threads_of(EPI), 1) ffn_gemm_kernel(const __gr
             if (drawn && rank == 0) {
                 current = atomicAdd(p.tickets, 1);
                 if (current >= p.tiles) current = -1;
-                next = current >= 0 ? atomicAdd(p.tickets, 1) : p.tiles;
                 publish(0, current);
             }
             int armed[STAGES];
@@ -418,11 +421,6 @@ __global__ void __launch_bounds__(threads_of(EPI), 1) ffn_gemm_kernel(const __gr
                 int tile;
                 if (drawn && rank == 0) {
                     tile = current;
-                    if (tile >= 0) {
-                        current = next < p.tiles ? next : -1;
-                        publish(k + 1, current);
-                        if (current >= 0) next = atomicAdd(p.tickets, 1);
-                    }
                 } else if (!tile_of(k, &tile)) {
                     ok = false;
                     break;
@@ -443,29 +441,44 @@ __global__ void __launch_bounds__(threads_of(EPI), 1) ffn_gemm_kernel(const __gr
                 // block past their half of W1 give columns that are not stored)
                 const int b0 = EPI == GATED ? t.n0 + static_cast<int>(rank) * p.product[0].N
                                             : t.n0 + static_cast<int>(rank) * (t.width / 2);
-                for (int kb = 0; kb < KB; ++kb) {
-                    if (!mbar_wait<true>(&empty[stage], phase ^ 1u, s_abort, p.status, p.timeout_ns)) {
-                        ok = false;
-                        break;
+                auto load = [&](int from, int to) {
+                    for (int kb = from; kb < to; ++kb) {
+                        if (!mbar_wait<true>(&empty[stage], phase ^ 1u, s_abort, p.status, p.timeout_ns)) {
+                            ok = false;
+                            return;
+                        }
+                        uint8_t *sa = smem + stage * STAGE, *sb = sa + 2 * BOX;
+                        const uint32_t bar = full0 + 8u * stage;
+                        if (rank == 0) mbar_arrive_expect_tx(&full[stage], whole ? 2 * STAGE : 2 * (STAGE - BOX));
+                        if (a_mn) {
+                            tma_load_2d_pair(sa, ma, bar, a0, kb * BK);
+                            tma_load_2d_pair(sa + BOX, ma, bar, a0 + 64, kb * BK);
+                        } else {
+                            tma_load_2d_pair(sa, ma, bar, kb * BK, a0);
+                        }
+                        if (B_MN) {
+                            tma_load_2d_pair(sb, mb, bar, b0, kb * BK);
+                            if (whole) tma_load_2d_pair(sb + BOX, mb, bar, b0 + 64, kb * BK);
+                        } else {
+                            tma_load_2d_pair(sb, mb, bar, kb * BK, b0);
+                        }
+                        armed[stage] = static_cast<int>(phase);
+                        if (++stage == STAGES) stage = 0, phase ^= 1u;
                     }
-                    uint8_t *sa = smem + stage * STAGE, *sb = sa + 2 * BOX;
-                    const uint32_t bar = full0 + 8u * stage;
-                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], whole ? 2 * STAGE : 2 * (STAGE - BOX));
-                    if (a_mn) {
-                        tma_load_2d_pair(sa, ma, bar, a0, kb * BK);
-                        tma_load_2d_pair(sa + BOX, ma, bar, a0 + 64, kb * BK);
-                    } else {
-                        tma_load_2d_pair(sa, ma, bar, kb * BK, a0);
-                    }
-                    if (B_MN) {
-                        tma_load_2d_pair(sb, mb, bar, b0, kb * BK);
-                        if (whole) tma_load_2d_pair(sb + BOX, mb, bar, b0 + 64, kb * BK);
-                    } else {
-                        tma_load_2d_pair(sb, mb, bar, kb * BK, b0);
-                    }
-                    armed[stage] = static_cast<int>(phase);
-                    if (++stage == STAGES) stage = 0, phase ^= 1u;
+                };
+                int at = 0;
+                if (drawn && rank == 0) {
+                    load(0, at = max(KB - 24, 0));
+                    if (!ok) break;
+                    next = atomicAdd(p.tickets, 1);
+                    const int then = max(KB - 16, min(KB, 1));
+                    load(at, then);
+                    at = then;
+                    if (!ok) break;
+                    current = next < p.tiles ? next : -1;
+                    publish(k + 1, current);
                 }
+                load(at, KB);
             }
             if (!ok) {
                 volatile int no_abort = 0;
