@@ -412,16 +412,17 @@ class NormResidual(_Buffers):
         return (_ptr(self.r) if y else None, _ptr(self.n) if pre else None, _ptr(self.rstd_post) if post else None,
                 _ptr(self.rstd_pre) if pre else None)
 
-    def _rng_pointer(self, like, stream):
-        """Where a call with dropout leaves its state."""
-        if self.rng is None:
-            self.rng = _empty((2,), torch.int64, like, stream)
-        return _in(self.rng, torch.int64, (2,), "out.rng")
-
-    def _pointers(self, key):
-        """The addresses, checked."""
+    def _pointers(self, key, rng=None, stream=None):
+        """The addresses, checked; with dropout also of its state and of where a call leaves it."""
         at = self._addresses(key)
+        if rng is not None:
+            if self.rng is None:
+                self.rng = _empty((2,), torch.int64, rng, stream)
+            at = (*at, rng.data_ptr(), self.rng.data_ptr())
         if (key, at) != self._checked:
+            if rng is not None:
+                _rng_in(rng)
+                _need(self.rng, torch.int64, (2,), "out.rng")
             T, d, dtype, y, post, pre = key
             if y:
                 _need(self.r, dtype, (T, d), "out.r")
@@ -430,7 +431,7 @@ class NormResidual(_Buffers):
                 _need(self.rstd_pre, torch.float32, (T,), "out.rstd_pre")
             if post:
                 _need(self.rstd_post, torch.float32, (T,), "out.rstd_post")
-            self._hold((key, at), self.r, self.n, self.rstd_post, self.rstd_pre)
+            self._hold((key, at), self.r, self.n, self.rstd_post, self.rstd_pre, rng, self.rng)
         return at
 
 
@@ -463,13 +464,17 @@ class NormResidualGrads(_Buffers):
                 _ptr(self.dgamma_post) if post else None, _ptr(self.dgate) if gate != "none" else None, ws.data_ptr(),
                 ws.numel())
 
-    def _pointers(self, key, stream=None):
-        """The addresses, checked."""
+    def _pointers(self, key, stream=None, rng=None):
+        """The addresses, checked; with dropout also of its state."""
         if self.workspace is None:
             n = int(lib.moe_norm_residual_backward_workspace_size(*key[:2]))
             self.workspace = _empty((n,), torch.uint8, _need(self.dr, key[2], key[:2], "out.dr"), stream)
         at = self._addresses(key)
+        if rng is not None:
+            at = (*at, rng.data_ptr())
         if (key, at) != self._checked:
+            if rng is not None:
+                _rng_in(rng)
             T, d, dtype, y, post, pre, gate = key
             ws = self.workspace
             _need(self.dr, dtype, (T, d), "out.dr")
@@ -482,7 +487,7 @@ class NormResidualGrads(_Buffers):
             if gate != "none":
                 _need(self.dgate, torch.float32, (d,) if gate == "channel" else (T, 1), "out.dgate")
             _need(ws, torch.uint8, (ws.numel(),), "out.workspace")
-            self._hold((key, at), self.dr, self.dy, self.dgamma_pre, self.dgamma_post, self.dgate, ws)
+            self._hold((key, at), self.dr, self.dy, self.dgamma_pre, self.dgamma_post, self.dgate, ws, rng)
         return at
 
 
@@ -506,7 +511,7 @@ def _norm_args(r, y, gamma_post, gate, gamma_pre):
 
 
 def _rng_in(rng) -> int:
-    """The address of a dropout's state."""
+    """The address of a dropout's state, checked."""
     if rng is None:
         raise ValueError("dropout needs rng, its seed and call number: an int64 CUDA tensor [2]")
     return _in(rng, torch.int64, (2,), "rng")
@@ -529,14 +534,21 @@ def norm_residual(r, y=None, *, gamma_post=None, gate=None, gamma_pre=None, res_
     0 drops nothing, and rng is not read."""
     T, d, kind, rp, yp, postp, gatep, prep = _norm_args(r, y, gamma_post, gate, gamma_pre)
     key = (T, d, r.dtype, yp is not None, postp is not None, prep is not None)
-    if out is None:
-        out = _on(stream, lambda: NormResidual.empty(*key, r.device))
-        at = out._addresses(key)
+    if dropout:
+        if rng is None or out is None:
+            _rng_in(rng)
     else:
-        at = out._pointers(key)
+        rng = None
+    if out is None:
+        out = _on(stream, lambda: NormResidual.empty(*key, r.device, rng is not None))
+        at = out._addresses(key)
+        if dropout:
+            at = (*at, rng.data_ptr(), out.rng.data_ptr())
+    else:
+        at = out._pointers(key, rng, stream)
     if dropout:
         _check(lib.moe_norm_residual_dropout(rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep,
-                                             eps, dropout, _rng_in(rng), T, d, *at, out._rng_pointer(r, stream),
+                                             eps, dropout, at[4], T, d, at[0], at[1], at[2], at[3], at[5],
                                              _stream_of(r, stream)), "moe_norm_residual_dropout")
     else:
         _check(lib.moe_norm_residual(rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep, eps,
@@ -560,14 +572,19 @@ def norm_residual_backward(r, dr, dn=None, y=None, *, gamma_post=None, gate=None
     rqp = _in(rstd_pre, torch.float32, (T,), "rstd_pre") if prep is not None else None
     rpp = _in(rstd_post, torch.float32, (T,), "rstd_post") if postp is not None else None
     key = (T, d, r.dtype, yp is not None, postp is not None, prep is not None, _GATES[kind])
+    if dropout:
+        if rng is None or out is None:
+            _rng_in(rng)
+    else:
+        rng = None
     if out is None:
         out = _on(stream, lambda: NormResidualGrads.empty(*key, r.device))
         at = out._addresses(key)
     else:
-        at = out._pointers(key, stream)
+        at = out._pointers(key, stream, rng)[:7]
     if dropout:
         _check(lib.moe_norm_residual_dropout_backward(
-            rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep, dropout, _rng_in(rng), rpp, rqp,
+            rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep, dropout, rng.data_ptr(), rpp, rqp,
             drp, dnp, T, d, *at, _stream_of(r, stream)), "moe_norm_residual_dropout_backward")
     else:
         _check(lib.moe_norm_residual_backward(
@@ -1162,11 +1179,12 @@ class MoELayer:
         )
 
 
-class GatedFFN:
+class GatedFFN(_Buffers):
     """A gated feed-forward's weights (see gated_ffn) and a persistent workspace
     for up to T_max tokens: a dense layer, or the ``shared`` expert of a MoEBlock.
     ``__call__(x)`` runs the forward; with ``save_preact`` it keeps what
-    backward() needs of it (its last call's), as MoELayer does."""
+    backward() needs of it (its last call's), as MoELayer does.  The weights
+    may be replaced between calls by others of their shapes."""
     rule = None
 
     def __init__(self, W1, W2, act: str = "silu", T_max: int = 1):
@@ -1192,8 +1210,24 @@ class GatedFFN:
             pre = self._preact_buf[:T]
         self.preact = pre
         self.calls += 1
-        return gated_ffn(x, self.W1, self.W2, self.act, add=add, out=out, preact=pre, workspace=self.workspace,
-                         stream=stream)
+        bf16, shape = torch.bfloat16, (T, self.d)
+        xp, ap = _in(x, bf16, shape, "x"), None if add is None else _in(add, bf16, shape, "add")
+        if out is None:
+            out = _empty(shape, bf16, x, stream)
+        w1, w2, ws, n = self._pointers()
+        _check(lib.moe_gated_ffn(xp, w1, w2, ap, _act(self.act), T, self.d, self.f, _in(out, bf16, shape, "y"), _ptr(pre),
+                                 ws, n, _stream_of(x, stream)), "moe_gated_ffn")
+        return out
+
+    def _pointers(self):
+        """Addresses of the weights and of the workspace, and its bytes; checked where they are new."""
+        at = (self.W1.data_ptr(), self.W2.data_ptr(), self.workspace.data_ptr(), self.workspace.numel())
+        if at != self._checked:
+            _need(self.W1, torch.bfloat16, (2 * self.f, self.d), "W1")
+            _need(self.W2, torch.bfloat16, (self.d, self.f), "W2")
+            _need(self.workspace, torch.uint8, (self.workspace.numel(),), "workspace")
+            self._hold(at, self.W1, self.W2, self.workspace)
+        return at
 
     def backward(self, x, dy, grads=None, workspace=None, stream=None, add=None):
         """Gradients of sum(dy * y) for the last call (same x, with
