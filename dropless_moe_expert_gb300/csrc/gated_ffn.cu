@@ -95,7 +95,6 @@ struct Params {
     bool add;                   // GRADS: dx has a matrix to be added
     int act;
     bool keep;                  // GATED: store a
-    bool behind;                // launched before the kernel that writes the operands has ended
     int *tickets;               // GRADS, nullable: of the order of tiles (gg::Params::sched)
     int *status;
     uint64_t timeout_ns;
@@ -374,8 +373,6 @@ __global__ void __launch_bounds__(threads_of(EPI), 1) ffn_gemm_kernel(const __gr
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *s_tmem;
-    // the kernel behind this one may take the SMs that fall free, up to where it reads what this one writes
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // The k-th tile of the pair (a negative one ends the list) for the roles that do not decide it.
     auto tile_of = [&](int k, int *tile) {
@@ -392,7 +389,9 @@ __global__ void __launch_bounds__(threads_of(EPI), 1) ffn_gemm_kernel(const __gr
 
     if (warp == 0) {
         if (lane == 0) {
-            if (p.behind) grid_dependency_wait();
+            // (only now may the next kernel start: it goes by what was written before this one)
+            grid_dependency_wait();
+            grid_dependency_launch();
             const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);  // both CTAs' copies signal CTA 0's barriers
             const uint32_t queue1 = mapa_shared(smem_u32(const_cast<int *>(queue)), 1);
             const uint32_t queued1 = mapa_shared(smem_u32(queued), 1);
@@ -551,6 +550,7 @@ __global__ void __launch_bounds__(threads_of(EPI), 1) ffn_gemm_kernel(const __gr
                          half + 32 * q, (warp - 2) >> 2};
         const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
         uint32_t acc = 0, acc_phase = 0;
+        grid_dependency_wait();  // its loads and stores are behind the kernel before, too
         for (int k = 0;; ++k) {
             int tile;
             if (!tile_of(k, &tile) || tile < 0) break;
@@ -644,7 +644,6 @@ struct FewParams {
     int act;
     __nv_bfloat16 *out, *preact;  // [T, N]; GATED, nullable: [T, 2N]
     const __nv_bfloat16 *add;     // nullable, not GATED: [T, N]
-    bool behind;                  // launched before the kernel that writes B has ended
     int *status;
     uint64_t timeout_ns;
 };
@@ -688,8 +687,6 @@ __global__ void __launch_bounds__(FEW_THREADS) ffn_few_kernel(const __grid_const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    // the kernel behind this one (the product with W2) may start, up to where it needs h
-    if (GATE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (threadIdx.x == 0) {
         auto weights = [&](int i, int stage) {
@@ -709,13 +706,15 @@ __global__ void __launch_bounds__(FEW_THREADS) ffn_few_kernel(const __grid_const
             const int k = (kb0 + i) * SLICES * BK;
             for (int s = 0; s < SLICES; ++s) tma_load_2d(sb + s * box, &maps.x, &full[stage], k + s * BK, t0);
         };
-        // the weights of the first stages do not wait for the kernel before
+        // W2 does not wait for the kernel before, which is this one's own for W1
+        if (GATE) grid_dependency_wait();
         const int first = min(kbs, p.stages);
         for (int i = 0; i < first; ++i) weights(i, i);
-        if (p.behind) {
+        if (!GATE) {
             grid_dependency_wait();
             asm volatile("fence.proxy.async;" ::: "memory");  // its plain stores before these copies
         }
+        grid_dependency_launch();
         for (int i = 0; i < first; ++i) activations(i, i);
         int stage = 0;
         uint32_t phase = 0;
@@ -782,7 +781,7 @@ __global__ void __launch_bounds__(FEW_THREADS) ffn_few_kernel(const __grid_const
         }
     };
     if (p.split == 1) {
-        if (!GATE && p.behind) grid_dependency_wait();  // before plain loads and stores of this thread
+        grid_dependency_wait();  // before plain loads and stores of this thread
         for (int c = 0; c < p.tokens; c += 16) {
             if (t0 + c >= p.T) break;
             uint32_t a[16], u[16];
@@ -830,7 +829,7 @@ __global__ void __launch_bounds__(FEW_THREADS) ffn_few_kernel(const __grid_const
             }
             __syncwarp();
             cluster_sync();  // every CTA's sums are there
-            if (!GATE && p.behind) grid_dependency_wait();
+            grid_dependency_wait();
             for (int g = 0; g < groups; ++g) {
                 const int t = t0 + rank * share + g * V;
                 if (t >= p.T) break;
@@ -879,7 +878,6 @@ struct TinyParams {
     int act;
     __nv_bfloat16 *out, *preact;
     const __nv_bfloat16 *add;
-    bool behind;
     int split;  // CTAs of a cluster that share K
 };
 
@@ -911,7 +909,10 @@ __global__ void __launch_bounds__(32 * TINY_WARPS, 2) ffn_tiny_kernel(const Tiny
     const bool on = row < p.N, on2 = GATE ? on : row2 < p.N;
     const int64_t K = p.K;
     const uint16_t *w = p.w + row * K, *w2 = p.w + row2 * K, *x = p.x + g * K;
-    if (GATE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (GATE) {
+        grid_dependency_wait();
+        grid_dependency_launch();
+    }
     if (p.split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA runs
     float c[EIGHTS][4] = {};
     const int first_k = 64 * (rank * TINY_WARPS + warp), step = 64 * TINY_WARPS * p.split;
@@ -925,7 +926,10 @@ __global__ void __launch_bounds__(32 * TINY_WARPS, 2) ffn_tiny_kernel(const Tiny
                 a[i][h] = load_once(w + k, on && k < p.K);
                 b[i][h] = load_once(w2 + k, on2 && k < p.K);
             }
-        if (p.behind && k0 == first_k) grid_dependency_wait();  // the weights' first loads did not wait for it
+        if (!GATE && k0 == first_k) {  // W2's first loads did not wait for the kernel that writes h
+            grid_dependency_wait();
+            grid_dependency_launch();
+        }
         uint4 t[DEEP][2][EIGHTS];
 #pragma unroll
         for (int i = 0; i < DEEP; ++i)
@@ -953,7 +957,7 @@ __global__ void __launch_bounds__(32 * TINY_WARPS, 2) ffn_tiny_kernel(const Tiny
 #pragma unroll
     for (int n = 0; n < EIGHTS; ++n) sums[warp][n][lane] = make_float4(c[n][0], c[n][1], c[n][2], c[n][3]);
     __syncthreads();
-    if (p.behind) grid_dependency_wait();  // (a warp without columns has not waited yet)
+    if (!GATE) grid_dependency_wait();  // (a warp without columns has not waited yet)
     // warp n: the n-th eight tokens
     auto add = [&](float4 &s, const float4 &v) { s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w; };
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1031,15 +1035,19 @@ bool boxes(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t
     return map2d(m, base, rows, cols, ld, CHUNK, CHUNK, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-// attr[0]: pairs; attr[1]: may start before the kernel in front of it ends.
-cudaLaunchConfig_t pair_config(int grid, int threads, int smem, cudaStream_t stream, cudaLaunchAttribute *attr, bool behind) {
+// Every kernel here may start before the one in front of it in the stream has ended:
+// it waits before it touches memory that another kernel writes or reads (W2 by
+// its own kernel excepted, which starts only behind one that has waited).  Calls that
+// follow one another so hide their launches (us a call, 7168 x 2048 at one token 20.0
+// and 18.1; 2048 x 768 at 37 12.3 and 9.4; 1003 x 2056 x 1368 32.7 and 29.3).
+cudaLaunchConfig_t pair_config(int grid, int threads, int smem, cudaStream_t stream, cudaLaunchAttribute *attr) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr, cfg.numAttrs = behind ? 2 : 1;
+    cfg.attrs = attr, cfg.numAttrs = 2;
     return cfg;
 }
 
@@ -1050,7 +1058,7 @@ cudaError_t set_up(int *pairs) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = pair_config(2, threads_of(EPI), smem, nullptr, attr, false);
+    cudaLaunchConfig_t cfg = pair_config(2, threads_of(EPI), smem, nullptr, attr);
     int n = 0;
     const cudaError_t q = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
     if (q != cudaSuccess) return q;
@@ -1079,7 +1087,7 @@ cudaError_t gemm(const Maps &maps, Params p, int M, int N, int K, const GemmLaun
     p.product[0] = q, p.products = 1, p.tiles = q.tiles;
     cudaLaunchAttribute attr[2];
     const int grid = 2 * std::min(q.tiles, lc.ffn_pairs);
-    cudaLaunchConfig_t cfg = pair_config(grid, threads_of(EPI), Layout<EPI, uint16_t>::BYTES, stream, attr, p.behind);
+    cudaLaunchConfig_t cfg = pair_config(grid, threads_of(EPI), Layout<EPI, uint16_t>::BYTES, stream, attr);
     return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<EPI, A_MN, B_MN, uint16_t, Maps>, maps, p);
 }
 
@@ -1087,7 +1095,7 @@ template <typename Out>
 cudaError_t gradients(const GradMaps &maps, const Params &p, const GemmLaunch &lc, cudaStream_t stream) {
     cudaLaunchAttribute attr[2];
     const int grid = 2 * std::min(p.tiles, lc.ffn_pairs);
-    cudaLaunchConfig_t cfg = pair_config(grid, threads_of(GRADS), Layout<GRADS, Out>::BYTES, stream, attr, p.behind);
+    cudaLaunchConfig_t cfg = pair_config(grid, threads_of(GRADS), Layout<GRADS, Out>::BYTES, stream, attr);
     return cudaLaunchKernelEx(&cfg, ffn_gemm_kernel<GRADS, true, true, Out, GradMaps>, maps, p);
 }
 
@@ -1130,16 +1138,15 @@ struct FewShape {
     }
 };
 
-// `behind`: launched while the kernel before it, which writes x, still runs.
 template <bool GATE>
-cudaError_t few(const uint16_t *w, const uint16_t *x, int T, int N, int K, FewParams p, bool behind,
+cudaError_t few(const uint16_t *w, const uint16_t *x, int T, int N, int K, FewParams p,
                 const GemmLaunch &lc, cudaStream_t stream) {
     const FewShape s(T, N, K, GATE, lc);
     FewMaps maps;
     if (!operand(&maps.w, w, GATE ? 2 * static_cast<int64_t>(N) : N, K, false) ||
         !map2d(&maps.x, x, T, K, K, s.tokens, BK, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    p.T = T, p.N = N, p.K = K, p.tokens = s.tokens, p.stages = s.stages, p.split = s.split, p.behind = behind;
+    p.T = T, p.N = N, p.K = K, p.tokens = s.tokens, p.stages = s.stages, p.split = s.split;
     p.tmem_cols = 32;
     while (p.tmem_cols < s.tokens * (GATE ? 2 : 1)) p.tmem_cols *= 2;
     cudaLaunchAttribute attr[2];
@@ -1150,7 +1157,7 @@ cudaError_t few(const uint16_t *w, const uint16_t *x, int T, int N, int K, FewPa
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(s.rows * s.split, s.blocks), cfg.blockDim = dim3(FEW_THREADS);
     cfg.dynamicSmemBytes = s.smem, cfg.stream = stream;
-    cfg.attrs = attr, cfg.numAttrs = behind ? 2 : 1;
+    cfg.attrs = attr, cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, ffn_few_kernel<GATE>, maps, p);
 }
 
@@ -1169,24 +1176,17 @@ struct TinyShape {
     }
 };
 template <bool GATE>
-cudaError_t tiny(TinyParams p, bool behind, const GemmLaunch &lc, cudaStream_t stream) {
+cudaError_t tiny(TinyParams p, const GemmLaunch &lc, cudaStream_t stream) {
     const TinyShape s(p.T, p.N, p.K, GATE, lc.num_sms);
     cudaLaunchAttribute attr[2];
-    int attrs = 0;
-    if (s.split > 1) {
-        attr[attrs].id = cudaLaunchAttributeClusterDimension;
-        attr[attrs].val.clusterDim.x = s.split, attr[attrs].val.clusterDim.y = attr[attrs].val.clusterDim.z = 1;
-        ++attrs;
-    }
-    if (behind) {
-        attr[attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[attrs].val.programmaticStreamSerializationAllowed = 1;
-        ++attrs;
-    }
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = s.split, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(s.units * s.split), cfg.blockDim = dim3(32 * TINY_WARPS), cfg.stream = stream;
-    cfg.attrs = attr, cfg.numAttrs = attrs;
-    p.behind = behind, p.split = s.split;
+    cfg.attrs = attr, cfg.numAttrs = s.split > 1 ? 2 : 1;
+    p.split = s.split;
     return p.T <= 8    ? cudaLaunchKernelEx(&cfg, ffn_tiny_kernel<GATE, 1>, p)
            : p.T <= 16 ? cudaLaunchKernelEx(&cfg, ffn_tiny_kernel<GATE, 2>, p)
            : p.T <= 32 ? cudaLaunchKernelEx(&cfg, ffn_tiny_kernel<GATE, 4>, p)
@@ -1275,10 +1275,10 @@ cudaError_t launch_ffn(const FfnArgs &a, const GemmLaunch &lc, cudaStream_t stre
     p.act = a.act, p.status = a.status, p.timeout_ns = a.timeout_ns;
     cudaError_t e;
     if (way.tiny) {
-        e = tiny<true>({a.W1, a.x, a.T, a.f, a.d, a.act, bf16(a.h), bf16(a.preact), nullptr}, false, lc, stream);
+        e = tiny<true>({a.W1, a.x, a.T, a.f, a.d, a.act, bf16(a.h), bf16(a.preact), nullptr}, lc, stream);
     } else if (way.few_up) {
         fp.out = bf16(a.h), fp.preact = bf16(a.preact);
-        e = few<true>(a.W1, a.x, a.T, a.f, a.d, fp, false, lc, stream);
+        e = few<true>(a.W1, a.x, a.T, a.f, a.d, fp, lc, stream);
     } else {
         Maps m = {};
         p.keep = a.preact != nullptr;
@@ -1290,13 +1290,12 @@ cudaError_t launch_ffn(const FfnArgs &a, const GemmLaunch &lc, cudaStream_t stre
     }
     if (e != cudaSuccess) return e;
     if (way.tiny)
-        return tiny<false>({a.W2, a.h, a.T, a.d, a.f, a.act, bf16(a.y), nullptr, bf16(a.add)}, true, lc, stream);
+        return tiny<false>({a.W2, a.h, a.T, a.d, a.f, a.act, bf16(a.y), nullptr, bf16(a.add)}, lc, stream);
     if (way.few_down) {
         fp.out = bf16(a.y), fp.preact = nullptr, fp.add = bf16(a.add);
-        return few<false>(a.W2, a.h, a.T, a.d, a.f, fp, true, lc, stream);
+        return few<false>(a.W2, a.h, a.T, a.d, a.f, fp, lc, stream);
     }
     Maps m = {};
-    p.behind = true;
     if (!operand(&m.a, a.h, a.T, f, false) || !operand(&m.b, a.W2, a.d, f, false) || !half_operand(&m.half_b, a.W2, a.d, f) ||
         !boxes(&m.out, a.y, a.T, a.d, a.d) || (a.add && !boxes(&m.in, a.add, a.T, a.d, a.d)))
         return cudaErrorInvalidValue;
@@ -1343,7 +1342,7 @@ cudaError_t launch_ffn_bwd(const FfnGradArgs &a, const GemmLaunch &lc, int *laun
         const Product q = product(list[i].M, list[i].N, list[i].K, false, 0);
         work += static_cast<int64_t>(q.tiles) * ((q.K + BK - 1) / BK);
     }
-    p.add = a.add != nullptr, p.behind = true, p.products = n;
+    p.add = a.add != nullptr, p.products = n;
     for (int i = 0; i < n; ++i) {
         const auto &l = list[i];
         const bool dx = l.kind == KIND_DX;

@@ -249,6 +249,7 @@ norm_residual_kernel(Args a, float inv_d, const R *r, R *r_out, uint16_t *__rest
     const int stage = warps * PART;
     uint8_t *const mine = ring + warp * PART;
     float2 c[VPT][4], w[VPT][4];
+    grid_dependency_wait();  // launched early
     if (HOLD) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) weights(a, own.col + 256 * j, own.on[j], c[j], w[j]);
@@ -407,6 +408,7 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
     const int stage = warps * PART;
     uint8_t *const mine = ring + team * stages * stage + warp * PART;
     float2 c[VPT][4], w[VPT][4], accq[VPT][4], accp[VPT][4];
+    grid_dependency_wait();  // launched early
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         weights(a, own.col + 256 * j, own.on[j], c[j], w[j]);
@@ -753,9 +755,14 @@ cudaError_t forward(const Shape &s, const NormResidualArgs &a, const void *r, vo
     const cudaError_t e = allow_ring(norm_residual_kernel<R, VPT, REGS, DROP>, done);
     if (e != cudaSuccess) return e;
     const Args args{a, s.stages, s.teams, reinterpret_cast<uintptr_t>(r_out) % 32 == 0};
-    norm_residual_kernel<R, VPT, REGS, DROP><<<s.ctas, s.threads, s.smem, stream>>>(
-        args, 1.0f / a.d, static_cast<const R *>(r), static_cast<R *>(r_out), n, rstd_post, rstd_pre);
-    return cudaGetLastError();
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(s.ctas), cfg.blockDim = dim3(s.threads), cfg.dynamicSmemBytes = s.smem, cfg.stream = stream;
+    cfg.attrs = &early, cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, norm_residual_kernel<R, VPT, REGS, DROP>, args, 1.0f / a.d,
+                              static_cast<const R *>(r), static_cast<R *>(r_out), n, rstd_post, rstd_pre);
 }
 
 template <typename R, int VPT, bool Y, bool PRE, bool DR, Split SPLIT, int REGS, bool DROP>
@@ -765,12 +772,14 @@ cudaError_t backward(const Shape &s, const NormResidualArgs &a, const NormResidu
     const cudaError_t e = allow_ring(norm_residual_bwd_kernel<R, VPT, Y, PRE, DR, SPLIT, REGS, DROP>, done);
     if (e != cudaSuccess) return e;
     const Args args{a, s.stages, s.teams, reinterpret_cast<uintptr_t>(g.dr) % 32 == 0};
-    cudaLaunchAttribute pairs;
-    pairs.id = cudaLaunchAttributeClusterDimension;
-    pairs.val.clusterDim.x = 2, pairs.val.clusterDim.y = pairs.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(s.ctas), cfg.blockDim = dim3(s.threads), cfg.dynamicSmemBytes = s.smem, cfg.stream = stream;
-    cfg.attrs = &pairs, cfg.numAttrs = SPLIT == HALVES;
+    cfg.attrs = attr, cfg.numAttrs = SPLIT == HALVES ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, norm_residual_bwd_kernel<R, VPT, Y, PRE, DR, SPLIT, REGS, DROP>, args, 1.0f / a.d,
                               static_cast<const R *>(g.r_out), static_cast<const R *>(g.dr_out),
                               static_cast<const uint16_t *>(g.dn), static_cast<const float *>(g.rstd_post),

@@ -140,6 +140,9 @@ __device__ __forceinline__ void cp_async_arrive_noinc(uint64_t *bar) {
 // Programmatic dependent launch: until the kernels that this one was launched
 // behind have ended and what they wrote can be read.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the kernel that is launched behind this one so start, once every CTA of
+// this one has got here (or ended).
+__device__ __forceinline__ void grid_dependency_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 

@@ -286,6 +286,48 @@ def test_streams_graphs_and_repeated_calls(c):
     assert moe.device_status() == 0
 
 
+@pytest.mark.parametrize("c", [(1, 1024, 2048, "silu"), (40, 2048, 768, "gelu"), (100, 4096, 1024, "silu"),
+                               (300, 1024, 2048, "relu"), (1500, 1024, 1024, "silu")], ids=str)
+def test_inputs_written_just_before(c):
+    """Weights, tokens and the kept pre-activations change in the stream right before each call, whose kernels start
+    before the ones in front of them have ended; eagerly, and in a captured graph that holds the changes too."""
+    T, d, f, act = c
+    sets = [_case(c, k) for k in range(3)]
+    want = []
+    for x, W1, W2, dy, _ in sets:
+        pre = torch.empty(T, 2 * f, dtype=BF16, device="cuda")
+        y = moe.gated_ffn(x, W1, W2, act, preact=pre)
+        g = moe.gated_ffn_backward(x, pre, dy, W1, W2, act)
+        torch.cuda.synchronize()
+        want.append((y, g.dx, g.dW1, g.dW2))
+    x, W1, W2, dy = (t.clone() for t in sets[2][:4])
+    ffn = moe.GatedFFN(W1, W2, act, T_max=T)
+    grads = moe.GatedFFNGrads.empty(T, d, f)
+
+    def step(k):
+        for to, of in ((x, 0), (W1, 1), (dy, 3), (W2, 2)):
+            to.copy_(sets[k][of])
+        y = ffn(x, save_preact=True)
+        moe.gated_ffn_backward(x, ffn.preact, dy, W1, W2, act, out=grads)
+        return [t.clone() for t in (y, grads.dx, grads.dW1, grads.dW2)]
+
+    got = [step(k % 3) for k in range(12)]
+    torch.cuda.synchronize()
+    for k, outs in enumerate(got):
+        for a, b in zip(outs, want[k % 3]):
+            assert torch.equal(a, b), k
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [step(k) for k in (1, 0, 2, 0)]
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for k, outs in zip((1, 0, 2, 0), got):
+        for a, b in zip(outs, want[k]):
+            assert torch.equal(a, b), k
+    assert moe.device_status() == 0
+
+
 def test_offsets_past_32_bits():
     """Pre-activations and their gradients that begin beyond 2^31 elements."""
     T, d, f = 70001, 8, 16384
