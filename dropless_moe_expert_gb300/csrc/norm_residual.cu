@@ -13,8 +13,14 @@
 //   dgp = sum_t g D y rp,   dg = u D summed over the axis that g is shared along
 // With dropout (DROP) what is added is g u / (1 - p) where an element is kept and 0 where it is not:
 //   r' = a r + m g u,   and D in all of the y side's gradients is m D,   m = 0 or 1 / (1 - p)
-// drawn again in the backward from the same state.  It adds no bytes, and about 10
-// integer instructions per element.
+// drawn again in the backward from the same state, before the row's bytes are
+// waited for.  It adds no bytes, about 10 integer instructions per element and, in
+// the backward, two tests.  Measured, 8192 x 4096 bf16 with both norms: forward 52.8 us
+// a call (46.2 without dropout), backward 87.5 (70.1); 4093 x 7168 with the stream in fp32
+// and without gamma_post 54.9 and 94.7.  One round of the generator instead of ten
+// would take 10 us off either; a mask held as bits in one register is better than the
+// draws themselves (2048 x 12288: 104 us), and predicates are than masks of the
+// operands' bits where rows are bf16 (63 and 59 us for the residual's sum alone).
 // The sums over t run in a fixed order: each CTA over its own rows, then the
 // CTAs' partial sums in their order.
 //
@@ -47,6 +53,8 @@ constexpr int FWD_STAGES = 2;
 constexpr int BWD_STAGES = 4;
 
 // Which backward kernels read a row ahead: of those whose ring always holds three rows, the one it makes faster.
+// With dropout none does, as the draws take its registers (us: 8192 x 4096 bf16
+// 99 ahead and in teams, 87 without and in pairs; 16384 x 1024 59 and 47).
 template <typename R>
 __host__ __device__ constexpr bool pipelined(int vpt, bool full) { return full && vpt == 2 && sizeof(R) == 2; }
 
@@ -389,7 +397,7 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
     // waits for this CTA's own of the next row.  The same order of events frees the third set of `red`.
     __shared__ uint64_t posted[MAX_THREADS / 32];
     __shared__ int abort;
-    constexpr bool PIPE = pipelined<R>(VPT, Y && PRE), TEAMS = SPLIT == TEAM;
+    constexpr bool PIPE = !DROP && pipelined<R>(VPT, Y && PRE), TEAMS = SPLIT == TEAM;
     // Whether the warps wait for the row's sums by an mbarrier, which lets the first ones through go on
     // (4093 x 7168 fp32: 90.0 us, 95.3 with __syncthreads).
     constexpr bool POSTS = PIPE || SPLIT == ALONE || SPLIT == HALVES;
@@ -716,7 +724,7 @@ Shape fwd_shape(int T, int d) {
 // with both needs its 128.  Teams are as many as rows spread over all SMs allow;
 // the ring also holds their partial sums in the end.
 template <typename R>
-Shape bwd_shape(int T, int d, bool y, bool pre) {
+Shape bwd_shape(int T, int d, bool y, bool pre, bool drop) {
     const int piece = (y + pre) * piece_bytes<uint16_t>() + (1 + pre) * piece_bytes<R>();
     const bool fewer = sizeof(R) == 2 && !(y && pre) && d > 4096 && sm_rows(d, 80) > sm_rows(d, 128);
     const bool ahead = pipelined<R>(2, y && pre);
@@ -728,7 +736,7 @@ Shape bwd_shape(int T, int d, bool y, bool pre) {
     }
     Shape s(T, d, d <= 256 ? 1 : 2, fewer ? 80 : 128, BWD_STAGES, piece);
     const int per_sm = s.per_sm();
-    s.split = per_sm == 1 ? ALONE : per_sm == 2 && !ahead ? PAIR : TEAM;
+    s.split = per_sm == 1 ? ALONE : per_sm == 2 && (!ahead || drop) ? PAIR : TEAM;
     if (s.split != TEAM) return s;
     s.teams = std::min(per_sm, (T + SMS - 1) / SMS);
     s.ctas = std::min(T, SMS);
@@ -807,7 +815,9 @@ size_t norm_residual_bwd_part_bytes(int T, int d) {
     int ctas = 0;  // the most of any form
     for (const bool y : {false, true})
         for (const bool pre : {!y, true})
-            ctas = std::max({ctas, nr::bwd_shape<float>(T, d, y, pre).ctas, nr::bwd_shape<uint16_t>(T, d, y, pre).ctas});
+            for (const bool drop : {false, true})
+                ctas = std::max({ctas, nr::bwd_shape<float>(T, d, y, pre, drop).ctas,
+                                 nr::bwd_shape<uint16_t>(T, d, y, pre, drop).ctas});
     return static_cast<size_t>(ctas) * 2 * d * 4;
 }
 
@@ -816,7 +826,7 @@ cudaError_t launch_norm_residual_bwd(const NormResidualArgs &a, const NormResidu
     int parts = 0;
     auto go = [&](auto type, auto dropout) {
         using R = decltype(type);
-        const nr::Shape s = nr::bwd_shape<R>(a.T, a.d, a.y, a.gamma_pre);
+        const nr::Shape s = nr::bwd_shape<R>(a.T, a.d, a.y, a.gamma_pre, a.rng);
         parts = s.split == nr::HALVES ? s.ctas / 2 : s.ctas;
         auto form = [&](auto y, auto pre, auto dr) {
             constexpr bool Y = decltype(y)::value, PRE = decltype(pre)::value, DR = decltype(dr)::value;
@@ -829,7 +839,7 @@ cudaError_t launch_norm_residual_bwd(const NormResidualArgs &a, const NormResidu
                 if (s.regs == 80) return nr::backward<R, 2, Y, PRE, DR, nr::ALONE, 80, DROP>(s, a, g, part, stream);
             }
             if (s.split == nr::TEAM) return nr::backward<R, 2, Y, PRE, DR, nr::TEAM, 128, DROP>(s, a, g, part, stream);
-            if constexpr (!nr::pipelined<R>(2, Y && PRE))
+            if constexpr (DROP || !nr::pipelined<R>(2, Y && PRE))
                 if (s.split == nr::PAIR) return nr::backward<R, 2, Y, PRE, DR, nr::PAIR, 128, DROP>(s, a, g, part, stream);
             return nr::backward<R, 2, Y, PRE, DR, nr::ALONE, 128, DROP>(s, a, g, part, stream);
         };
