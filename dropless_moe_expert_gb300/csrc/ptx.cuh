@@ -126,6 +126,11 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
         : "memory");
 }
 
+// Brings `bytes` (a multiple of 16) from a 16-byte aligned address into L2.
+__device__ __forceinline__ void l2_prefetch(const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // 16-byte asynchronous copy global -> shared (both 16-byte aligned), through
 // L2 only (.cg).
 __device__ __forceinline__ void cp_async_16(void *dst, const void *src) {
