@@ -195,6 +195,12 @@ def _in(t, dtype, shape, name) -> int:
     return _need(t, dtype, shape, name).data_ptr()
 
 
+def _here(t):
+    """The library works on the current device; a tensor of another one is refused."""
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on device {t.get_device()}, the current one is {torch._C._cuda_getDevice()}")
+
+
 class _Buffers:
     """Output buffers that are checked once.  ``_checked`` is what the last
     check went by, the tensors' addresses among it; tensors that stand at other
@@ -535,6 +541,7 @@ def norm_residual(r, y=None, *, gamma_post=None, gate=None, gamma_pre=None, res_
     T, d, kind, rp, yp, postp, gatep, prep = _norm_args(r, y, gamma_post, gate, gamma_pre)
     key = (T, d, r.dtype, yp is not None, postp is not None, prep is not None)
     if dropout:
+        _here(r)
         if rng is None or out is None:
             _rng_in(rng)
     else:
@@ -573,6 +580,7 @@ def norm_residual_backward(r, dr, dn=None, y=None, *, gamma_post=None, gate=None
     rpp = _in(rstd_post, torch.float32, (T,), "rstd_post") if postp is not None else None
     key = (T, d, r.dtype, yp is not None, postp is not None, prep is not None, _GATES[kind])
     if dropout:
+        _here(r)
         if rng is None or out is None:
             _rng_in(rng)
     else:
@@ -624,9 +632,11 @@ def gated_ffn(x, W1, W2, act: str = "silu", *, add=None, out=None, preact=None, 
     if out is None:
         out = _empty(shape, bf16, x, stream)
     yp = _in(out, bf16, shape, "y")
+    _here(x)
     if workspace is None:
         workspace = _empty((int(lib.moe_gated_ffn_workspace_size(T, d, f)),), torch.uint8, x, stream)
-    _check(lib.moe_gated_ffn(xp, w1, w2, ap, _act(act), T, d, f, yp, pp, workspace.data_ptr(), workspace.numel(),
+    n = workspace.numel()
+    _check(lib.moe_gated_ffn(xp, w1, w2, ap, _act(act), T, d, f, yp, pp, _in(workspace, torch.uint8, (n,), "workspace"), n,
                              _stream_of(x, stream)), "moe_gated_ffn")
     return out
 
@@ -687,6 +697,7 @@ def gated_ffn_backward(x, preact, dy, W1, W2, act: str = "silu", *, add=None, ou
     xp, dyp, ap = _in(x, bf16, shape, "x"), _in(dy, bf16, shape, "dy"), None if add is None else _in(add, bf16, shape,
                                                                                                     "add")
     pp = _in(preact, bf16, (T, 2 * f), "preact")
+    _here(x)
     if out is None:
         out = _on(stream, lambda: GatedFFNGrads.empty(T, d, f, device=x.device))
     _check(lib.moe_gated_ffn_backward(xp, pp, dyp, w1, w2, ap, _act(act), T, d, f, *out._pointers(T, d, f, stream),
@@ -1214,6 +1225,7 @@ class GatedFFN(_Buffers):
         xp, ap = _in(x, bf16, shape, "x"), None if add is None else _in(add, bf16, shape, "add")
         if out is None:
             out = _empty(shape, bf16, x, stream)
+        _here(x)
         w1, w2, ws, n = self._pointers()
         _check(lib.moe_gated_ffn(xp, w1, w2, ap, _act(self.act), T, self.d, self.f, _in(out, bf16, shape, "y"), _ptr(pre),
                                  ws, n, _stream_of(x, stream)), "moe_gated_ffn")

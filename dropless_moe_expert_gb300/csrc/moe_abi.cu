@@ -610,8 +610,15 @@ moe_status_t moe_gated_ffn_backward(const uint16_t *x, const uint16_t *preact, c
     const size_t rows = static_cast<size_t>(T) * d * 2;
     if (!same_or_apart(dx, add, rows)) return MOE_ERR_INVALID_ARG;
     if (workspace_bytes < 3 * ffn_bytes(T, f)) return MOE_ERR_WORKSPACE;
-    // dx is written beside the weights' gradients, which read these
-    if (!apart(dx, rows, dW1 ? x : nullptr, rows) || !apart(dx, rows, dW2 ? dy : nullptr, rows)) return MOE_ERR_INVALID_ARG;
+    // the gradients are written beside one another, from x (dW1), dy (dW2) and W1 (dx)
+    const size_t weights = static_cast<size_t>(d) * f * (weights_fp32 ? 4 : 2), w1 = 2 * weights;
+    const uint16_t *xr = dW1 ? x : nullptr, *dyr = dW2 ? dy : nullptr, *Wr = dx ? W1 : nullptr;
+    const size_t Wn = static_cast<size_t>(d) * f * 4;
+    if (!apart(dx, rows, xr, rows) || !apart(dx, rows, dyr, rows) || !apart(dW1, w1, xr, rows) ||
+        !apart(dW1, w1, dyr, rows) || !apart(dW2, weights, xr, rows) || !apart(dW2, weights, dyr, rows) ||
+        !apart(dx, rows, Wr, Wn) || !apart(dW1, w1, Wr, Wn) || !apart(dW2, weights, Wr, Wn) ||
+        !apart(dx, rows, dW1, w1) || !apart(dx, rows, dW2, weights) || !apart(dW1, w1, dW2, weights))
+        return MOE_ERR_INVALID_ARG;
     DeviceState *ds = nullptr;
     if ((st = device_state(&ds)) != MOE_OK) return st;
     uint16_t *da = static_cast<uint16_t *>(workspace);

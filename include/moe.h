@@ -274,8 +274,9 @@ moe_status_t moe_gated_ffn(const uint16_t *x, const uint16_t *W1, const uint16_t
  * dx [T, d] bf16; dW1 and dW2, shaped like the weights, bf16 (weights_fp32 0)
  * or fp32 (1).  Each of the three is NULL where it is not wanted (then W1, or
  * x, may be NULL too).  add [T, d] bf16 (nullable, with dx) may be dx itself,
- * else they are apart; dx overlaps neither x (with dW1) nor dy (with dW2).  dh
- * is not rounded, da and h to bf16 once each, as operands.  `workspace` (16-byte aligned) holds
+ * else they are apart; none of the three overlaps another one or x (with dW1),
+ * dy (with dW2) or W1 (with dx).  dh is not rounded, da and h to bf16 once
+ * each, as operands.  `workspace` (16-byte aligned) holds
  * moe_gated_ffn_backward_workspace_size(T, d, f) bytes.  Deterministic.
  * 2 kernel launches. */
 size_t moe_gated_ffn_backward_workspace_size(int T, int d, int f);

@@ -328,6 +328,46 @@ def test_inputs_written_just_before(c):
     assert moe.device_status() == 0
 
 
+@pytest.mark.parametrize("T", [1, 48, 700])
+def test_forks_and_joins_in_a_graph(T):
+    """A captured graph in which the operators' kernels follow a fork, a join, a copy and one another."""
+    c = (T, 512, 1024, "silu")
+    x, W1, W2, dy, _ = _case(c)
+    V1, V2 = _case(c, 7)[1:3]
+    a, b = moe.GatedFFN(W1, W2, T_max=T), moe.GatedFFN(V1, V2, T_max=T)
+    last = moe.GatedFFN(W1, W2, T_max=T)
+    gamma = 1 + 0.1 * torch.randn(512, device="cuda")
+    rng = torch.tensor([4, 2], device="cuda")
+    xs, side = x.clone(), torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            v = b(xs, save_preact=True)
+            gv = b.backward(xs, dy)
+        u = a(xs, save_preact=True)
+        main.wait_stream(side)
+        n = moe.norm_residual(u, v, gamma_pre=gamma, dropout=0.2, rng=rng)
+        y = last(n.n, save_preact=True)
+        g = last.backward(n.n, dy)
+        h = moe.norm_residual_backward(n.r, None, g["dx"], v, gamma_pre=gamma, rstd_pre=n.rstd_pre, dropout=0.2, rng=n.rng)
+        return [u, v, n.r, y, g["dx"], g["dW1"], h.dr, h.dy, h.dgamma_pre, gv["dx"]]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    xs.copy_(dy)
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in got]
+    for s, t in zip(step(), got):
+        assert torch.equal(s, t)
+    assert moe.device_status() == 0
+
+
 def test_offsets_past_32_bits():
     """Pre-activations and their gradients that begin beyond 2^31 elements."""
     T, d, f = 70001, 8, 16384

@@ -50,6 +50,12 @@ def test_feed_forward_refusals(moe):
     # dx over what the weights' gradients read beside it
     far = FAKE + (1 << 16)
     assert _bwd(moe) == 1 and _bwd(moe, x=far) == 1 and _bwd(moe, dy=far) == 1 and _bwd(moe, x=far, dy=FAKE + 496) == 1
+    # the weights' gradients over each other, or over what is read beside them (dW1: 144 x 64, in fp32 36864 bytes)
+    at = {k: FAKE + (i << 20) for i, k in enumerate(("x", "dy", "W1", "dx", "dW1", "dW2"))}
+    for name, over in (("dW1", "x"), ("dW1", "dy"), ("dW2", "x"), ("dW2", "dy"), ("dW1", "W1"), ("dW2", "W1"),
+                       ("dW2", "dW1"), ("dx", "W1"), ("dx", "dW1"), ("dx", "dW2")):
+        assert _bwd(moe, **{**at, name: at[over] + 16}) == 1, (name, over)
+    assert _bwd(moe, **{**at, "dW2": at["dW1"] + 36864 - 16, "wide": 1}) == 1
     for size in ((0, 64, 64), (4, 60, 64), (4, 64, 4), (4, 0, 8), (1 << 30, 64, 1 << 20)):
         assert moe.lib.moe_gated_ffn_workspace_size(*size) == 0
         assert moe.lib.moe_gated_ffn_backward_workspace_size(*size) == 0
