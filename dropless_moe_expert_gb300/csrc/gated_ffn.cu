@@ -391,6 +391,7 @@ __global__ void __launch_bounds__(threads_of(EPI), 1) ffn_gemm_kernel(const __gr
         if (lane == 0) {
             // (only now may the next kernel start: it goes by what was written before this one)
             grid_dependency_wait();
+            fence_proxy_async();  // its plain stores before these copies
             grid_dependency_launch();
             const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);  // both CTAs' copies signal CTA 0's barriers
             const uint32_t queue1 = mapa_shared(smem_u32(const_cast<int *>(queue)), 1);
@@ -551,6 +552,7 @@ __global__ void __launch_bounds__(threads_of(EPI), 1) ffn_gemm_kernel(const __gr
         const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
         uint32_t acc = 0, acc_phase = 0;
         grid_dependency_wait();  // its loads and stores are behind the kernel before, too
+        fence_proxy_async();
         for (int k = 0;; ++k) {
             int tile;
             if (!tile_of(k, &tile) || tile < 0) break;
@@ -629,7 +631,9 @@ __global__ void __launch_bounds__(threads_of(EPI), 1) ffn_gemm_kernel(const __gr
 // most SMs whatever their shape; the CTAs then send each other their partial
 // sums, each getting those of a share of the tokens, and add them in the
 // order of the CTAs (the same bits on every call).
-// GATED: two MMAs per step, the block's gate rows and its up rows.
+// GATED: two MMAs per step, the block's gate rows and its up rows.  The products of
+// the backward take the weights as stored, with the rows of the result along
+// memory: DACT (da and h from dh and a), and ADD for dx.
 // ======================================================================
 constexpr int FEW_ROWS = 128;
 constexpr int FEW_THREADS = 128;
@@ -642,8 +646,9 @@ struct FewParams {
     int stages, split;
     int tmem_cols;
     int act;
-    __nv_bfloat16 *out, *preact;  // [T, N]; GATED, nullable: [T, 2N]
-    const __nv_bfloat16 *add;     // nullable, not GATED: [T, N]
+    __nv_bfloat16 *out;           // [T, N]
+    __nv_bfloat16 *pair;          // [T, 2N]: GATED a (nullable), DACT da
+    const __nv_bfloat16 *in;      // PLAIN and ADD what is added (nullable) [T, N], DACT a [T, 2N]
     int *status;
     uint64_t timeout_ns;
 };
@@ -651,7 +656,8 @@ struct FewMaps {
     CUtensorMap w, x;
 };
 
-template <bool GATE>
+// EPI: GATED, PLAIN, DACT or ADD (PLAIN with the weights as dx reads them).
+template <Epi EPI>
 __global__ void __launch_bounds__(FEW_THREADS) ffn_few_kernel(const __grid_constant__ FewMaps maps, const FewParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -659,7 +665,9 @@ __global__ void __launch_bounds__(FEW_THREADS) ffn_few_kernel(const __grid_const
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     volatile int *abort = &s_abort;
+    constexpr bool GATE = EPI == GATED, MN = EPI == DACT || EPI == ADD;  // MN: weights [K, N], else [N, K]
     constexpr int SLICES = GATE ? 1 : 2;  // of K in a stage
+    constexpr int PARTS = GATE ? 2 : 1;   // sums per row and token: gate, up
     const int warp = threadIdx.x >> 5;
     const int rank = static_cast<int>(blockIdx.x) % p.split, row0 = static_cast<int>(blockIdx.x) / p.split * FEW_ROWS;
     const int t0 = static_cast<int>(blockIdx.y) * p.tokens;
@@ -696,6 +704,9 @@ __global__ void __launch_bounds__(FEW_THREADS) ffn_few_kernel(const __grid_const
             if (GATE) {
                 tma_load_2d(sa, &maps.w, &full[stage], k, row0);
                 tma_load_2d(sa + FEW_A / 2, &maps.w, &full[stage], k, p.N + row0);
+            } else if (MN) {
+                for (int i = 0; i < 4; ++i)
+                    tma_load_2d(sa + i * BOX, &maps.w, &full[stage], row0 + (i & 1) * 64, k + (i >> 1) * BK);
             } else {
                 tma_load_2d(sa, &maps.w, &full[stage], k, row0);
                 tma_load_2d(sa + FEW_A / 2, &maps.w, &full[stage], k + BK, row0);
@@ -706,13 +717,14 @@ __global__ void __launch_bounds__(FEW_THREADS) ffn_few_kernel(const __grid_const
             const int k = (kb0 + i) * SLICES * BK;
             for (int s = 0; s < SLICES; ++s) tma_load_2d(sb + s * box, &maps.x, &full[stage], k + s * BK, t0);
         };
-        // W2 does not wait for the kernel before, which is this one's own for W1
-        if (GATE) grid_dependency_wait();
+        // the weights do not wait for the kernel before, where that is one of this operator's
+        constexpr bool FIRST = EPI == GATED || EPI == DACT;
+        if (FIRST) grid_dependency_wait();
         const int first = min(kbs, p.stages);
         for (int i = 0; i < first; ++i) weights(i, i);
-        if (!GATE) {
+        if (!FIRST) {
             grid_dependency_wait();
-            asm volatile("fence.proxy.async;" ::: "memory");  // its plain stores before these copies
+            fence_proxy_async();  // its plain stores before these copies
         }
         grid_dependency_launch();
         for (int i = 0; i < first; ++i) activations(i, i);
@@ -736,7 +748,7 @@ __global__ void __launch_bounds__(FEW_THREADS) ffn_few_kernel(const __grid_const
                 mbar_wait(&full[i % p.stages], (i / p.stages) & 1, &no_abort, p.status, p.timeout_ns);
         }
     } else if (threadIdx.x == 32) {
-        const uint32_t idesc = idesc_bf16_f32(FEW_ROWS, p.tokens);
+        const uint32_t idesc = idesc_bf16_f32(FEW_ROWS, p.tokens, MN);
         int stage = 0;
         uint32_t phase = 0;
         for (int i = 0; i < kbs; ++i) {
@@ -745,11 +757,12 @@ __global__ void __launch_bounds__(FEW_THREADS) ffn_few_kernel(const __grid_const
             const uint32_t sa = smem_u32(smem + stage * stage_bytes), sb = sa + FEW_A;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {  // GATE: gate and up rows; else the two slices
-                const uint64_t adesc = smem_desc_kmajor_sw128(sa + s * (FEW_A / 2));
+                const uint64_t adesc = MN ? smem_desc_mnmajor_sw128(sa + s * (FEW_A / 2), BOX)
+                                          : smem_desc_kmajor_sw128(sa + s * (FEW_A / 2));
                 const uint64_t bdesc = smem_desc_kmajor_sw128(sb + (GATE ? 0 : s * box));
 #pragma unroll
                 for (int j = 0; j < BK / UMMA_K; ++j)
-                    umma_bf16(tmem + (GATE ? s * p.tokens : 0), adesc + 2 * j, bdesc + 2 * j, idesc,
+                    umma_bf16(tmem + (GATE ? s * p.tokens : 0), adesc + (MN ? 128 : 2) * j, bdesc + 2 * j, idesc,
                               GATE ? (i | j) != 0 : (i | s | j) != 0);
             }
             umma_commit(&empty[stage]);
@@ -758,6 +771,15 @@ __global__ void __launch_bounds__(FEW_THREADS) ffn_few_kernel(const __grid_const
         umma_commit(&done);
     }
     __syncwarp();
+    if (EPI == DACT && warp >= 2) {
+        // what the results are made from besides the sums, into L2 meanwhile: the CTA's share of
+        // the tokens, 128 bytes per lane
+        grid_dependency_wait();
+        const int share = p.tokens / p.split, first = t0 + rank * share, lane = threadIdx.x & 31;
+        const int col = row0 + (lane & 1) * 64;
+        for (int t = first + (warp - 2) * 8 + (lane >> 2); t < min(first + share, p.T); t += 16)
+            if (col < p.N) l2_prefetch_line(p.in + 2 * static_cast<size_t>(t) * p.N + (lane & 2 ? p.N : 0) + col);
+    }
     // every thread waits for the MMAs (after a wait that ran out: for those that were issued)
     volatile int no_abort = 0;
     mbar_wait(&done, 0, &no_abort, p.status, 2 * p.timeout_ns);
@@ -765,37 +787,87 @@ __global__ void __launch_bounds__(FEW_THREADS) ffn_few_kernel(const __grid_const
     tc_fence_after();
     const uint32_t tbase = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     const int row = row0 + static_cast<int>(threadIdx.x);  // the lane's weight row is the result's column
-    auto store = [&](int t, float a, float u) {
-        if (t >= p.T || row >= p.N) return;
-        const size_t at = static_cast<size_t>(t) * p.N + row;
+    // V tokens' sums (of GATED the gate's, u the up row's; of DACT dh) from token t on. What
+    // is read for them is asked for before the first is used, and they are worked on side
+    // by side: one by one, 128 tokens of DACT took 60 us.
+    auto store = [&](int t, auto values, const float *a, const float *u) {
+        constexpr int V = values.value;
+        if (row >= p.N) return;
+        const size_t N = p.N, at = static_cast<size_t>(t) * N + row;
+        [[maybe_unused]] const size_t pair = at + static_cast<size_t>(t) * N;  // in [T, N], [T, 2N]
+        const int n = min(V, p.T - t);
         if constexpr (GATE) {
-            float act;
-            with_activation(p.act, [&](auto k) { act = activate<k.value>(a); });
-            p.out[at] = __float2bfloat16_rn(act * u);
-            if (p.preact) {
-                p.preact[2 * static_cast<size_t>(t) * p.N + row] = __float2bfloat16_rn(a);
-                p.preact[(2 * static_cast<size_t>(t) + 1) * p.N + row] = __float2bfloat16_rn(u);
+            with_activation(p.act, [&](auto k) {
+#pragma unroll
+                for (int i = 0; i < V; i += 2) {
+                    const float2 h = mul2(activate<k.value>(make_float2(a[i], a[i + 1])), make_float2(u[i], u[i + 1]));
+                    if (i < n) p.out[at + N * i] = __float2bfloat16_rn(h.x);
+                    if (i + 1 < n) p.out[at + N * i + N] = __float2bfloat16_rn(h.y);
+                }
+            });
+            if (p.pair) {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (i < n) {
+                        p.pair[pair + 2 * N * i] = __float2bfloat16_rn(a[i]);
+                        p.pair[pair + 2 * N * i + N] = __float2bfloat16_rn(u[i]);
+                    }
             }
+        } else if constexpr (EPI == DACT) {
+            float g[V], up[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                g[i] = up[i] = 0.0f;
+                if (i < n) {
+                    g[i] = __bfloat162float(p.in[pair + 2 * N * i]);
+                    up[i] = __bfloat162float(p.in[pair + 2 * N * i + N]);
+                }
+            }
+            with_activation(p.act, [&](auto k) {
+#pragma unroll
+                for (int i = 0; i < V; i += 2) {
+                    const float2 dh = make_float2(a[i], a[i + 1]), up2 = make_float2(up[i], up[i + 1]);
+                    float2 slope;
+                    const float2 act = activate<k.value>(make_float2(g[i], g[i + 1]), slope);
+                    const float2 h = mul2(act, up2), dg = mul2(mul2(dh, up2), slope), du = mul2(dh, act);
+                    if (i < n) {
+                        p.out[at + N * i] = __float2bfloat16_rn(h.x);
+                        p.pair[pair + 2 * N * i] = __float2bfloat16_rn(dg.x);
+                        p.pair[pair + 2 * N * i + N] = __float2bfloat16_rn(du.x);
+                    }
+                    if (i + 1 < n) {
+                        p.out[at + N * i + N] = __float2bfloat16_rn(h.y);
+                        p.pair[pair + 2 * N * i + 2 * N] = __float2bfloat16_rn(dg.y);
+                        p.pair[pair + 2 * N * i + 3 * N] = __float2bfloat16_rn(du.y);
+                    }
+                }
+            });
         } else {
-            p.out[at] = __float2bfloat16_rn(p.add ? a + __bfloat162float(p.add[at]) : a);
+            float in[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) in[i] = p.in && i < n ? __bfloat162float(p.in[at + N * i]) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i < n) p.out[at + N * i] = __float2bfloat16_rn(p.in ? a[i] + in[i] : a[i]);
         }
     };
     if (p.split == 1) {
         grid_dependency_wait();  // before plain loads and stores of this thread
         for (int c = 0; c < p.tokens; c += 16) {
             if (t0 + c >= p.T) break;
-            uint32_t a[16], u[16];
-            tmem_ld_32x32b_x16(tbase + c, a);
-            if (GATE) tmem_ld_32x32b_x16(tbase + p.tokens + c, u);
+            uint32_t v[PARTS][16];
+            tmem_ld_32x32b_x16(tbase + c, v[0]);
+            if (GATE) tmem_ld_32x32b_x16(tbase + p.tokens + c, v[PARTS - 1]);
             tmem_ld_wait();
+            float sum[PARTS][16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) store(t0 + c + i, __uint_as_float(a[i]), GATE ? __uint_as_float(u[i]) : 0.0f);
+            for (int i = 0; i < 16; ++i) sum[0][i] = __uint_as_float(v[0][i]), sum[PARTS - 1][i] = __uint_as_float(v[PARTS - 1][i]);
+            store(t0 + c, std::integral_constant<int, 16>{}, sum[0], sum[PARTS - 1]);
         }
     } else {
         // The partial sums that this CTA gets, over its ring: of each CTA and part (gate,
         // up) a row of its share of the tokens, in groups of V that the lanes of
         // a warp write and read side by side.
-        constexpr int PARTS = GATE ? 2 : 1;
         const int share = p.tokens / p.split;
         auto exchange = [&](auto vector) {
             using Vec = decltype(vector);
@@ -841,8 +913,7 @@ __global__ void __launch_bounds__(FEW_THREADS) ffn_few_kernel(const __grid_const
 #pragma unroll
                         for (int i = 0; i < V; ++i) v[k][i] += reinterpret_cast<const float *>(&u)[i];
                     }
-#pragma unroll
-                for (int i = 0; i < V; ++i) store(t + i, v[0][i], v[PARTS - 1][i]);
+                store(t, std::integral_constant<int, V>{}, v[0], v[PARTS - 1]);
             }
         };
         if (share % 4 == 0)
@@ -1118,6 +1189,11 @@ cudaError_t gradients(const GradMaps &maps, const Params &p, const GemmLaunch &l
 }
 
 constexpr int FEW_SMEM = 224 * 1024;
+// For da and h, beside the models below, in ns: what a token of a block takes longer in the
+// kernel for few tokens (what it reads and stores besides the sums), and what a launch of
+// pairs takes longer. By them the choice between the two is 0.1 us behind the better one
+// on the mean and 2.4 at most, over 9 sizes at 16 to 1500 tokens.
+constexpr double DACT_TOKEN_NS = 120, DACT_NS = 8000;
 
 // How a product of few tokens is cut: the block of tokens and the split of K of
 // the least time by a model of a CTA's steps, fitted to the times of 12 cuts of 14
@@ -1128,7 +1204,7 @@ constexpr int FEW_SMEM = 224 * 1024;
 struct FewShape {
     int tokens, blocks, rows, split, stages, smem;
     double ns = 1e30;
-    FewShape(int T, int N, int K, bool gate, const GemmLaunch &lc) {
+    FewShape(int T, int N, int K, bool gate, const GemmLaunch &lc, double each = 0) {
         rows = (N + FEW_ROWS - 1) / FEW_ROWS;
         const int slices = gate ? 1 : 2, KB = (K + slices * BK - 1) / (slices * BK);
         for (int most = 16; most <= FEW_MAX_TOKENS; most *= 2) {
@@ -1141,7 +1217,7 @@ struct FewShape {
                 const double rounds = std::ceil(static_cast<double>(rows) * nb / at_once);
                 const double bytes = static_cast<double>((KB + s - 1) / s) * stage;
                 const double t = rounds * (2700 + bytes * std::max(1 / 109.0, at_once * s / 14000) +
-                                           (s == 1 ? 9.0 : 55.0) * nt);
+                                           ((s == 1 ? 9.0 : 55.0) + each / s) * nt);
                 if (t < ns) {
                     ns = t, tokens = nt, blocks = nb, split = s;
                     const int room = (FEW_SMEM / per_sm - 2048) / stage;
@@ -1156,12 +1232,13 @@ struct FewShape {
     }
 };
 
-template <bool GATE>
+template <Epi EPI>
 cudaError_t few(const uint16_t *w, const uint16_t *x, int T, int N, int K, FewParams p,
                 const GemmLaunch &lc, cudaStream_t stream) {
-    const FewShape s(T, N, K, GATE, lc);
+    constexpr bool GATE = EPI == GATED, MN = EPI == DACT || EPI == ADD;
+    const FewShape s(T, N, K, GATE, lc, EPI == DACT ? DACT_TOKEN_NS : 0);
     FewMaps maps;
-    if (!operand(&maps.w, w, GATE ? 2 * static_cast<int64_t>(N) : N, K, false) ||
+    if (!(MN ? operand(&maps.w, w, K, N, true) : operand(&maps.w, w, GATE ? 2 * static_cast<int64_t>(N) : N, K, false)) ||
         !map2d(&maps.x, x, T, K, K, s.tokens, BK, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     p.T = T, p.N = N, p.K = K, p.tokens = s.tokens, p.stages = s.stages, p.split = s.split;
@@ -1176,7 +1253,7 @@ cudaError_t few(const uint16_t *w, const uint16_t *x, int T, int N, int K, FewPa
     cfg.gridDim = dim3(s.rows * s.split, s.blocks), cfg.blockDim = dim3(FEW_THREADS);
     cfg.dynamicSmemBytes = s.smem, cfg.stream = stream;
     cfg.attrs = attr, cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, ffn_few_kernel<GATE>, maps, p);
+    return cudaLaunchKernelEx(&cfg, ffn_few_kernel<EPI>, maps, p);
 }
 
 // How a product of at most 64 tokens is cut without tiles.  K is shared by a cluster
@@ -1223,6 +1300,9 @@ bool prefer_few(int T, int N, int K, bool gate, double few_ns, int pairs) {
     const double last = rest == 0 ? 0 : 2 * rest <= pairs ? 185 + 274 * KB : 370 + 346 * KB;
     return few_ns + 600 < 3200 + rounds * (370 + 346 * KB) + last;
 }
+// A bf16 matrix that a kernel takes as one.
+__nv_bfloat16 *bf16(const uint16_t *t) { return reinterpret_cast<__nv_bfloat16 *>(const_cast<uint16_t *>(t)); }
+
 struct Ways {
     bool tiny = false, few_up = false, few_down = false;
     Ways(int T, int d, int f, const GemmLaunch &lc) {
@@ -1264,8 +1344,9 @@ cudaError_t ffn_setup(GemmLaunch *cfg) {
         return e;
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     cfg->ffn_pairs = pairs;
-    for (const void *k : {reinterpret_cast<const void *>(ffn_few_kernel<true>),
-                          reinterpret_cast<const void *>(ffn_few_kernel<false>)})
+    for (const void *k :
+         {reinterpret_cast<const void *>(ffn_few_kernel<GATED>), reinterpret_cast<const void *>(ffn_few_kernel<PLAIN>),
+          reinterpret_cast<const void *>(ffn_few_kernel<DACT>), reinterpret_cast<const void *>(ffn_few_kernel<ADD>)})
         if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM)) != cudaSuccess ||
             (e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, 100)) != cudaSuccess)
             return e;
@@ -1277,7 +1358,7 @@ cudaError_t ffn_setup(GemmLaunch *cfg) {
         cudaLaunchConfig_t c = {};
         c.gridDim = dim3(1 << i), c.blockDim = dim3(FEW_THREADS), c.dynamicSmemBytes = FEW_SMEM;
         c.attrs = &attr, c.numAttrs = 1;
-        if ((e = cudaOccupancyMaxActiveClusters(&cfg->few_clusters[i], ffn_few_kernel<true>, &c)) != cudaSuccess) return e;
+        if ((e = cudaOccupancyMaxActiveClusters(&cfg->few_clusters[i], ffn_few_kernel<GATED>, &c)) != cudaSuccess) return e;
     }
     return cfg->few_clusters[0] < 1 ? cudaErrorInvalidConfiguration : cudaSuccess;
 }
@@ -1286,7 +1367,6 @@ cudaError_t launch_ffn(const FfnArgs &a, const GemmLaunch &lc, cudaStream_t stre
     using namespace ff;
     const Ways way(a.T, a.d, a.f, lc);
     const int64_t f = a.f;
-    const auto bf16 = [](auto *t) { return reinterpret_cast<__nv_bfloat16 *>(const_cast<uint16_t *>(t)); };
     FewParams fp = {};
     fp.act = a.act, fp.status = a.status, fp.timeout_ns = a.timeout_ns;
     Params p = {};
@@ -1296,8 +1376,8 @@ cudaError_t launch_ffn(const FfnArgs &a, const GemmLaunch &lc, cudaStream_t stre
         const int64_t bytes = std::min<int64_t>(static_cast<int64_t>(a.d) * a.f * 2, AHEAD_BYTES);
         e = tiny<true>({a.W1, a.x, a.T, a.f, a.d, a.act, bf16(a.h), bf16(a.preact), nullptr, {a.W2, bytes}}, lc, stream);
     } else if (way.few_up) {
-        fp.out = bf16(a.h), fp.preact = bf16(a.preact);
-        e = few<true>(a.W1, a.x, a.T, a.f, a.d, fp, lc, stream);
+        fp.out = bf16(a.h), fp.pair = bf16(a.preact);
+        e = few<GATED>(a.W1, a.x, a.T, a.f, a.d, fp, lc, stream);
     } else {
         Maps m = {};
         p.keep = a.preact != nullptr;
@@ -1311,8 +1391,8 @@ cudaError_t launch_ffn(const FfnArgs &a, const GemmLaunch &lc, cudaStream_t stre
     if (way.tiny)
         return tiny<false>({a.W2, a.h, a.T, a.d, a.f, a.act, bf16(a.y), nullptr, bf16(a.add), {}}, lc, stream);
     if (way.few_down) {
-        fp.out = bf16(a.y), fp.preact = nullptr, fp.add = bf16(a.add);
-        return few<false>(a.W2, a.h, a.T, a.d, a.f, fp, lc, stream);
+        fp.out = bf16(a.y), fp.pair = nullptr, fp.in = bf16(a.add);
+        return few<PLAIN>(a.W2, a.h, a.T, a.d, a.f, fp, lc, stream);
     }
     Maps m = {};
     if (!operand(&m.a, a.h, a.T, f, false) || !operand(&m.b, a.W2, a.d, f, false) || !half_operand(&m.half_b, a.W2, a.d, f) ||
@@ -1328,8 +1408,15 @@ cudaError_t launch_ffn_bwd(const FfnGradArgs &a, const GemmLaunch &lc, int *laun
     Params p = {};
     p.act = a.act, p.status = a.status, p.timeout_ns = a.timeout_ns;
     *launches = 0;
+    const bool small = a.T <= 4096;  // (as in Ways)
     // da and h, from dh = dy W2 (W2 read as stored)
-    {
+    if (small && prefer_few(a.T, a.f, a.d, false, FewShape(a.T, a.f, a.d, false, lc, DACT_TOKEN_NS).ns - DACT_NS, lc.ffn_pairs)) {
+        FewParams fp = {};
+        fp.act = a.act, fp.status = a.status, fp.timeout_ns = a.timeout_ns;
+        fp.out = bf16(a.h), fp.pair = bf16(a.da), fp.in = bf16(a.preact);
+        const cudaError_t e = few<DACT>(a.W2, a.dy, a.T, a.f, a.d, fp, lc, stream);
+        if (e != cudaSuccess) return e;
+    } else {
         Maps m = {};
         if (!operand(&m.a, a.dy, a.T, a.d, false) || !operand(&m.b, a.W2, a.d, f, true) ||
             !boxes(&m.in, a.preact, a.T, f, 2 * f) || !boxes(&m.in2, a.preact + f, a.T, f, 2 * f) ||
@@ -1338,8 +1425,8 @@ cudaError_t launch_ffn_bwd(const FfnGradArgs &a, const GemmLaunch &lc, int *laun
             return cudaErrorInvalidValue;
         const cudaError_t e = gemm<DACT, false, true>(m, p, a.T, a.f, a.d, lc, stream);
         if (e != cudaSuccess) return e;
-        ++*launches;
     }
+    ++*launches;
     // The three products of these: one list of tiles, the longest ones first, handed
     // out as pairs fall free, so that one tail is left instead of three.
     GradMaps m = {};
@@ -1353,21 +1440,40 @@ cudaError_t launch_ffn_bwd(const FfnGradArgs &a, const GemmLaunch &lc, int *laun
         if (a.dW1) list[n++] = {KIND_WEIGHTS, 2 * a.f, a.d, a.T, a.da, a.x, a.dW1};
         if (a.dW2) list[n++] = {KIND_WEIGHTS, a.d, a.f, a.T, a.dy, a.h, a.dW2};
     };
-    if (a.T > 2 * a.f) weights();
-    if (a.dx) list[n++] = {KIND_DX, a.T, a.d, 2 * a.f, a.da, a.W1, a.dx};
-    if (a.T <= 2 * a.f) weights();
-    int64_t work = 0;  // slices of all tiles
-    for (int i = 0; i < n; ++i) {
-        const Product q = product(list[i].M, list[i].N, list[i].K, false, 0);
-        work += static_cast<int64_t>(q.tiles) * ((q.K + BK - 1) / BK);
+    // Slices of a product's tile, and of all tiles of the list.
+    const auto slices = [](const Product &q) { return static_cast<int64_t>((q.K + BK - 1) / BK); };
+    int64_t work = 0;
+    double work_ns = 0;
+    const auto count = [&](int M, int N, int K) {
+        const Product q = product(M, N, K, false, 0);
+        work += q.tiles * slices(q);
+        work_ns += q.tiles * std::max(346.0 * slices(q), 1000.0);
+    };
+    if (a.dW1) count(2 * a.f, a.d, a.T);
+    if (a.dW2) count(a.d, a.f, a.T);
+    // dx has the longest tiles, and few of them where tokens and d are few: then it is better
+    // made by the kernel that shares K, behind the others. By a model of both: 346 ns per slice
+    // of a tile and 1000 at least, 274 per slice for the one that ends last, and 500 for
+    // the launch. us in the list and apart: 200 tokens of d = 256, f = 8192 91 and 34,
+    // d = 1024, f = 4096 58 and 41; d = 4096, f = 1536 51 and 59.
+    bool few_dx = false;
+    if (a.dx) {
+        const double others = work_ns / lc.ffn_pairs;
+        count(a.T, a.d, 2 * a.f);
+        const double KB = (2 * a.f + BK - 1) / BK, listed = std::max(work_ns / lc.ffn_pairs, 274 * KB);
+        few_dx = small && others + FewShape(a.T, a.d, 2 * a.f, false, lc).ns + 500 < listed;
+        if (few_dx) work -= product(a.T, a.d, 2 * a.f, false, 0).tiles * static_cast<int64_t>(KB);
     }
+    if (a.T > 2 * a.f) weights();
+    if (a.dx && !few_dx) list[n++] = {KIND_DX, a.T, a.d, 2 * a.f, a.da, a.W1, a.dx};
+    if (a.T <= 2 * a.f) weights();
     p.add = a.add != nullptr, p.products = n;
     for (int i = 0; i < n; ++i) {
         const auto &l = list[i];
         const bool dx = l.kind == KIND_DX;
         Product q = product(l.M, l.N, l.K, false, p.tiles);
         // tiles that take longer than a pair's share of all work are halved
-        if (static_cast<int64_t>((q.K + BK - 1) / BK) * lc.ffn_pairs > work) cut(&q, 0);
+        if (slices(q) * lc.ffn_pairs > work) cut(&q, 0);
         p.product[i] = q, p.kind[i] = l.kind, p.tiles += q.tiles;
         // the weights' gradients sum over the tokens, the rows of both operands; dx over W1's rows
         const int64_t K = l.K;
@@ -1380,9 +1486,18 @@ cudaError_t launch_ffn_bwd(const FfnGradArgs &a, const GemmLaunch &lc, int *laun
             return cudaErrorInvalidValue;
     }
     if (a.add && !boxes(&m.in, a.add, a.T, a.d, a.d)) return cudaErrorInvalidValue;
-    p.tickets = p.tiles > lc.ffn_pairs ? gemm_tickets(lc, stream) : nullptr;
+    if (n > 0) {
+        p.tickets = p.tiles > lc.ffn_pairs ? gemm_tickets(lc, stream) : nullptr;
+        const cudaError_t e = a.weights_f32 ? gradients<float>(m, p, lc, stream) : gradients<uint16_t>(m, p, lc, stream);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+    }
+    if (!few_dx) return cudaSuccess;
     ++*launches;
-    return a.weights_f32 ? gradients<float>(m, p, lc, stream) : gradients<uint16_t>(m, p, lc, stream);
+    FewParams fp = {};
+    fp.status = a.status, fp.timeout_ns = a.timeout_ns;
+    fp.out = bf16(a.dx), fp.in = bf16(a.add);
+    return few<ADD>(a.W1, a.da, a.T, a.d, 2 * a.f, fp, lc, stream);
 }
 
 }  // namespace moe

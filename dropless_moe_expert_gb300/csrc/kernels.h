@@ -246,7 +246,7 @@ struct FfnArgs {
     uint64_t timeout_ns;
 };
 // Its gradients, dx, dW1 and dW2 nullable (not computed); add (which may be
-// dx) is nullable; da [T, 2f] and h [T, f] are scratch.  Two launches, counted.
+// dx) is nullable; da [T, 2f] and h [T, f] are scratch.  Two or three launches, counted.
 struct FfnGradArgs {
     const uint16_t *x, *preact, *dy, *W1, *W2, *add;
     int act, T, d, f;

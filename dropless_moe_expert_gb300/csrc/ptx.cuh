@@ -130,6 +130,10 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
 __device__ __forceinline__ void l2_prefetch(const void *src, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
+// The same for the line that holds an address, without the copy engine.
+__device__ __forceinline__ void l2_prefetch_line(const void *src) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(src) : "memory");
+}
 
 // 16-byte asynchronous copy global -> shared (both 16-byte aligned), through
 // L2 only (.cg).
@@ -156,6 +160,9 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
+// The same for all memory that this thread has seen written: its later copies
+// (and MMAs) read it.
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 // L2 policy that marks lines first in line for eviction.
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
     uint64_t pol;

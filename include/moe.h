@@ -277,8 +277,9 @@ moe_status_t moe_gated_ffn(const uint16_t *x, const uint16_t *W1, const uint16_t
  * else they are apart; none of the three overlaps another one or x (with dW1),
  * dy (with dW2) or W1 (with dx).  dh is not rounded, da and h to bf16 once
  * each, as operands.  `workspace` (16-byte aligned) holds
- * moe_gated_ffn_backward_workspace_size(T, d, f) bytes.  Deterministic.
- * 2 kernel launches. */
+ * moe_gated_ffn_backward_workspace_size(T, d, f) bytes.  Deterministic (the
+ * order of dx's sums is another one for other sizes, and may be where not all
+ * three are wanted).  2 or 3 kernel launches. */
 size_t moe_gated_ffn_backward_workspace_size(int T, int d, int f);
 moe_status_t moe_gated_ffn_backward(const uint16_t *x, const uint16_t *preact, const uint16_t *dy, const uint16_t *W1,
                                     const uint16_t *W2, const uint16_t *add, int act, int T, int d, int f, uint16_t *dx,

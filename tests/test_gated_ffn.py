@@ -163,6 +163,40 @@ def test_backward(c):
     assert moe.device_status() == 0
 
 
+# what the sizes choose between: da and h, and dx, each with K shared or in large tiles
+FEW = [(2, 64, 4096, "gelu"), (17, 1032, 520, "relu"), (100, 256, 2048, "silu"), (130, 96, 3000, "gelu_tanh"),
+       (300, 264, 2504, "silu"), (333, 2000, 96, "gelu"), (777, 256, 4096, "silu"), (1030, 1032, 520, "gelu")]
+
+
+@pytest.mark.parametrize("c", FEW, ids=str)
+def test_backward_of_few_tokens_or_columns(c):
+    test_backward(c)
+
+
+@pytest.mark.parametrize("c", [FEW[1], FEW[3], FEW[5], FEW[6]], ids=str)
+def test_few_tokens_or_columns_around_and_behind_other_work(c):
+    test_what_lies_around_the_outputs_stays(c)
+    test_inputs_written_just_before(c)
+    test_streams_graphs_and_repeated_calls(c)
+
+
+@pytest.mark.parametrize("wanted", ["dx", "dW1", "dW2", "dx dW1", "dx dW2", "dW1 dW2"])
+@pytest.mark.parametrize("c", [FEW[2], FEW[6]], ids=str)
+def test_only_some_of_the_gradients_of_few_tokens(c, wanted):
+    """Each within the roundings of the one beside all three: dx may be summed in another order."""
+    T, d, f, act = c
+    x, W1, W2, dy, _ = _case(c, 1)
+    pre = torch.empty(T, 2 * f, dtype=BF16, device="cuda")
+    moe.gated_ffn(x, W1, W2, act, preact=pre)
+    full = moe.gated_ffn_backward(x, pre, dy, W1, W2, act)
+    empty = moe.GatedFFNGrads.empty(T, d, f)
+    some = moe.GatedFFNGrads(*(getattr(empty, n) if n in wanted.split() else None for n in ("dx", "dW1", "dW2")))
+    moe.gated_ffn_backward(x, pre, dy, W1, W2, act, out=some)
+    for n in wanted.split():
+        a, b = getattr(some, n), getattr(full, n)
+        assert torch.equal(a, b) if n != "dx" else rel_l2(to_np(a), to_np(b).astype(np.float64)) <= HALF, n
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("T", [3, 700])
 def test_large_and_special_pre_activations(act, T):
