@@ -6,16 +6,19 @@
 // are operands of the next product; dh and, in the forward, a are not rounded
 // before the activation.  Backward reads a as the forward stored it.
 //
-// One persistent kernel makes all five products, on CTA pairs: a 256 x 256
-// tile of the result per pair through cta_group::2 MMAs, each CTA loading its
+// Three kernels make the five products; which one, goes by models of their times at the
+// sizes (Ways, prefer_few, launch_ffn_bwd): ffn_tiny_kernel and ffn_few_kernel for few tokens,
+// below, and for the rest one persistent kernel on CTA pairs: a 256 x 256 tile (or
+// half of one, where tiles are few) of the result per pair through cta_group::2 MMAs, each CTA loading its
 // 128 rows of A and half of the columns of B per 64-wide slice of K (32 KB),
 // two accumulators in TMEM so that a tile's epilogue runs beside the next
 // tile's products.  The sizes are known on the host, so tensor maps cut every
 // matrix to its own size: loads past it read zeros, stores past it do nothing,
 // and no size has to fill a tile.
 //   epilogue GATED   h (and a) from a tile whose B rows are 128 gate and 128 up rows
-//            PLAIN   the product, plus a matrix (ADD); fp32 for weight gradients on request
+//            PLAIN   the product, plus a matrix (ADD)
 //            DACT    da and h from the tile of dh and the tiles of g and u
+//            GRADS   dx, dW1 and dW2 from one list of tiles; the weights' in fp32 on request
 // Warps: 0 TMA loads, 1 MMAs and TMEM, the others epilogue.  Every wait is bounded.
 #include <algorithm>
 #include <cmath>
@@ -1155,13 +1158,14 @@ cudaError_t set_up(int *pairs) {
     return cudaSuccess;
 }
 
-// The tiles of a product that the list goes on with; those from the `whole`-th on are cut in two.
+// The tiles of a product that the list goes on with.
 Product product(int M, int N, int K, bool gate, int first) {
     const int n = gate ? TILE_N / 2 : TILE_N;
     Product q{M, N, K, (M + TILE_M - 1) / TILE_M, (N + n - 1) / n, 0, first, 0};
     q.halves = q.tiles = q.MT * q.NT;
     return q;
 }
+// Those from the `whole`-th on in two halves each.
 void cut(Product *q, int whole) {
     q->tiles = 2 * q->tiles - whole;
     q->halves = whole;

@@ -582,6 +582,15 @@ moe_status_t moe_gated_ffn(const uint16_t *x, const uint16_t *W1, const uint16_t
     if (st != MOE_OK) return st;
     if (!same_or_apart(y, add, static_cast<size_t>(T) * d * 2)) return MOE_ERR_INVALID_ARG;
     if (workspace_bytes < ffn_bytes(T, f)) return MOE_ERR_WORKSPACE;
+    // preact and h are written beside x and W1 and read beside y, W2 and add
+    const size_t rows = static_cast<size_t>(T) * d * 2, h = static_cast<size_t>(T) * f * 2, w2 = static_cast<size_t>(d) * f * 2;
+    const struct {
+        const void *p;
+        size_t n;
+    } with_h[] = {{x, rows}, {W1, 2 * w2}, {W2, w2}, {y, rows}, {add, rows}};
+    for (const auto &o : with_h)
+        if (!apart(workspace, h, o.p, o.n) || !apart(preact, 2 * h, o.p, o.n)) return MOE_ERR_INVALID_ARG;
+    if (!apart(workspace, h, preact, 2 * h) || !apart(y, rows, W2, w2)) return MOE_ERR_INVALID_ARG;
     DeviceState *ds = nullptr;
     if ((st = device_state(&ds)) != MOE_OK) return st;
     const moe::FfnArgs a{x, W1, W2, add, act, T, d, f, y, static_cast<uint16_t *>(workspace), preact, ds->status,
@@ -610,15 +619,24 @@ moe_status_t moe_gated_ffn_backward(const uint16_t *x, const uint16_t *preact, c
     const size_t rows = static_cast<size_t>(T) * d * 2;
     if (!same_or_apart(dx, add, rows)) return MOE_ERR_INVALID_ARG;
     if (workspace_bytes < 3 * ffn_bytes(T, f)) return MOE_ERR_WORKSPACE;
-    // the gradients are written beside one another, from x (dW1), dy (dW2) and W1 (dx)
+    // the gradients are written beside one another, from x (dW1), dy (dW2), W1 and add (dx), and
+    // all from the workspace, which is made from the rest
     const size_t weights = static_cast<size_t>(d) * f * (weights_fp32 ? 4 : 2), w1 = 2 * weights;
     const uint16_t *xr = dW1 ? x : nullptr, *dyr = dW2 ? dy : nullptr, *Wr = dx ? W1 : nullptr;
     const size_t Wn = static_cast<size_t>(d) * f * 4;
     if (!apart(dx, rows, xr, rows) || !apart(dx, rows, dyr, rows) || !apart(dW1, w1, xr, rows) ||
         !apart(dW1, w1, dyr, rows) || !apart(dW2, weights, xr, rows) || !apart(dW2, weights, dyr, rows) ||
         !apart(dx, rows, Wr, Wn) || !apart(dW1, w1, Wr, Wn) || !apart(dW2, weights, Wr, Wn) ||
-        !apart(dx, rows, dW1, w1) || !apart(dx, rows, dW2, weights) || !apart(dW1, w1, dW2, weights))
+        !apart(dx, rows, dW1, w1) || !apart(dx, rows, dW2, weights) || !apart(dW1, w1, dW2, weights) ||
+        !apart(dW1, w1, add, rows) || !apart(dW2, weights, add, rows))
         return MOE_ERR_INVALID_ARG;
+    const struct {
+        const void *p;
+        size_t n;
+    } with_da[] = {{xr, rows},     {preact, static_cast<size_t>(T) * f * 4}, {dy, rows}, {Wr, Wn},
+                   {W2, Wn / 2}, {add, rows}, {dx, rows}, {dW1, w1}, {dW2, weights}};
+    for (const auto &o : with_da)
+        if (!apart(workspace, 3 * ffn_bytes(T, f), o.p, o.n)) return MOE_ERR_INVALID_ARG;
     DeviceState *ds = nullptr;
     if ((st = device_state(&ds)) != MOE_OK) return st;
     uint16_t *da = static_cast<uint16_t *>(workspace);

@@ -262,7 +262,9 @@ moe_status_t moe_norm_residual_dropout_backward(const void *r_out, int residual_
  * once, as the second product's operand, y once after add.  preact [T, 2f] bf16
  * (nullable) receives [g | u], which the backward needs.  `workspace` (16-byte
  * aligned, moe_gated_ffn_workspace_size(T, d, f) bytes) holds h.  d and f
- * multiples of 8.  Sums have a fixed order: deterministic.  2 kernel launches. */
+ * multiples of 8.  preact and the workspace are apart from each other and from
+ * the rest, y from W2 (it may be x).  Sums have a fixed order: deterministic.
+ * 2 kernel launches. */
 enum { MOE_ACT_SILU = 0, MOE_ACT_GELU = 1, MOE_ACT_GELU_TANH = 2, MOE_ACT_RELU = 3 };
 size_t moe_gated_ffn_workspace_size(int T, int d, int f);
 moe_status_t moe_gated_ffn(const uint16_t *x, const uint16_t *W1, const uint16_t *W2, const uint16_t *add, int act,
@@ -275,7 +277,7 @@ moe_status_t moe_gated_ffn(const uint16_t *x, const uint16_t *W1, const uint16_t
  * or fp32 (1).  Each of the three is NULL where it is not wanted (then W1, or
  * x, may be NULL too).  add [T, d] bf16 (nullable, with dx) may be dx itself,
  * else they are apart; none of the three overlaps another one or x (with dW1),
- * dy (with dW2) or W1 (with dx).  dh is not rounded, da and h to bf16 once
+ * dy (with dW2), W1 (with dx) or, but for dx, add; the workspace nothing.  dh is not rounded, da and h to bf16 once
  * each, as operands.  `workspace` (16-byte aligned) holds
  * moe_gated_ffn_backward_workspace_size(T, d, f) bytes.  Deterministic (the
  * order of dx's sums is another one for other sizes, and may be where not all

@@ -61,6 +61,22 @@ def test_feed_forward_refusals(moe):
         assert moe.lib.moe_gated_ffn_backward_workspace_size(*size) == 0
 
 
+def test_what_is_written_beside_what_is_read(moe):
+    """4 tokens of 64 x 72: rows of 512 bytes in all, preact 1152, h 576, W1 18432, W2 9216."""
+    at = {k: FAKE + (i << 20) for i, k in enumerate(("x", "W1", "W2", "y", "pre", "ws", "add"))}
+    for a, b in ([("pre", k) for k in ("x", "W1", "W2", "y", "ws", "add")] + [("ws", k) for k in ("x", "W1", "W2", "y", "add")] +
+                 [("y", "W2")]):
+        for shift in (0, 16, 496):
+            assert _ffn(moe, **{**at, a: at[b] + shift}) == 1, (a, b, shift)
+            assert _ffn(moe, **{**at, b: at[a] + shift}) == 1, (a, b, shift)
+    assert _ffn(moe, **{**at, "y": at["W2"] + 9200}) == 1 and _ffn(moe, **{**at, "pre": at["W1"] + 18416}) == 1
+    at = {k: FAKE + (i << 20) for i, k in enumerate(("x", "pre", "dy", "W1", "W2", "add", "dx", "dW1", "dW2", "ws"))}
+    for a, b in [("ws", k) for k in at if k != "ws"] + [("dW1", "add"), ("dW2", "add")]:
+        for shift in (0, 16, 496):
+            assert _bwd(moe, **{**at, a: at[b] + shift}) == 1, (a, b, shift)
+            assert _bwd(moe, **{**at, b: at[a] + shift}) == 1, (a, b, shift)
+
+
 def test_dropout_refusals(moe):
     def fwd(**kw):
         p = {**dict(r=FAKE, f32=0, y=FAKE, gp=None, gate=None, kind=0, a=1.0, gq=None, eps=1e-6, p=0.1, rng=FAKE, T=4,
