@@ -44,7 +44,8 @@ constexpr int BAND = 8;         // row blocks that sweep the column blocks toget
 // Epilogue warps: of GATED eight, two per lane quarter with half of a tile's columns
 // each, as the last tile's epilogue is waited for (1003 x 2056 x 1368: 30.9 us with
 // four, 30.0); DACT's buffers would leave eight a shorter ring (its backward 64
-// and 66.5 us, 4096 x 7168 x 2048 400 and 411).
+// and 66.5 us, 4096 x 7168 x 2048 400 and 411), or no input ahead (level: two warps per
+// scheduler then take twice as long for a chunk).
 __host__ __device__ constexpr int epi_warps(Epi epi) { return epi == GATED ? 8 : 4; }
 __host__ __device__ constexpr int threads_of(Epi epi) { return 64 + 32 * epi_warps(epi); }
 constexpr int BOX = 64 * 64 * 2;  // an MN-major box: 64 rows of K x 64 columns
@@ -53,17 +54,19 @@ constexpr int CHUNK = 32;         // the epilogue takes 32 rows x 32 columns per
 constexpr int BUF = CHUNK * CHUNK * 2;
 
 // An epilogue warp's buffers in shared memory.  A chunk without inputs takes
-// one of two boxes in turn.  One with inputs takes one of `sets` of `boxes`
-// boxes, of which TMA fills the first `in` before it is computed.
+// one of two boxes in turn.  TMA fills the `in` boxes of one of `sets` sets before a chunk
+// with inputs is computed; the output takes their place, but for DACT, whose three outputs
+// have boxes of their own: a chunk's inputs can so be asked for two chunks ahead, and
+// none waits for stores (a chunk 1.6 us with outputs over inputs, 1.2).
 struct Buffers {
-    int sets, boxes, in, bytes;
+    int sets, in, bytes;
 };
 template <Epi EPI, typename Out>
 __host__ __device__ constexpr Buffers buffers() {
     constexpr int plain = 2 * CHUNK * CHUNK * static_cast<int>(sizeof(Out));
-    return EPI == DACT                  ? Buffers{2, 3, 2, 2 * 3 * BUF}
-           : EPI == ADD || EPI == GRADS ? Buffers{3, 1, 1, 3 * BUF > plain ? 3 * BUF : plain}
-                                        : Buffers{2, 1, 0, plain};
+    return EPI == DACT                  ? Buffers{2, 2, (2 * 2 + 3) * BUF}
+           : EPI == ADD || EPI == GRADS ? Buffers{3, 1, 3 * BUF > plain ? 3 * BUF : plain}
+                                        : Buffers{2, 0, plain};
 }
 
 template <Epi EPI, typename Out>
@@ -199,13 +202,15 @@ struct Warp {
         ++boxes;
     }
 
-    // Asks for the inputs of the next chunk.  FIRST: of a tile, whose buffers may be in other use.
+    // Asks for the inputs of the next chunk.  FIRST: of a tile, whose buffers may be in other
+    // use.  (DACT: the set's inputs have been read.)
     template <bool FIRST>
     __device__ __forceinline__ void ask(const CUtensorMap *in, const CUtensorMap *in2, int col, int row) {
         if (lane == 0) {
             const int set = asked % L::B.sets;
-            uint8_t *box = bufs + set * L::B.boxes * BUF;
-            bulk_wait_read<FIRST ? 0 : L::B.sets - 2>();  // the stores of the chunk that used the set have read it
+            uint8_t *box = bufs + set * L::B.in * BUF;
+            // the store of the chunk that used the set has read it
+            if (EPI != DACT) bulk_wait_read<FIRST ? 0 : L::B.sets - 2>();
             mbar_arrive_expect_tx(&landed[set], L::B.in * BUF);
             tma_load_2d(box, in, &landed[set], col, row);
             if (EPI == DACT) tma_load_2d(box + BUF, in2, &landed[set], col, row);
@@ -272,21 +277,25 @@ struct Warp {
         }
     }
 
-    // A chunk's inputs are on their way while the one before it is computed; the outputs take their place.
+    // A chunk's inputs are on their way while the one (DACT: the two) before it are computed.
     __device__ __forceinline__ bool with_inputs(const CUtensorMap *in, const CUtensorMap *in2, const CUtensorMap *out,
                                                 const CUtensorMap *out2, const CUtensorMap *out3, const Product &q,
                                                 const Tile &t, uint32_t tbase, int row) {
 #pragma unroll 1
         for (int c = begin(t.width); c < end(t.width) && t.n0 + c < q.N; c += CHUNK) {
             const int col = t.n0 + c;
-            if (c + CHUNK < end(t.width) && col + CHUNK < q.N) ask<false>(in, in2, col + CHUNK, row);
+            const auto ask_for = [&](int chunks) {  // the inputs that lie so many on
+                if (c + chunks * CHUNK < end(t.width) && col + chunks * CHUNK < q.N)
+                    ask<false>(in, in2, col + chunks * CHUNK, row);
+            };
+            if (EPI != DACT) ask_for(1);
             uint32_t v[32], e[16];
             tmem_ld_32x32b_x32(tbase + c, v);
             tmem_ld_wait();
             const uint32_t set = taken % L::B.sets;
             if (!mbar_wait(&landed[set], (taken / L::B.sets) & 1, abort, p.status, p.timeout_ns)) return false;
             ++taken;
-            uint8_t *box = bufs + set * L::B.boxes * BUF;
+            uint8_t *box = bufs + set * L::B.in * BUF;
             read_row(box, lane, e);
             if constexpr (EPI != DACT) {
 #pragma unroll
@@ -295,6 +304,8 @@ struct Warp {
             } else {
                 uint32_t u[16], h[16];
                 read_row(box + BUF, lane, u);
+                __syncwarp();  // the whole warp has read them
+                ask_for(2);
                 with_activation(p.act, [&](auto act) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -305,6 +316,9 @@ struct Warp {
                         u[i] = pack(mul2(d, a));
                     }
                 });
+                box = bufs + L::B.sets * L::B.in * BUF;
+                if (lane == 0) bulk_wait_read<0>();  // the last chunk's stores have read the boxes
+                __syncwarp();
                 write_row(box, lane, e);
                 write_row(box + BUF, lane, u);
                 write_row(box + 2 * BUF, lane, h);
@@ -567,10 +581,12 @@ __global__ void __launch_bounds__(threads_of(EPI), 1) ffn_gemm_kernel(const __gr
             const bool inputs = EPI == DACT || EPI == ADD || (MANY && p.add && p.kind[t.product] == KIND_DX);
             if constexpr (L::B.in > 0)
                 if (any && inputs) {
-                    if constexpr (EPI == DACT)
+                    if constexpr (EPI == DACT) {
                         w.template ask<true>(&maps.in, &maps.in2, col, row);
-                    else
+                        if (col + CHUNK < pr.N) w.template ask<true>(&maps.in, &maps.in2, col + CHUNK, row);
+                    } else {
                         w.template ask<true>(&maps.in, nullptr, col, row);
+                    }
                 }
             if (!mbar_wait<true>(&tfull[acc], acc_phase, s_abort, p.status, p.timeout_ns)) break;
             tc_fence_after();
