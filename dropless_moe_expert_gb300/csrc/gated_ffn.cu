@@ -377,19 +377,33 @@ __global__ void __launch_bounds__(threads_of(EPI), 1) ffn_gemm_kernel(const __gr
         for (int i = 0; i < QUEUE; ++i) mbar_init(&queued[i], 1);
         *s_abort = 0;
         fence_mbar_init();
+    } else if (threadIdx.x == 32) {
+        if constexpr (MANY) {
+            for (int i = 0; i < p.products; ++i) {
+                tma_prefetch_desc(&maps.a[i]);
+                tma_prefetch_desc(&maps.b[i]);
+                tma_prefetch_desc(&maps.out[i]);
+            }
+        } else {
+            tma_prefetch_desc(&maps.a);
+            tma_prefetch_desc(&maps.b);
+            tma_prefetch_desc(&maps.out);
+        }
     }
-    __syncthreads();
     // both CTAs' barriers exist before anything crosses the pair, and before
-    // the collective allocation
+    // the collective allocation, which the loads need not wait for
     cluster_sync();
-    if (warp == 1) {
-        tmem_alloc_pair(s_tmem, 2 * TILE_N);
-        tmem_relinquish_pair();
+    uint32_t tmem_base = 0;
+    if (warp != 0) {
+        if (warp == 1) {
+            tmem_alloc_pair(s_tmem, 2 * TILE_N);
+            tmem_relinquish_pair();
+        }
+        tc_fence_before();
+        asm volatile("bar.sync 1, %0;" ::"n"(threads_of(EPI) - 32) : "memory");
+        tc_fence_after();
+        tmem_base = *s_tmem;
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem_base = *s_tmem;
 
     // The k-th tile of the pair (a negative one ends the list) for the roles that do not decide it.
     auto tile_of = [&](int k, int *tile) {
