@@ -421,8 +421,7 @@ __global__ void __launch_bounds__(threads_of(EPI), 1) ffn_gemm_kernel(const __gr
     if (warp == 0) {
         if (lane == 0) {
             // (only now may the next kernel start: it goes by what was written before this one)
-            grid_dependency_wait();
-            fence_proxy_async();  // its plain stores before these copies
+            grid_dependency_wait_to_copy();
             grid_dependency_launch();
             const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);  // both CTAs' copies signal CTA 0's barriers
             const uint32_t queue1 = mapa_shared(smem_u32(const_cast<int *>(queue)), 1);
@@ -582,8 +581,7 @@ __global__ void __launch_bounds__(threads_of(EPI), 1) ffn_gemm_kernel(const __gr
                          half + 32 * q, (warp - 2) >> 2};
         const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
         uint32_t acc = 0, acc_phase = 0;
-        grid_dependency_wait();  // its loads and stores are behind the kernel before, too
-        fence_proxy_async();
+        grid_dependency_wait_to_copy();  // its loads and stores are behind the kernel before, too
         for (int k = 0;; ++k) {
             int tile;
             if (!tile_of(k, &tile) || tile < 0) break;
@@ -752,13 +750,10 @@ __global__ void __launch_bounds__(FEW_THREADS) ffn_few_kernel(const __grid_const
         };
         // the weights do not wait for the kernel before, where that is one of this operator's
         constexpr bool FIRST = EPI == GATED || EPI == DACT;
-        if (FIRST) grid_dependency_wait();
+        if (FIRST) grid_dependency_wait_to_copy();
         const int first = min(kbs, p.stages);
         for (int i = 0; i < first; ++i) weights(i, i);
-        if (!FIRST) {
-            grid_dependency_wait();
-            fence_proxy_async();  // its plain stores before these copies
-        }
+        if (!FIRST) grid_dependency_wait_to_copy();
         grid_dependency_launch();
         for (int i = 0; i < first; ++i) activations(i, i);
         int stage = 0;

@@ -163,6 +163,13 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 // The same for all memory that this thread has seen written: its later copies
 // (and MMAs) read it.
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+// grid_dependency_wait() for a thread whose bulk or tensor copies read what the
+// kernels before wrote: they may have written it by plain stores, and behind a
+// kernel that let this one start early no kernel boundary orders those before copies.
+__device__ __forceinline__ void grid_dependency_wait_to_copy() {
+    grid_dependency_wait();
+    fence_proxy_async();
+}
 // L2 policy that marks lines first in line for eviction.
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
     uint64_t pol;

@@ -1,0 +1,62 @@
+"""Kernels that start before the one in front of them has ended, on what that one
+wrote by plain stores and these read by bulk or tensor copies: the same bits as
+with a synchronize between the calls."""
+import pytest
+import torch
+
+import dropless_moe_expert_gb300 as moe
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+def _normal(*shape, seed, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return scale * torch.randn(*shape, generator=g, device="cuda")
+
+
+def _weights(d, f, seed):
+    return _normal(2 * f, d, seed=seed, scale=d ** -0.5).to(BF16), _normal(d, f, seed=seed + 1, scale=f ** -0.5).to(BF16)
+
+
+def _bits(step, n=20):
+    """step(between) calls between() after each of its calls: nothing, or a synchronize."""
+    want = [t.clone() for t in step(torch.cuda.synchronize)]
+    torch.cuda.synchronize()
+    for _ in range(n):
+        for a, b in zip(step(lambda: None), want):
+            assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(lambda: None)
+    for _ in range(n):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert moe.device_status() == 0
+
+
+# T, d, f: both layers without tiles, with K shared, either behind the other, and CTA pairs behind both
+@pytest.mark.parametrize("T,d,f", [(1, 1024, 512), (48, 4096, 1536), (64, 512, 4096), (100, 1416, 520), (129, 328, 776),
+                                   (300, 1024, 2048), (700, 512, 640)])
+def test_feed_forwards_in_a_row(T, d, f):
+    """y of one layer is x of the next; and back, where dx of one is dy of the other."""
+    x, dy = _normal(T, d, seed=0).to(BF16), _normal(T, d, seed=1).to(BF16)
+    layers = [moe.GatedFFN(*_weights(d, n, seed), act, T_max=T)
+              for n, act, seed in ((f, "silu", 2), (f, "gelu", 4), (f + 128, "gelu_tanh", 6))]
+
+    def step(between):
+        xs, g = [x], dy
+        for layer in layers:
+            xs.append(layer(xs[-1], save_preact=True))
+            between()
+        out = [*xs[1:]]
+        for layer, a in zip(reversed(layers), reversed(xs[:-1])):
+            d_ = layer.backward(a, g)
+            between()
+            g = d_["dx"]
+            out += [g, d_["dW1"], d_["dW2"]]
+        return out
+
+    _bits(step)
