@@ -257,7 +257,7 @@ norm_residual_kernel(Args a, float inv_d, const R *r, R *r_out, uint16_t *__rest
     const int stage = warps * PART;
     uint8_t *const mine = ring + warp * PART;
     float2 c[VPT][4], w[VPT][4];
-    grid_dependency_wait();  // launched early
+    grid_dependency_wait_to_copy();  // launched early
     if (HOLD) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) weights(a, own.col + 256 * j, own.on[j], c[j], w[j]);
@@ -416,7 +416,7 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
     const int stage = warps * PART;
     uint8_t *const mine = ring + team * stages * stage + warp * PART;
     float2 c[VPT][4], w[VPT][4], accq[VPT][4], accp[VPT][4];
-    grid_dependency_wait();  // launched early
+    grid_dependency_wait_to_copy();  // launched early
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         weights(a, own.col + 256 * j, own.on[j], c[j], w[j]);

@@ -60,3 +60,40 @@ def test_feed_forwards_in_a_row(T, d, f):
         return out
 
     _bits(step)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, BF16])
+@pytest.mark.parametrize("T,d,f", [(1, 1024, 512), (16, 4096, 512), (48, 2048, 768), (129, 2624, 776), (700, 512, 640)])
+def test_norms_between_feed_forwards(T, d, f, dt):
+    """Norms read by bulk copies what a layer, or the norm before them, has just written, and the other way round."""
+    r0, dr = _normal(T, d, seed=0).to(dt), _normal(T, d, seed=1).to(dt)
+    gammas = [1 + _normal(d, seed=10 + k, scale=0.1) for k in range(3)]
+    layers = [moe.GatedFFN(*_weights(d, f, 2 * k), T_max=T) for k in range(2)]
+    rng = torch.tensor([4, 2], device="cuda")
+
+    def step(between):
+        def do(call, *a, **kw):
+            out = call(*a, **kw)
+            between()
+            return out
+
+        n = do(moe.norm_residual, r0, gamma_pre=gammas[0])
+        rows, out = [], []
+        for k, layer in enumerate(layers):
+            y = do(layer, n.n, save_preact=True)
+            drop = dict(dropout=0.2, rng=rng) if k else {}
+            m = do(moe.norm_residual, n.r, y, gamma_post=gammas[1], gamma_pre=gammas[k + 1], **drop)
+            rows.append((n, y, m, drop))
+            out += [y, m.r, m.n]
+            n = m
+        g, dn = dr, n.n
+        for k in (1, 0):
+            n, y, m, drop = rows[k]
+            h = do(moe.norm_residual_backward, m.r, g, dn, y, gamma_post=gammas[1], gamma_pre=gammas[k + 1],
+                   rstd_post=m.rstd_post, rstd_pre=m.rstd_pre, **drop)
+            w = do(layers[k].backward, n.n, h.dy)
+            g, dn = h.dr, w["dx"]
+            out += [h.dr, h.dy, h.dgamma_pre, h.dgamma_post, w["dx"], w["dW1"], w["dW2"]]
+        return out
+
+    _bits(step)
