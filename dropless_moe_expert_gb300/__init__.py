@@ -201,11 +201,17 @@ def _here(t):
         raise ValueError(f"the tensors are on device {t.get_device()}, the current one is {torch._C._cuda_getDevice()}")
 
 
+def _forms(*tensors):
+    """What a check of tensors goes by besides their addresses (contiguous ones of a shape have one order)."""
+    return [None if t is None else (t.dtype, t.shape, t.is_contiguous()) for t in tensors]
+
+
 class _Buffers:
-    """Output buffers that are checked once.  ``_checked`` is what the last
-    check went by, the tensors' addresses among it; tensors that stand at other
-    addresses (replaced, resized, copied) are checked again.  ``_held`` keeps
-    that memory, so that another tensor cannot come to lie at an old address."""
+    """Buffers that are checked once.  ``_checked`` is what the last check
+    went by: the tensors' addresses, types, shapes and orders; tensors of other
+    ones (replaced, resized, copied, another view of the same memory) are
+    checked again.  ``_held`` keeps that memory, so that another tensor cannot
+    come to lie at an old address."""
     _checked, _held = None, ()
 
     def _hold(self, checked, *tensors):
@@ -348,7 +354,8 @@ class RouteBuffers(_Buffers):
         r, ws = self.routing, self.workspace
         at = (r.topk_idx.data_ptr(), r.topk_w.data_ptr(), r.counts.data_ptr(), r.offsets.data_ptr(),
               r.row_of.data_ptr(), r.src_tok.data_ptr(), ws.data_ptr(), ws.numel())
-        if (self.size, at) != self._checked:
+        checked = (self.size, at, _forms(r.topk_idx, r.topk_w, r.counts, r.offsets, r.row_of, r.src_tok, ws))
+        if checked != self._checked:
             (T, E, K), i32 = self.size, torch.int32
             _need(r.topk_idx, i32, (T, K), "buffers.routing.topk_idx")
             _need(r.topk_w, torch.float32, (T, K), "buffers.routing.topk_w")
@@ -357,7 +364,7 @@ class RouteBuffers(_Buffers):
             _need(r.row_of, i32, (T, K), "buffers.routing.row_of")
             _need(r.src_tok, i32, (T * K,), "buffers.routing.src_tok")
             _need(ws, torch.uint8, (ws.numel(),), "buffers.workspace")
-            self._hold((self.size, at), r.topk_idx, r.topk_w, r.counts, r.offsets, r.row_of, r.src_tok, ws)
+            self._hold(checked, r.topk_idx, r.topk_w, r.counts, r.offsets, r.row_of, r.src_tok, ws)
         return at
 
 
@@ -412,11 +419,14 @@ class NormResidual(_Buffers):
         return cls(make(y, dtype, T, d), make(pre, torch.bfloat16, T, d), make(post, torch.float32, T),
                    make(pre, torch.float32, T), make(rng, torch.int64, 2))
 
-    def _addresses(self, key):
-        """Of the buffers that the call (T, d, dtype, y, post, pre) writes."""
+    def _written(self, key):
+        """The buffers that the call (T, d, dtype, y, post, pre) writes."""
         _, _, _, y, post, pre = key
-        return (_ptr(self.r) if y else None, _ptr(self.n) if pre else None, _ptr(self.rstd_post) if post else None,
-                _ptr(self.rstd_pre) if pre else None)
+        return (self.r if y else None, self.n if pre else None, self.rstd_post if post else None,
+                self.rstd_pre if pre else None)
+
+    def _addresses(self, key):
+        return tuple([None if t is None else t.data_ptr() for t in self._written(key)])
 
     def _pointers(self, key, rng=None, stream=None):
         """The addresses, checked; with dropout also of its state and of where a call leaves it."""
@@ -425,7 +435,8 @@ class NormResidual(_Buffers):
             if self.rng is None:
                 self.rng = _empty((2,), torch.int64, rng, stream)
             at = (*at, rng.data_ptr(), self.rng.data_ptr())
-        if (key, at) != self._checked:
+        checked = (key, at, _forms(*self._written(key), *(() if rng is None else (rng, self.rng))))
+        if checked != self._checked:
             if rng is not None:
                 _rng_in(rng)
                 _need(self.rng, torch.int64, (2,), "out.rng")
@@ -437,7 +448,7 @@ class NormResidual(_Buffers):
                 _need(self.rstd_pre, torch.float32, (T,), "out.rstd_pre")
             if post:
                 _need(self.rstd_post, torch.float32, (T,), "out.rstd_post")
-            self._hold((key, at), self.r, self.n, self.rstd_post, self.rstd_pre, rng, self.rng)
+            self._hold(checked, self.r, self.n, self.rstd_post, self.rstd_pre, rng, self.rng)
         return at
 
 
@@ -462,13 +473,15 @@ class NormResidualGrads(_Buffers):
         return cls(make(True, dtype, T, d), make(y, torch.bfloat16, T, d), make(pre, f32, d), make(post, f32, d),
                    make(gate != "none", f32, *((d,) if gate == "channel" else (T, 1))), make(True, torch.uint8, n))
 
-    def _addresses(self, key):
-        """Of the buffers that the call (T, d, dtype, y, post, pre, gate) writes, and the workspace's bytes."""
+    def _written(self, key):
+        """The buffers that the call (T, d, dtype, y, post, pre, gate) writes."""
         _, _, _, y, post, pre, gate = key
-        ws = self.workspace
-        return (_ptr(self.dr), _ptr(self.dy) if y else None, _ptr(self.dgamma_pre) if pre else None,
-                _ptr(self.dgamma_post) if post else None, _ptr(self.dgate) if gate != "none" else None, ws.data_ptr(),
-                ws.numel())
+        return (self.dr, self.dy if y else None, self.dgamma_pre if pre else None, self.dgamma_post if post else None,
+                self.dgate if gate != "none" else None, self.workspace)
+
+    def _addresses(self, key):
+        """Theirs, and the workspace's bytes."""
+        return (*[None if t is None else t.data_ptr() for t in self._written(key)], self.workspace.numel())
 
     def _pointers(self, key, stream=None, rng=None):
         """The addresses, checked; with dropout also of its state."""
@@ -478,7 +491,8 @@ class NormResidualGrads(_Buffers):
         at = self._addresses(key)
         if rng is not None:
             at = (*at, rng.data_ptr())
-        if (key, at) != self._checked:
+        checked = (key, at, _forms(*self._written(key), rng))
+        if checked != self._checked:
             if rng is not None:
                 _rng_in(rng)
             T, d, dtype, y, post, pre, gate = key
@@ -493,7 +507,7 @@ class NormResidualGrads(_Buffers):
             if gate != "none":
                 _need(self.dgate, torch.float32, (d,) if gate == "channel" else (T, 1), "out.dgate")
             _need(ws, torch.uint8, (ws.numel(),), "out.workspace")
-            self._hold((key, at), self.dr, self.dy, self.dgamma_pre, self.dgamma_post, self.dgate, ws, rng)
+            self._hold(checked, self.dr, self.dy, self.dgamma_pre, self.dgamma_post, self.dgate, ws, rng)
         return at
 
 
@@ -671,10 +685,10 @@ class GatedFFNGrads(_Buffers):
             self.workspace = _empty((n,), torch.uint8, like, stream)
         ws = self.workspace
         at = (_ptr(self.dx), _ptr(self.dW1), _ptr(self.dW2), ws.data_ptr(), ws.numel())
-        kinds = tuple(None if t is None else t.dtype for t in (self.dW1, self.dW2))
-        key = (T, d, f, at, kinds)
-        if key != self._checked:
-            wide = torch.float32 if torch.float32 in kinds else torch.bfloat16
+        f32 = any(t is not None and t.dtype is torch.float32 for t in (self.dW1, self.dW2))
+        checked = (T, d, f, at, _forms(self.dx, self.dW1, self.dW2, ws))
+        if checked != self._checked:
+            wide = torch.float32 if f32 else torch.bfloat16
             if self.dx is not None:
                 _need(self.dx, torch.bfloat16, (T, d), "out.dx")
             if self.dW1 is not None:
@@ -682,8 +696,8 @@ class GatedFFNGrads(_Buffers):
             if self.dW2 is not None:
                 _need(self.dW2, wide, (d, f), "out.dW2")
             _need(ws, torch.uint8, (ws.numel(),), "out.workspace")
-            self._hold(key, self.dx, self.dW1, self.dW2, ws)
-        return (*at[:3], int(torch.float32 in kinds), *at[3:])
+            self._hold(checked, self.dx, self.dW1, self.dW2, ws)
+        return (*at[:3], int(f32), *at[3:])
 
 
 def gated_ffn_backward(x, preact, dy, W1, W2, act: str = "silu", *, add=None, out: GatedFFNGrads | None = None,
@@ -1234,11 +1248,12 @@ class GatedFFN(_Buffers):
     def _pointers(self):
         """Addresses of the weights and of the workspace, and its bytes; checked where they are new."""
         at = (self.W1.data_ptr(), self.W2.data_ptr(), self.workspace.data_ptr(), self.workspace.numel())
-        if at != self._checked:
+        checked = (at, _forms(self.W1, self.W2, self.workspace))
+        if checked != self._checked:
             _need(self.W1, torch.bfloat16, (2 * self.f, self.d), "W1")
             _need(self.W2, torch.bfloat16, (self.d, self.f), "W2")
             _need(self.workspace, torch.uint8, (self.workspace.numel(),), "workspace")
-            self._hold(at, self.W1, self.W2, self.workspace)
+            self._hold(checked, self.W1, self.W2, self.workspace)
         return at
 
     def backward(self, x, dy, grads=None, workspace=None, stream=None, add=None):
