@@ -196,10 +196,13 @@ def _in(t, dtype, shape, name) -> int:
     return _need(t, dtype, shape, name).data_ptr()
 
 
-def _here(t):
-    """The library works on the current device; a tensor of another one is refused."""
-    if t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"the tensors are on device {t.get_device()}, the current one is {torch._C._cuda_getDevice()}")
+def _here(*tensors) -> int:
+    """The current device, on which the library works; tensors of another one are refused (None: not given)."""
+    device = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"a tensor is on device {t.get_device()}, the current one is {device}")
+    return device
 
 
 class _Buffers:
@@ -432,8 +435,9 @@ class NormResidual(_Buffers):
         return (_ptr(self.r) if y else None, _ptr(self.n) if pre else None, _ptr(self.rstd_post) if post else None,
                 _ptr(self.rstd_pre) if pre else None)
 
-    def _pointers(self, key, rng=None, stream=None):
-        """The addresses, checked; with dropout also of its state and of where a call leaves it."""
+    def _pointers(self, key, rng=None, stream=None, device=None):
+        """The addresses, checked; with dropout (then on the current `device`) also of its state and of
+        where a call leaves it."""
         T, d, dtype, y, post, pre = key
         tensors = [self.r] if y else []
         if pre:
@@ -444,12 +448,13 @@ class NormResidual(_Buffers):
             if self.rng is None:
                 self.rng = _empty((2,), torch.int64, rng, stream)
             tensors += (rng, self.rng)
-            key = (*key, "rng")
+            key = (*key, device)
         at = self._same(key, tensors)
         if at is None:
             if rng is not None:
                 _rng_in(rng)
                 _need(self.rng, torch.int64, (2,), "out.rng")
+                _here(*tensors)
             if y:
                 _need(self.r, dtype, (T, d), "out.r")
             if pre:
@@ -491,8 +496,8 @@ class NormResidualGrads(_Buffers):
                 _ptr(self.dgamma_post) if post else None, _ptr(self.dgate) if gate != "none" else None, ws.data_ptr(),
                 ws.numel())
 
-    def _pointers(self, key, stream=None, rng=None):
-        """The addresses, checked; with dropout also of its state."""
+    def _pointers(self, key, stream=None, rng=None, device=None):
+        """The addresses, checked; with dropout (then on the current `device`) also of its state."""
         if self.workspace is None:
             n = int(lib.moe_norm_residual_backward_workspace_size(*key[:2]))
             self.workspace = _empty((n,), torch.uint8, _need(self.dr, key[2], key[:2], "out.dr"), stream)
@@ -509,11 +514,12 @@ class NormResidualGrads(_Buffers):
             tensors.append(self.dgate)
         if rng is not None:
             tensors.append(rng)
-            key = (*key, "rng")
+            key = (*key, device)
         at = self._same(key, tensors)
         if at is None:
             if rng is not None:
                 _rng_in(rng)
+                _here(*tensors)
             _need(self.dr, dtype, (T, d), "out.dr")
             if y:
                 _need(self.dy, torch.bfloat16, (T, d), "out.dy")
@@ -572,10 +578,12 @@ def norm_residual(r, y=None, *, gamma_post=None, gate=None, gamma_pre=None, res_
     0 drops nothing, and rng is not read."""
     T, d, kind, rp, yp, postp, gatep, prep = _norm_args(r, y, gamma_post, gate, gamma_pre)
     key = (T, d, r.dtype, yp is not None, postp is not None, prep is not None)
+    device = None
     if dropout:
-        _here(r)
+        device = _here(r, y, gamma_post, gate, gamma_pre)
         if rng is None or out is None:
             _rng_in(rng)
+            _here(rng)
     else:
         rng = None
     if out is None:
@@ -584,7 +592,7 @@ def norm_residual(r, y=None, *, gamma_post=None, gate=None, gamma_pre=None, res_
         if dropout:
             at = (*at, rng.data_ptr(), out.rng.data_ptr())
     else:
-        at = out._pointers(key, rng, stream)
+        at = out._pointers(key, rng, stream, device)
     if dropout:
         _check(lib.moe_norm_residual_dropout(rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep,
                                              eps, dropout, at[4], T, d, at[0], at[1], at[2], at[3], at[5],
@@ -611,17 +619,19 @@ def norm_residual_backward(r, dr, dn=None, y=None, *, gamma_post=None, gate=None
     rqp = _in(rstd_pre, torch.float32, (T,), "rstd_pre") if prep is not None else None
     rpp = _in(rstd_post, torch.float32, (T,), "rstd_post") if postp is not None else None
     key = (T, d, r.dtype, yp is not None, postp is not None, prep is not None, _GATES[kind])
+    device = None
     if dropout:
-        _here(r)
+        device = _here(r, dr, dn, y, gamma_post, gate, gamma_pre, rstd_post, rstd_pre)
         if rng is None or out is None:
             _rng_in(rng)
+            _here(rng)
     else:
         rng = None
     if out is None:
         out = _on(stream, lambda: NormResidualGrads.empty(*key, r.device))
         at = out._addresses(key)
     else:
-        at = out._pointers(key, stream, rng)[:7]
+        at = out._pointers(key, stream, rng, device)[:7]
     if dropout:
         _check(lib.moe_norm_residual_dropout_backward(
             rp, int(r.dtype is torch.float32), yp, postp, gatep, kind, res_scale, prep, dropout, rng.data_ptr(), rpp, rqp,
@@ -661,10 +671,10 @@ def gated_ffn(x, W1, W2, act: str = "silu", *, add=None, out=None, preact=None, 
     bf16, shape = torch.bfloat16, (T, d)
     xp, ap = _in(x, bf16, shape, "x"), None if add is None else _in(add, bf16, shape, "add")
     pp = None if preact is None else _in(preact, bf16, (T, 2 * f), "preact")
+    _here(x, W1, W2, add, out, preact, workspace)
     if out is None:
         out = _empty(shape, bf16, x, stream)
     yp = _in(out, bf16, shape, "y")
-    _here(x)
     if workspace is None:
         workspace = _empty((int(lib.moe_gated_ffn_workspace_size(T, d, f)),), torch.uint8, x, stream)
     n = workspace.numel()
@@ -693,8 +703,9 @@ class GatedFFNGrads(_Buffers):
         return cls(make(dx, torch.bfloat16, T, d), make(weights, dtype, 2 * f, d), make(weights, dtype, d, f),
                    make(True, torch.uint8, n))
 
-    def _pointers(self, T, d, f, stream):
-        """Addresses of dx, dW1, dW2, whether the weights' are fp32, the workspace and its bytes; checked."""
+    def _pointers(self, T, d, f, stream, device):
+        """Addresses of dx, dW1, dW2, whether the weights' are fp32, the workspace and its bytes; checked
+        (to be on the current `device`, too)."""
         if self.workspace is None:
             n = int(lib.moe_gated_ffn_backward_workspace_size(T, d, f))
             like = next((t for t in (self.dx, self.dW1, self.dW2) if t is not None), None)
@@ -702,7 +713,7 @@ class GatedFFNGrads(_Buffers):
                 raise ValueError("out has none of dx, dW1 and dW2")
             self.workspace = _empty((n,), torch.uint8, like, stream)
         dx, dW1, dW2, ws = self.dx, self.dW1, self.dW2, self.workspace
-        key = (T, d, f, dx is None, dW1 is None, dW2 is None)
+        key = (T, d, f, dx is None, dW1 is None, dW2 is None, device)
         tensors = [t for t in (dx, dW1, dW2, ws) if t is not None]
         at = self._same(key, tensors)
         if at is None:
@@ -715,6 +726,7 @@ class GatedFFNGrads(_Buffers):
             if dW2 is not None:
                 _need(dW2, wide, (d, f), "out.dW2")
             _need(ws, torch.uint8, (ws.numel(),), "out.workspace")
+            _here(*tensors)
             at = self._keep(key, tensors, (_ptr(dx), _ptr(dW1), _ptr(dW2), int(wide is f32), ws.data_ptr(), ws.numel()))
         return at
 
@@ -730,10 +742,10 @@ def gated_ffn_backward(x, preact, dy, W1, W2, act: str = "silu", *, add=None, ou
     xp, dyp, ap = _in(x, bf16, shape, "x"), _in(dy, bf16, shape, "dy"), None if add is None else _in(add, bf16, shape,
                                                                                                     "add")
     pp = _in(preact, bf16, (T, 2 * f), "preact")
-    _here(x)
+    device = _here(x, preact, dy, W1, W2, add)
     if out is None:
         out = _on(stream, lambda: GatedFFNGrads.empty(T, d, f, device=x.device))
-    _check(lib.moe_gated_ffn_backward(xp, pp, dyp, w1, w2, ap, _act(act), T, d, f, *out._pointers(T, d, f, stream),
+    _check(lib.moe_gated_ffn_backward(xp, pp, dyp, w1, w2, ap, _act(act), T, d, f, *out._pointers(T, d, f, stream, device),
                                       _stream_of(x, stream)), "moe_gated_ffn_backward")
     return out
 
@@ -1256,23 +1268,24 @@ class GatedFFN(_Buffers):
         self.calls += 1
         bf16, shape = torch.bfloat16, (T, self.d)
         xp, ap = _in(x, bf16, shape, "x"), None if add is None else _in(add, bf16, shape, "add")
+        device = _here(x, add, out, pre)
         if out is None:
             out = _empty(shape, bf16, x, stream)
-        _here(x)
-        w1, w2, ws, n = self._pointers()
+        w1, w2, ws, n = self._pointers(device)
         _check(lib.moe_gated_ffn(xp, w1, w2, ap, _act(self.act), T, self.d, self.f, _in(out, bf16, shape, "y"), _ptr(pre),
                                  ws, n, _stream_of(x, stream)), "moe_gated_ffn")
         return out
 
-    def _pointers(self):
+    def _pointers(self, device):
         """Addresses of the weights and of the workspace, and its bytes; checked where they are new."""
         tensors = [self.W1, self.W2, self.workspace]
-        at = self._same(None, tensors)
+        at = self._same(device, tensors)
         if at is None:
             W1, W2, ws = tensors
             at = (_in(W1, torch.bfloat16, (2 * self.f, self.d), "W1"), _in(W2, torch.bfloat16, (self.d, self.f), "W2"),
                   _in(ws, torch.uint8, (ws.numel(),), "workspace"), ws.numel())
-            self._keep(None, tensors, at)
+            _here(*tensors)
+            self._keep(device, tensors, at)
         return at
 
     def backward(self, x, dy, grads=None, workspace=None, stream=None, add=None):
