@@ -1147,18 +1147,19 @@ class MoELayer:
         if x.shape[0] > self.T_max:
             raise ValueError("more tokens than the workspace was sized for")
         self.calls += 1
-        pre = None
+        self.preact = pre = None   # until they are written: backward() takes nothing of a call that was refused
         if save_preact:
             n = x.shape[0] * self.K * 2 * self.f
             if self._preact_buf is None or self._preact_buf.numel() < n:
                 self._preact_buf = _empty((self.T_max * self.K * 2 * self.f,), torch.bfloat16, x, stream)
             pre = self._preact_buf[:n].view(x.shape[0] * self.K, 2 * self.f)
+        out = forward(x, self.Wr, self.bias, self.W1, self.W2, self.K, out=out, workspace=self.workspace,
+                      stream=stream, preact=pre, rule=self.rule, sel_bias=self.sel_bias)
         self.preact = pre
         # moe_forward may fuse the permute into GEMM1 and leave x_perm
         # unwritten; the training forward (save_preact) always writes it
         self._x_perm_written = save_preact or not forward_fuses_permute(x.shape[0], self.d, self.E, self.K, self.f)
-        return forward(x, self.Wr, self.bias, self.W1, self.W2, self.K, out=out, workspace=self.workspace,
-                       stream=stream, preact=pre, rule=self.rule, sel_bias=self.sel_bias)
+        return out
 
     def backward(self, x, dy, grads=None, workspace=None, stream=None):
         """Gradients of sum(dy * y) for the last call (same x): dict of dx
@@ -1259,21 +1260,22 @@ class GatedFFN(_Buffers):
         T = x.shape[0]
         if T > self.T_max:
             raise ValueError("more tokens than the workspace was sized for")
+        self.calls += 1
+        self.preact = None   # until they are written: backward() takes nothing of a call that was refused
+        bf16, shape = torch.bfloat16, (T, self.d)
+        xp, ap = _in(x, bf16, shape, "x"), None if add is None else _in(add, bf16, shape, "add")
         pre = None
         if save_preact:
             if self._preact_buf is None:
-                self._preact_buf = _empty((self.T_max, 2 * self.f), torch.bfloat16, x, stream)
+                self._preact_buf = _empty((self.T_max, 2 * self.f), bf16, x, stream)
             pre = self._preact_buf[:T]
-        self.preact = pre
-        self.calls += 1
-        bf16, shape = torch.bfloat16, (T, self.d)
-        xp, ap = _in(x, bf16, shape, "x"), None if add is None else _in(add, bf16, shape, "add")
         device = _here(x, add, out, pre)
         if out is None:
             out = _empty(shape, bf16, x, stream)
         w1, w2, ws, n = self._pointers(device)
         _check(lib.moe_gated_ffn(xp, w1, w2, ap, _act(self.act), T, self.d, self.f, _in(out, bf16, shape, "y"), _ptr(pre),
                                  ws, n, _stream_of(x, stream)), "moe_gated_ffn")
+        self.preact = pre
         return out
 
     def _pointers(self, device):
