@@ -462,6 +462,7 @@ moe_status_t norm_residual_impl(const void *r, int residual_fp32, const uint16_t
     if (dropout) {
         if ((st = check_dropout(p, rng, &a)) != MOE_OK) return st;
         if (!rng_out || !aligned(rng_out, 8)) return MOE_ERR_INVALID_ARG;
+        if (rng_out + 1 == rng || rng_out == rng + 1) return MOE_ERR_INVALID_ARG;  // every row reads rng
         a.rng_out = rng_out;
     }
     if (!r || !aligned(r, 16)) return MOE_ERR_INVALID_ARG;

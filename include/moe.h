@@ -238,8 +238,9 @@ moe_status_t moe_norm_residual_backward(const void *r_out, int residual_fp32, co
  * key seed and the counter (i / 8, call), and is kept where that is at least
  * round(65536 p).  p counts in those steps of 2^-16, in the scale too; 0 <= p
  * and round(65536 p) < 65536.  y is required.  The mask is not stored:
- * rng_out [2] (which may be rng) receives the two words, and the backward draws
- * the same again from them.  As many launches and the same workspace as without. */
+ * rng_out [2] (rng itself, or apart from it) receives the two words, and the
+ * backward draws the same again from them.  As many launches and the same
+ * workspace as without. */
 moe_status_t moe_norm_residual_dropout(const void *r, int residual_fp32, const uint16_t *y, const float *gamma_post,
                                        const float *gate, int gate_kind, float res_scale, const float *gamma_pre,
                                        float eps, double p, const uint64_t *rng, int T, int d, void *r_out, uint16_t *n,
