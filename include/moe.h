@@ -263,7 +263,7 @@ moe_status_t moe_norm_residual_dropout_backward(const void *r_out, int residual_
  * once, as the second product's operand, y once after add.  preact [T, 2f] bf16
  * (nullable) receives [g | u], which the backward needs.  `workspace` (16-byte
  * aligned, moe_gated_ffn_workspace_size(T, d, f) bytes) holds h.  d and f
- * multiples of 8.  preact and the workspace are apart from each other and from
+ * multiples of 8, d and 2 f up to 2^27, T up to 2^31 - 256.  preact and the workspace are apart from each other and from
  * the rest, y from W2 (it may be x).  Sums have a fixed order: deterministic.
  * 2 kernel launches. */
 enum { MOE_ACT_SILU = 0, MOE_ACT_GELU = 1, MOE_ACT_GELU_TANH = 2, MOE_ACT_RELU = 3 };
@@ -280,7 +280,8 @@ moe_status_t moe_gated_ffn(const uint16_t *x, const uint16_t *W1, const uint16_t
  * else they are apart; none of the three overlaps another one or x (with dW1),
  * dy (with dW2), W1 (with dx) or, but for dx, add; the workspace nothing.  dh is not rounded, da and h to bf16 once
  * each, as operands.  `workspace` (16-byte aligned) holds
- * moe_gated_ffn_backward_workspace_size(T, d, f) bytes.  Deterministic (the
+ * moe_gated_ffn_backward_workspace_size(T, d, f) bytes.  T up to 2^27 with dW1
+ * or dW2, which are sums over it.  Deterministic (the
  * order of dx's sums is another one for other sizes, and may be where not all
  * three are wanted).  2 or 3 kernel launches. */
 size_t moe_gated_ffn_backward_workspace_size(int T, int d, int f);
