@@ -208,8 +208,6 @@ __device__ __forceinline__ void weights(const NormResidualArgs &a, uint32_t col,
 // at most); without dropout, nothing.
 template <bool DROP, int VPT>
 struct Draws {
-    uint4 w[VPT];
-    static constexpr uint32_t bar = 0;
     __device__ __forceinline__ explicit Draws(const NormResidualArgs &) {}
     __device__ __forceinline__ void row(int64_t, int, uint32_t) {}
     __device__ __forceinline__ uint32_t mask(int64_t, int, uint32_t) { return 0; }
@@ -543,11 +541,10 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
     Row f = factors(begin), next = factors(begin + step);
     int slot = 0, turn = 0;
     int phase = 0;  // of the slot that first_pass reads next
-    uint32_t k = 0, kept = 0, kept_next = 0;
-    if (PIPE && begin < rows_end) {
-        kept = draws.mask(begin, a.d, own.col);
+    uint32_t k = 0, kept = 0;
+    if (PIPE && begin < rows_end) {  // (never with dropout)
         rows.wait(0, 0);
-        first_pass(0, f.rq, red[0], 0, kept);
+        first_pass(0, f.rq, red[0], 0, 0);
     }
     for (uint32_t t = begin; t < rows_end; t += step) {
         const Row after = factors(t + 2 * step);
@@ -557,12 +554,11 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
             s = collect(red[turn], k);
             if (ahead == 0) phase ^= 1;
             if (t + step < rows_end) {
-                kept_next = draws.mask(t + step, a.d, own.col);  // while the row is on its way
                 rows.wait(ahead, phase);
-                first_pass(ahead, next.rq, red[other], k + 1, kept_next);
+                first_pass(ahead, next.rq, red[other], k + 1, 0);
             }
         } else {
-            kept = draws.mask(t, a.d, own.col);
+            kept = draws.mask(t, a.d, own.col);  // while the row is on its way
             rows.wait(slot, phase);
             first_pass(slot, f.rq, red[turn], k, kept);
             s = collect(red[turn], k);
@@ -624,7 +620,6 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
         slot = ahead;
         f = next;
         next = after;
-        if (PIPE) kept = kept_next;
     }
     // the CTA's sums: the teams' ones in the rings, now empty, added in the teams' order
     float *out = part + static_cast<size_t>(group) * 2 * a.d, *held = reinterpret_cast<float *>(ring);
