@@ -304,7 +304,10 @@ struct Warp {
             } else {
                 uint32_t u[16], h[16];
                 read_row(box + BUF, lane, u);
-                __syncwarp();  // the whole warp has read them
+                // the whole warp has read them: without the fence a copy could land before a
+                // read that was still on its way (once in 2e6 chunks)
+                fence_proxy_async_smem();
+                __syncwarp();
                 ask_for(2);
                 with_activation(p.act, [&](auto act) {
 #pragma unroll
