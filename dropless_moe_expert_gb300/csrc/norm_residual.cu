@@ -133,6 +133,13 @@ struct Ring {
     }
 };
 
+// The warp has read a slot: its refill lands behind that.  (Without the fence a
+// copy may overtake a read that is still on its way.)
+__device__ __forceinline__ void read_before_copies() {
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
@@ -304,7 +311,7 @@ norm_residual_kernel(Args a, float inv_d, const R *r, R *r_out, uint16_t *__rest
                 for (int i = 0; i < 4; ++i) ss = fma2(y[j][i], y[j][i], ss);
             }
         }
-        __syncwarp();  // the warp has read the row
+        read_before_copies();
         issue(t + stages * step, slot);
         slot = slot + 1 == stages ? 0 : slot + 1;
         if (slot == 0) phase ^= 1;
@@ -593,7 +600,7 @@ norm_residual_bwd_kernel(Args a, float inv_d, const R *__restrict__ r_out, const
                 if (has_y) read8<uint16_t>(at16 + j * 512, y);
             }
             if (j == VPT - 1) {
-                __syncwarp();  // the warp has read the row
+                read_before_copies();
                 issue(t + stages * step, slot);
             }
             if (!own.on[j]) continue;

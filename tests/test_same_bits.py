@@ -45,3 +45,25 @@ def test_feed_forward(T, d, f, act, dtype, calls):
 
     assert _count(run, lambda: run(1), calls) == 0
     assert moe.device_status() == 0
+
+
+@pytest.mark.parametrize("dropout", [0.0, 0.1])
+@pytest.mark.parametrize("T,d,dt,post,pre", [(8192, 4096, BF16, 1, 1), (4093, 7168, F32, 0, 1), (4096, 1024, BF16, 1, 1),
+                                             (2048, 12288, BF16, 1, 1), (8192, 512, F32, 1, 0), (8192, 2048, BF16, 0, 0)])
+def test_norms(T, d, dt, post, pre, dropout):
+    sets = []
+    for k in range(2):
+        r, y, dr, dn = (_normal(T, d, seed=4 * k + i).to(t) for i, t in enumerate((dt, BF16, dt, BF16)))
+        kw = dict(gamma_post=1 + _normal(d, seed=9, scale=0.1) if post else None, dropout=dropout,
+                  gamma_pre=1 + _normal(d, seed=8, scale=0.1) if pre else None, rng=torch.tensor([3, k], device="cuda"))
+        sets.append((r, y, dr, dn if pre else None, kw, moe.NormResidual.empty(T, d, dt, post=bool(post), pre=bool(pre), rng=True),
+                     moe.NormResidualGrads.empty(T, d, dt, post=bool(post), pre=bool(pre))))
+
+    def run(k=0):
+        r, y, dr, dn, kw, o, g = sets[k]
+        moe.norm_residual(r, y, out=o, **kw)
+        moe.norm_residual_backward(o.r, dr, dn, y, rstd_post=o.rstd_post, rstd_pre=o.rstd_pre, out=g, **kw)
+        return [t for t in (o.r, o.n, o.rstd_post, o.rstd_pre, g.dr, g.dy, g.dgamma_pre, g.dgamma_post) if t is not None]
+
+    assert _count(run, lambda: run(1), 400) == 0
+    assert moe.device_status() == 0
