@@ -573,7 +573,8 @@ def norm_residual(r, y=None, *, gamma_post=None, gate=None, gamma_pre=None, res_
 
     ``dropout`` > 0 drops that share of what is added to res_scale * r (and
     scales the rest by 1 / (1 - dropout)), by draws from ``rng``, a seed and a
-    call number [2] int64 on the device: another number in each call draws anew.
+    call number [2] int64 on the device: another number in each call draws anew,
+    the same one the same mask again.
     The result's ``rng`` is a copy of them for the backward; no mask is kept.
     0 drops nothing, and rng is not read."""
     T, d, kind, rp, yp, postp, gatep, prep = _norm_args(r, y, gamma_post, gate, gamma_pre)
@@ -685,6 +686,8 @@ def gated_ffn(x, W1, W2, act: str = "silu", *, add=None, out=None, preact=None, 
 
 @dataclass
 class GatedFFNGrads(_Buffers):
+    """Outputs and workspace of gated_ffn_backward, written over by each call
+    (so calls that may run at the same time need buffers of their own)."""
     dx: torch.Tensor | None = None    # [T, d] bf16
     dW1: torch.Tensor | None = None   # shaped like the weights, bf16 or fp32
     dW2: torch.Tensor | None = None
@@ -1241,7 +1244,8 @@ class GatedFFN(_Buffers):
     for up to T_max tokens: a dense layer, or the ``shared`` expert of a MoEBlock.
     ``__call__(x)`` runs the forward; with ``save_preact`` it keeps what
     backward() needs of it (its last call's), as MoELayer does.  The weights
-    may be replaced between calls by others of their shapes."""
+    may be replaced between calls by others of their shapes.  Calls (and
+    captured graphs) that may run at the same time need objects of their own."""
     rule = None
 
     def __init__(self, W1, W2, act: str = "silu", T_max: int = 1):
@@ -1335,7 +1339,10 @@ class MoEBlock:
         next block.  ``pre``: what the block before returned for this block's
         gamma_pre (else the norm is taken here).  ``save`` keeps what backward()
         needs.  ``rng`` (see norm_residual) turns the dropout on: without it
-        nothing is dropped, as when a model answers."""
+        nothing is dropped, as when a model answers.  It is neither advanced nor
+        told apart by block: give each block of each step a call number of its
+        own (``rng[1] += 1`` between them will do, the backward goes by a copy),
+        as blocks with the same one drop the same elements."""
         rule = self.layer.rule
         if save and rule is not None and rule.score == "softmax" and not rule.renorm:
             raise ValueError("raw softmax scores have no backward in the layer: save=True needs a rule with renorm")

@@ -43,9 +43,9 @@ constexpr int TILE_M = 256, TILE_N = 256;
 constexpr int BAND = 8;         // row blocks that sweep the column blocks together
 // Epilogue warps: of GATED eight, two per lane quarter with half of a tile's columns
 // each, as the last tile's epilogue is waited for (1003 x 2056 x 1368: 30.9 us with
-// four, 30.0); DACT's buffers would leave eight a shorter ring (its backward 64
-// and 66.5 us, 4096 x 7168 x 2048 400 and 411), or no input ahead (level: two warps per
-// scheduler then take twice as long for a chunk).
+// four, 30.0); DACT's buffers would leave eight a shorter ring (as measured when its
+// outputs still took their inputs' place and that backward 64 us: 66.5, 4096 x 7168 x 2048 400
+// and 411), or no input ahead (level: two warps per scheduler then take twice as long for a chunk).
 __host__ __device__ constexpr int epi_warps(Epi epi) { return epi == GATED ? 8 : 4; }
 __host__ __device__ constexpr int threads_of(Epi epi) { return 64 + 32 * epi_warps(epi); }
 constexpr int BOX = 64 * 64 * 2;  // an MN-major box: 64 rows of K x 64 columns

@@ -3,8 +3,10 @@
 // silu(g) = g s(g) with the logistic function s, gelu_tanh(g) = g s(z) with
 // z = 2 sqrt(2 / pi) (g + 0.044715 g^3), because (1 + tanh(z / 2)) / 2 = s(z);
 // gelu(g) = g Phi(g) with the normal distribution function, relu(g) = max(g, 0).
-// Each is within a few 2^-22 of its value (and 2^-22 of the exponent that it
-// takes), far below the bf16 rounding of what it feeds.
+// Each is within a few 2^-22 of the magnitudes of its terms (and 2^-22 of the
+// exponent that they take), far below the bf16 rounding of what it feeds: of its
+// value too, but for a derivative whose terms cancel (silu's near g = -1.28)
+// and a factor below 2^-126, which is 0.
 //
 // Two values at a time: what an epilogue warp issues is what bounds the tiles
 // with few slices of K, and packed fp32 instructions are half as many.
@@ -48,8 +50,8 @@ __device__ __forceinline__ float2 logistic(float2 z) {
 
 // Phi(g) of the normal distribution, and e = exp(-g^2 / 2).  The smaller tail is
 // e t Q(t) with t = 1 / (1 + 0.3 |g| / sqrt 2): Q, a polynomial of degree 8, was fitted
-// to exp(x^2) erfc(x) / (2 t) at x = |g| / sqrt 2, from 0 to 10, least relative error
-// at most 2e-8 (in fp32 about 5e-7 near 0; the rounding of g^2 / 2 counts beyond).
+// to exp(x^2) erfc(x) / (2 t) at x = |g| / sqrt 2, from 0 to 10, for a small relative error:
+// 3.4e-8 at most, at x = 10 (in fp32 about 5e-7 near 0; the rounding of g^2 / 2 counts beyond).
 __device__ __forceinline__ float2 normal_cdf(float2 g, float2 &e) {
     const float2 a = make_float2(fabsf(g.x), fabsf(g.y));
     const float2 t = rcp_approx(fma2(both(0.21213203435596426f), a, both(1.0f)));

@@ -15,19 +15,19 @@
 //   r' = a r + m g u,   and D in all of the y side's gradients is m D,   m = 0 or 1 / (1 - p)
 // drawn again in the backward from the same state, before the row's bytes are
 // waited for.  It adds no bytes, about 10 integer instructions per element and, in
-// the backward, two tests.  Measured, 8192 x 4096 bf16 with both norms: forward 52.8 us
-// a call (43.8 without dropout), backward 87.5 (68.0); 4093 x 7168 with the stream in fp32
-// and without gamma_post 54.9 and 94.7.  One round of the generator instead of ten
+// the backward, two tests.  Measured, 8192 x 4096 bf16 with both norms: forward 53.3 us
+// a call (43.5 without dropout), backward 89.3 (68.1); 4093 x 7168 with the stream in fp32
+// and without gamma_post 54.9 and 95.0.  One round of the generator instead of ten
 // would take 10 us off either; a mask held as bits in one register is better than the
 // draws themselves (2048 x 12288: 104 us), and predicates are than masks of the
 // operands' bits where rows are bf16 (63 and 59 us for the residual's sum alone).
 // The sums over t run in a fixed order: each CTA over its own rows, then the
 // CTAs' partial sums in their order.
 //
-// Memory bounds both.  Measured: forward of 8192 x 4096 bf16 43.8 us, 6.1 TB/s,
-// where a plain copy of as many bytes takes 46.8; backward 68.0 us, 5.9 TB/s,
+// Memory bounds both.  Measured: forward of 8192 x 4096 bf16 43.5 us, 6.2 TB/s,
+// where a plain copy of as many bytes takes 46.8; backward 68.1 us, 5.9 TB/s,
 // 4 of it the column sums; the main kernel takes as long with its arithmetic left out;
-// backward of 4093 x 7168 with the stream in fp32 86.5 us, 6.1 TB/s.
+// backward of 4093 x 7168 with the stream in fp32 84.5 us, 6.3 TB/s.
 #include "kernels.h"
 #include "philox.cuh"
 #include "ptx.cuh"

@@ -197,3 +197,18 @@ def test_nothing_is_checked_twice(calls, monkeypatch):
     ffn.W2 = ffn.W2.view(D, F)
     ffn(x, out=out)
     assert "x" in asked and not {"W1", "W2", "workspace"} & set(asked) and len(calls) == 2
+
+
+def test_in_other_modes_of_torch(calls):
+    """Checks that were made in one mode hold, or are made again, in another."""
+    ffn, x, out = _ffn(), here(T, D), here(T, D)
+    for mode in (torch.no_grad, torch.inference_mode, torch.enable_grad, torch.inference_mode):
+        with mode():
+            for _ in range(2):
+                ffn(x, out=out)
+    ffn.W2 = torch.nn.Parameter(ffn.W2, requires_grad=False)
+    assert len(calls) == 8
+    with pytest.raises(ValueError, match="W2"), torch.inference_mode():
+        ffn.W2 = here(D, F).t()
+        ffn(x, out=out)
+    assert len(calls) == 8
