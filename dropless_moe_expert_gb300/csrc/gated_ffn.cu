@@ -753,7 +753,10 @@ __global__ void __launch_bounds__(FEW_THREADS) ffn_few_kernel(const __grid_const
         };
         // the weights do not wait for the kernel before, where that is one of this operator's
         constexpr bool FIRST = EPI == GATED || EPI == DACT;
-        if (FIRST) grid_dependency_wait_to_copy();
+        if (FIRST)
+            grid_dependency_wait_to_copy();
+        else
+            fence_proxy_async();  // what was stored before the kernel in front, which has waited for it
         const int first = min(kbs, p.stages);
         for (int i = 0; i < first; ++i) weights(i, i);
         if (!FIRST) grid_dependency_wait_to_copy();

@@ -97,3 +97,33 @@ def test_norms_between_feed_forwards(T, d, f, dt):
         return out
 
     _bits(step)
+
+
+@pytest.mark.parametrize("T,d,f", [(1, 1024, 512), (48, 4096, 1536), (100, 1416, 520), (129, 328, 776), (200, 256, 8192)])
+def test_weights_made_just_before(T, d, f):
+    """Weights that a plain kernel has stored right before the call: the second and the third kernel of it ask
+    for theirs before the ones in front of them have ended."""
+    x, dy = _normal(T, d, seed=0).to(BF16), _normal(T, d, seed=1).to(BF16)
+    made = [_weights(d, f, 2 * k) for k in range(3)]
+    W1, W2 = (torch.empty_like(t) for t in made[0])
+    ffn, pre = moe.GatedFFN(W1, W2, T_max=T), torch.empty(T, 2 * f, dtype=BF16, device="cuda")
+    one = torch.ones((), dtype=BF16, device="cuda")
+
+    def step(between):
+        out = []
+        for a, b in made:
+            torch.mul(a, one, out=W1)
+            torch.mul(b, one, out=W2)
+            between()
+            y = ffn(x, save_preact=True)
+            between()
+            pre.copy_(ffn.preact)
+            torch.mul(b, one, out=W2)
+            torch.mul(a, one, out=W1)
+            between()
+            g = moe.gated_ffn_backward(x, pre, dy, W1, W2)
+            between()
+            out += [y, g.dx, g.dW1, g.dW2]
+        return out
+
+    _bits(step)
